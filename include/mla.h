@@ -339,6 +339,147 @@ mla_status_t mla_decode_fp8_planned(const void *q, void *cache8, const void *kv_
                                     int32_t *dev_status, void *stream);
 
 /*
+ * mla_rope_append — a step's new tokens from the projections into the cache:
+ * the latent's norm, the position rotation and the paged store in one launch,
+ * with the rotation of the tokens' rotary query dims beside them.
+ *
+ * mla_cache_append stores rows that are finished; this takes them as
+ * kv_a_proj_with_mqa leaves them (512 latent dims, then the 64 shared key dims
+ * without a position [MLA 的 TP 切分 (10100.com), section 2.2]).  For token t
+ * with c = kv[t, 0:512], k = kv[t, 512:576] and position n = positions[t]:
+ *     c' = norm_weight * c / sqrt(mean(c^2) + eps)     (c itself without a weight)
+ *     k' = k with each of its 32 pairs (a, b), pair i, replaced by
+ *          (a cos - b sin, b cos + a sin), cos = cos_sin[n, i], sin = cos_sin[n, 32 + i]
+ *     cache row slot_mapping[t] = [c', k']
+ *     q_out[t, h, :] = the same rotation of q_pe[t, h, :], for every head
+ * all in fp32, rounded once to bf16.  Pair i is elements 2i and 2i + 1 when
+ * interleaved is 1, elements i and i + 32 when it is 0.
+ *
+ *   kv            bf16, row t at kv + t * kv_stride (elements; a multiple of 8, >= 576)
+ *   positions     int64 [num_tokens]; outside [0, max_position): the token is
+ *                 left out (neither row nor query is written) and reported as
+ *                 MLA_ERR_DEVICE_RANGE
+ *   cos_sin       fp32 [max_position, 64]: 32 cosines, then 32 sines
+ *   slot_mapping  int64 [num_tokens], as in mla_cache_append: -1 stores no row
+ *                 (the query is rotated all the same); an out-of-pool slot is
+ *                 skipped and reported; two tokens with one slot race
+ *   norm_weight   bf16 [512], or NULL: the latent is stored as it is
+ *   eps           >= 0 and finite (not looked at without a weight)
+ *   cache         bf16 [num_blocks, block_size, 576], updated in place
+ *   q_pe, q_out   bf16, head h of token t at q_pe + t * q_token_stride + h *
+ *                 q_head_stride (elements; multiples of 8, not negative; the
+ *                 same for q_out, where heads may not overlap).  Both NULL: no
+ *                 query.  They may be one tensor with the same strides (in
+ *                 place), and q_out may be the rotary dims of mla_decode's q.
+ *   num_heads     1 to 128 (not looked at without a query)
+ * Pointers to bf16 and fp32 data 16-byte aligned, to int64 data 8-byte.
+ * num_tokens = 0 is a no-op; num_tokens < 2^31, block_size >= 1.
+ *
+ * mla_rope_append_fp8 — the same into an FP8 latent cache (uint8 [num_blocks,
+ * block_size, 576], see below): each fp32 value x of the row is stored as the
+ * E4M3 code nearest to x * fp32(1 / kv_scale), ties to even, saturating to
+ * +-448; it is not rounded to bf16 on the way.  kv_scale and 1 / kv_scale must
+ * be positive and finite.
+ */
+mla_status_t mla_rope_append(const void *kv, int64_t kv_stride, const int64_t *positions,
+                             const float *cos_sin, int64_t max_position,
+                             const int64_t *slot_mapping, int64_t num_tokens,
+                             const void *norm_weight, float eps, int32_t interleaved, void *cache,
+                             int64_t num_blocks, int32_t block_size, const void *q_pe,
+                             int64_t q_token_stride, int64_t q_head_stride, void *q_out,
+                             int64_t q_out_token_stride, int64_t q_out_head_stride,
+                             int32_t num_heads, int32_t *dev_status, void *stream);
+mla_status_t mla_rope_append_fp8(const void *kv, int64_t kv_stride, const int64_t *positions,
+                                 const float *cos_sin, int64_t max_position,
+                                 const int64_t *slot_mapping, int64_t num_tokens,
+                                 const void *norm_weight, float eps, int32_t interleaved,
+                                 void *cache8, int64_t num_blocks, int32_t block_size,
+                                 float kv_scale, const void *q_pe, int64_t q_token_stride,
+                                 int64_t q_head_stride, void *q_out, int64_t q_out_token_stride,
+                                 int64_t q_out_head_stride, int32_t num_heads,
+                                 int32_t *dev_status, void *stream);
+
+/*
+ * mla_expand_kv — cached latent rows as per-head keys and values, for
+ * mla_prefill (the expanded form that prompts are attended in; decode keeps
+ * the absorbed form).  The weights are those of mla_absorb_q / mla_absorb_out.
+ * Request b's tokens are output rows [kv_offsets[b], kv_offsets[b+1]); with C
+ * the 512 latent dims of token j's cached row and t = kv_offsets[b] + j:
+ *     k_nope[t, h, d] = sum_l C[l] W_UK[h, d, l]
+ *     v[t, h, n]      = sum_l C[l] W_UV[h, l, n]      (fp32 sums, one rounding)
+ *     k_pe[t, :]      = the row's 64 rotary dims
+ *   cache        bf16 [num_blocks, block_size, 576], any block_size >= 1
+ *   block_table  int32 [batch, max_blocks_per_seq], as in mla_decode
+ *   kv_offsets   int32 [batch + 1] (device), non-decreasing, within [0, total_kv]
+ *                (others are reported as MLA_ERR_DEVICE_RANGE, nothing is
+ *                touched out of place); rows before the first and behind the
+ *                last are left as they are
+ *   w_uk bf16 [num_heads, 128, 512]   w_uv bf16 [num_heads, 512, 128]
+ *   k_nope, v    bf16 [total_kv, num_heads, 128]   k_pe bf16 [total_kv, 64]
+ * num_heads 1 to 128 (else MLA_ERR_UNSUPPORTED).  A token whose page lies
+ * outside the table or the pool is reported as MLA_ERR_DEVICE_RANGE and its
+ * rows are unspecified.
+ *
+ * mla_expand_kv_fp8 — the same from an FP8 latent cache: the elements are
+ * value(code) * kv_scale.  The products run on the codes' values and kv_scale
+ * multiplies the fp32 sums.
+ */
+mla_status_t mla_expand_kv(const void *cache, int64_t num_blocks, int32_t block_size,
+                           const int32_t *block_table, int32_t max_blocks_per_seq,
+                           const int32_t *kv_offsets, int32_t batch, int64_t total_kv,
+                           const void *w_uk, const void *w_uv, int32_t num_heads, void *k_nope,
+                           void *v, void *k_pe, int32_t *dev_status, void *stream);
+mla_status_t mla_expand_kv_fp8(const void *cache8, int64_t num_blocks, int32_t block_size,
+                               const int32_t *block_table, int32_t max_blocks_per_seq,
+                               const int32_t *kv_offsets, int32_t batch, int64_t total_kv,
+                               const void *w_uk, const void *w_uv, int32_t num_heads,
+                               float kv_scale, void *k_nope, void *v, void *k_pe,
+                               int32_t *dev_status, void *stream);
+
+/*
+ * mla_prefill — attention of prompt tokens in the expanded form.  Each head
+ * has its own 128 key dims and 128 value dims; the 64 rotary key dims are
+ * shared by all heads.  Request b's queries are rows [q_offsets[b],
+ * q_offsets[b+1]) and its keys rows [kv_offsets[b], kv_offsets[b+1]); with nq
+ * and nk their counts and i, j counted inside the request:
+ *     s_ij = softmax_scale * (q_nope_i . k_nope_j + q_pe_i . k_pe_j)
+ *     key j is visible to query i when j < nk and, if causal, j <= nk - nq + i
+ *     out_i = sum_j softmax(s_i)_j v_j      lse_i = log sum_j exp(s_ij)
+ * over the visible keys: causal queries are the last nq tokens of the context.
+ * A query that sees no key (nk = 0, or i < nq - nk) gets out = 0, lse = -inf.
+ *   q_nope [total_q, heads, 128]  q_pe [total_q, heads, 64]
+ *   k_nope [total_kv, heads, 128]  k_pe [total_kv, 64]  v [total_kv, heads, 128]
+ *                bf16, rows of contiguous dims at the given token and head
+ *                strides (elements: multiples of 8, at least a row's width,
+ *                below 2^38), 16-byte aligned
+ *   q_offsets, kv_offsets   int32 [batch + 1] (device), non-decreasing, within
+ *                [0, total_q] and [0, total_kv].  Others are reported as
+ *                MLA_ERR_DEVICE_RANGE; nothing is read or written out of place
+ *   softmax_scale  positive and finite
+ *   out          bf16 [total_q, heads, 128]   lse fp32 [total_q, heads] or NULL
+ *                (rows of no request are left as they are)
+ *   workspace    NULL, or mla_prefill_workspace_size() bytes, 256-byte
+ *                aligned, contents free: lets a call of few queries on long
+ *                contexts spread the keys over the whole GPU.  Calls that
+ *                share one must not overlap on the GPU
+ * num_heads 1 to 128 (else MLA_ERR_UNSUPPORTED).  The keys and values of a
+ * request must be finite: a non-finite value row reaches, through a zero
+ * weight, queries of its own request that do not see it.  What other rows
+ * hold never matters.
+ */
+size_t mla_prefill_workspace_size(void);
+mla_status_t mla_prefill(const void *q_nope, int64_t q_nope_token_stride,
+                         int64_t q_nope_head_stride, const void *q_pe, int64_t q_pe_token_stride,
+                         int64_t q_pe_head_stride, const void *k_nope,
+                         int64_t k_nope_token_stride, int64_t k_nope_head_stride,
+                         const void *k_pe, int64_t k_pe_token_stride, const void *v,
+                         int64_t v_token_stride, int64_t v_head_stride, const int32_t *q_offsets,
+                         const int32_t *kv_offsets, int32_t batch, int64_t total_q,
+                         int64_t total_kv, int32_t num_heads, int32_t causal, float softmax_scale,
+                         void *out, float *lse, void *workspace, size_t workspace_bytes,
+                         int32_t *dev_status, void *stream);
+
+/*
  * mla_decode_noalloc — mla_decode for callers that cannot allocate device
  * memory.  The pages have no counterpart to this entry point; it exists for
  * users of this library.

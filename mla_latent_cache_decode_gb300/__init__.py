@@ -31,7 +31,8 @@ EXPORTED = ("mla_status_string", "mla_last_error_detail", "mla_abi_version", "ml
             "mla_combine", "mla_decode_noalloc", "mla_decode_partial", "mla_combine_planned",
             "mla_decode_append_planned", "mla_place_requests", "mla_place_one", "mla_absorb_q",
             "mla_absorb_out", "mla_selftest_wait_timeout", "mla_cache_append_fp8",
-            "mla_decode_fp8", "mla_decode_fp8_planned")
+            "mla_decode_fp8", "mla_decode_fp8_planned", "mla_rope_append", "mla_rope_append_fp8",
+            "mla_expand_kv", "mla_expand_kv_fp8", "mla_prefill_workspace_size", "mla_prefill")
 
 
 class MlaError(RuntimeError):
@@ -93,6 +94,22 @@ def _load():
     lib.mla_decode_fp8_planned.argtypes = [P, P, P, i64, i32, P, i32, P, i32, i32, i32, f32, f32,
                                            P, P, P, sz, P, P]
     lib.mla_decode_fp8_planned.restype = ctypes.c_int
+    lib.mla_rope_append.argtypes = [P, i64, P, P, i64, P, i64, P, f32, i32, P, i64, i32, P, i64,
+                                    i64, P, i64, i64, i32, P, P]
+    lib.mla_rope_append.restype = ctypes.c_int
+    lib.mla_rope_append_fp8.argtypes = [P, i64, P, P, i64, P, i64, P, f32, i32, P, i64, i32, f32,
+                                        P, i64, i64, P, i64, i64, i32, P, P]
+    lib.mla_rope_append_fp8.restype = ctypes.c_int
+    lib.mla_expand_kv.argtypes = [P, i64, i32, P, i32, P, i32, i64, P, P, i32, P, P, P, P, P]
+    lib.mla_expand_kv.restype = ctypes.c_int
+    lib.mla_expand_kv_fp8.argtypes = [P, i64, i32, P, i32, P, i32, i64, P, P, i32, f32, P, P, P, P,
+                                      P]
+    lib.mla_expand_kv_fp8.restype = ctypes.c_int
+    lib.mla_prefill_workspace_size.argtypes = []
+    lib.mla_prefill_workspace_size.restype = sz
+    lib.mla_prefill.argtypes = [P, i64, i64, P, i64, i64, P, i64, i64, P, i64, P, i64, i64, P, P,
+                                i32, i64, i64, i32, i32, f32, P, P, P, sz, P, P]
+    lib.mla_prefill.restype = ctypes.c_int
     lib.mla_selftest_wait_timeout.argtypes = [ctypes.c_uint64, P, P, P]
     lib.mla_selftest_wait_timeout.restype = ctypes.c_int
     return lib
@@ -390,6 +407,189 @@ def _decode_fp8(fn, kv_new, q, cache8, block_table, seq_lens, softmax_scale, out
              _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
              _ptr(dev_status), _stream(stream)]
     _check(fn(*args))
+    return out
+
+
+def _need_rows(t, dtype, ndim, name):
+    """t as rows of contiguous elements, its outer dims at any strides."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype or t.dim() != ndim or not t.is_cuda or t.stride(-1) != 1:
+        raise ValueError(f"{name}: need CUDA {dtype} with {ndim} dims, the last contiguous, got "
+                         f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+
+
+def _strides(t, row):
+    """Element strides of t's outer dims; a dim of one entry, whose stride says
+    nothing, gets that of a dense tensor with rows of `row` elements."""
+    dense = [row]
+    for n in reversed(t.shape[1:-1]):
+        dense.insert(0, dense[0] * n)
+    return [d if n == 1 else st for n, st, d in zip(t.shape[:-1], t.stride(), dense)]
+
+
+def _on_current(*tensors):
+    """All given tensors live on the current device, whose stream the call uses."""
+    import torch
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+
+
+def _rope_append(fn, cache_dtype, scale, kv, positions, cos_sin, slot_mapping, cache, norm_weight,
+                 eps, interleaved, q_pe, q_pe_out, dev_status, stream):
+    import torch
+    _need_rows(kv, torch.bfloat16, 2, "kv")
+    _need(positions, torch.int64, 1, "positions")
+    _need(cos_sin, torch.float32, 2, "cos_sin")
+    _need(slot_mapping, torch.int64, 1, "slot_mapping")
+    _need(cache, cache_dtype, 3, "cache")
+    T = kv.shape[0]
+    if kv.shape[1] != ROW_DIM or cache.shape[2] != ROW_DIM:
+        raise ValueError("rows must be 576 wide")
+    if cos_sin.shape[1] != ROPE_DIM:
+        raise ValueError("cos_sin must be [positions, 64]")
+    if positions.shape[0] != T or slot_mapping.shape[0] != T:
+        raise ValueError("kv, positions and slot_mapping disagree on the token count")
+    if norm_weight is not None:
+        _need(norm_weight, torch.bfloat16, 1, "norm_weight")
+        if norm_weight.shape[0] != KV_LORA_RANK:
+            raise ValueError("norm_weight must be [512]")
+    if (q_pe is None) != (q_pe_out is None):
+        raise ValueError("q_pe and q_pe_out go together")
+    heads, qs, os = 0, (0, 0), (0, 0)
+    if q_pe is not None:
+        _need_rows(q_pe, torch.bfloat16, 3, "q_pe")
+        _need_rows(q_pe_out, torch.bfloat16, 3, "q_pe_out")
+        heads = q_pe.shape[1]
+        if tuple(q_pe.shape) != (T, heads, ROPE_DIM) or q_pe_out.shape != q_pe.shape:
+            raise ValueError("q_pe and q_pe_out must be [T, H, 64]")
+        qs, os = _strides(q_pe, ROPE_DIM), _strides(q_pe_out, ROPE_DIM)
+    _on_current(kv, positions, cos_sin, slot_mapping, cache, norm_weight, q_pe, q_pe_out,
+                dev_status)
+    _check(fn(_ptr(kv), _strides(kv, ROW_DIM)[0], _ptr(positions), _ptr(cos_sin), cos_sin.shape[0],
+              _ptr(slot_mapping), T, _ptr(norm_weight), float(eps), int(bool(interleaved)),
+              _ptr(cache), cache.shape[0], cache.shape[1], *scale, _ptr(q_pe), qs[0], qs[1],
+              _ptr(q_pe_out), os[0], os[1], heads, _ptr(dev_status), _stream(stream)))
+
+
+def mla_rope_append(kv, positions, cos_sin, slot_mapping, cache, norm_weight=None, eps=1e-6,
+                    interleaved=True, q_pe=None, q_pe_out=None, dev_status=None, stream=None):
+    """New tokens into the cache as the projections leave them: the 512 latent dims of
+    kv [T, 576] normalised (with norm_weight), its 64 rotary key dims rotated by
+    cos_sin[positions] (fp32 [P, 64]: cosines, sines), both stored at slot_mapping; and
+    q_pe_out [T, H, 64] = q_pe rotated alike (may be q_pe itself, or q[..., 512:])."""
+    import torch
+    _rope_append(get_lib().mla_rope_append, torch.bfloat16, (), kv, positions, cos_sin,
+                 slot_mapping, cache, norm_weight, eps, interleaved, q_pe, q_pe_out, dev_status,
+                 stream)
+
+
+def mla_rope_append_fp8(kv, positions, cos_sin, slot_mapping, cache8, kv_scale=1.0,
+                        norm_weight=None, eps=1e-6, interleaved=True, q_pe=None, q_pe_out=None,
+                        dev_status=None, stream=None):
+    """mla_rope_append into an FP8 (E4M3) cache: each fp32 value is stored as the code nearest
+    to x / kv_scale (ties to even, saturating to 448)."""
+    import torch
+    _rope_append(get_lib().mla_rope_append_fp8, torch.uint8, (float(kv_scale),), kv, positions,
+                 cos_sin, slot_mapping, cache8, norm_weight, eps, interleaved, q_pe, q_pe_out,
+                 dev_status, stream)
+
+
+def _expand_kv(fn, cache_dtype, scale, cache, block_table, kv_offsets, w_uk, w_uv, k_nope, v,
+               k_pe, dev_status, stream):
+    import torch
+    _need(cache, cache_dtype, 3, "cache")
+    _need(block_table, torch.int32, 2, "block_table")
+    _need(kv_offsets, torch.int32, 1, "kv_offsets")
+    _need(w_uk, torch.bfloat16, 3, "w_uk")
+    _need(w_uv, torch.bfloat16, 3, "w_uv")
+    _need(k_nope, torch.bfloat16, 3, "k_nope")
+    _need(v, torch.bfloat16, 3, "v")
+    _need(k_pe, torch.bfloat16, 2, "k_pe")
+    T, H = k_nope.shape[0], k_nope.shape[1]
+    B = block_table.shape[0]
+    if cache.shape[2] != ROW_DIM or kv_offsets.shape[0] != B + 1:
+        raise ValueError("shapes: cache [NB,BS,576], block_table [B,M], kv_offsets [B+1]")
+    if (tuple(w_uk.shape) != (H, 128, 512) or tuple(w_uv.shape) != (H, 512, 128)
+            or tuple(k_nope.shape) != (T, H, 128) or tuple(v.shape) != (T, H, 128)
+            or tuple(k_pe.shape) != (T, ROPE_DIM)):
+        raise ValueError("shapes: w_uk [H,128,512], w_uv [H,512,128], k_nope and v [T,H,128], "
+                         "k_pe [T,64]")
+    _on_current(cache, block_table, kv_offsets, w_uk, w_uv, k_nope, v, k_pe, dev_status)
+    _check(fn(_ptr(cache), cache.shape[0], cache.shape[1], _ptr(block_table),
+              block_table.shape[1], _ptr(kv_offsets), B, T, _ptr(w_uk), _ptr(w_uv), H, *scale,
+              _ptr(k_nope), _ptr(v), _ptr(k_pe), _ptr(dev_status), _stream(stream)))
+    return k_nope, v, k_pe
+
+
+def mla_expand_kv(cache, block_table, kv_offsets, w_uk, w_uv, k_nope, v, k_pe, dev_status=None,
+                  stream=None):
+    """Cached latent rows as per-head keys and values for mla_prefill: rows kv_offsets[b] ..
+    kv_offsets[b+1]-1 of k_nope [T,H,128], v [T,H,128] and k_pe [T,64] are tokens 0, 1, ... of
+    request b, through the absorption weights w_uk and w_uv."""
+    import torch
+    return _expand_kv(get_lib().mla_expand_kv, torch.bfloat16, (), cache, block_table, kv_offsets,
+                      w_uk, w_uv, k_nope, v, k_pe, dev_status, stream)
+
+
+def mla_expand_kv_fp8(cache8, block_table, kv_offsets, w_uk, w_uv, k_nope, v, k_pe, kv_scale=1.0,
+                      dev_status=None, stream=None):
+    """mla_expand_kv from an FP8 (E4M3) cache: row elements are value(code) * kv_scale."""
+    import torch
+    return _expand_kv(get_lib().mla_expand_kv_fp8, torch.uint8, (float(kv_scale),), cache8,
+                      block_table, kv_offsets, w_uk, w_uv, k_nope, v, k_pe, dev_status, stream)
+
+
+def make_prefill_workspace(device=None):
+    """A workspace tensor for mla_prefill (one for all calls that do not overlap)."""
+    import torch
+    return torch.empty(int(get_lib().mla_prefill_workspace_size()), dtype=torch.uint8,
+                       device=device or "cuda")
+
+
+def mla_prefill(q_nope, q_pe, k_nope, k_pe, v, q_offsets, kv_offsets, softmax_scale, out, lse=None,
+                causal=True, workspace=None, dev_status=None, stream=None):
+    """Attention of prompt tokens over expanded keys and values, ragged over requests:
+    q_nope [Tq,H,128], q_pe [Tq,H,64], k_nope [Tk,H,128], k_pe [Tk,64], v [Tk,H,128] (outer dims
+    at any strides that are multiples of 8), out [Tq,H,128], lse fp32 [Tq,H].  Causal: the
+    queries of a request are the last tokens of its context.  With a workspace
+    (make_prefill_workspace) few queries on long contexts use the whole GPU."""
+    import torch
+    for t, ndim, name in ((q_nope, 3, "q_nope"), (q_pe, 3, "q_pe"), (k_nope, 3, "k_nope"),
+                          (k_pe, 2, "k_pe"), (v, 3, "v")):
+        _need_rows(t, torch.bfloat16, ndim, name)
+    _need(q_offsets, torch.int32, 1, "q_offsets")
+    _need(kv_offsets, torch.int32, 1, "kv_offsets")
+    _need(out, torch.bfloat16, 3, "out")
+    Tq, H = q_nope.shape[0], q_nope.shape[1]
+    Tk = k_nope.shape[0]
+    B = q_offsets.shape[0] - 1
+    if (tuple(q_nope.shape) != (Tq, H, 128) or tuple(q_pe.shape) != (Tq, H, ROPE_DIM)
+            or tuple(k_nope.shape) != (Tk, H, 128) or tuple(k_pe.shape) != (Tk, ROPE_DIM)
+            or tuple(v.shape) != (Tk, H, 128) or tuple(out.shape) != (Tq, H, 128)):
+        raise ValueError("shapes: q_nope [Tq,H,128], q_pe [Tq,H,64], k_nope [Tk,H,128], "
+                         "k_pe [Tk,64], v [Tk,H,128], out [Tq,H,128]")
+    if B < 0 or kv_offsets.shape[0] != B + 1:
+        raise ValueError("q_offsets and kv_offsets must both be [B+1]")
+    if lse is not None:
+        _need(lse, torch.float32, 2, "lse")
+        if tuple(lse.shape) != (Tq, H):
+            raise ValueError(f"lse must be [Tq, H] = [{Tq}, {H}], got {tuple(lse.shape)}")
+    nbytes = 0
+    if workspace is not None:
+        _need(workspace, torch.uint8, 1, "workspace")
+        nbytes = workspace.numel()
+    _on_current(q_nope, q_pe, k_nope, k_pe, v, q_offsets, kv_offsets, out, lse, workspace,
+                dev_status)
+    _check(get_lib().mla_prefill(
+        _ptr(q_nope), *_strides(q_nope, 128), _ptr(q_pe), *_strides(q_pe, ROPE_DIM), _ptr(k_nope),
+        *_strides(k_nope, 128), _ptr(k_pe), *_strides(k_pe, ROPE_DIM), _ptr(v),
+        *_strides(v, 128), _ptr(q_offsets), _ptr(kv_offsets), B, Tq, Tk, H, int(bool(causal)),
+        float(softmax_scale), _ptr(out), _ptr(lse), _ptr(workspace), nbytes, _ptr(dev_status),
+        _stream(stream)))
     return out
 
 

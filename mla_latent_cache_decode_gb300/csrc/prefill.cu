@@ -5,133 +5,669 @@
 //   j visible to i: j < nk, and when causal also j <= nk - nq + i
 //   out_i = sum_j softmax(s_i)_j v_j,   lse_i = log sum_j exp(s_ij)
 // A row that sees no key gets out = 0 and lse = -inf.
+//
+// Work.  An item is 256 query rows of one request and head: two tiles (A, B)
+// of 128 rows that share every key and value tile of 128 rows.  Per key tile
+// and query tile the tensor cores run S = Q K^T (12 MMAs of 128 x 128 x 16)
+// and O += P V (8 of them): 1,280 cycles of their dense rate, against which
+// the softmax of the other tile runs.  Items are ordered head by head, a
+// request's last tiles (the longest when causal) first, so the SMs that run
+// at one time read few heads' keys and values, mostly from L2.
+//
+// Memory.  Shared: Q of both tiles (96 KB), keys in a ring of four 64-dim
+// chunks of 16 KB (a key tile has three; each is handed back as soon as both
+// tiles' MMAs on it are issued and done), values in two stages of 32 KB.
+// Tensor memory: S of A and B (128 columns each; P overwrites its S as bf16),
+// O of A and B (128 columns each).
+//
+// Warp roles: warps 0-3 softmax and epilogue of tile A, warps 4-7 of tile B
+// (one thread per row; O is rescaled only when the running maximum grows by
+// more than 2^8), warp 8 issues all MMAs in the order PV_A(j-1) S_A(j)
+// PV_B(j-1) S_B(j), across items too, warp 9 issues the TMA loads, warp 10
+// hands out the items.  Every MMA is issued by one thread, so S_A(j) complete
+// means PV_A(j-1) complete: O may be rescaled then without a further wait.
+#include <atomic>
 #include <cmath>
 
 #include "common.cuh"
 #include "ragged.cuh"
+#include "sm100.cuh"
+#include "tmap.h"
 #include "trace.h"
 
 namespace mla {
 void set_error_detail(const char *msg);
 
 namespace prefill {
+using namespace sm100;
 
 constexpr int kNope = 128, kRope = MLA_ROPE_DIM, kV = 128;
-constexpr int kWarps = 8;
+constexpr int kTile = 128;                // query rows and key rows of a tile
+constexpr int kChunk = kTile * 128;       // 64 dims of 128 rows, 128-byte swizzle: 16 KB
+constexpr int kQChunks = 3, kVChunks = 2; // 64-dim chunks of a query (key) and of a value tile
+constexpr int kKSlots = 4, kVSlots = 2;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kThreads = 32 * (kSoftmaxWarps + 3);
+constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;  // tile t at + 128 t
+// The longest legal wait is for another role's whole item: 2^26 keys, at half
+// a million tiles of 1.3 us, 0.7 s.
+constexpr int64_t kMaxKv = 1 << 26;
+constexpr uint64_t kWaitNs = 3000000000ull;
+constexpr uint64_t kDrainNs = 10000000ull;
+constexpr float kRescale = 8.0f;  // log2
 
 struct Strided {
   const __nv_bfloat16 *p;
   int64_t token, head;  // elements
 };
 
+struct Maps {
+  CUtensorMap q_nope, q_pe, k_nope, k_pe, v;
+};
+
 struct Params {
+  const int32_t *q_offsets, *kv_offsets;
+  int32_t batch, heads, total_q, total_kv, causal;
+  float scale_log2;
+  __nv_bfloat16 *out;
+  float *lse;
+  int32_t *dev_status;
+};
+
+// One item: rows [q0, q0 + rows) of head h over key rows [k0, k0 + nk).  Row r
+// of the item sees keys [0, min(nk, see + r)); tile t runs n[t] key tiles.
+struct Work {
+  int32_t h, q0, rows, k0, nk, see, n[2];
+};
+
+struct __align__(1024) Smem {
+  uint8_t q[2][kQChunks][kChunk];
+  uint8_t k[kKSlots][kChunk];
+  uint8_t v[kVSlots][kVChunks][kChunk];
+  uint64_t q_full[2], q_empty[2], k_full[kKSlots], k_empty[kKSlots], v_full[kVSlots], v_empty[kVSlots];
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t work_full[2], work_empty[2];
+  uint64_t fin, roles_done;
+  Work work[2];  // rows = 0: no more items
+  uint32_t tmem_base;
+  int abort;
+};
+static_assert(sizeof(Smem) + 1024 <= 232448, "shared memory of one SM");
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t *>(&v);
+}
+
+__device__ __forceinline__ void set_abort(Smem &s, int32_t *dev_status) {
+  s.abort = 1;
+  report(dev_status, MLA_ERR_DEVICE_TIMEOUT);
+}
+
+// A wait by one thread; on giving up the other roles are told.
+__device__ __forceinline__ bool wait_or_abort(Smem &s, const Params &p, uint64_t &bar, uint32_t parity) {
+  if (mbar_wait(smem_u32(&bar), parity, &s.abort, kWaitNs)) return true;
+  if (!*(volatile int *)&s.abort) set_abort(s, p.dev_status);
+  return false;
+}
+
+// The same by every lane of a warp, which then agrees.
+__device__ __forceinline__ bool warp_wait(Smem &s, const Params &p, uint64_t &bar, uint32_t parity) {
+  const bool ok = mbar_wait(smem_u32(&bar), parity, &s.abort, kWaitNs);
+  if (__all_sync(0xffffffffu, ok)) return true;
+  if ((threadIdx.x & 31) == 0 && !*(volatile int *)&s.abort) set_abort(s, p.dev_status);
+  return false;
+}
+
+// ---------------------------------------------------------------- items
+
+__device__ __forceinline__ int32_t rows_of(const int32_t *o, int32_t b, int32_t total) {
+  return max(ragged::cut(o[b + 1], total) - ragged::cut(o[b], total), 0);
+}
+
+// Item tiles of 256 rows of all requests, by one warp.
+__device__ __forceinline__ int64_t count_tiles(const Params &p, int lane) {
+  int64_t n = 0;
+  for (int32_t b = lane; b < p.batch; b += 32)
+    n += (rows_of(p.q_offsets, b, p.total_q) + 2 * kTile - 1) / (2 * kTile);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  return n;
+}
+
+// Tile r (of all requests' tiles; a request's tiles counted from its end), by
+// one warp; every lane gets the result.
+__device__ __forceinline__ Work find_work(const Params &p, int64_t r, int32_t h, int lane) {
+  Work w = {};
+  int64_t before = 0;
+  for (int32_t b0 = 0; b0 < p.batch; b0 += 32) {
+    const int32_t b = b0 + lane;
+    const int32_t nq = b < p.batch ? rows_of(p.q_offsets, b, p.total_q) : 0;
+    const int32_t mine = (nq + 2 * kTile - 1) / (2 * kTile);
+    int64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    upto += before;
+    const uint32_t hit = __ballot_sync(0xffffffffu, r >= upto - mine && r < upto);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      if (lane == src) {
+        const int32_t tile = (int32_t)(upto - 1 - r);  // counted from the request's start
+        const int32_t first = tile * 2 * kTile;
+        w.h = h;
+        w.q0 = ragged::cut(p.q_offsets[b], p.total_q) + first;
+        w.rows = min(2 * kTile, nq - first);
+        w.k0 = ragged::cut(p.kv_offsets[b], p.total_kv);
+        w.nk = rows_of(p.kv_offsets, b, p.total_kv);
+        w.see = p.causal ? w.nk - nq + first + 1 : w.nk;
+        for (int t = 0; t < 2; ++t) {
+          const int32_t last = min(w.rows, (t + 1) * kTile) - 1;  // the tile's last row sees most
+          const int32_t keys = p.causal ? min(w.nk, w.see + last) : w.nk;
+          w.n[t] = w.rows > t * kTile && keys > 0 ? (keys + kTile - 1) / kTile : 0;
+        }
+      }
+      w.h = __shfl_sync(0xffffffffu, w.h, src);
+      w.q0 = __shfl_sync(0xffffffffu, w.q0, src);
+      w.rows = __shfl_sync(0xffffffffu, w.rows, src);
+      w.k0 = __shfl_sync(0xffffffffu, w.k0, src);
+      w.nk = __shfl_sync(0xffffffffu, w.nk, src);
+      w.see = __shfl_sync(0xffffffffu, w.see, src);
+      w.n[0] = __shfl_sync(0xffffffffu, w.n[0], src);
+      w.n[1] = __shfl_sync(0xffffffffu, w.n[1], src);
+      return w;
+    }
+    before = __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return w;
+}
+
+// A role's view of the items: next() waits for one and copies it, done()
+// hands its slot back.
+struct Items {
+  uint32_t i = 0;
+  __device__ __forceinline__ bool ready(Smem &s, const Params &p) {
+    return wait_or_abort(s, p, s.work_full[i & 1], (i >> 1) & 1);
+  }
+  __device__ __forceinline__ Work get(Smem &s) const { return s.work[i & 1]; }
+  __device__ __forceinline__ void done(Smem &s) {
+    mbar_arrive(smem_u32(&s.work_empty[i & 1]));
+    ++i;
+  }
+};
+
+// ---------------------------------------------------------------- softmax
+
+// One key tile of one row: S from tensor memory, running maximum and sum, P
+// back over S.  `lim`: keys of this tile that the row sees (may be <= 0 or
+// >= 128).
+__device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, float scale_log2, bool masked, int lim,
+                                             bool first, float &m, float &l) {
+  uint32_t xr[kTile];
+#pragma unroll
+  for (int c = 0; c < kTile; c += 32) tmem_ld32(s_addr + c, xr + c);
+  tmem_wait_ld();
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  if (masked) {
+#pragma unroll
+    for (int k = 0; k < kTile; ++k)
+      if (k >= lim) xr[k] = 0xff800000u;  // -inf
+  }
+#pragma unroll
+  for (int k = 0; k < kTile; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(xr[k]));
+  const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale_log2;
+  const bool grow = top > m + kRescale || (m == -INFINITY && top > -INFINITY);
+  float alpha = 1.f;
+  if (grow) {
+    alpha = ex2_approx(m - top);  // 0 when nothing was seen before
+    m = top;
+  }
+  if (!first && __any_sync(0xffffffffu, grow)) {
+#pragma unroll 1
+    for (int c = 0; c < kV; c += 32) {
+      uint32_t o[32];
+      tmem_ld32(o_addr + c, o);
+      tmem_wait_ld();
+#pragma unroll
+      for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+      tmem_st32(o_addr + c, o);
+    }
+  }
+  const float nm = m == -INFINITY ? 0.f : -m;  // a row that has seen nothing: every weight is 0
+  float ps[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int c = 0; c < kTile; c += 32) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int k = 0; k < 32; k += 2) {
+      const float a = ex2_approx(fmaf(__uint_as_float(xr[c + k]), scale_log2, nm));
+      const float b = ex2_approx(fmaf(__uint_as_float(xr[c + k + 1]), scale_log2, nm));
+      ps[(k >> 1) & 3] += a + b;
+      pk[k / 2] = pack2(a, b);
+    }
+    tmem_st16(s_addr + c / 2, pk);
+  }
+  l = l * alpha + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
+}
+
+__device__ __forceinline__ void softmax_role(Smem &s, const Params &p, int warp, int lane, uint32_t tmem) {
+  const int t = warp >> 2, q4 = warp & 3;
+  const int row = q4 * 32 + lane;  // of the tile: TMEM lane
+  const uint32_t lanes = tmem + ((uint32_t)(q4 * 32) << 16);
+  const uint32_t s_addr = lanes + kColS + 128 * t, o_addr = lanes + kColO + 128 * t;
+  Items items;
+  uint32_t g = 0, vg = 0, outs = 0;  // key tiles of this query tile, key tiles loaded, outputs
+  while (true) {
+    if (!warp_wait(s, p, s.work_full[items.i & 1], (items.i >> 1) & 1)) return;
+    const Work w = items.get(s);
+    __syncwarp();
+    if (lane == 0) items.done(s); else ++items.i;
+    if (w.rows == 0) return;
+    const int n = w.n[t], all = max(w.n[0], w.n[1]);
+    const int sees = min(w.nk, p.causal ? w.see + t * kTile + row : w.nk);  // keys this row sees
+    float m = -INFINITY, l = 0.f;
+    for (int j = 0; j < n; ++j, ++g) {
+      if (!warp_wait(s, p, s.s_full[t], g & 1)) return;
+      tc_fence_after();
+      const int lim = sees - j * kTile;
+      softmax_tile(s_addr, o_addr, p.scale_log2, __any_sync(0xffffffffu, lim < kTile), lim, j == 0, m, l);
+      // A last key tile's P V reads value rows up to a multiple of 16: those
+      // behind the request's last key hold anything (0 * NaN = NaN), so they
+      // are zeroed first, by both query tiles alike.
+      const int valid = w.nk - j * kTile;
+      if (valid < kTile && (valid & 15)) {
+        const uint32_t vi = vg + j;
+        if (!warp_wait(s, p, s.v_full[vi % kVSlots], (vi / kVSlots) & 1)) return;
+        const int pad = 16 - (valid & 15);
+        for (int k = (warp & 3) * 32 + lane; k < pad * 16; k += 128) {
+          const int r = valid + (k >> 4), c = (k >> 3) & 1;
+          *reinterpret_cast<uint4 *>(&s.v[vi % kVSlots][c][r * 128 + (k & 7) * 16]) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_shared();
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(smem_u32(&s.p_full[t]));
+    }
+    vg += all;
+    const int64_t out_row = (int64_t)w.q0 + t * kTile + row;
+    const bool real = t * kTile + row < w.rows;
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    if (n > 0) {
+      if (!warp_wait(s, p, s.o_full[t], outs & 1)) return;
+      ++outs;
+      tc_fence_after();
+    }
+    uint4 *dst = reinterpret_cast<uint4 *>(p.out + (out_row * p.heads + w.h) * kV);
+#pragma unroll 1
+    for (int c = 0; c < kV; c += 32) {
+      uint32_t o[32];
+      if (n > 0) {
+        tmem_ld32(o_addr + c, o);
+        tmem_wait_ld();
+      }
+      if (real) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = l > 0.f ? __uint_as_float(o[8 * k + e]) * inv : 0.f;
+          dst[c / 8 + k] = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+        }
+      }
+    }
+    tc_fence_before();
+    if (real && p.lse)
+      p.lse[out_row * p.heads + w.h] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  }
+}
+
+// ---------------------------------------------------------------- MMA issuer
+
+// P V of a query tile's latest key tile, issued once its softmax is done.
+struct Pending {
+  bool on, first, last, free_v;
+  int v, ksteps;
+};
+
+__device__ __forceinline__ void mma_role(Smem &s, const Params &p, uint32_t tmem) {
+  const uint32_t id_s = idesc_bf16_f32(kTile, kTile, 0), id_o = idesc_bf16_f32(kTile, kV, 1);
+  const uint64_t d_q = smem_desc(smem_u32(s.q[0][0]), 16, 1024, kSwizzle128B);
+  const uint64_t d_k = smem_desc(smem_u32(s.k[0]), 16, 1024, kSwizzle128B);
+  const uint64_t d_v = smem_desc(smem_u32(s.v[0][0]), kChunk, 1024, kSwizzle128B);
+  Items items;
+  Pending pend[2] = {};
+  uint32_t g[2] = {0, 0}, q_used[2] = {0, 0};  // key tiles and items of each query tile
+  uint32_t kv = 0;                             // key tiles so far
+  bool ok = true;
+
+  auto run_pv = [&](int t) -> bool {
+    Pending &a = pend[t];
+    const int slot = a.v % kVSlots;
+    if (!wait_or_abort(s, p, s.v_full[slot], (a.v / kVSlots) & 1) ||
+        !wait_or_abort(s, p, s.p_full[t], (g[t] - 1) & 1))
+      return false;
+    tc_fence_after();
+    const uint64_t dv = d_v + (uint64_t)((slot * kVChunks * kChunk) >> 4);
+    const uint32_t d = tmem + kColO + 128 * t, pa = tmem + kColS + 128 * t;
+    for (int k = 0; k < a.ksteps; ++k)
+      mma_ts(d, pa + 8 * k, dv + (uint64_t)((k * 2048) >> 4), id_o, (a.first && k == 0) ? 0u : 1u);
+    if (a.free_v) mma_commit(smem_u32(&s.v_empty[slot]));
+    if (a.last) mma_commit(smem_u32(&s.o_full[t]));
+    a.on = false;
+    return true;
+  };
+
+  while (ok && items.ready(s, p)) {
+    const Work w = items.get(s);
+    items.done(s);
+    const int all = max(w.n[0], w.n[1]);
+    if (all == 0) {  // no key to see, or no more items: what is pending has no S to wait behind
+      for (int t = 0; t < 2 && ok; ++t)
+        if (pend[t].on) ok = run_pv(t);
+      if (w.rows == 0) break;
+    }
+    for (int j = 0; j < all && ok; ++j, ++kv) {
+      for (int t = 0; t < 2 && ok; ++t) {
+        if (pend[t].on && !(ok = run_pv(t))) break;
+        if (j >= w.n[t]) continue;
+        if (j == 0 && !(ok = wait_or_abort(s, p, s.q_full[t], q_used[t]++ & 1))) break;
+        const bool last_user = t == 1 || j >= w.n[1];
+        const uint32_t d = tmem + kColS + 128 * t;
+        for (int c = 0; c < kQChunks; ++c) {
+          const uint32_t chunk = kv * kQChunks + c, slot = chunk % kKSlots;
+          if (!(ok = wait_or_abort(s, p, s.k_full[slot], (chunk / kKSlots) & 1))) break;
+          tc_fence_after();
+          const uint64_t a = d_q + (uint64_t)(((t * kQChunks + c) * kChunk) >> 4);
+          const uint64_t b = d_k + (uint64_t)((slot * kChunk) >> 4);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ss(d, a + 2 * k, b + 2 * k, id_s, (c > 0 || k > 0) ? 1u : 0u);
+          if (last_user) mma_commit(smem_u32(&s.k_empty[slot]));
+        }
+        if (!ok) break;
+        mma_commit(smem_u32(&s.s_full[t]));
+        if (j == w.n[t] - 1) mma_commit(smem_u32(&s.q_empty[t]));
+        ++g[t];
+        const int keys = min(kTile, w.nk - j * kTile);
+        pend[t] = Pending{true, j == 0, j == w.n[t] - 1, last_user, (int)kv, (keys + 15) >> 4};
+      }
+    }
+  }
+  // every MMA issued is finished before the tensor memory is given back
+  mma_commit(smem_u32(&s.fin));
+  if (!mbar_wait(smem_u32(&s.fin), 0, nullptr, kWaitNs)) report(p.dev_status, MLA_ERR_DEVICE_TIMEOUT);
+}
+
+// ---------------------------------------------------------------- TMA producer
+
+__device__ __forceinline__ void load_role(Smem &s, const Params &p, const Maps &maps) {
+  Items items;
+  uint32_t nq[2] = {0, 0}, nk = 0, nv = 0;  // loads issued: query tiles, key chunks, value tiles
+  const uint64_t hint = policy_evict_normal();
+  bool ok = true;
+  auto load_q = [&](const Work &w, int t) -> bool {
+    if (w.n[t] == 0) return true;
+    if (!wait_or_abort(s, p, s.q_empty[t], (nq[t] & 1) ^ 1)) return false;
+    const uint32_t bar = smem_u32(&s.q_full[t]);
+    mbar_arrive_expect_tx(bar, kQChunks * kChunk);
+    const int32_t y = w.q0 + t * kTile;
+    tma_load_3d_hint(smem_u32(s.q[t][0]), &maps.q_nope, 0, w.h, y, bar, hint);
+    tma_load_3d_hint(smem_u32(s.q[t][1]), &maps.q_nope, 64, w.h, y, bar, hint);
+    tma_load_3d_hint(smem_u32(s.q[t][2]), &maps.q_pe, 0, w.h, y, bar, hint);
+    ++nq[t];
+    return true;
+  };
+  auto load_k = [&](const Work &w, int j) -> bool {
+    const int32_t y = w.k0 + j * kTile;
+    for (int c = 0; c < kQChunks; ++c, ++nk) {
+      const uint32_t slot = nk % kKSlots;
+      if (!wait_or_abort(s, p, s.k_empty[slot], ((nk / kKSlots) & 1) ^ 1)) return false;
+      const uint32_t bar = smem_u32(&s.k_full[slot]);
+      mbar_arrive_expect_tx(bar, kChunk);
+      if (c < 2) tma_load_3d_hint(smem_u32(s.k[slot]), &maps.k_nope, 64 * c, w.h, y, bar, hint);
+      else tma_load_3d_hint(smem_u32(s.k[slot]), &maps.k_pe, 0, 0, y, bar, hint);
+    }
+    return true;
+  };
+  auto load_v = [&](const Work &w, int j) -> bool {
+    const uint32_t slot = nv % kVSlots;
+    if (!wait_or_abort(s, p, s.v_empty[slot], ((nv / kVSlots) & 1) ^ 1)) return false;
+    const uint32_t bar = smem_u32(&s.v_full[slot]);
+    mbar_arrive_expect_tx(bar, kVChunks * kChunk);
+    for (int c = 0; c < kVChunks; ++c)
+      tma_load_3d_hint(smem_u32(s.v[slot][c]), &maps.v, 64 * c, w.h, w.k0 + j * kTile, bar, hint);
+    ++nv;
+    return true;
+  };
+  prefetch_tmap(&maps.q_nope);
+  prefetch_tmap(&maps.q_pe);
+  prefetch_tmap(&maps.k_nope);
+  prefetch_tmap(&maps.k_pe);
+  prefetch_tmap(&maps.v);
+  while (ok && items.ready(s, p)) {
+    const Work w = items.get(s);
+    items.done(s);
+    if (w.rows == 0) break;
+    const int all = max(w.n[0], w.n[1]);
+    ok = load_q(w, 0);
+    for (int j = 0; j < all && ok; ++j) {
+      ok = load_k(w, j) && (j > 0 || load_q(w, 1)) && load_v(w, j);
+    }
+  }
+  if (*(volatile int *)&s.abort) {  // no copy may still be landing when the shared memory is given up
+    for (int t = 0; t < 2; ++t)
+      if (nq[t]) (void)mbar_wait(smem_u32(&s.q_full[t]), (nq[t] - 1) & 1, nullptr, kDrainNs);
+    for (uint32_t i = nk > kKSlots ? nk - kKSlots : 0; i < nk; ++i)
+      (void)mbar_wait(smem_u32(&s.k_full[i % kKSlots]), (i / kKSlots) & 1, nullptr, kDrainNs);
+    for (uint32_t i = nv > kVSlots ? nv - kVSlots : 0; i < nv; ++i)
+      (void)mbar_wait(smem_u32(&s.v_full[i % kVSlots]), (i / kVSlots) & 1, nullptr, kDrainNs);
+  }
+}
+
+// ---------------------------------------------------------------- scheduler
+
+__device__ __forceinline__ void schedule_role(Smem &s, const Params &p, int lane) {
+  const int64_t tiles = count_tiles(p, lane);
+  const int64_t items = tiles * p.heads;
+  uint32_t i = 0;
+  for (int64_t at = blockIdx.x;; at += gridDim.x, ++i) {
+    Work w = {};
+    const bool more = at < items;
+    if (more) w = find_work(p, at % tiles, (int32_t)(at / tiles), lane);
+    if (!warp_wait(s, p, s.work_empty[i & 1], ((i >> 1) & 1) ^ 1)) return;
+    if (lane == 0) {
+      s.work[i & 1] = w;
+      mbar_arrive(smem_u32(&s.work_full[i & 1]));
+    }
+    if (!more) return;
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ Maps maps, const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  Smem &s = *reinterpret_cast<Smem *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(smem_u32(&s.q_full[t]), 1);
+      mbar_init(smem_u32(&s.q_empty[t]), 1);
+      mbar_init(smem_u32(&s.s_full[t]), 1);
+      mbar_init(smem_u32(&s.p_full[t]), kTile);
+      mbar_init(smem_u32(&s.o_full[t]), 1);
+      mbar_init(smem_u32(&s.work_full[t]), 1);
+      mbar_init(smem_u32(&s.work_empty[t]), kSoftmaxWarps + 2);
+    }
+    for (int i = 0; i < kKSlots; ++i) {
+      mbar_init(smem_u32(&s.k_full[i]), 1);
+      mbar_init(smem_u32(&s.k_empty[i]), 1);
+    }
+    for (int i = 0; i < kVSlots; ++i) {
+      mbar_init(smem_u32(&s.v_full[i]), 1);
+      mbar_init(smem_u32(&s.v_empty[i]), 1);
+    }
+    mbar_init(smem_u32(&s.fin), 1);
+    mbar_init(smem_u32(&s.roles_done), kThreads / 32);
+    s.abort = 0;
+    fence_mbarrier_init_cluster();
+  }
+  if (blockIdx.x == 0) {
+    ragged::check_offsets(p.q_offsets, p.batch, p.total_q, threadIdx.x, kThreads, p.dev_status);
+    ragged::check_offsets(p.kv_offsets, p.batch, p.total_kv, threadIdx.x, kThreads, p.dev_status);
+  }
+  if (warp == 0) {
+    tmem_alloc(smem_u32(&s.tmem_base), kTmemCols);
+    tmem_relinquish();
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s.tmem_base;
+
+  if (warp < kSoftmaxWarps) {
+    softmax_role(s, p, warp, lane, tmem);
+  } else if (warp == kSoftmaxWarps) {
+    if (elect_one_sync()) mma_role(s, p, tmem);
+  } else if (warp == kSoftmaxWarps + 1) {
+    if (elect_one_sync()) load_role(s, p, maps);
+  } else {
+    schedule_role(s, p, lane);
+  }
+
+  // the tensor memory is freed once every warp has reported the end of its role
+  __syncwarp();
+  tc_fence_before();
+  if (lane == 0) mbar_arrive(smem_u32(&s.roles_done));
+  if (warp == 0) {
+    if (lane == 0 && !mbar_wait(smem_u32(&s.roles_done), 0, nullptr, kWaitNs))
+      report(p.dev_status, MLA_ERR_DEVICE_TIMEOUT);
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------- host
+
+struct Args {
   Strided q_nope, q_pe, k_nope, k_pe, v;
   const int32_t *q_offsets, *kv_offsets;
   int32_t batch, heads;
   int64_t total_q, total_kv;
   int32_t causal;
   float scale;
-  __nv_bfloat16 *out;
+  void *out;
   float *lse;
   int32_t *dev_status;
 };
-
-// One warp per query row and head, one pass over its keys with the running
-// maximum and sum.
-__global__ void __launch_bounds__(32 * kWarps) prefill_kernel(const Params p) {
-  const int64_t t = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32;
-  const int h = blockIdx.y, lane = threadIdx.x & 31;
-  if (blockIdx.x == 0 && h == 0) {
-    ragged::check_offsets(p.q_offsets, p.batch, (int32_t)p.total_q, threadIdx.x, 32 * kWarps,
-                          p.dev_status);
-    ragged::check_offsets(p.kv_offsets, p.batch, (int32_t)p.total_kv, threadIdx.x, 32 * kWarps,
-                          p.dev_status);
-  }
-  if (t >= p.total_q || t < p.q_offsets[0] || t >= p.q_offsets[p.batch]) return;
-  const int32_t lo = ragged::request_of(p.q_offsets, p.batch, (int32_t)t);
-  const int64_t i = t - p.q_offsets[lo], nq = p.q_offsets[lo + 1] - p.q_offsets[lo];
-  const int64_t k0 = p.kv_offsets[lo], k1 = p.kv_offsets[lo + 1];
-  if (k0 < 0 || k1 < k0 || k1 > p.total_kv) {
-    if (lane == 0) report(p.dev_status, MLA_ERR_DEVICE_RANGE);
-    return;
-  }
-  const int64_t nk = k1 - k0;
-  const int64_t last = p.causal ? min(nk, nk - nq + i + 1) : nk;
-  float q[6], o[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
-  for (int e = 0; e < 4; ++e)
-    q[e] = __bfloat162float(p.q_nope.p[t * p.q_nope.token + h * p.q_nope.head + lane + 32 * e]);
-  for (int e = 0; e < 2; ++e)
-    q[4 + e] = __bfloat162float(p.q_pe.p[t * p.q_pe.token + h * p.q_pe.head + lane + 32 * e]);
-  for (int64_t j = k0; j < k0 + last; ++j) {
-    float s = 0.f;
-    for (int e = 0; e < 4; ++e)
-      s += q[e] * __bfloat162float(p.k_nope.p[j * p.k_nope.token + h * p.k_nope.head + lane + 32 * e]);
-    for (int e = 0; e < 2; ++e)
-      s += q[4 + e] * __bfloat162float(p.k_pe.p[j * p.k_pe.token + lane + 32 * e]);
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= p.scale;
-    const float m_new = fmaxf(m, s);
-    const float a = expf(m - m_new), w = expf(s - m_new);
-    l = l * a + w;
-    for (int e = 0; e < 4; ++e)
-      o[e] = o[e] * a + w * __bfloat162float(p.v.p[j * p.v.token + h * p.v.head + lane + 32 * e]);
-    m = m_new;
-  }
-  const float inv = last > 0 ? 1.f / l : 0.f;
-  for (int e = 0; e < 4; ++e)
-    p.out[(t * p.heads + h) * kV + lane + 32 * e] = __float2bfloat16(o[e] * inv);
-  if (p.lse && lane == 0) p.lse[t * p.heads + h] = last > 0 ? m + logf(l) : -INFINITY;
-}
 
 mla_status_t invalid(const char *why) {
   set_error_detail(why);
   return MLA_ERR_INVALID_ARGUMENT;
 }
 
+mla_status_t cuda_failed(cudaError_t e) {
+  set_error_detail(cudaGetErrorString(e));
+  return MLA_ERR_CUDA;
+}
+
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
-// Strides of 16-byte multiples that keep rows of n elements apart
+// Strides of 16-byte multiples, at least a row's width
 bool strides_ok(const Strided &s, int n) {
-  return s.token % 8 == 0 && s.head % 8 == 0 && s.token >= n && s.head >= n &&
-         s.token < (1ll << 38) && s.head < (1ll << 38);
+  return s.token % 8 == 0 && s.head % 8 == 0 && s.token >= n && s.head >= n && s.token < (1ll << 38) &&
+         s.head < (1ll << 38);
+}
+
+// [tokens][heads][dims] in boxes of 128 tokens of one head, 64 dims each;
+// rows behind the last read as zero.  A tensor without rows is never loaded
+// from: its map names one row of `instead`.
+bool encode(CUtensorMap *m, const Strided &s, int64_t tokens, int32_t heads, int dims, const void *instead) {
+  tmap::EncodeTiledFn fn = tmap::encode_fn();
+  if (!fn) return false;
+  const bool none = tokens == 0;
+  cuuint64_t size[3] = {(cuuint64_t)dims, (cuuint64_t)heads, (cuuint64_t)(none ? 1 : tokens)};
+  cuuint64_t strides[2] = {(cuuint64_t)s.head * 2, (cuuint64_t)s.token * 2};
+  cuuint32_t box[3] = {64, 1, kTile}, each[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(none ? instead : (const void *)s.p), size,
+            strides, box, each, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 constexpr size_t kWorkspaceBytes = 32u << 20;
 
-mla_status_t run(const Params &p, void *workspace, size_t workspace_bytes, void *stream) {
+// SMs of a device; the kernel's shared-memory opt-in is set on the way.
+cudaError_t prepare_device(int dev, int *sms) {
+  static std::atomic<int> known[64];
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  *sms = known[dev].load(std::memory_order_acquire);
+  if (*sms > 0) return cudaSuccess;
+  cudaError_t e = cudaFuncSetAttribute(prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)sizeof(Smem) + 1024);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) known[dev].store(*sms, std::memory_order_release);
+  return e;
+}
+
+mla_status_t run(const Args &a, void *workspace, size_t workspace_bytes, void *stream) {
   set_error_detail("");
-  if (p.batch < 0 || p.total_q < 0 || p.total_kv < 0 || p.total_q > INT32_MAX ||
-      p.total_kv > INT32_MAX)
-    return invalid("batch < 0, or total_q or total_kv outside [0, 2^31)");
-  if (p.heads < 1 || p.heads > kHeads) {
+  if (a.batch < 0 || a.total_q < 0 || a.total_kv < 0 || a.total_q > INT32_MAX || a.total_kv > kMaxKv)
+    return invalid("batch < 0, total_q outside [0, 2^31) or total_kv outside [0, 2^26]");
+  if (a.heads < 1 || a.heads > kHeads) {
     set_error_detail("num_heads outside [1, 128]");
     return MLA_ERR_UNSUPPORTED;
   }
-  if (p.causal != 0 && p.causal != 1) return invalid("causal must be 0 or 1");
-  if (!std::isfinite(p.scale) || !(p.scale > 0.f))
-    return invalid("softmax_scale must be positive and finite");
-  if (p.batch == 0 || p.total_q == 0) return MLA_OK;
-  if (!p.q_nope.p || !p.q_pe.p || !p.q_offsets || !p.kv_offsets || !p.out ||
-      (p.total_kv > 0 && (!p.k_nope.p || !p.k_pe.p || !p.v.p)))
+  if (a.causal != 0 && a.causal != 1) return invalid("causal must be 0 or 1");
+  if (!std::isfinite(a.scale) || !(a.scale > 0.f)) return invalid("softmax_scale must be positive and finite");
+  if (a.batch == 0 || a.total_q == 0) return MLA_OK;
+  if (!a.q_nope.p || !a.q_pe.p || !a.q_offsets || !a.kv_offsets || !a.out ||
+      (a.total_kv > 0 && (!a.k_nope.p || !a.k_pe.p || !a.v.p)))
     return invalid("null pointer");
-  if (!aligned(p.q_nope.p, 16) || !aligned(p.q_pe.p, 16) || !aligned(p.k_nope.p, 16) ||
-      !aligned(p.k_pe.p, 16) || !aligned(p.v.p, 16) || !aligned(p.out, 16))
+  if (!aligned(a.q_nope.p, 16) || !aligned(a.q_pe.p, 16) || !aligned(a.k_nope.p, 16) || !aligned(a.k_pe.p, 16) ||
+      !aligned(a.v.p, 16) || !aligned(a.out, 16))
     return invalid("queries, keys, values and out must be 16-byte aligned");
-  if (!aligned(p.q_offsets, 4) || !aligned(p.kv_offsets, 4) || !aligned(p.lse, 4))
+  if (!aligned(a.q_offsets, 4) || !aligned(a.kv_offsets, 4) || !aligned(a.lse, 4))
     return invalid("q_offsets, kv_offsets and lse must be 4-byte aligned");
-  if (!strides_ok(p.q_nope, kNope) || !strides_ok(p.q_pe, kRope) || !strides_ok(p.k_nope, kNope) ||
-      !strides_ok(p.v, kV) || p.k_pe.token % 8 || p.k_pe.token < kRope)
-    return invalid("strides must be multiples of 8 elements and at least a row's width");
+  if (!strides_ok(a.q_nope, kNope) || !strides_ok(a.q_pe, kRope) || !strides_ok(a.k_nope, kNope) ||
+      !strides_ok(a.v, kV) || !strides_ok(a.k_pe, kRope))
+    return invalid("strides must be multiples of 8 elements, at least a row's width and below 2^38");
   if (workspace && (!aligned(workspace, 256) || workspace_bytes < kWorkspaceBytes)) {
     set_error_detail("workspace must be 256-byte aligned and of mla_prefill_workspace_size()");
     return aligned(workspace, 256) ? MLA_ERR_WORKSPACE_TOO_SMALL : MLA_ERR_INVALID_ARGUMENT;
   }
-  const dim3 grid((unsigned)((p.total_q + kWarps - 1) / kWarps), (unsigned)p.heads);
-  prefill_kernel<<<grid, 32 * kWarps, 0, (cudaStream_t)stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) return MLA_OK;
-  set_error_detail(cudaGetErrorString(e));
-  return MLA_ERR_CUDA;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = prepare_device(dev, &sms);
+  if (e != cudaSuccess) return cuda_failed(e);
+  Maps maps;
+  if (!encode(&maps.q_nope, a.q_nope, a.total_q, a.heads, kNope, a.out) ||
+      !encode(&maps.q_pe, a.q_pe, a.total_q, a.heads, kRope, a.out) ||
+      !encode(&maps.k_nope, a.k_nope, a.total_kv, a.heads, kNope, a.out) ||
+      !encode(&maps.k_pe, a.k_pe, a.total_kv, 1, kRope, a.out) ||
+      !encode(&maps.v, a.v, a.total_kv, a.heads, kV, a.out)) {
+    set_error_detail("cannot describe an operand to TMA");
+    return MLA_ERR_CUDA;
+  }
+  Params p;
+  p.q_offsets = a.q_offsets;
+  p.kv_offsets = a.kv_offsets;
+  p.batch = a.batch;
+  p.heads = a.heads;
+  p.total_q = (int32_t)a.total_q;
+  p.total_kv = (int32_t)a.total_kv;
+  p.causal = a.causal;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.out = (__nv_bfloat16 *)a.out;
+  p.lse = a.lse;
+  p.dev_status = a.dev_status;
+  // no more items than this, whatever the offsets say
+  const int64_t most = (a.total_q / (2 * kTile) + a.batch) * (int64_t)a.heads;
+  prefill_kernel<<<(unsigned)(most < sms ? most : sms), kThreads, sizeof(Smem) + 1024, (cudaStream_t)stream>>>(maps, p);
+  e = cudaGetLastError();
+  return e == cudaSuccess ? MLA_OK : cuda_failed(e);
 }
 
 }  // namespace prefill
@@ -156,24 +692,24 @@ mla_status_t mla_prefill(const void *q_nope, int64_t q_nope_token_stride,
   TraceRange trace_range("mla_prefill");
   using prefill::Strided;
   typedef const __nv_bfloat16 *Bf16;
-  prefill::Params p;
-  p.q_nope = Strided{(Bf16)q_nope, q_nope_token_stride, q_nope_head_stride};
-  p.q_pe = Strided{(Bf16)q_pe, q_pe_token_stride, q_pe_head_stride};
-  p.k_nope = Strided{(Bf16)k_nope, k_nope_token_stride, k_nope_head_stride};
-  p.k_pe = Strided{(Bf16)k_pe, k_pe_token_stride, 0};
-  p.v = Strided{(Bf16)v, v_token_stride, v_head_stride};
-  p.q_offsets = q_offsets;
-  p.kv_offsets = kv_offsets;
-  p.batch = batch;
-  p.heads = num_heads;
-  p.total_q = total_q;
-  p.total_kv = total_kv;
-  p.causal = causal;
-  p.scale = softmax_scale;
-  p.out = (__nv_bfloat16 *)out;
-  p.lse = lse;
-  p.dev_status = dev_status;
-  return prefill::run(p, workspace, workspace_bytes, stream);
+  prefill::Args a;
+  a.q_nope = Strided{(Bf16)q_nope, q_nope_token_stride, q_nope_head_stride};
+  a.q_pe = Strided{(Bf16)q_pe, q_pe_token_stride, q_pe_head_stride};
+  a.k_nope = Strided{(Bf16)k_nope, k_nope_token_stride, k_nope_head_stride};
+  a.k_pe = Strided{(Bf16)k_pe, k_pe_token_stride, prefill::kRope};
+  a.v = Strided{(Bf16)v, v_token_stride, v_head_stride};
+  a.q_offsets = q_offsets;
+  a.kv_offsets = kv_offsets;
+  a.batch = batch;
+  a.heads = num_heads;
+  a.total_q = total_q;
+  a.total_kv = total_kv;
+  a.causal = causal;
+  a.scale = softmax_scale;
+  a.out = out;
+  a.lse = lse;
+  a.dev_status = dev_status;
+  return prefill::run(a, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

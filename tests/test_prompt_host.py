@@ -92,7 +92,7 @@ def prefill(lib, **kw):
 
 
 @pytest.mark.parametrize("bad, status", [
-    (dict(batch=-1), 1), (dict(tq=-1), 1), (dict(tk=-1), 1), (dict(tq=1 << 31), 1), (dict(tk=1 << 31), 1), (dict(heads=0), 2),
+    (dict(batch=-1), 1), (dict(tq=-1), 1), (dict(tk=-1), 1), (dict(tq=1 << 31), 1), (dict(tk=(1 << 26) + 1), 1), (dict(heads=0), 2),
     (dict(heads=129), 2), (dict(causal=2), 1), (dict(scale=0.0), 1), (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1),
     (dict(scale=-1.0), 1), (dict(qn=None), 1), (dict(qp=None), 1), (dict(kn=None), 1), (dict(kp=None), 1), (dict(v=None), 1),
     (dict(qo=None), 1), (dict(ko=None), 1), (dict(out=None), 1), (dict(qn=A + 2), 1), (dict(kp=A + 8), 1), (dict(out=A + 8), 1),

@@ -6,21 +6,53 @@
 //   v[t, h, n]      = sum_j C[t, j] W_UV[h, j, n]     (n < 128)
 //   k_pe[t, :]      = the row's 64 rotary dims
 // Sums in fp32, one rounding to bf16.
+//
+// A product of [tokens x 512] with [512 x 256 heads]: 262,144 flops and 512
+// output bytes per token and head.  With all heads it is bound by the tensor
+// cores from about 300 tokens on (below, by the 256 KB a head of weights).
+//
+// A CTA keeps 128 output rows: their 512 latent dims sit in tensor memory as
+// the A operand (256 columns), gathered from the pages once, one thread per
+// row (so any page size and request boundary will do, and E4M3 codes are
+// widened to bf16, exactly, on the way), and every head's weights stream past
+// through a ring of 16 KB stages (128 output dims x 64 of K).  A from tensor
+// memory leaves shared memory's bandwidth to the weights.  A cluster of
+// CTAs holds neighbouring rows and walks the same heads: each loads a part of
+// every stage and multicasts it, so L2 delivers a weight once per cluster.
+// Accumulators are double-buffered (2 x 128 columns); four warps round them to
+// bf16, stage them in shared memory and store them by TMA.
+//
+// An item is one head's keys or values of a group of kCluster x 128 rows; the
+// items (group by group, head by head) are cut into equal runs, one a cluster.
+#include <atomic>
 #include <cmath>
 
 #include "common.cuh"
 #include "fp8.cuh"
 #include "ragged.cuh"
+#include "sm100.cuh"
+#include "tmap.h"
 #include "trace.h"
 
 namespace mla {
 void set_error_detail(const char *msg);
 
 namespace expand {
+using namespace sm100;
 
-constexpr int kRows = 16;   // output rows of a block
-constexpr int kDims = 128;  // key dims and value dims of a head
-constexpr int kThreads = 256;
+constexpr int kRows = 128;              // output rows of a CTA
+constexpr int kDims = 128;              // key dims, value dims of a head
+constexpr int kKChunks = kVDim / 64;    // 64-dim chunks of the latent
+constexpr int kStage = kDims * 128;     // 128 output dims x 64 of K: 16 KB
+constexpr int kStages = 10;
+constexpr int kThreads = 192;           // warps 0-3 rows in, results out; 4 weights; 5 MMA
+constexpr uint32_t kTmemCols = 512, kColA = 0, kColD = 256;
+constexpr uint64_t kWaitNs = 1000000000ull;
+constexpr uint64_t kDrainNs = 10000000ull;
+
+struct Maps {
+  CUtensorMap w_uk, w_uv, k_nope, v;
+};
 
 struct Params {
   const void *cache;
@@ -29,77 +61,358 @@ struct Params {
   const int32_t *block_table;
   int32_t max_blocks_per_seq;
   const int32_t *kv_offsets;
-  int32_t batch;
-  int64_t total_kv;
-  const __nv_bfloat16 *w_uk, *w_uv;
-  int32_t heads;
+  int32_t batch, total_kv, heads;
   float kv_scale;
+  const __nv_bfloat16 *w_uk, *w_uv;
   __nv_bfloat16 *k_nope, *v, *k_pe;
   int32_t *dev_status;
 };
 
-// Cache row of output row t, -1 for a row behind the last request (left as it
-// is), -2 for one whose page lies outside the pool or the table (reported).
-__device__ int64_t cache_row(const Params &p, int64_t t) {
+struct __align__(1024) Smem {
+  uint8_t w[kStages][kStage];
+  uint8_t out[2][2][kRows * 128];  // two results: 64-dim halves of 128 rows, 128-byte swizzle
+  uint64_t w_full[kStages], w_empty[kStages], d_full[2], d_empty[2], a_full, fin;
+  uint32_t tmem_base;
+  int abort;
+};
+static_assert(sizeof(Smem) + 1024 <= 232448, "shared memory of one SM");
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t *>(&v);
+}
+
+// Two E4M3 codes (low byte first) as bf16x2, exactly.
+__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t two) {
+  const uint32_t h = e4m3x2_to_f16x2(two);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+  return pack2(f.x, f.y);
+}
+
+__device__ __forceinline__ void set_abort(Smem &s, int32_t *dev_status) {
+  s.abort = 1;
+  report(dev_status, MLA_ERR_DEVICE_TIMEOUT);
+}
+
+__device__ __forceinline__ bool wait_or_abort(Smem &s, const Params &p, uint64_t &bar, uint32_t parity) {
+  if (mbar_wait(smem_u32(&bar), parity, &s.abort, kWaitNs)) return true;
+  if (!*(volatile int *)&s.abort) set_abort(s, p.dev_status);
+  return false;
+}
+
+__device__ __forceinline__ bool warp_wait(Smem &s, const Params &p, uint64_t &bar, uint32_t parity) {
+  const bool ok = mbar_wait(smem_u32(&bar), parity, &s.abort, kWaitNs);
+  if (__all_sync(0xffffffffu, ok)) return true;
+  if ((threadIdx.x & 31) == 0 && !*(volatile int *)&s.abort) set_abort(s, p.dev_status);
+  return false;
+}
+
+// Cache row of output row t, -1 for a row of no request (left as it is), -2
+// for one whose page lies outside the table or the pool.
+__device__ __forceinline__ int64_t cache_row(const Params &p, int32_t t) {
   if (t >= p.total_kv || t < p.kv_offsets[0] || t >= p.kv_offsets[p.batch]) return -1;
-  const int32_t lo = ragged::request_of(p.kv_offsets, p.batch, (int32_t)t);
-  const int64_t pos = t - p.kv_offsets[lo];
-  const int64_t page = pos / p.block_size;
-  if (page >= p.max_blocks_per_seq) return -2;
-  const int32_t blk = p.block_table[(int64_t)lo * p.max_blocks_per_seq + page];
+  const int32_t b = ragged::request_of(p.kv_offsets, p.batch, t);
+  const int64_t pos = (int64_t)t - p.kv_offsets[b], page = pos / p.block_size;
+  if (pos < 0 || page >= p.max_blocks_per_seq) return -2;
+  const int32_t blk = p.block_table[(int64_t)b * p.max_blocks_per_seq + page];
   const int64_t row = (int64_t)blk * p.block_size + pos % p.block_size;
   return blk < 0 || row >= p.num_slots ? -2 : row;
 }
 
+// The thread's row into its tensor-memory lane (zeros without a row); with
+// `copy_rope` its rotary dims go out as k_pe.
 template <bool kFp8>
-__device__ float element(const Params &p, int64_t row, int j) {
-  if (!kFp8) return __bfloat162float(static_cast<const __nv_bfloat16 *>(p.cache)[row * kRow + j]);
-  const uint32_t two = e4m3x2_to_f16x2(static_cast<const uint8_t *>(p.cache)[row * kRow + j]);
-  __half_raw h;
-  h.x = (unsigned short)two;
-  return __half2float(__half(h)) * p.kv_scale;
+__device__ __forceinline__ void load_row(const Params &p, int64_t row, int32_t t, bool copy_rope, uint32_t lane_addr) {
+  constexpr int kWords = kFp8 ? 32 : 64;  // 16-byte words of 512 elements
+  constexpr int kBatch = kFp8 ? 8 : 16;   // words in flight: 128 elements
+  const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.cache) +
+                                                     (row < 0 ? 0 : row) * (kFp8 ? kRow : 2 * kRow));
+#pragma unroll 1
+  for (int w0 = 0; w0 < kWords; w0 += kBatch) {
+    uint4 in[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) in[i] = row < 0 ? make_uint4(0, 0, 0, 0) : src[w0 + i];
+    uint32_t a[64];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const uint32_t u[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (kFp8) {
+          a[8 * i + 2 * e] = e4m3x2_to_bf16x2(u[e] & 0xffffu);
+          a[8 * i + 2 * e + 1] = e4m3x2_to_bf16x2(u[e] >> 16);
+        } else {
+          a[4 * i + e] = u[e];
+        }
+      }
+    }
+    const uint32_t at = lane_addr + kColA + (w0 / kBatch) * 64;
+    tmem_st32(at, a);
+    tmem_st32(at + 32, a + 32);
+  }
+  if (copy_rope && row >= 0) {
+    uint4 *dst = reinterpret_cast<uint4 *>(p.k_pe + (int64_t)t * MLA_ROPE_DIM);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (kFp8) {
+        const uint2 c = reinterpret_cast<const uint2 *>(src + kWords)[i];
+        const uint32_t u[4] = {c.x & 0xffffu, c.x >> 16, c.y & 0xffffu, c.y >> 16};
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t h = e4m3x2_to_f16x2(u[e]);
+          const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+          o[e] = pack2(f.x * p.kv_scale, f.y * p.kv_scale);
+        }
+        dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
+      } else {
+        dst[i] = src[kWords + i];
+      }
+    }
+  }
 }
 
-// grid = (ceil(total_kv / 16), heads): thread n < 128 sums key dim n of 16
-// rows, thread 128 + n value dim n.
-template <bool kFp8>
-__global__ void __launch_bounds__(kThreads) expand_kernel(const Params p) {
-  __shared__ int64_t row[kRows];
-  __shared__ float latent[kRows][kVDim];
-  const int64_t t0 = (int64_t)blockIdx.x * kRows;
-  const int h = blockIdx.y;
-  if (blockIdx.x == 0 && h == 0)
-    ragged::check_offsets(p.kv_offsets, p.batch, (int32_t)p.total_kv, threadIdx.x, kThreads,
-                          p.dev_status);
-  if (threadIdx.x < kRows) {
-    row[threadIdx.x] = cache_row(p, t0 + threadIdx.x);
-    if (row[threadIdx.x] == -2) report(p.dev_status, MLA_ERR_DEVICE_RANGE);
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < kRows * kVDim; i += kThreads)
-    latent[i / kVDim][i % kVDim] = row[i / kVDim] < 0 ? 0.f : element<kFp8>(p, row[i / kVDim], i % kVDim);
-  __syncthreads();
-  const bool value = threadIdx.x >= kDims;
-  const int n = threadIdx.x % kDims;
-  float sum[kRows];
-#pragma unroll
-  for (int r = 0; r < kRows; ++r) sum[r] = 0.f;
-  for (int j = 0; j < kVDim; ++j) {
-    const float w = __bfloat162float(value ? p.w_uv[((int64_t)h * kVDim + j) * kDims + n]
-                                           : p.w_uk[((int64_t)h * kDims + n) * kVDim + j]);
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) sum[r] += latent[r][j] * w;
-  }
-  __nv_bfloat16 *out = value ? p.v : p.k_nope;
-  for (int r = 0; r < kRows; ++r)
-    if (row[r] >= 0) out[((t0 + r) * p.heads + h) * kDims + n] = __float2bfloat16(sum[r]);
-  if (h == 0)
-    for (int i = threadIdx.x; i < kRows * MLA_ROPE_DIM; i += kThreads) {
-      const int r = i / MLA_ROPE_DIM, e = i % MLA_ROPE_DIM;
-      if (row[r] >= 0)
-        p.k_pe[(t0 + r) * MLA_ROPE_DIM + e] = __float2bfloat16(element<kFp8>(p, row[r], kVDim + e));
-    }
+template <int kCluster>
+__device__ __forceinline__ uint32_t cluster_rank() {
+  if (kCluster == 1) return 0;
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
 }
+
+template <int kCluster>
+__device__ __forceinline__ void cluster_sync() {
+  if (kCluster == 1) {
+    __syncthreads();
+  } else {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+}
+
+// The barrier at this offset in every CTA of the cluster.
+template <int kCluster>
+__device__ __forceinline__ void commit_all(uint32_t bar) {
+  if (kCluster == 1) {
+    mma_commit(bar);
+  } else {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)((1 << kCluster) - 1))
+        : "memory");
+  }
+}
+
+template <int kCluster>
+__device__ __forceinline__ void load_weights(uint32_t dst, const CUtensorMap *m, int32_t x, int32_t y, uint32_t bar,
+                                             uint64_t policy) {
+  if (kCluster == 1) {
+    tma_load_2d_hint(dst, m, x, y, bar, policy);
+  } else {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
+        ".L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5, %6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar), "h"((uint16_t)((1 << kCluster) - 1)),
+        "l"(policy)
+        : "memory");
+  }
+}
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *m, int32_t x, int32_t y, int32_t z, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(x), "r"(y), "r"(z), "r"(src)
+               : "memory");
+}
+
+template <bool kFp8, int kCluster>
+__global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_constant__ Maps maps, const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  Smem &s = *reinterpret_cast<Smem *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank<kCluster>();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_u32(&s.w_full[i]), 1);
+      mbar_init(smem_u32(&s.w_empty[i]), kCluster);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&s.d_full[i]), 1);
+      mbar_init(smem_u32(&s.d_empty[i]), kRows);
+    }
+    mbar_init(smem_u32(&s.a_full), kRows);
+    mbar_init(smem_u32(&s.fin), 1);
+    s.abort = 0;
+    fence_mbarrier_init_cluster();
+  }
+  if (blockIdx.x == 0)
+    ragged::check_offsets(p.kv_offsets, p.batch, p.total_kv, threadIdx.x, kThreads, p.dev_status);
+  if (warp == 0) {
+    tmem_alloc(smem_u32(&s.tmem_base), kTmemCols);
+    tmem_relinquish();
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync<kCluster>();
+  tc_fence_after();
+  const uint32_t tmem = s.tmem_base;
+
+  // this cluster's run of items [i0, i1): group i / per, head and kind i % per
+  const int32_t clusters = gridDim.x / kCluster, c = blockIdx.x / kCluster;
+  const int32_t per = 2 * p.heads;
+  const int32_t rows_end = ragged::cut(p.kv_offsets[p.batch], p.total_kv);
+  const int64_t all = (int64_t)((rows_end + kCluster * kRows - 1) / (kCluster * kRows)) * per;
+  const int64_t i0 = all * c / clusters, i1 = all * (c + 1) / clusters;
+
+  if (warp < 4) {
+    // ------------------------------------------------ rows in, results out
+    const int r = warp * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+    const int32_t rows_begin = ragged::cut(p.kv_offsets[0], p.total_kv);
+    int32_t group = -1, t0 = 0;
+    int64_t row = -1;
+    bool whole = false;  // every row of the tile (that the tensors have) is a request's
+    uint32_t n = 0;
+    bool ok = true;
+    for (int64_t i = i0; i < i1 && ok; ++i, ++n) {
+      const int32_t g = (int32_t)(i / per), item = (int32_t)(i % per);
+      if (g != group) {
+        // Every product of the previous group is complete: its results were
+        // read below.  The first item's CTAs also copy the rotary dims.
+        group = g;
+        t0 = (g * kCluster + (int32_t)rank) * kRows;
+        row = t0 < p.total_kv ? cache_row(p, t0 + r) : -1;
+        if (row == -2) report(p.dev_status, MLA_ERR_DEVICE_RANGE);
+        whole = t0 < p.total_kv && t0 >= rows_begin && min(t0 + kRows, p.total_kv) <= rows_end;
+        tc_fence_after();
+        load_row<kFp8>(p, row, t0 + r, item == 0, lanes);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&s.a_full));
+      }
+      const uint32_t buf = n & 1;
+      if (!(ok = warp_wait(s, p, s.d_full[buf], (n >> 1) & 1))) break;
+      tc_fence_after();
+      uint32_t d[kDims];
+#pragma unroll
+      for (int k = 0; k < kDims; k += 32) tmem_ld32(lanes + kColD + 128 * buf + k, d + k);
+      tmem_wait_ld();
+      tc_fence_before();
+      mbar_arrive(smem_u32(&s.d_empty[buf]));
+      const float by = kFp8 ? p.kv_scale : 1.f;
+      uint4 o[kDims / 8];
+#pragma unroll
+      for (int k = 0; k < kDims / 8; ++k) {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(d[8 * k + e]) * by;
+        o[k] = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+      }
+      const int h = item >> 1;
+      if (whole) {
+        // the store that used this staging buffer two items ago has read it
+        if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        named_barrier_sync(1, kRows);
+#pragma unroll
+        for (int k = 0; k < kDims / 8; ++k)
+          *reinterpret_cast<uint4 *>(&s.out[buf][k >> 3][r * 128 + (((k & 7) ^ (r & 7)) << 4)]) = o[k];
+        fence_proxy_async_shared();
+        named_barrier_sync(1, kRows);
+        if (threadIdx.x == 0) {
+          const CUtensorMap *m = item & 1 ? &maps.v : &maps.k_nope;
+          tma_store_3d(m, 0, h, t0, smem_u32(s.out[buf][0]));
+          tma_store_3d(m, 64, h, t0, smem_u32(s.out[buf][1]));
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+      } else if (row != -1) {
+        uint4 *dst = reinterpret_cast<uint4 *>((item & 1 ? p.v : p.k_nope) +
+                                               ((int64_t)(t0 + r) * p.heads + h) * kDims);
+#pragma unroll
+        for (int k = 0; k < kDims / 8; ++k) dst[k] = o[k];
+      }
+    }
+    if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  } else if (warp == 4) {
+    // ------------------------------------------------ weights
+    if (elect_one_sync()) {
+      prefetch_tmap(&maps.w_uk);
+      prefetch_tmap(&maps.w_uv);
+      prefetch_tmap(&maps.k_nope);
+      prefetch_tmap(&maps.v);
+      const uint64_t hint = policy_evict_normal();
+      // a stage is 128 rows of 128 bytes, loaded in boxes of kBox rows
+      constexpr int kBox = kCluster <= 2 ? 64 : 128 / kCluster;
+      constexpr int kMine = kDims / kBox / kCluster;  // boxes of this CTA
+      uint32_t n = 0;
+      bool ok = true;
+      for (int64_t i = i0; i < i1 && ok; ++i) {
+        const int32_t item = (int32_t)(i % per), h = item >> 1;
+        for (int kc = 0; kc < kKChunks; ++kc, ++n) {
+          const uint32_t st = n % kStages;
+          if (!(ok = wait_or_abort(s, p, s.w_empty[st], ((n / kStages) & 1) ^ 1))) break;
+          const uint32_t bar = smem_u32(&s.w_full[st]);
+          mbar_arrive_expect_tx(bar, kStage);
+#pragma unroll
+          for (int b = 0; b < kMine; ++b) {
+            const int at = ((int)rank * kMine + b) * kBox;  // first row of the stage
+            const uint32_t dst = smem_u32(s.w[st]) + at * 128;
+            if (item & 1)  // rows: 64 of K for output dims 0-63, then for 64-127
+              load_weights<kCluster>(dst, &maps.w_uv, 64 * (at / 64), h * kVDim + kc * 64 + at % 64, bar, hint);
+            else           // rows: output dims
+              load_weights<kCluster>(dst, &maps.w_uk, kc * 64, h * kDims + at, bar, hint);
+          }
+        }
+      }
+      if (*(volatile int *)&s.abort)  // no copy may still be landing when the shared memory is given up
+        for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i)
+          (void)mbar_wait(smem_u32(&s.w_full[i % kStages]), (i / kStages) & 1, nullptr, kDrainNs);
+    }
+  } else {
+    // ------------------------------------------------ MMA issuer
+    if (elect_one_sync()) {
+      const uint32_t id_k = idesc_bf16_f32(kRows, kDims, 0), id_v = idesc_bf16_f32(kRows, kDims, 1);
+      const uint64_t d_k = smem_desc(smem_u32(s.w[0]), 16, 1024, kSwizzle128B);
+      const uint64_t d_v = smem_desc(smem_u32(s.w[0]), kStage / 2, 1024, kSwizzle128B);
+      int32_t group = -1;
+      uint32_t n = 0, st_n = 0, loads = 0;
+      bool ok = true;
+      for (int64_t i = i0; i < i1 && ok; ++i, ++n) {
+        const int32_t g = (int32_t)(i / per);
+        const bool value = i & 1;  // per is even
+        if (g != group) {
+          group = g;
+          if (!(ok = wait_or_abort(s, p, s.a_full, loads++ & 1))) break;
+        }
+        const uint32_t buf = n & 1;
+        if (!(ok = wait_or_abort(s, p, s.d_empty[buf], ((n >> 1) & 1) ^ 1))) break;
+        tc_fence_after();
+        for (int kc = 0; kc < kKChunks; ++kc, ++st_n) {
+          const uint32_t st = st_n % kStages;
+          if (!(ok = wait_or_abort(s, p, s.w_full[st], (st_n / kStages) & 1))) break;
+          tc_fence_after();
+          const uint64_t b = (value ? d_v : d_k) + (uint64_t)((st * kStage) >> 4);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ts(tmem + kColD + 128 * buf, tmem + kColA + 32 * kc + 8 * k, b + (uint64_t)(value ? 128 * k : 2 * k),
+                   value ? id_v : id_k, (kc > 0 || k > 0) ? 1u : 0u);
+          commit_all<kCluster>(smem_u32(&s.w_empty[st]));
+        }
+        if (ok) mma_commit(smem_u32(&s.d_full[buf]));
+      }
+      mma_commit(smem_u32(&s.fin));
+      if (!mbar_wait(smem_u32(&s.fin), 0, nullptr, kWaitNs)) report(p.dev_status, MLA_ERR_DEVICE_TIMEOUT);
+    }
+  }
+  // no CTA leaves while another may still write into it or arrive at it
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync<kCluster>();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------- host
 
 mla_status_t invalid(const char *why) {
   set_error_detail(why);
@@ -108,10 +421,60 @@ mla_status_t invalid(const char *why) {
 
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
-mla_status_t run(Params p, int64_t num_blocks, bool fp8, void *stream) {
+bool encode(CUtensorMap *m, const void *base, int rank, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t b1, uint32_t b2) {
+  tmap::EncodeTiledFn fn = tmap::encode_fn();
+  if (!fn) return false;
+  cuuint64_t size[3] = {d0, d1, d2}, strides[2] = {d0 * 2, d0 * d1 * 2};
+  cuuint32_t box[3] = {64, b1, b2}, each[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), size, strides, box, each,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool kFp8, int kCluster>
+cudaError_t launch(const Params &p, cudaStream_t stream) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  static std::atomic<int> known[64];
+  int sms = known[dev].load(std::memory_order_acquire);
+  if (sms == 0) {
+    e = cudaFuncSetAttribute(expand_kernel<kFp8, kCluster>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)sizeof(Smem) + 1024);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    known[dev].store(sms, std::memory_order_release);
+  }
+  constexpr uint32_t kBox = kCluster <= 2 ? 64 : 128 / kCluster;
+  Maps maps;
+  if (!encode(&maps.w_uk, p.w_uk, 2, kVDim, (uint64_t)p.heads * kDims, 1, kBox, 1) ||
+      !encode(&maps.w_uv, p.w_uv, 2, kDims, (uint64_t)p.heads * kVDim, 1, kBox, 1) ||
+      !encode(&maps.k_nope, p.k_nope, 3, kDims, p.heads, p.total_kv, 1, kRows) ||
+      !encode(&maps.v, p.v, 3, kDims, p.heads, p.total_kv, 1, kRows))
+    return cudaErrorInvalidValue;
+  // one cluster per item at most, and as many as the SMs hold
+  const int64_t items = ((int64_t)p.total_kv + kCluster * kRows - 1) / (kCluster * kRows) * 2 * p.heads;
+  const int64_t clusters = items < sms / kCluster ? items : sms / kCluster;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(clusters * kCluster));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = sizeof(Smem) + 1024;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kCluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, expand_kernel<kFp8, kCluster>, maps, p);
+}
+
+mla_status_t run(Params p, int64_t num_blocks, int64_t total_kv, bool fp8, void *stream) {
   set_error_detail("");
-  if (p.batch < 0 || p.total_kv < 0 || p.total_kv > INT32_MAX)
-    return invalid("batch < 0, or total_kv outside [0, 2^31)");
+  if (p.batch < 0 || total_kv < 0 || total_kv > INT32_MAX - 1024)
+    return invalid("batch < 0, or total_kv outside [0, 2^31 - 1024)");
+  p.total_kv = (int32_t)total_kv;
   if (p.block_size <= 0 || num_blocks <= 0 || num_blocks > INT32_MAX)
     return invalid("block_size and num_blocks must be > 0");
   if (p.max_blocks_per_seq <= 0) return invalid("max_blocks_per_seq must be > 0");
@@ -129,10 +492,10 @@ mla_status_t run(Params p, int64_t num_blocks, bool fp8, void *stream) {
   if (!aligned(p.block_table, 4) || !aligned(p.kv_offsets, 4))
     return invalid("block_table and kv_offsets must be 4-byte aligned");
   p.num_slots = num_blocks * (int64_t)p.block_size;
-  const dim3 grid((unsigned)((p.total_kv + kRows - 1) / kRows), (unsigned)p.heads);
-  if (fp8) expand_kernel<true><<<grid, kThreads, 0, (cudaStream_t)stream>>>(p);
-  else expand_kernel<false><<<grid, kThreads, 0, (cudaStream_t)stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  // One tile of rows has no neighbour to share weights with.
+  const cudaStream_t st = (cudaStream_t)stream;
+  const cudaError_t e = p.total_kv <= kRows ? (fp8 ? launch<true, 1>(p, st) : launch<false, 1>(p, st))
+                                            : (fp8 ? launch<true, 2>(p, st) : launch<false, 2>(p, st));
   if (e == cudaSuccess) return MLA_OK;
   set_error_detail(cudaGetErrorString(e));
   return MLA_ERR_CUDA;
@@ -140,17 +503,17 @@ mla_status_t run(Params p, int64_t num_blocks, bool fp8, void *stream) {
 
 Params params(const void *cache, int32_t block_size, const int32_t *block_table,
               int32_t max_blocks_per_seq, const int32_t *kv_offsets, int32_t batch,
-              int64_t total_kv, const void *w_uk, const void *w_uv, int32_t num_heads,
-              float kv_scale, void *k_nope, void *v, void *k_pe, int32_t *dev_status) {
+              const void *w_uk, const void *w_uv, int32_t num_heads, float kv_scale,
+              void *k_nope, void *v, void *k_pe, int32_t *dev_status) {
   Params p;
   p.cache = cache;
   p.num_slots = 0;
+  p.total_kv = 0;
   p.block_size = block_size;
   p.block_table = block_table;
   p.max_blocks_per_seq = max_blocks_per_seq;
   p.kv_offsets = kv_offsets;
   p.batch = batch;
-  p.total_kv = total_kv;
   p.w_uk = (const __nv_bfloat16 *)w_uk;
   p.w_uv = (const __nv_bfloat16 *)w_uv;
   p.heads = num_heads;
@@ -176,9 +539,9 @@ mla_status_t mla_expand_kv(const void *cache, int64_t num_blocks, int32_t block_
                            void *v, void *k_pe, int32_t *dev_status, void *stream) {
   TraceRange trace_range("mla_expand_kv");
   return expand::run(expand::params(cache, block_size, block_table, max_blocks_per_seq, kv_offsets,
-                                    batch, total_kv, w_uk, w_uv, num_heads, 1.f, k_nope, v, k_pe,
+                                    batch, w_uk, w_uv, num_heads, 1.f, k_nope, v, k_pe,
                                     dev_status),
-                     num_blocks, false, stream);
+                     num_blocks, total_kv, false, stream);
 }
 
 mla_status_t mla_expand_kv_fp8(const void *cache8, int64_t num_blocks, int32_t block_size,
@@ -191,9 +554,9 @@ mla_status_t mla_expand_kv_fp8(const void *cache8, int64_t num_blocks, int32_t b
   if (!std::isfinite(kv_scale) || !(kv_scale > 0.f))
     return expand::invalid("kv_scale must be positive and finite");
   return expand::run(expand::params(cache8, block_size, block_table, max_blocks_per_seq,
-                                    kv_offsets, batch, total_kv, w_uk, w_uv, num_heads, kv_scale,
-                                    k_nope, v, k_pe, dev_status),
-                     num_blocks, true, stream);
+                                    kv_offsets, batch, w_uk, w_uv, num_heads, kv_scale, k_nope,
+                                    v, k_pe, dev_status),
+                     num_blocks, total_kv, true, stream);
 }
 
 }  // extern "C"

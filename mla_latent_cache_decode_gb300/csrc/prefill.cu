@@ -24,8 +24,9 @@
 // (one thread per row; O is rescaled only when the running maximum grows by
 // more than 2^8), warp 8 issues all MMAs in the order PV_A(j-1) S_A(j)
 // PV_B(j-1) S_B(j), across items too, warp 9 issues the TMA loads, warp 10
-// hands out the items.  Every MMA is issued by one thread, so S_A(j) complete
+// claims the items.  Every MMA is issued by one thread, so S_A(j) complete
 // means PV_A(j-1) complete: O may be rescaled then without a further wait.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 
@@ -47,7 +48,11 @@ constexpr int kChunk = kTile * 128;       // 64 dims of 128 rows, 128-byte swizz
 constexpr int kQChunks = 3, kVChunks = 2; // 64-dim chunks of a query (key) and of a value tile
 constexpr int kKSlots = 4, kVSlots = 2;
 constexpr int kSoftmaxWarps = 8;
-constexpr int kThreads = 32 * (kSoftmaxWarps + 3);
+constexpr int kThreads = 32 * (kSoftmaxWarps + 4);  // the last warp completes a warpgroup
+// Registers a thread: 384 x 168 at launch; the softmax warpgroups, which hold
+// a row of S, take over what the third one gives up.
+constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "register split");
 constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;  // tile t at + 128 t
 // The longest legal wait is for another role's whole item: 2^26 keys, at half
 // a million tiles of 1.3 us, 0.7 s.
@@ -67,7 +72,7 @@ struct Maps {
 
 struct Params {
   const int32_t *q_offsets, *kv_offsets;
-  int32_t batch, heads, total_q, total_kv, causal;
+  int32_t batch, heads, total_q, total_kv, causal, group_heads;
   float scale_log2;
   __nv_bfloat16 *out;
   float *lse;
@@ -87,7 +92,8 @@ struct __align__(1024) Smem {
   uint64_t q_full[2], q_empty[2], k_full[kKSlots], k_empty[kKSlots], v_full[kVSlots], v_empty[kVSlots];
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t work_full[2], work_empty[2];
-  uint64_t fin, roles_done;
+  uint64_t fin, roles_done, claim_full;
+  uint4 claim;  // the answer of cluster launch control
   Work work[2];  // rows = 0: no more items
   uint32_t tmem_base;
   int abort;
@@ -200,23 +206,45 @@ struct Items {
 
 // ---------------------------------------------------------------- softmax
 
-// One key tile of one row: S from tensor memory, running maximum and sum, P
-// back over S.  `lim`: keys of this tile that the row sees (may be <= 0 or
-// >= 128).
-__device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, float scale_log2, bool masked, int lim,
-                                             bool first, float &m, float &l) {
-  uint32_t xr[kTile];
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Two fp32 in one 64-bit register pair: one instruction for two operations.
+__device__ __forceinline__ void fma2(float &x, float &y, float a, float b) {  // x, y = x * a + b, y * a + b
+  asm("{\n .reg .b64 v, m, n;\n mov.b64 v, {%0, %1};\n mov.b64 m, {%2, %2};\n mov.b64 n, {%3, %3};\n"
+      " fma.rn.f32x2 v, v, m, n;\n mov.b64 {%0, %1}, v;\n}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+__device__ __forceinline__ void add2(float &x, float &y, float a, float b) {  // x, y += a, b
+  asm("{\n .reg .b64 v, m;\n mov.b64 v, {%0, %1};\n mov.b64 m, {%2, %3};\n"
+      " add.rn.f32x2 v, v, m;\n mov.b64 {%0, %1}, v;\n}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+
+// One key tile of one row: S from tensor memory, its maximum, and the weights
+// back over S as bf16; x holds the weights in fp32 afterwards.  `lim`: keys of
+// this tile that the row sees (may be <= 0 or >= 128).  Returns what the sum
+// so far is to be multiplied with.
+__device__ __forceinline__ float softmax_tile(uint32_t s_addr, uint32_t o_addr, float scale_log2, bool masked, int lim,
+                                              bool first, float &m, float (&x)[kTile]) {
+  uint32_t *xr = reinterpret_cast<uint32_t *>(x);
 #pragma unroll
   for (int c = 0; c < kTile; c += 32) tmem_ld32(s_addr + c, xr + c);
   tmem_wait_ld();
-  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
   if (masked) {
 #pragma unroll
-    for (int k = 0; k < kTile; ++k)
-      if (k >= lim) xr[k] = 0xff800000u;  // -inf
+    for (int k = 0; k < kTile; ++k) x[k] = k < lim ? x[k] : -INFINITY;
   }
+  float mx[4];
 #pragma unroll
-  for (int k = 0; k < kTile; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(xr[k]));
+  for (int k = 0; k < 4; ++k) mx[k] = fmaxf(x[2 * k], x[2 * k + 1]);
+#pragma unroll
+  for (int k = 8; k < kTile; k += 2) mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], x[k], x[k + 1]);
   const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale_log2;
   const bool grow = top > m + kRescale || (m == -INFINITY && top > -INFINITY);
   float alpha = 1.f;
@@ -226,30 +254,40 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, f
   }
   if (!first && __any_sync(0xffffffffu, grow)) {
 #pragma unroll 1
-    for (int c = 0; c < kV; c += 32) {
-      uint32_t o[32];
-      tmem_ld32(o_addr + c, o);
+    for (int c = 0; c < kV; c += 16) {
+      uint32_t o[16];
+      tmem_ld16(o_addr + c, o);
       tmem_wait_ld();
 #pragma unroll
-      for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-      tmem_st32(o_addr + c, o);
+      for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+      tmem_st16(o_addr + c, o);
     }
   }
   const float nm = m == -INFINITY ? 0.f : -m;  // a row that has seen nothing: every weight is 0
-  float ps[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int c = 0; c < kTile; c += 32) {
     uint32_t pk[16];
 #pragma unroll
     for (int k = 0; k < 32; k += 2) {
-      const float a = ex2_approx(fmaf(__uint_as_float(xr[c + k]), scale_log2, nm));
-      const float b = ex2_approx(fmaf(__uint_as_float(xr[c + k + 1]), scale_log2, nm));
-      ps[(k >> 1) & 3] += a + b;
-      pk[k / 2] = pack2(a, b);
+      fma2(x[c + k], x[c + k + 1], scale_log2, nm);
+      x[c + k] = ex2_approx(x[c + k]);
+      x[c + k + 1] = ex2_approx(x[c + k + 1]);
+      pk[k / 2] = pack2(x[c + k], x[c + k + 1]);
     }
     tmem_st16(s_addr + c / 2, pk);
   }
-  l = l * alpha + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
+  return alpha;
+}
+
+// The sum of a tile's weights, off the path to P V.
+__device__ __forceinline__ float sum_tile(const float (&x)[kTile]) {
+  float a = x[0], b = x[1], c = x[2], d = x[3];
+#pragma unroll
+  for (int k = 4; k < kTile; k += 4) {
+    add2(a, b, x[k], x[k + 1]);
+    add2(c, d, x[k + 2], x[k + 3]);
+  }
+  return (a + b) + (c + d);
 }
 
 __device__ __forceinline__ void softmax_role(Smem &s, const Params &p, int warp, int lane, uint32_t tmem) {
@@ -265,14 +303,16 @@ __device__ __forceinline__ void softmax_role(Smem &s, const Params &p, int warp,
     __syncwarp();
     if (lane == 0) items.done(s); else ++items.i;
     if (w.rows == 0) return;
-    const int n = w.n[t], all = max(w.n[0], w.n[1]);
+    const int n = t ? w.n[1] : w.n[0], all = max(w.n[0], w.n[1]);
     const int sees = min(w.nk, p.causal ? w.see + t * kTile + row : w.nk);  // keys this row sees
     float m = -INFINITY, l = 0.f;
     for (int j = 0; j < n; ++j, ++g) {
       if (!warp_wait(s, p, s.s_full[t], g & 1)) return;
       tc_fence_after();
       const int lim = sees - j * kTile;
-      softmax_tile(s_addr, o_addr, p.scale_log2, __any_sync(0xffffffffu, lim < kTile), lim, j == 0, m, l);
+      float x[kTile];
+      const float alpha =
+          softmax_tile(s_addr, o_addr, p.scale_log2, __any_sync(0xffffffffu, lim < kTile), lim, j == 0, m, x);
       // A last key tile's P V reads value rows up to a multiple of 16: those
       // behind the request's last key hold anything (0 * NaN = NaN), so they
       // are zeroed first, by both query tiles alike.
@@ -290,6 +330,7 @@ __device__ __forceinline__ void softmax_role(Smem &s, const Params &p, int warp,
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(smem_u32(&s.p_full[t]));
+      l = l * alpha + sum_tile(x);
     }
     vg += all;
     const int64_t out_row = (int64_t)w.q0 + t * kTile + row;
@@ -365,13 +406,15 @@ __device__ __forceinline__ void mma_role(Smem &s, const Params &p, uint32_t tmem
     items.done(s);
     const int all = max(w.n[0], w.n[1]);
     if (all == 0) {  // no key to see, or no more items: what is pending has no S to wait behind
-      for (int t = 0; t < 2 && ok; ++t)
-        if (pend[t].on) ok = run_pv(t);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        if (ok && pend[t].on) ok = run_pv(t);
       if (w.rows == 0) break;
     }
     for (int j = 0; j < all && ok; ++j, ++kv) {
-      for (int t = 0; t < 2 && ok; ++t) {
-        if (pend[t].on && !(ok = run_pv(t))) break;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (!ok || (pend[t].on && !(ok = run_pv(t)))) break;
         if (j >= w.n[t]) continue;
         if (j == 0 && !(ok = wait_or_abort(s, p, s.q_full[t], q_used[t]++ & 1))) break;
         const bool last_user = t == 1 || j >= w.n[1];
@@ -469,20 +512,62 @@ __device__ __forceinline__ void load_role(Smem &s, const Params &p, const Maps &
 
 // ---------------------------------------------------------------- scheduler
 
+// The grid has a block for every item there may be (the host does not know
+// the lengths).  A running block claims the items of blocks that have not
+// started yet (cluster launch control): first come, first served, without a
+// counter in memory.
+struct Claims {
+  uint32_t phase = 0;
+  // By one warp: the next item's index, -1 when none is left, -2 on giving up.
+  __device__ __forceinline__ int64_t next(Smem &s, const Params &p, int lane) {
+    if (lane == 0) {
+      fence_proxy_async_shared();  // the last answer has been read
+      mbar_arrive_expect_tx(smem_u32(&s.claim_full), 16);
+      asm volatile(
+          "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+              smem_u32(&s.claim)),
+          "r"(smem_u32(&s.claim_full))
+          : "memory");
+    }
+    if (!warp_wait(s, p, s.claim_full, phase)) return -2;
+    phase ^= 1;
+    uint64_t a0, a1;
+    asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(a0), "=l"(a1) : "r"(smem_u32(&s.claim)) : "memory");
+    uint32_t got, x;
+    asm("{\n .reg .pred p;\n .reg .b128 a;\n mov.b128 a, {%2, %3};\n"
+        " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n selp.u32 %0, 1, 0, p;\n mov.u32 %1, 0;\n"
+        " @p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, _, _, _}, a;\n}"
+        : "=r"(got), "=r"(x)
+        : "l"(a0), "l"(a1));
+    __syncwarp();
+    return got ? (int64_t)x : -1;
+  }
+};
+
+// Order of the items: groups of `group_heads` heads whose keys and values fit
+// L2 together; in a group the tiles of a request from its last (the longest
+// when causal) to its first, each for all the group's heads.
 __device__ __forceinline__ void schedule_role(Smem &s, const Params &p, int lane) {
   const int64_t tiles = count_tiles(p, lane);
   const int64_t items = tiles * p.heads;
+  Claims claims;
   uint32_t i = 0;
-  for (int64_t at = blockIdx.x;; at += gridDim.x, ++i) {
+  for (int64_t at = blockIdx.x; at != -2; at = claims.next(s, p, lane)) {
+    if (at >= items) continue;  // a block more than there are items
     Work w = {};
-    const bool more = at < items;
-    if (more) w = find_work(p, at % tiles, (int32_t)(at / tiles), lane);
+    if (at >= 0) {
+      const int64_t first = at / (tiles * p.group_heads) * p.group_heads;  // the group's first head
+      const int32_t heads = (int32_t)min((int64_t)p.group_heads, p.heads - first);
+      const int64_t in_group = at - first * tiles;
+      w = find_work(p, in_group / heads, (int32_t)(first + in_group % heads), lane);
+    }
     if (!warp_wait(s, p, s.work_empty[i & 1], ((i >> 1) & 1) ^ 1)) return;
     if (lane == 0) {
       s.work[i & 1] = w;
       mbar_arrive(smem_u32(&s.work_full[i & 1]));
     }
-    if (!more) return;
+    ++i;
+    if (at < 0) return;
   }
 }
 
@@ -508,6 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       mbar_init(smem_u32(&s.v_full[i]), 1);
       mbar_init(smem_u32(&s.v_empty[i]), 1);
     }
+    mbar_init(smem_u32(&s.claim_full), 1);
     mbar_init(smem_u32(&s.fin), 1);
     mbar_init(smem_u32(&s.roles_done), kThreads / 32);
     s.abort = 0;
@@ -528,13 +614,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   const uint32_t tmem = s.tmem_base;
 
   if (warp < kSoftmaxWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     softmax_role(s, p, warp, lane, tmem);
-  } else if (warp == kSoftmaxWarps) {
-    if (elect_one_sync()) mma_role(s, p, tmem);
-  } else if (warp == kSoftmaxWarps + 1) {
-    if (elect_one_sync()) load_role(s, p, maps);
   } else {
-    schedule_role(s, p, lane);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kSoftmaxWarps) {
+      if (elect_one_sync()) mma_role(s, p, tmem);
+    } else if (warp == kSoftmaxWarps + 1) {
+      if (elect_one_sync()) load_role(s, p, maps);
+    } else if (warp == kSoftmaxWarps + 2) {
+      schedule_role(s, p, lane);
+    }
   }
 
   // the tensor memory is freed once every warp has reported the end of its role
@@ -599,16 +689,14 @@ bool encode(CUtensorMap *m, const Strided &s, int64_t tokens, int32_t heads, int
 
 constexpr size_t kWorkspaceBytes = 32u << 20;
 
-// SMs of a device; the kernel's shared-memory opt-in is set on the way.
-cudaError_t prepare_device(int dev, int *sms) {
-  static std::atomic<int> known[64];
+// The kernel's shared-memory opt-in, once per device.
+cudaError_t prepare_device(int dev) {
+  static std::atomic<bool> done[64];
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  *sms = known[dev].load(std::memory_order_acquire);
-  if (*sms > 0) return cudaSuccess;
-  cudaError_t e = cudaFuncSetAttribute(prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)sizeof(Smem) + 1024);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess) known[dev].store(*sms, std::memory_order_release);
+  if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)sizeof(Smem) + 1024);
+  if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
   return e;
 }
 
@@ -638,9 +726,9 @@ mla_status_t run(const Args &a, void *workspace, size_t workspace_bytes, void *s
     set_error_detail("workspace must be 256-byte aligned and of mla_prefill_workspace_size()");
     return aligned(workspace, 256) ? MLA_ERR_WORKSPACE_TOO_SMALL : MLA_ERR_INVALID_ARGUMENT;
   }
-  int dev = 0, sms = 0;
+  int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = prepare_device(dev, &sms);
+  if (e == cudaSuccess) e = prepare_device(dev);
   if (e != cudaSuccess) return cuda_failed(e);
   Maps maps;
   if (!encode(&maps.q_nope, a.q_nope, a.total_q, a.heads, kNope, a.out) ||
@@ -663,9 +751,13 @@ mla_status_t run(const Args &a, void *workspace, size_t workspace_bytes, void *s
   p.out = (__nv_bfloat16 *)a.out;
   p.lse = a.lse;
   p.dev_status = a.dev_status;
+  // heads whose keys and values take up to 48 MB (of 129 MB of L2)
+  const int64_t head_bytes = a.total_kv * (kNope + kV) * 2 + 1;
+  p.group_heads = (int32_t)std::min<int64_t>(a.heads, std::max<int64_t>(1, (48 << 20) / head_bytes));
   // no more items than this, whatever the offsets say
   const int64_t most = (a.total_q / (2 * kTile) + a.batch) * (int64_t)a.heads;
-  prefill_kernel<<<(unsigned)(most < sms ? most : sms), kThreads, sizeof(Smem) + 1024, (cudaStream_t)stream>>>(maps, p);
+  if (most > INT32_MAX) return invalid("more than 2^31 tiles of 256 queries and a head");
+  prefill_kernel<<<(unsigned)most, kThreads, sizeof(Smem) + 1024, (cudaStream_t)stream>>>(maps, p);
   e = cudaGetLastError();
   return e == cudaSuccess ? MLA_OK : cuda_failed(e);
 }

@@ -60,6 +60,8 @@ constexpr int64_t kMaxKv = 1 << 26;
 constexpr uint64_t kWaitNs = 3000000000ull;
 constexpr uint64_t kDrainNs = 10000000ull;
 constexpr float kRescale = 8.0f;  // log2
+constexpr int64_t kGroupBytes = 48 << 20;  // keys and values walked together, of 129 MB of L2
+constexpr int kMinPart = 4;                // key tiles of a part, at least
 
 struct Strided {
   const __nv_bfloat16 *p;
@@ -72,17 +74,23 @@ struct Maps {
 
 struct Params {
   const int32_t *q_offsets, *kv_offsets;
-  int32_t batch, heads, total_q, total_kv, causal, group_heads;
+  int32_t batch, heads, total_q, total_kv, causal;
   float scale_log2;
   __nv_bfloat16 *out;
   float *lse;
+  float *partial, *partial_lse;  // split form: [blocks][256][128], [blocks][256]; else null
   int32_t *dev_status;
 };
 
-// One item: rows [q0, q0 + rows) of head h over key rows [k0, k0 + nk).  Row r
-// of the item sees keys [0, min(nk, see + r)); tile t runs n[t] key tiles.
+// One item: rows [q0, q0 + rows) of head h over key tiles [kt, kt + .) of key
+// rows [k0, k0 + nk).  Row r of the item sees keys [0, min(nk, see + r)).
+// More than 128 rows: query tile t holds rows 128 t .. and runs n[t] key tiles
+// from kt on (n[0] <= n[1]).  Up to 128 rows (shared): both query tiles hold
+// the same rows, tile t runs key tiles kt + t, kt + t + 2, ...: two chains of
+// softmax and MMA instead of one, joined in the epilogue.
 struct Work {
-  int32_t h, q0, rows, k0, nk, see, n[2];
+  int32_t h, q0, rows, k0, nk, see, kt, n[2], shared;
+  int32_t part, parts, slot, slot_step;  // parts > 1: a part of the keys, joined later
 };
 
 struct __align__(1024) Smem {
@@ -91,6 +99,9 @@ struct __align__(1024) Smem {
   uint8_t v[kVSlots][kVChunks][kChunk];
   uint64_t q_full[2], q_empty[2], k_full[kKSlots], k_empty[kKSlots], v_full[kVSlots], v_empty[kVSlots];
   uint64_t s_full[2], p_full[2], o_full[2];
+  // a shared item: tile 1's maxima and sums, then both tiles' factors
+  float2 join[kTile];
+  uint64_t join_sums, join_factors, join_end;
   uint64_t work_full[2], work_empty[2];
   uint64_t fin, roles_done, claim_full;
   uint4 claim;  // the answer of cluster launch control
@@ -131,63 +142,162 @@ __device__ __forceinline__ int32_t rows_of(const int32_t *o, int32_t b, int32_t 
   return max(ragged::cut(o[b + 1], total) - ragged::cut(o[b], total), 0);
 }
 
-// Item tiles of 256 rows of all requests, by one warp.
-__device__ __forceinline__ int64_t count_tiles(const Params &p, int lane) {
-  int64_t n = 0;
-  for (int32_t b = lane; b < p.batch; b += 32)
-    n += (rows_of(p.q_offsets, b, p.total_q) + 2 * kTile - 1) / (2 * kTile);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-  return n;
+// A lane's request.
+struct Request {
+  int32_t q0, nq, k0, nk, tiles;  // tiles of 256 queries
+};
+
+__device__ __forceinline__ Request request(const Params &p, int32_t b) {
+  Request r = {};
+  if (b >= p.batch) return r;
+  r.q0 = ragged::cut(p.q_offsets[b], p.total_q);
+  r.nq = rows_of(p.q_offsets, b, p.total_q);
+  r.k0 = ragged::cut(p.kv_offsets[b], p.total_kv);
+  r.nk = rows_of(p.kv_offsets, b, p.total_kv);
+  r.tiles = (r.nq + 2 * kTile - 1) / (2 * kTile);
+  return r;
 }
 
-// Tile r (of all requests' tiles; a request's tiles counted from its end), by
-// one warp; every lane gets the result.
-__device__ __forceinline__ Work find_work(const Params &p, int64_t r, int32_t h, int lane) {
+__device__ __forceinline__ Request shuffle(const Request &r, int src) {
+  Request o;
+  o.q0 = __shfl_sync(0xffffffffu, r.q0, src);
+  o.nq = __shfl_sync(0xffffffffu, r.nq, src);
+  o.k0 = __shfl_sync(0xffffffffu, r.k0, src);
+  o.nk = __shfl_sync(0xffffffffu, r.nk, src);
+  o.tiles = __shfl_sync(0xffffffffu, r.tiles, src);
+  return o;
+}
+
+// Up to 32 requests in the order of their contexts, longest first, so that
+// the longest items start first and short ones fill the end.
+__device__ __forceinline__ Request sorted(const Request &r, int lane) {
+  int rank = 0, src = 0;
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i) {
+    const int32_t nk = __shfl_sync(0xffffffffu, r.nk, i);
+    rank += nk > r.nk || (nk == r.nk && i < lane);
+  }
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i)
+    if (__shfl_sync(0xffffffffu, rank, i) == lane) src = i;
+  return shuffle(r, src);
+}
+
+__device__ __forceinline__ int64_t prefix(int64_t x, int lane) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+// Key tiles that rows [first, first + rows) of a request run over.
+__device__ __forceinline__ int32_t key_tiles(const Params &p, const Request &r, int32_t first, int32_t rows) {
+  const int32_t keys = p.causal ? min(r.nk, r.nk - r.nq + first + rows) : r.nk;
+  return rows > 0 && keys > 0 ? (keys + kTile - 1) / kTile : 0;
+}
+
+// Tile `tile` (from the request's start) of head h, key tiles
+// [n part / parts, n (part + 1) / parts) of its n.
+__device__ __forceinline__ Work make_work(const Params &p, const Request &r, int32_t tile, int32_t h, int32_t part,
+                                          int32_t parts) {
   Work w = {};
+  const int32_t first = tile * 2 * kTile;
+  w.h = h;
+  w.q0 = r.q0 + first;
+  w.rows = min(2 * kTile, r.nq - first);
+  w.k0 = r.k0;
+  w.nk = r.nk;
+  w.see = p.causal ? r.nk - r.nq + first + 1 : r.nk;
+  w.part = part;
+  w.parts = parts;
+  const int32_t n = key_tiles(p, r, first, w.rows);
+  w.kt = (int32_t)((int64_t)n * part / parts);
+  const int32_t end = (int32_t)((int64_t)n * (part + 1) / parts);
+  w.shared = w.rows <= kTile;
+  if (w.shared) {
+    w.n[0] = (end - w.kt + 1) / 2;
+    w.n[1] = (end - w.kt) / 2;
+  } else {
+    w.n[0] = max(min(key_tiles(p, r, first, kTile), end) - w.kt, 0);
+    w.n[1] = end - w.kt;
+  }
+  return w;
+}
+
+// Item `at` in the order: requests (up to 32: longest context first), groups of
+// heads whose keys and values fit L2 together, tiles from the request's last
+// (the longest when causal) to its first, heads of the group.  By one warp;
+// rows = 0 behind the last.
+__device__ __forceinline__ Work find_work(const Params &p, const Request &few, int64_t at, int lane) {
   int64_t before = 0;
   for (int32_t b0 = 0; b0 < p.batch; b0 += 32) {
-    const int32_t b = b0 + lane;
-    const int32_t nq = b < p.batch ? rows_of(p.q_offsets, b, p.total_q) : 0;
-    const int32_t mine = (nq + 2 * kTile - 1) / (2 * kTile);
-    int64_t upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += x;
-    }
-    upto += before;
-    const uint32_t hit = __ballot_sync(0xffffffffu, r >= upto - mine && r < upto);
+    const Request mine = p.batch <= 32 ? few : request(p, b0 + lane);
+    const int64_t items = (int64_t)mine.tiles * p.heads, upto = before + prefix(items, lane);
+    const uint32_t hit = __ballot_sync(0xffffffffu, at >= upto - items && at < upto);
     if (hit) {
       const int src = __ffs(hit) - 1;
-      if (lane == src) {
-        const int32_t tile = (int32_t)(upto - 1 - r);  // counted from the request's start
-        const int32_t first = tile * 2 * kTile;
-        w.h = h;
-        w.q0 = ragged::cut(p.q_offsets[b], p.total_q) + first;
-        w.rows = min(2 * kTile, nq - first);
-        w.k0 = ragged::cut(p.kv_offsets[b], p.total_kv);
-        w.nk = rows_of(p.kv_offsets, b, p.total_kv);
-        w.see = p.causal ? w.nk - nq + first + 1 : w.nk;
-        for (int t = 0; t < 2; ++t) {
-          const int32_t last = min(w.rows, (t + 1) * kTile) - 1;  // the tile's last row sees most
-          const int32_t keys = p.causal ? min(w.nk, w.see + last) : w.nk;
-          w.n[t] = w.rows > t * kTile && keys > 0 ? (keys + kTile - 1) / kTile : 0;
-        }
-      }
-      w.h = __shfl_sync(0xffffffffu, w.h, src);
-      w.q0 = __shfl_sync(0xffffffffu, w.q0, src);
-      w.rows = __shfl_sync(0xffffffffu, w.rows, src);
-      w.k0 = __shfl_sync(0xffffffffu, w.k0, src);
-      w.nk = __shfl_sync(0xffffffffu, w.nk, src);
-      w.see = __shfl_sync(0xffffffffu, w.see, src);
-      w.n[0] = __shfl_sync(0xffffffffu, w.n[0], src);
-      w.n[1] = __shfl_sync(0xffffffffu, w.n[1], src);
-      return w;
+      const Request r = shuffle(mine, src);
+      const int64_t i = at - __shfl_sync(0xffffffffu, upto - items, src);
+      const int64_t head_bytes = (int64_t)r.nk * (kNope + kV) * 2 + 1;
+      const int32_t group = (int32_t)min((int64_t)p.heads, max((int64_t)1, kGroupBytes / head_bytes));
+      const int32_t first = (int32_t)(i / ((int64_t)r.tiles * group)) * group;
+      const int32_t heads = min(group, p.heads - first);
+      const int32_t in_group = (int32_t)(i - (int64_t)first * r.tiles);
+      return make_work(p, r, r.tiles - 1 - in_group / heads, first + in_group % heads, 0, 1);
     }
     before = __shfl_sync(0xffffffffu, upto, 31);
   }
-  return w;
+  return Work{};
+}
+
+// Split form: few items on long contexts.  Every item is cut into parts of at
+// most `most` key tiles, such that the parts are no more than the blocks; part
+// `at` leaves its output in slot `at` of the workspace.  By one warp; rows = 0
+// behind the last.
+__device__ __forceinline__ Work find_part(const Params &p, int64_t at, int32_t blocks, int lane) {
+  int64_t items = 0, total = 0;
+  for (int32_t b = lane; b < p.batch; b += 32) {
+    const Request r = request(p, b);
+    items += r.tiles;
+    for (int32_t t = 0; t < r.tiles; ++t)
+      total += key_tiles(p, r, t * 2 * kTile, min(2 * kTile, r.nq - t * 2 * kTile));
+  }
+  items = __shfl_sync(0xffffffffu, prefix(items, lane), 31) * p.heads;
+  total = __shfl_sync(0xffffffffu, prefix(total, lane), 31) * p.heads;
+  // sum of ceil(n / most) <= total / most + items <= blocks (items <= blocks / 2)
+  const int64_t most = max((int64_t)kMinPart, (total + blocks - items - 1) / max((int64_t)1, blocks - items));
+  int64_t before = 0;
+  for (int32_t b0 = 0; b0 < p.batch; b0 += 32) {
+    const Request mine = request(p, b0 + lane);
+    int64_t parts = 0;
+    for (int32_t t = 0; t < mine.tiles; ++t) {
+      const int32_t n = key_tiles(p, mine, t * 2 * kTile, min(2 * kTile, mine.nq - t * 2 * kTile));
+      parts += max((int64_t)1, (n + most - 1) / most) * p.heads;
+    }
+    const int64_t upto = before + prefix(parts, lane);
+    const uint32_t hit = __ballot_sync(0xffffffffu, at >= upto - parts && at < upto);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      const Request r = shuffle(mine, src);
+      int64_t first = __shfl_sync(0xffffffffu, upto - parts, src);
+      for (int32_t t = 0; t < r.tiles; ++t) {
+        const int32_t n = key_tiles(p, r, t * 2 * kTile, min(2 * kTile, r.nq - t * 2 * kTile));
+        const int32_t cut = (int32_t)max((int64_t)1, (n + most - 1) / most);
+        if (at < first + (int64_t)cut * p.heads) {
+          const int32_t i = (int32_t)(at - first);
+          Work w = make_work(p, r, t, i % p.heads, i / p.heads, cut);
+          w.slot = (int32_t)at;
+          w.slot_step = p.heads;
+          return w;
+        }
+        first += (int64_t)cut * p.heads;
+      }
+    }
+    before = __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return Work{};
 }
 
 // A role's view of the items: next() waits for one and copies it, done()
@@ -226,12 +336,12 @@ __device__ __forceinline__ void add2(float &x, float &y, float a, float b) {  //
       : "f"(a), "f"(b));
 }
 
-// One key tile of one row: S from tensor memory, its maximum, and the weights
-// back over S as bf16; x holds the weights in fp32 afterwards.  `lim`: keys of
-// this tile that the row sees (may be <= 0 or >= 128).  Returns what the sum
-// so far is to be multiplied with.
-__device__ __forceinline__ float softmax_tile(uint32_t s_addr, uint32_t o_addr, float scale_log2, bool masked, int lim,
-                                              bool first, float &m, float (&x)[kTile]) {
+// One key tile of one row: S from tensor memory, its maximum and the sum of the
+// weights, and the weights back over S as bf16.  `lim`: keys of this tile that
+// the row sees (may be <= 0 or >= 128).
+__device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, float scale_log2, bool masked, int lim,
+                                             bool first, float &m, float &l) {
+  float x[kTile];
   uint32_t *xr = reinterpret_cast<uint32_t *>(x);
 #pragma unroll
   for (int c = 0; c < kTile; c += 32) tmem_ld32(s_addr + c, xr + c);
@@ -247,121 +357,196 @@ __device__ __forceinline__ float softmax_tile(uint32_t s_addr, uint32_t o_addr, 
   for (int k = 8; k < kTile; k += 2) mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], x[k], x[k + 1]);
   const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale_log2;
   const bool grow = top > m + kRescale || (m == -INFINITY && top > -INFINITY);
-  float alpha = 1.f;
-  if (grow) {
-    alpha = ex2_approx(m - top);  // 0 when nothing was seen before
-    m = top;
-  }
-  if (!first && __any_sync(0xffffffffu, grow)) {
+  if (__any_sync(0xffffffffu, grow)) {
+    const float alpha = grow ? ex2_approx(m - top) : 1.f;  // 0 when nothing was seen before
+    if (grow) m = top;
+    l *= alpha;
+    if (!first) {
 #pragma unroll 1
-    for (int c = 0; c < kV; c += 16) {
-      uint32_t o[16];
-      tmem_ld16(o_addr + c, o);
-      tmem_wait_ld();
+      for (int c = 0; c < kV; c += 8) {
+        uint32_t o[8];
+        tmem_ld8(o_addr + c, o);
+        tmem_wait_ld();
 #pragma unroll
-      for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-      tmem_st16(o_addr + c, o);
+        for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+        tmem_st8(o_addr + c, o);
+      }
     }
   }
   const float nm = m == -INFINITY ? 0.f : -m;  // a row that has seen nothing: every weight is 0
+  float ps[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int c = 0; c < kTile; c += 32) {
     uint32_t pk[16];
 #pragma unroll
     for (int k = 0; k < 32; k += 2) {
-      fma2(x[c + k], x[c + k + 1], scale_log2, nm);
-      x[c + k] = ex2_approx(x[c + k]);
-      x[c + k + 1] = ex2_approx(x[c + k + 1]);
-      pk[k / 2] = pack2(x[c + k], x[c + k + 1]);
+      float a = x[c + k], b = x[c + k + 1];
+      fma2(a, b, scale_log2, nm);
+      a = ex2_approx(a);
+      b = ex2_approx(b);
+      add2(ps[k & 2], ps[(k & 2) + 1], a, b);
+      pk[k / 2] = pack2(a, b);
     }
     tmem_st16(s_addr + c / 2, pk);
   }
-  return alpha;
+  l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
 }
 
-// The sum of a tile's weights, off the path to P V.
-__device__ __forceinline__ float sum_tile(const float (&x)[kTile]) {
-  float a = x[0], b = x[1], c = x[2], d = x[3];
+// 16 outputs of a row as 32 bytes; `wide`: the address is a multiple of 32.
+__device__ __forceinline__ void store16(__nv_bfloat16 *dst, const float *x, bool wide) {
+  uint32_t u[8];
 #pragma unroll
-  for (int k = 4; k < kTile; k += 4) {
-    add2(a, b, x[k], x[k + 1]);
-    add2(c, d, x[k + 2], x[k + 3]);
+  for (int k = 0; k < 8; ++k) u[k] = pack2(x[2 * k], x[2 * k + 1]);
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(u[0]), "r"(u[1]),
+                 "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4 *>(dst)[0] = make_uint4(u[0], u[1], u[2], u[3]);
+    reinterpret_cast<uint4 *>(dst)[1] = make_uint4(u[4], u[5], u[6], u[7]);
   }
-  return (a + b) + (c + d);
+}
+
+// Columns [c0, c1) of a row's output: a * O_a (+ b * O_b with `two`), to `out`
+// as bf16 or, for a part of the keys, to `partial` as fp32.  `any`: O holds
+// something.
+// (Not inlined: the softmax loop around it needs the registers.)
+__device__ __noinline__ void store_row(uint32_t oa, float a, uint32_t ob, float b, bool two, bool any, int c0, int c1,
+                                          bool real, __nv_bfloat16 *out, bool wide, float *partial) {
+#pragma unroll 1
+  for (int c = c0; c < c1; c += 32) {
+    float x[32];
+    uint32_t *xr = reinterpret_cast<uint32_t *>(x);
+    if (any) {
+      tmem_ld32(oa + c, xr);
+      tmem_wait_ld();
+    }
+#pragma unroll
+    for (int k = 0; k < 32; ++k) x[k] = a > 0.f ? x[k] * a : 0.f;
+    if (two) {
+      uint32_t y[32];
+      tmem_ld32(ob + c, y);
+      tmem_wait_ld();
+#pragma unroll
+      for (int k = 0; k < 32; ++k) x[k] += b > 0.f ? __uint_as_float(y[k]) * b : 0.f;
+    }
+    if (!real) continue;
+    if (partial) {
+#pragma unroll
+      for (int k = 0; k < 32; k += 4)
+        *reinterpret_cast<float4 *>(partial + c + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+    } else {
+      store16(out + c, x, wide);
+      store16(out + c + 16, x + 16, wide);
+    }
+  }
 }
 
 __device__ __forceinline__ void softmax_role(Smem &s, const Params &p, int warp, int lane, uint32_t tmem) {
   const int t = warp >> 2, q4 = warp & 3;
   const int row = q4 * 32 + lane;  // of the tile: TMEM lane
   const uint32_t lanes = tmem + ((uint32_t)(q4 * 32) << 16);
-  const uint32_t s_addr = lanes + kColS + 128 * t, o_addr = lanes + kColO + 128 * t;
+  const uint32_t s_addr = lanes + kColS + 128 * t;
+  const bool wide = ((uintptr_t)p.out & 31) == 0;
   Items items;
-  uint32_t g = 0, vg = 0, outs = 0;  // key tiles of this query tile, key tiles loaded, outputs
+  // key tiles of this query tile, key tiles loaded, outputs of either query tile, shared items
+  uint32_t g = 0, vg = 0, outs0 = 0, outs1 = 0, joins = 0;
   while (true) {
     if (!warp_wait(s, p, s.work_full[items.i & 1], (items.i >> 1) & 1)) return;
-    const Work w = items.get(s);
+    // read from shared memory where it is needed: the registers are S's
+    const Work &w = s.work[items.i & 1];
+    if (w.rows == 0) return;
+    const int n = t ? w.n[1] : w.n[0];
+    const int at = w.shared ? row : t * kTile + row;  // row of the item
+    float m = -INFINITY, l = 0.f;
+    {
+      // of this query tile's first key tile: the keys the row sees from there
+      // on, the keys there are, and its number among all tiles loaded
+      const int key = (w.kt + (w.shared ? t : 0)) * kTile;
+      int lim = min(w.nk, p.causal ? w.see + at : w.nk) - key;
+      const int step = w.shared ? 2 : 1;
+      for (int j = 0; j < n; ++j, ++g, lim -= step * kTile) {
+        if (!warp_wait(s, p, s.s_full[t], g & 1)) return;
+        tc_fence_after();
+        softmax_tile(s_addr, s_addr + (kColO - kColS), p.scale_log2, __any_sync(0xffffffffu, lim < kTile), lim, j == 0, m,
+                     l);
+        if (j == n - 1) {
+          // A last key tile's P V reads value rows up to a multiple of 16: those
+          // behind the request's last key hold anything (0 * NaN = NaN), so they
+          // are zeroed first, by both query tiles alike.
+          const int jt = w.shared ? 2 * j + t : j, valid = w.nk - (w.kt + jt) * kTile;
+          if (valid < kTile && (valid & 15)) {
+            const uint32_t vi = vg + jt;
+            if (!warp_wait(s, p, s.v_full[vi % kVSlots], (vi / kVSlots) & 1)) return;
+            const int pad = 16 - (valid & 15);
+            for (int k = q4 * 32 + lane; k < pad * 16; k += 128) {
+              const int r = valid + (k >> 4), c = (k >> 3) & 1;
+              *reinterpret_cast<uint4 *>(&s.v[vi % kVSlots][c][r * 128 + (k & 7) * 16]) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_shared();
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&s.p_full[t]));
+      }
+    }
+    vg += w.shared ? w.n[0] + w.n[1] : w.n[1];
+    // ---- epilogue: O / l
+    const bool real = at < w.rows;
+    const int64_t out_row = ((int64_t)w.q0 + at) * p.heads + w.h;
+    __nv_bfloat16 *out = p.out + out_row * kV;
+    float *partial = nullptr, *lse = p.lse ? p.lse + out_row : nullptr;
+    if (w.parts > 1) {
+      partial = p.partial + ((int64_t)w.slot * 2 * kTile + at) * kV;
+      lse = p.partial_lse + (int64_t)w.slot * 2 * kTile + at;
+    }
+    if (!w.shared) {
+      if (n > 0) {
+        if (!warp_wait(s, p, s.o_full[t], (t ? outs1 : outs0) & 1)) return;
+        tc_fence_after();
+      }
+      store_row(s_addr + (kColO - kColS), l > 0.f ? 1.f / l : 0.f, 0, 0.f, false, n > 0, 0, kV, real, out, wide, partial);
+      if (real && lse) *lse = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+      tc_fence_before();
+    } else {
+      // tile 1 tells its maxima and sums, tile 0 answers with the factors of
+      // both O, and tile t writes dims 64 t .. 64 t + 63 of the rows
+      float2 f;
+      if (t == 1) {
+        s.join[row] = make_float2(m, l);
+        mbar_arrive(smem_u32(&s.join_sums));
+        if (!warp_wait(s, p, s.join_factors, joins & 1)) return;
+        f = s.join[row];
+      } else {
+        if (!warp_wait(s, p, s.join_sums, joins & 1)) return;
+        const float2 other = s.join[row];
+        const float top = fmaxf(m, other.x);
+        f.x = l > 0.f ? ex2_approx(m - top) : 0.f;
+        f.y = other.y > 0.f ? ex2_approx(other.x - top) : 0.f;
+        const float sum = f.x * l + f.y * other.y, inv = sum > 0.f ? 1.f / sum : 0.f;
+        f.x *= inv;
+        f.y *= inv;
+        s.join[row] = f;
+        mbar_arrive(smem_u32(&s.join_factors));
+        if (real && lse) *lse = sum > 0.f ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+      }
+      if ((w.n[0] > 0 && !warp_wait(s, p, s.o_full[0], outs0 & 1)) ||
+          (w.n[1] > 0 && !warp_wait(s, p, s.o_full[1], outs1 & 1)))
+        return;
+      tc_fence_after();
+      store_row(lanes + kColO, f.x, lanes + kColO + 128, f.y, w.n[1] > 0, w.n[0] > 0, 64 * t, 64 * t + 64, real, out,
+                wide, partial);
+      tc_fence_before();
+      // neither O nor the meeting place is reused before both have read it
+      mbar_arrive(smem_u32(&s.join_end));
+      if (!warp_wait(s, p, s.join_end, joins & 1)) return;
+      ++joins;
+    }
+    outs0 += w.n[0] > 0;
+    outs1 += w.n[1] > 0;
     __syncwarp();
     if (lane == 0) items.done(s); else ++items.i;
-    if (w.rows == 0) return;
-    const int n = t ? w.n[1] : w.n[0], all = max(w.n[0], w.n[1]);
-    const int sees = min(w.nk, p.causal ? w.see + t * kTile + row : w.nk);  // keys this row sees
-    float m = -INFINITY, l = 0.f;
-    for (int j = 0; j < n; ++j, ++g) {
-      if (!warp_wait(s, p, s.s_full[t], g & 1)) return;
-      tc_fence_after();
-      const int lim = sees - j * kTile;
-      float x[kTile];
-      const float alpha =
-          softmax_tile(s_addr, o_addr, p.scale_log2, __any_sync(0xffffffffu, lim < kTile), lim, j == 0, m, x);
-      // A last key tile's P V reads value rows up to a multiple of 16: those
-      // behind the request's last key hold anything (0 * NaN = NaN), so they
-      // are zeroed first, by both query tiles alike.
-      const int valid = w.nk - j * kTile;
-      if (valid < kTile && (valid & 15)) {
-        const uint32_t vi = vg + j;
-        if (!warp_wait(s, p, s.v_full[vi % kVSlots], (vi / kVSlots) & 1)) return;
-        const int pad = 16 - (valid & 15);
-        for (int k = (warp & 3) * 32 + lane; k < pad * 16; k += 128) {
-          const int r = valid + (k >> 4), c = (k >> 3) & 1;
-          *reinterpret_cast<uint4 *>(&s.v[vi % kVSlots][c][r * 128 + (k & 7) * 16]) = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_shared();
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(smem_u32(&s.p_full[t]));
-      l = l * alpha + sum_tile(x);
-    }
-    vg += all;
-    const int64_t out_row = (int64_t)w.q0 + t * kTile + row;
-    const bool real = t * kTile + row < w.rows;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    if (n > 0) {
-      if (!warp_wait(s, p, s.o_full[t], outs & 1)) return;
-      ++outs;
-      tc_fence_after();
-    }
-    uint4 *dst = reinterpret_cast<uint4 *>(p.out + (out_row * p.heads + w.h) * kV);
-#pragma unroll 1
-    for (int c = 0; c < kV; c += 32) {
-      uint32_t o[32];
-      if (n > 0) {
-        tmem_ld32(o_addr + c, o);
-        tmem_wait_ld();
-      }
-      if (real) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float x[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = l > 0.f ? __uint_as_float(o[8 * k + e]) * inv : 0.f;
-          dst[c / 8 + k] = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
-        }
-      }
-    }
-    tc_fence_before();
-    if (real && p.lse)
-      p.lse[out_row * p.heads + w.h] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
   }
 }
 
@@ -370,78 +555,126 @@ __device__ __forceinline__ void softmax_role(Smem &s, const Params &p, int warp,
 // P V of a query tile's latest key tile, issued once its softmax is done.
 struct Pending {
   bool on, first, last, free_v;
-  int v, ksteps;
+  uint32_t v;  // key tile, among all loaded
+  int ksteps;
 };
 
-__device__ __forceinline__ void mma_role(Smem &s, const Params &p, uint32_t tmem) {
-  const uint32_t id_s = idesc_bf16_f32(kTile, kTile, 0), id_o = idesc_bf16_f32(kTile, kV, 1);
-  const uint64_t d_q = smem_desc(smem_u32(s.q[0][0]), 16, 1024, kSwizzle128B);
-  const uint64_t d_k = smem_desc(smem_u32(s.k[0]), 16, 1024, kSwizzle128B);
-  const uint64_t d_v = smem_desc(smem_u32(s.v[0][0]), kChunk, 1024, kSwizzle128B);
-  Items items;
-  Pending pend[2] = {};
-  uint32_t g[2] = {0, 0}, q_used[2] = {0, 0};  // key tiles and items of each query tile
-  uint32_t kv = 0;                             // key tiles so far
-  bool ok = true;
+// Kept small and free of run-time choices in the loops: the time between a
+// softmax's end and the first MMA behind it is on every tile's path.
+struct MmaRole {
+  Smem &s;
+  const Params &p;
+  uint32_t tmem;
+  uint64_t d_q, d_k, d_v;  // descriptors of q[0][0], k[0], v[0]
+  Pending pend[2];
+  uint32_t g[2], q_used[2];  // key tiles and items of each query tile
+  uint32_t kv;               // key tiles of the items before
 
-  auto run_pv = [&](int t) -> bool {
+  template <int t>
+  __device__ __forceinline__ bool run_pv() {
     Pending &a = pend[t];
-    const int slot = a.v % kVSlots;
+    const uint32_t slot = a.v % kVSlots;
     if (!wait_or_abort(s, p, s.v_full[slot], (a.v / kVSlots) & 1) ||
         !wait_or_abort(s, p, s.p_full[t], (g[t] - 1) & 1))
       return false;
     tc_fence_after();
-    const uint64_t dv = d_v + (uint64_t)((slot * kVChunks * kChunk) >> 4);
+    constexpr uint32_t id = idesc_bf16_f32(kTile, kV, 1);
+    const uint64_t dv = d_v + (uint64_t)(slot * (kVChunks * kChunk >> 4));
     const uint32_t d = tmem + kColO + 128 * t, pa = tmem + kColS + 128 * t;
-    for (int k = 0; k < a.ksteps; ++k)
-      mma_ts(d, pa + 8 * k, dv + (uint64_t)((k * 2048) >> 4), id_o, (a.first && k == 0) ? 0u : 1u);
+    if (a.ksteps == kTile / 16) {
+      mma_ts(d, pa, dv, id, a.first ? 0u : 1u);
+#pragma unroll
+      for (int k = 1; k < kTile / 16; ++k) mma_ts_acc(d, pa + 8 * k, dv + (uint64_t)(128 * k), id);
+    } else {
+      for (int k = 0; k < a.ksteps; ++k)
+        mma_ts(d, pa + 8 * k, dv + (uint64_t)(128 * k), id, (a.first && k == 0) ? 0u : 1u);
+    }
     if (a.free_v) mma_commit(smem_u32(&s.v_empty[slot]));
     if (a.last) mma_commit(smem_u32(&s.o_full[t]));
     a.on = false;
     return true;
-  };
+  }
 
-  while (ok && items.ready(s, p)) {
-    const Work w = items.get(s);
-    items.done(s);
-    const int all = max(w.n[0], w.n[1]);
-    if (all == 0) {  // no key to see, or no more items: what is pending has no S to wait behind
+  // S of query tile t (its Q in tile tq's place) and a key tile.
+  template <int t, int tq, bool kFreeK>
+  __device__ __forceinline__ bool run_s(uint32_t tile) {
+    constexpr uint32_t id = idesc_bf16_f32(kTile, kTile, 0);
+    const uint32_t d = tmem + kColS + 128 * t;
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-        if (ok && pend[t].on) ok = run_pv(t);
-      if (w.rows == 0) break;
+    for (int c = 0; c < kQChunks; ++c) {
+      const uint32_t chunk = tile * kQChunks + c, slot = chunk % kKSlots;
+      if (!wait_or_abort(s, p, s.k_full[slot], (chunk / kKSlots) & 1)) return false;
+      tc_fence_after();
+      const uint64_t a = d_q + (uint64_t)((tq * kQChunks + c) * (kChunk >> 4));
+      const uint64_t b = d_k + (uint64_t)(slot * (kChunk >> 4));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (c == 0 && k == 0) mma_ss(d, a, b, id, 0u);
+        else mma_ss_acc(d, a + 2 * k, b + 2 * k, id);
+      }
+      if (kFreeK) mma_commit(smem_u32(&s.k_empty[slot]));
     }
-    for (int j = 0; j < all && ok; ++j, ++kv) {
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if (!ok || (pend[t].on && !(ok = run_pv(t)))) break;
-        if (j >= w.n[t]) continue;
-        if (j == 0 && !(ok = wait_or_abort(s, p, s.q_full[t], q_used[t]++ & 1))) break;
-        const bool last_user = t == 1 || j >= w.n[1];
-        const uint32_t d = tmem + kColS + 128 * t;
-        for (int c = 0; c < kQChunks; ++c) {
-          const uint32_t chunk = kv * kQChunks + c, slot = chunk % kKSlots;
-          if (!(ok = wait_or_abort(s, p, s.k_full[slot], (chunk / kKSlots) & 1))) break;
-          tc_fence_after();
-          const uint64_t a = d_q + (uint64_t)(((t * kQChunks + c) * kChunk) >> 4);
-          const uint64_t b = d_k + (uint64_t)((slot * kChunk) >> 4);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_ss(d, a + 2 * k, b + 2 * k, id_s, (c > 0 || k > 0) ? 1u : 0u);
-          if (last_user) mma_commit(smem_u32(&s.k_empty[slot]));
-        }
-        if (!ok) break;
-        mma_commit(smem_u32(&s.s_full[t]));
-        if (j == w.n[t] - 1) mma_commit(smem_u32(&s.q_empty[t]));
-        ++g[t];
-        const int keys = min(kTile, w.nk - j * kTile);
-        pend[t] = Pending{true, j == 0, j == w.n[t] - 1, last_user, (int)kv, (keys + 15) >> 4};
+    mma_commit(smem_u32(&s.s_full[t]));
+    ++g[t];
+    return true;
+  }
+
+  template <int t, bool kShared>
+  __device__ __forceinline__ bool step(int j, int n, int total, int tail_keys) {
+    if (pend[t].on && !run_pv<t>()) return false;
+    if (j >= n) return true;
+    if (j == 0 && (t == 0 || !kShared) && !wait_or_abort(s, p, s.q_full[t], q_used[t]++ & 1)) return false;
+    const int jt = kShared ? 2 * j + t : j;  // key tile of the item
+    if (!run_s<t, kShared ? 0 : t, kShared || t == 1>(kv + jt)) return false;
+    if (kShared ? jt == total - 1 : j == n - 1) mma_commit(smem_u32(&s.q_empty[kShared ? 0 : t]));
+    const int keys = tail_keys - jt * kTile;  // from this tile on
+    pend[t] = Pending{true, j == 0, j == n - 1, kShared || t == 1, kv + jt, keys >= kTile ? kTile / 16 : (keys + 15) >> 4};
+    return true;
+  }
+
+  template <bool kShared>
+  __device__ __forceinline__ bool item(int n0, int n1, int tail_keys) {
+    const int rounds = max(n0, n1), total = kShared ? n0 + n1 : n1;
+#pragma unroll 1
+    for (int j = 0; j < rounds; ++j)
+      if (!step<0, kShared>(j, n0, total, tail_keys) || !step<1, kShared>(j, n1, total, tail_keys)) return false;
+    kv += total;
+    return true;
+  }
+
+  __device__ __forceinline__ void run() {
+    Items items;
+    bool ok = true;
+    while (ok && items.ready(s, p)) {
+      const Work &w = s.work[items.i & 1];
+      const int rows = w.rows, n0 = w.n[0], n1 = w.n[1], tail_keys = w.nk - w.kt * kTile;
+      const bool shared = w.shared;
+      items.done(s);
+      if (max(n0, n1) == 0) {  // no key to see, or no more items: what is pending has no S to wait behind
+        ok = (!pend[0].on || run_pv<0>()) && (!pend[1].on || run_pv<1>());
+        if (rows == 0) break;
+      } else {
+        ok = shared ? item<true>(n0, n1, tail_keys) : item<false>(n0, n1, tail_keys);
       }
     }
+    // every MMA issued is finished before the tensor memory is given back
+    mma_commit(smem_u32(&s.fin));
+    if (!mbar_wait(smem_u32(&s.fin), 0, nullptr, kWaitNs)) report(p.dev_status, MLA_ERR_DEVICE_TIMEOUT);
   }
-  // every MMA issued is finished before the tensor memory is given back
-  mma_commit(smem_u32(&s.fin));
-  if (!mbar_wait(smem_u32(&s.fin), 0, nullptr, kWaitNs)) report(p.dev_status, MLA_ERR_DEVICE_TIMEOUT);
+};
+
+__device__ __forceinline__ void mma_role(Smem &s, const Params &p, uint32_t tmem) {
+  MmaRole r{s,
+            p,
+            tmem,
+            smem_desc(smem_u32(s.q[0][0]), 16, 1024, kSwizzle128B),
+            smem_desc(smem_u32(s.k[0]), 16, 1024, kSwizzle128B),
+            smem_desc(smem_u32(s.v[0][0]), kChunk, 1024, kSwizzle128B),
+            {},
+            {0, 0},
+            {0, 0},
+            0};
+  r.run();
 }
 
 // ---------------------------------------------------------------- TMA producer
@@ -452,7 +685,7 @@ __device__ __forceinline__ void load_role(Smem &s, const Params &p, const Maps &
   const uint64_t hint = policy_evict_normal();
   bool ok = true;
   auto load_q = [&](const Work &w, int t) -> bool {
-    if (w.n[t] == 0) return true;
+    if ((t ? w.n[1] : w.n[0]) == 0 || (t == 1 && w.shared)) return true;
     if (!wait_or_abort(s, p, s.q_empty[t], (nq[t] & 1) ^ 1)) return false;
     const uint32_t bar = smem_u32(&s.q_full[t]);
     mbar_arrive_expect_tx(bar, kQChunks * kChunk);
@@ -464,7 +697,7 @@ __device__ __forceinline__ void load_role(Smem &s, const Params &p, const Maps &
     return true;
   };
   auto load_k = [&](const Work &w, int j) -> bool {
-    const int32_t y = w.k0 + j * kTile;
+    const int32_t y = w.k0 + (w.kt + j) * kTile;
     for (int c = 0; c < kQChunks; ++c, ++nk) {
       const uint32_t slot = nk % kKSlots;
       if (!wait_or_abort(s, p, s.k_empty[slot], ((nk / kKSlots) & 1) ^ 1)) return false;
@@ -481,7 +714,7 @@ __device__ __forceinline__ void load_role(Smem &s, const Params &p, const Maps &
     const uint32_t bar = smem_u32(&s.v_full[slot]);
     mbar_arrive_expect_tx(bar, kVChunks * kChunk);
     for (int c = 0; c < kVChunks; ++c)
-      tma_load_3d_hint(smem_u32(s.v[slot][c]), &maps.v, 64 * c, w.h, w.k0 + j * kTile, bar, hint);
+      tma_load_3d_hint(smem_u32(s.v[slot][c]), &maps.v, 64 * c, w.h, w.k0 + (w.kt + j) * kTile, bar, hint);
     ++nv;
     return true;
   };
@@ -494,7 +727,7 @@ __device__ __forceinline__ void load_role(Smem &s, const Params &p, const Maps &
     const Work w = items.get(s);
     items.done(s);
     if (w.rows == 0) break;
-    const int all = max(w.n[0], w.n[1]);
+    const int all = w.shared ? w.n[0] + w.n[1] : w.n[1];
     ok = load_q(w, 0);
     for (int j = 0; j < all && ok; ++j) {
       ok = load_k(w, j) && (j > 0 || load_q(w, 1)) && load_v(w, j);
@@ -518,7 +751,7 @@ __device__ __forceinline__ void load_role(Smem &s, const Params &p, const Maps &
 // counter in memory.
 struct Claims {
   uint32_t phase = 0;
-  // By one warp: the next item's index, -1 when none is left, -2 on giving up.
+  // By one warp: the next item's index, -1 when none is left (or on giving up).
   __device__ __forceinline__ int64_t next(Smem &s, const Params &p, int lane) {
     if (lane == 0) {
       fence_proxy_async_shared();  // the last answer has been read
@@ -529,7 +762,7 @@ struct Claims {
           "r"(smem_u32(&s.claim_full))
           : "memory");
     }
-    if (!warp_wait(s, p, s.claim_full, phase)) return -2;
+    if (!warp_wait(s, p, s.claim_full, phase)) return -1;
     phase ^= 1;
     uint64_t a0, a1;
     asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(a0), "=l"(a1) : "r"(smem_u32(&s.claim)) : "memory");
@@ -544,31 +777,30 @@ struct Claims {
   }
 };
 
-// Order of the items: groups of `group_heads` heads whose keys and values fit
-// L2 together; in a group the tiles of a request from its last (the longest
-// when causal) to its first, each for all the group's heads.
 __device__ __forceinline__ void schedule_role(Smem &s, const Params &p, int lane) {
-  const int64_t tiles = count_tiles(p, lane);
-  const int64_t items = tiles * p.heads;
-  Claims claims;
   uint32_t i = 0;
-  for (int64_t at = blockIdx.x; at != -2; at = claims.next(s, p, lane)) {
-    if (at >= items) continue;  // a block more than there are items
-    Work w = {};
-    if (at >= 0) {
-      const int64_t first = at / (tiles * p.group_heads) * p.group_heads;  // the group's first head
-      const int32_t heads = (int32_t)min((int64_t)p.group_heads, p.heads - first);
-      const int64_t in_group = at - first * tiles;
-      w = find_work(p, in_group / heads, (int32_t)(first + in_group % heads), lane);
-    }
-    if (!warp_wait(s, p, s.work_empty[i & 1], ((i >> 1) & 1) ^ 1)) return;
+  auto publish = [&](const Work &w) -> bool {
+    if (!warp_wait(s, p, s.work_empty[i & 1], ((i >> 1) & 1) ^ 1)) return false;
     if (lane == 0) {
       s.work[i & 1] = w;
       mbar_arrive(smem_u32(&s.work_full[i & 1]));
     }
     ++i;
-    if (at < 0) return;
+    return true;
+  };
+  if (p.partial) {  // one part a block
+    const Work w = find_part(p, blockIdx.x, gridDim.x, lane);
+    if (w.rows == 0 || publish(w)) (void)publish(Work{});
+    return;
   }
+  Request few = {};
+  if (p.batch <= 32) few = sorted(request(p, lane), lane);
+  Claims claims;
+  for (int64_t at = blockIdx.x; at >= 0; at = claims.next(s, p, lane)) {
+    const Work w = find_work(p, few, at, lane);
+    if (w.rows > 0 && !publish(w)) return;  // a block more than there are items brings none
+  }
+  (void)publish(Work{});
 }
 
 __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ Maps maps, const Params p) {
@@ -593,6 +825,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       mbar_init(smem_u32(&s.v_full[i]), 1);
       mbar_init(smem_u32(&s.v_empty[i]), 1);
     }
+    mbar_init(smem_u32(&s.join_sums), kTile);
+    mbar_init(smem_u32(&s.join_factors), kTile);
+    mbar_init(smem_u32(&s.join_end), 2 * kTile);
     mbar_init(smem_u32(&s.claim_full), 1);
     mbar_init(smem_u32(&s.fin), 1);
     mbar_init(smem_u32(&s.roles_done), kThreads / 32);
@@ -637,6 +872,39 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Split form: joins the parts of an item.  Block `at` takes every parts-th row
+// of the item that part `at` belongs to, a warp per row:
+//   out = sum_i 2^(lse_i - top) O_i / sum_i 2^(lse_i - top)
+constexpr int kJoinThreads = 256;
+
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p) {
+  griddep_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Work w = find_part(p, blockIdx.x, gridDim.x, lane);
+  if (w.rows == 0 || w.parts == 1) return;
+  const int64_t first = w.slot - (int64_t)w.part * w.slot_step;
+  for (int r = w.part + warp * w.parts; r < w.rows; r += kJoinThreads / 32 * w.parts) {
+    float top = -INFINITY;
+    for (int i = 0; i < w.parts; ++i) top = fmaxf(top, p.partial_lse[(first + i * w.slot_step) * 2 * kTile + r]);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+    for (int i = 0; i < w.parts && top > -INFINITY; ++i) {
+      const int64_t at = (first + i * w.slot_step) * 2 * kTile + r;
+      const float a = expf(p.partial_lse[at] - top);
+      const float4 x = reinterpret_cast<const float4 *>(p.partial + at * kV)[lane];
+      sum += a;
+      o.x += a * x.x;
+      o.y += a * x.y;
+      o.z += a * x.z;
+      o.w += a * x.w;
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const int64_t row = ((int64_t)w.q0 + r) * p.heads + w.h;
+    reinterpret_cast<uint2 *>(p.out + row * kV)[lane] = make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv));
+    if (p.lse && lane == 0) p.lse[row] = sum > 0.f ? top + logf(sum) : -INFINITY;
   }
 }
 
@@ -687,16 +955,22 @@ bool encode(CUtensorMap *m, const Strided &s, int64_t tokens, int32_t heads, int
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The split form runs one part a block and at most one block an SM; a part
+// leaves 256 rows of 128 fp32 and their log-sum-exps.
+constexpr size_t kPartBytes = 2 * kTile * (kV + 1) * sizeof(float);
 constexpr size_t kWorkspaceBytes = 32u << 20;
+constexpr int kMaxParts = (int)(kWorkspaceBytes / kPartBytes);
 
-// The kernel's shared-memory opt-in, once per device.
-cudaError_t prepare_device(int dev) {
-  static std::atomic<bool> done[64];
+// SMs of a device; the kernel's shared-memory opt-in is set on the way.
+cudaError_t prepare_device(int dev, int *sms) {
+  static std::atomic<int> known[64];
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)sizeof(Smem) + 1024);
-  if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
+  *sms = known[dev].load(std::memory_order_acquire);
+  if (*sms > 0) return cudaSuccess;
+  cudaError_t e = cudaFuncSetAttribute(prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)sizeof(Smem) + 1024);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) known[dev].store(*sms, std::memory_order_release);
   return e;
 }
 
@@ -726,9 +1000,9 @@ mla_status_t run(const Args &a, void *workspace, size_t workspace_bytes, void *s
     set_error_detail("workspace must be 256-byte aligned and of mla_prefill_workspace_size()");
     return aligned(workspace, 256) ? MLA_ERR_WORKSPACE_TOO_SMALL : MLA_ERR_INVALID_ARGUMENT;
   }
-  int dev = 0;
+  int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = prepare_device(dev);
+  if (e == cudaSuccess) e = prepare_device(dev, &sms);
   if (e != cudaSuccess) return cuda_failed(e);
   Maps maps;
   if (!encode(&maps.q_nope, a.q_nope, a.total_q, a.heads, kNope, a.out) ||
@@ -751,13 +1025,31 @@ mla_status_t run(const Args &a, void *workspace, size_t workspace_bytes, void *s
   p.out = (__nv_bfloat16 *)a.out;
   p.lse = a.lse;
   p.dev_status = a.dev_status;
-  // heads whose keys and values take up to 48 MB (of 129 MB of L2)
-  const int64_t head_bytes = a.total_kv * (kNope + kV) * 2 + 1;
-  p.group_heads = (int32_t)std::min<int64_t>(a.heads, std::max<int64_t>(1, (48 << 20) / head_bytes));
+  p.partial = p.partial_lse = nullptr;
   // no more items than this, whatever the offsets say
   const int64_t most = (a.total_q / (2 * kTile) + a.batch) * (int64_t)a.heads;
   if (most > INT32_MAX) return invalid("more than 2^31 tiles of 256 queries and a head");
-  prefill_kernel<<<(unsigned)most, kThreads, sizeof(Smem) + 1024, (cudaStream_t)stream>>>(maps, p);
+  const cudaStream_t st = (cudaStream_t)stream;
+  const int blocks = std::min(sms, kMaxParts);
+  if (workspace && most <= blocks / 2) {  // see find_part
+    p.partial = (float *)workspace;
+    p.partial_lse = p.partial + (int64_t)blocks * 2 * kTile * kV;
+    prefill_kernel<<<blocks, kThreads, sizeof(Smem) + 1024, st>>>(maps, p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_failed(e);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, join_kernel, p);
+    return e == cudaSuccess ? MLA_OK : cuda_failed(e);
+  }
+  prefill_kernel<<<(unsigned)most, kThreads, sizeof(Smem) + 1024, st>>>(maps, p);
   e = cudaGetLastError();
   return e == cudaSuccess ? MLA_OK : cuda_failed(e);
 }

@@ -148,7 +148,8 @@ def _ptr(t):
 def _stream(stream):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # torch.cuda.current_stream().cuda_stream without building a Stream object (3 us)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -410,16 +411,6 @@ def _decode_fp8(fn, kv_new, q, cache8, block_table, seq_lens, softmax_scale, out
     return out
 
 
-def _need_rows(t, dtype, ndim, name):
-    """t as rows of contiguous elements, its outer dims at any strides."""
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype or t.dim() != ndim or not t.is_cuda or t.stride(-1) != 1:
-        raise ValueError(f"{name}: need CUDA {dtype} with {ndim} dims, the last contiguous, got "
-                         f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
-
-
 def _strides(t, row):
     """Element strides of t's outer dims; a dim of one entry, whose stride says
     nothing, gets that of a dense tensor with rows of `row` elements."""
@@ -429,50 +420,92 @@ def _strides(t, row):
     return [d if n == 1 else st for n, st, d in zip(t.shape[:-1], t.stride(), dense)]
 
 
-def _on_current(*tensors):
-    """All given tensors live on the current device, whose stream the call uses."""
+def _refuse(t, dtype, shape, dev, name):
     import torch
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    raise ValueError(f"{name}: need {dtype} of shape {tuple(shape)} on the current device cuda:{dev}, "
+                     f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+
+
+def _dense(t, dtype, shape, dev, name):
+    """t's address, once it is a contiguous tensor of this type and shape on the current device
+    (whose stream the call uses)."""
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == dev
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, dtype, shape, dev, name)
+
+
+def _rows(t, dtype, shape, dev, name):
+    """t's address and outer strides, once it holds rows of contiguous elements of this type and
+    shape on the current device."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+            st = t.stride()
+            if st[-1] == 1:
+                if 1 in shape[:-1]:
+                    st = _strides(t, shape[-1])
+                return (t.data_ptr(), *st[:len(shape) - 1])
+    except AttributeError:
+        pass
+    _refuse(t, dtype, shape, dev, name)
+
+
+def _shape(t, ndim, name):
+    """t's shape, once it is a tensor of ndim dims."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != ndim:
+        raise ValueError(f"{name}: need {ndim} dims, got {tuple(t.shape)}")
+    return t.shape
+
+
+def _current(t, name):
+    """The current device, for a call on CUDA tensors."""
+    import torch
+    if not t.is_cuda:
+        raise ValueError(f"{name}: need a CUDA tensor, got one on {t.device}")
+    return torch.cuda.current_device()
+
+
+def _status_word(dev_status, dev):
+    import torch
+    if dev_status is None or isinstance(dev_status, int):
+        return dev_status
+    if dev_status.dtype is not torch.int32 or dev_status.numel() < 1 or dev_status.get_device() != dev:
+        raise ValueError(f"dev_status: need int32 on the current device cuda:{dev}")
+    return dev_status.data_ptr()
 
 
 def _rope_append(fn, cache_dtype, scale, kv, positions, cos_sin, slot_mapping, cache, norm_weight,
                  eps, interleaved, q_pe, q_pe_out, dev_status, stream):
     import torch
-    _need_rows(kv, torch.bfloat16, 2, "kv")
-    _need(positions, torch.int64, 1, "positions")
-    _need(cos_sin, torch.float32, 2, "cos_sin")
-    _need(slot_mapping, torch.int64, 1, "slot_mapping")
-    _need(cache, cache_dtype, 3, "cache")
-    T = kv.shape[0]
-    if kv.shape[1] != ROW_DIM or cache.shape[2] != ROW_DIM:
-        raise ValueError("rows must be 576 wide")
-    if cos_sin.shape[1] != ROPE_DIM:
-        raise ValueError("cos_sin must be [positions, 64]")
-    if positions.shape[0] != T or slot_mapping.shape[0] != T:
-        raise ValueError("kv, positions and slot_mapping disagree on the token count")
-    if norm_weight is not None:
-        _need(norm_weight, torch.bfloat16, 1, "norm_weight")
-        if norm_weight.shape[0] != KV_LORA_RANK:
-            raise ValueError("norm_weight must be [512]")
-    if (q_pe is None) != (q_pe_out is None):
-        raise ValueError("q_pe and q_pe_out go together")
-    heads, qs, os = 0, (0, 0), (0, 0)
-    if q_pe is not None:
-        _need_rows(q_pe, torch.bfloat16, 3, "q_pe")
-        _need_rows(q_pe_out, torch.bfloat16, 3, "q_pe_out")
-        heads = q_pe.shape[1]
-        if tuple(q_pe.shape) != (T, heads, ROPE_DIM) or q_pe_out.shape != q_pe.shape:
-            raise ValueError("q_pe and q_pe_out must be [T, H, 64]")
-        qs, os = _strides(q_pe, ROPE_DIM), _strides(q_pe_out, ROPE_DIM)
-    _on_current(kv, positions, cos_sin, slot_mapping, cache, norm_weight, q_pe, q_pe_out,
-                dev_status)
-    _check(fn(_ptr(kv), _strides(kv, ROW_DIM)[0], _ptr(positions), _ptr(cos_sin), cos_sin.shape[0],
-              _ptr(slot_mapping), T, _ptr(norm_weight), float(eps), int(bool(interleaved)),
-              _ptr(cache), cache.shape[0], cache.shape[1], *scale, _ptr(q_pe), qs[0], qs[1],
-              _ptr(q_pe_out), os[0], os[1], heads, _ptr(dev_status), _stream(stream)))
+    bf16 = torch.bfloat16
+    T = _shape(kv, 2, "kv")[0]
+    dev = _current(kv, "kv")
+    P = _shape(cos_sin, 2, "cos_sin")[0]
+    NB, BS, _ = _shape(cache, 3, "cache")
+    kv_args = _rows(kv, bf16, (T, ROW_DIM), dev, "kv")
+    q_args, out_args, heads = (None, 0, 0), (None, 0, 0), 0
+    if q_pe is not None or q_pe_out is not None:
+        if q_pe is None or q_pe_out is None:
+            raise ValueError("q_pe and q_pe_out go together")
+        heads = _shape(q_pe, 3, "q_pe")[1]
+        q_args = _rows(q_pe, bf16, (T, heads, ROPE_DIM), dev, "q_pe")
+        out_args = _rows(q_pe_out, bf16, (T, heads, ROPE_DIM), dev, "q_pe_out")
+    _check(fn(*kv_args, _dense(positions, torch.int64, (T,), dev, "positions"),
+              _dense(cos_sin, torch.float32, (P, ROPE_DIM), dev, "cos_sin"), P,
+              _dense(slot_mapping, torch.int64, (T,), dev, "slot_mapping"), T,
+              None if norm_weight is None
+              else _dense(norm_weight, bf16, (KV_LORA_RANK,), dev, "norm_weight"),
+              eps, 1 if interleaved else 0, _dense(cache, cache_dtype, (NB, BS, ROW_DIM), dev, "cache"),
+              NB, BS, *scale, *q_args, *out_args, heads, _status_word(dev_status, dev),
+              _stream(stream)))
 
 
 def mla_rope_append(kv, positions, cos_sin, slot_mapping, cache, norm_weight=None, eps=1e-6,
@@ -501,27 +534,19 @@ def mla_rope_append_fp8(kv, positions, cos_sin, slot_mapping, cache8, kv_scale=1
 def _expand_kv(fn, cache_dtype, scale, cache, block_table, kv_offsets, w_uk, w_uv, k_nope, v,
                k_pe, dev_status, stream):
     import torch
-    _need(cache, cache_dtype, 3, "cache")
-    _need(block_table, torch.int32, 2, "block_table")
-    _need(kv_offsets, torch.int32, 1, "kv_offsets")
-    _need(w_uk, torch.bfloat16, 3, "w_uk")
-    _need(w_uv, torch.bfloat16, 3, "w_uv")
-    _need(k_nope, torch.bfloat16, 3, "k_nope")
-    _need(v, torch.bfloat16, 3, "v")
-    _need(k_pe, torch.bfloat16, 2, "k_pe")
-    T, H = k_nope.shape[0], k_nope.shape[1]
-    B = block_table.shape[0]
-    if cache.shape[2] != ROW_DIM or kv_offsets.shape[0] != B + 1:
-        raise ValueError("shapes: cache [NB,BS,576], block_table [B,M], kv_offsets [B+1]")
-    if (tuple(w_uk.shape) != (H, 128, 512) or tuple(w_uv.shape) != (H, 512, 128)
-            or tuple(k_nope.shape) != (T, H, 128) or tuple(v.shape) != (T, H, 128)
-            or tuple(k_pe.shape) != (T, ROPE_DIM)):
-        raise ValueError("shapes: w_uk [H,128,512], w_uv [H,512,128], k_nope and v [T,H,128], "
-                         "k_pe [T,64]")
-    _on_current(cache, block_table, kv_offsets, w_uk, w_uv, k_nope, v, k_pe, dev_status)
-    _check(fn(_ptr(cache), cache.shape[0], cache.shape[1], _ptr(block_table),
-              block_table.shape[1], _ptr(kv_offsets), B, T, _ptr(w_uk), _ptr(w_uv), H, *scale,
-              _ptr(k_nope), _ptr(v), _ptr(k_pe), _ptr(dev_status), _stream(stream)))
+    bf16, i32 = torch.bfloat16, torch.int32
+    NB, BS, _ = _shape(cache, 3, "cache")
+    dev = _current(cache, "cache")
+    B, M = _shape(block_table, 2, "block_table")
+    T, H, _ = _shape(k_nope, 3, "k_nope")
+    _check(fn(_dense(cache, cache_dtype, (NB, BS, ROW_DIM), dev, "cache"), NB, BS,
+              _dense(block_table, i32, (B, M), dev, "block_table"), M,
+              _dense(kv_offsets, i32, (B + 1,), dev, "kv_offsets"), B, T,
+              _dense(w_uk, bf16, (H, 128, KV_LORA_RANK), dev, "w_uk"),
+              _dense(w_uv, bf16, (H, KV_LORA_RANK, 128), dev, "w_uv"), H, *scale,
+              _dense(k_nope, bf16, (T, H, 128), dev, "k_nope"), _dense(v, bf16, (T, H, 128), dev, "v"),
+              _dense(k_pe, bf16, (T, ROPE_DIM), dev, "k_pe"), _status_word(dev_status, dev),
+              _stream(stream)))
     return k_nope, v, k_pe
 
 
@@ -558,38 +583,27 @@ def mla_prefill(q_nope, q_pe, k_nope, k_pe, v, q_offsets, kv_offsets, softmax_sc
     queries of a request are the last tokens of its context.  With a workspace
     (make_prefill_workspace) few queries on long contexts use the whole GPU."""
     import torch
-    for t, ndim, name in ((q_nope, 3, "q_nope"), (q_pe, 3, "q_pe"), (k_nope, 3, "k_nope"),
-                          (k_pe, 2, "k_pe"), (v, 3, "v")):
-        _need_rows(t, torch.bfloat16, ndim, name)
-    _need(q_offsets, torch.int32, 1, "q_offsets")
-    _need(kv_offsets, torch.int32, 1, "kv_offsets")
-    _need(out, torch.bfloat16, 3, "out")
-    Tq, H = q_nope.shape[0], q_nope.shape[1]
-    Tk = k_nope.shape[0]
-    B = q_offsets.shape[0] - 1
-    if (tuple(q_nope.shape) != (Tq, H, 128) or tuple(q_pe.shape) != (Tq, H, ROPE_DIM)
-            or tuple(k_nope.shape) != (Tk, H, 128) or tuple(k_pe.shape) != (Tk, ROPE_DIM)
-            or tuple(v.shape) != (Tk, H, 128) or tuple(out.shape) != (Tq, H, 128)):
-        raise ValueError("shapes: q_nope [Tq,H,128], q_pe [Tq,H,64], k_nope [Tk,H,128], "
-                         "k_pe [Tk,64], v [Tk,H,128], out [Tq,H,128]")
-    if B < 0 or kv_offsets.shape[0] != B + 1:
-        raise ValueError("q_offsets and kv_offsets must both be [B+1]")
-    if lse is not None:
-        _need(lse, torch.float32, 2, "lse")
-        if tuple(lse.shape) != (Tq, H):
-            raise ValueError(f"lse must be [Tq, H] = [{Tq}, {H}], got {tuple(lse.shape)}")
-    nbytes = 0
+    bf16, i32 = torch.bfloat16, torch.int32
+    Tq, H, _ = _shape(q_nope, 3, "q_nope")
+    dev = _current(q_nope, "q_nope")
+    Tk = _shape(k_nope, 3, "k_nope")[0]
+    B = _shape(q_offsets, 1, "q_offsets")[0] - 1
+    if B < 0:
+        raise ValueError("q_offsets must be [B+1]")
+    ws = nbytes = None
     if workspace is not None:
-        _need(workspace, torch.uint8, 1, "workspace")
-        nbytes = workspace.numel()
-    _on_current(q_nope, q_pe, k_nope, k_pe, v, q_offsets, kv_offsets, out, lse, workspace,
-                dev_status)
+        nbytes = _shape(workspace, 1, "workspace")[0]
+        ws = _dense(workspace, torch.uint8, (nbytes,), dev, "workspace")
     _check(get_lib().mla_prefill(
-        _ptr(q_nope), *_strides(q_nope, 128), _ptr(q_pe), *_strides(q_pe, ROPE_DIM), _ptr(k_nope),
-        *_strides(k_nope, 128), _ptr(k_pe), *_strides(k_pe, ROPE_DIM), _ptr(v),
-        *_strides(v, 128), _ptr(q_offsets), _ptr(kv_offsets), B, Tq, Tk, H, int(bool(causal)),
-        float(softmax_scale), _ptr(out), _ptr(lse), _ptr(workspace), nbytes, _ptr(dev_status),
-        _stream(stream)))
+        *_rows(q_nope, bf16, (Tq, H, 128), dev, "q_nope"),
+        *_rows(q_pe, bf16, (Tq, H, ROPE_DIM), dev, "q_pe"),
+        *_rows(k_nope, bf16, (Tk, H, 128), dev, "k_nope"),
+        *_rows(k_pe, bf16, (Tk, ROPE_DIM), dev, "k_pe"), *_rows(v, bf16, (Tk, H, 128), dev, "v"),
+        _dense(q_offsets, i32, (B + 1,), dev, "q_offsets"),
+        _dense(kv_offsets, i32, (B + 1,), dev, "kv_offsets"), B, Tq, Tk, H, 1 if causal else 0,
+        softmax_scale, _dense(out, bf16, (Tq, H, 128), dev, "out"),
+        None if lse is None else _dense(lse, torch.float32, (Tq, H), dev, "lse"), ws, nbytes or 0,
+        _status_word(dev_status, dev), _stream(stream)))
     return out
 
 

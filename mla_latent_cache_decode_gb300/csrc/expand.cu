@@ -19,13 +19,15 @@
 // memory leaves shared memory's bandwidth to the weights.  A cluster of
 // CTAs holds neighbouring rows and walks the same heads: each loads a part of
 // every stage and multicasts it, so L2 delivers a weight once per cluster.
-// Accumulators are double-buffered (2 x 128 columns); four warps round them to
-// bf16, stage them in shared memory and store them by TMA.
+// Accumulators are double-buffered (2 x 128 columns); two groups of four warps
+// take turns to round them to bf16, stage them in shared memory and store them
+// by TMA (one group cannot keep up with the MMAs: 2,048 cycles a result).
 //
 // An item is one head's keys or values of a group of kCluster x 128 rows; the
 // items (group by group, head by head) are cut into equal runs, one a cluster.
 #include <atomic>
 #include <cmath>
+#include <type_traits>
 
 #include "common.cuh"
 #include "fp8.cuh"
@@ -45,7 +47,8 @@ constexpr int kDims = 128;              // key dims, value dims of a head
 constexpr int kKChunks = kVDim / 64;    // 64-dim chunks of the latent
 constexpr int kStage = kDims * 128;     // 128 output dims x 64 of K: 16 KB
 constexpr int kStages = 10;
-constexpr int kThreads = 192;           // warps 0-3 rows in, results out; 4 weights; 5 MMA
+constexpr int kOutWarps = 8;            // rows in, results out: two groups of four warps
+constexpr int kThreads = 32 * (kOutWarps + 2);  // and one warp for the weights, one for the MMAs
 constexpr uint32_t kTmemCols = 512, kColA = 0, kColD = 256;
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr uint64_t kDrainNs = 10000000ull;
@@ -70,7 +73,7 @@ struct Params {
 
 struct __align__(1024) Smem {
   uint8_t w[kStages][kStage];
-  uint8_t out[2][2][kRows * 128];  // two results: 64-dim halves of 128 rows, 128-byte swizzle
+  uint8_t out[2][2][kRows * 128];  // a result for each group: 64-dim halves of 128 rows, 128-byte swizzle
   uint64_t w_full[kStages], w_empty[kStages], d_full[2], d_empty[2], a_full, fin;
   uint32_t tmem_base;
   int abort;
@@ -107,68 +110,102 @@ __device__ __forceinline__ bool warp_wait(Smem &s, const Params &p, uint64_t &ba
   return false;
 }
 
-// Cache row of output row t, -1 for a row of no request (left as it is), -2
-// for one whose page lies outside the table or the pool.
-__device__ __forceinline__ int64_t cache_row(const Params &p, int32_t t) {
-  if (t >= p.total_kv || t < p.kv_offsets[0] || t >= p.kv_offsets[p.batch]) return -1;
-  const int32_t b = ragged::request_of(p.kv_offsets, p.batch, t);
-  const int64_t pos = (int64_t)t - p.kv_offsets[b], page = pos / p.block_size;
-  if (pos < 0 || page >= p.max_blocks_per_seq) return -2;
-  const int32_t blk = p.block_table[(int64_t)b * p.max_blocks_per_seq + page];
-  const int64_t row = (int64_t)blk * p.block_size + pos % p.block_size;
+// Cache row of each lane's output row t (by a whole warp), -1 for a row of no
+// request (left as it is), -2 for one whose page lies outside the table or the
+// pool.
+__device__ __forceinline__ int64_t cache_row(const Params &p, int32_t t, int32_t begin, int32_t end) {
+  const ragged::Place at = ragged::place_of(p.kv_offsets, p.batch, t);
+  if (t < begin || t >= end) return -1;
+  if (t < at.offset) return -2;
+  const uint32_t pos = (uint32_t)t - (uint32_t)at.offset, page = pos / (uint32_t)p.block_size;
+  if (page >= (uint32_t)p.max_blocks_per_seq) return -2;
+  const int32_t blk = p.block_table[(int64_t)at.request * p.max_blocks_per_seq + page];
+  const int64_t row = (int64_t)blk * p.block_size + pos % (uint32_t)p.block_size;
   return blk < 0 || row >= p.num_slots ? -2 : row;
 }
 
-// The thread's row into its tensor-memory lane (zeros without a row); with
-// `copy_rope` its rotary dims go out as k_pe.
+// Half of 32 rows' latent dims (256 each) by a warp: from the cache, half a
+// warp per row and load so that every access is whole lines ...
 template <bool kFp8>
-__device__ __forceinline__ void load_row(const Params &p, int64_t row, int32_t t, bool copy_rope, uint32_t lane_addr) {
-  constexpr int kWords = kFp8 ? 32 : 64;  // 16-byte words of 512 elements
-  constexpr int kBatch = kFp8 ? 8 : 16;   // words in flight: 128 elements
-  const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.cache) +
-                                                     (row < 0 ? 0 : row) * (kFp8 ? kRow : 2 * kRow));
-#pragma unroll 1
-  for (int w0 = 0; w0 < kWords; w0 += kBatch) {
-    uint4 in[kBatch];
+struct HalfRows {
+  static constexpr int kParts = kFp8 ? 1 : 2;  // of 256 bytes a row
+  uint4 v[kParts][16];
+
+  // `row`: the lane's own cache row (< 0: zeros)
+  __device__ __forceinline__ void load(const Params &p, int64_t row, int half, int lane) {
+    const uint8_t *cache = static_cast<const uint8_t *>(p.cache) + half * kParts * 256 + (lane & 15) * 16;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) in[i] = row < 0 ? make_uint4(0, 0, 0, 0) : src[w0 + i];
-    uint32_t a[64];
+    for (int i = 0; i < 16; ++i) {
+      const int64_t r = __shfl_sync(0xffffffffu, row, 2 * i + (lane >> 4));
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const uint32_t u[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (kFp8) {
-          a[8 * i + 2 * e] = e4m3x2_to_bf16x2(u[e] & 0xffffu);
-          a[8 * i + 2 * e + 1] = e4m3x2_to_bf16x2(u[e] >> 16);
-        } else {
-          a[4 * i + e] = u[e];
-        }
-      }
+      for (int k = 0; k < kParts; ++k)
+        v[k][i] = r < 0 ? make_uint4(0, 0, 0, 0)
+                        : *reinterpret_cast<const uint4 *>(cache + r * (kFp8 ? kRow : 2 * kRow) + k * 256);
     }
-    const uint32_t at = lane_addr + kColA + (w0 / kBatch) * 64;
-    tmem_st32(at, a);
-    tmem_st32(at + 32, a + 32);
   }
-  if (copy_rope && row >= 0) {
-    uint4 *dst = reinterpret_cast<uint4 *>(p.k_pe + (int64_t)t * MLA_ROPE_DIM);
+
+  // ... and through 8 KB of the warp's own shared memory (16-byte units
+  // swizzled by the row) into the tensor-memory lane of each row, E4M3 codes
+  // as bf16.
+  __device__ __forceinline__ void store(uint8_t *stage, uint32_t a_addr, int lane) const {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (kFp8) {
-        const uint2 c = reinterpret_cast<const uint2 *>(src + kWords)[i];
-        const uint32_t u[4] = {c.x & 0xffffu, c.x >> 16, c.y & 0xffffu, c.y >> 16};
-        uint32_t o[4];
+    for (int k = 0; k < kParts; ++k) {
+      __syncwarp();
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t h = e4m3x2_to_f16x2(u[e]);
-          const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-          o[e] = pack2(f.x * p.kv_scale, f.y * p.kv_scale);
+      for (int i = 0; i < 16; ++i) {
+        const int r = 2 * i + (lane >> 4);
+        *reinterpret_cast<uint4 *>(stage + r * 256 + (((lane & 15) ^ (r & 7)) << 4)) = v[k][i];
+      }
+      __syncwarp();
+#pragma unroll
+      for (int w0 = 0; w0 < 16; w0 += kFp8 ? 4 : 8) {  // 32 columns at a time
+        uint32_t a[32];
+#pragma unroll
+        for (int w = 0; w < (kFp8 ? 4 : 8); ++w) {
+          const uint4 u = *reinterpret_cast<const uint4 *>(stage + lane * 256 + (((w0 + w) ^ (lane & 7)) << 4));
+          const uint32_t e[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (kFp8) {
+              a[8 * w + 2 * c] = e4m3x2_to_bf16x2(e[c] & 0xffffu);
+              a[8 * w + 2 * c + 1] = e4m3x2_to_bf16x2(e[c] >> 16);
+            } else {
+              a[4 * w + c] = e[c];
+            }
+          }
         }
-        dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
-      } else {
-        dst[i] = src[kWords + i];
+        tmem_st32(a_addr + k * 64 + w0 * (kFp8 ? 8 : 4), a);
       }
     }
+  }
+};
+
+// The 64 rotary dims of a warp's 32 rows (first of them t) as k_pe: eight lanes
+// a row.
+template <bool kFp8>
+__device__ __forceinline__ void copy_rope(const Params &p, int64_t row, int32_t t, int lane) {
+  const uint8_t *cache = static_cast<const uint8_t *>(p.cache) + kVDim * (kFp8 ? 1 : 2) + (lane & 7) * (kFp8 ? 8 : 16);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int at = 4 * i + (lane >> 3);
+    const int64_t r = __shfl_sync(0xffffffffu, row, at);
+    if (r < 0) continue;
+    uint4 o;
+    if (kFp8) {
+      const uint2 c = *reinterpret_cast<const uint2 *>(cache + r * kRow);
+      const uint32_t u[4] = {c.x & 0xffffu, c.x >> 16, c.y & 0xffffu, c.y >> 16};
+      uint32_t e[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t h = e4m3x2_to_f16x2(u[k]);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+        e[k] = pack2(f.x * p.kv_scale, f.y * p.kv_scale);
+      }
+      o = make_uint4(e[0], e[1], e[2], e[3]);
+    } else {
+      o = *reinterpret_cast<const uint4 *>(cache + r * 2 * kRow);
+    }
+    reinterpret_cast<uint4 *>(p.k_pe + (int64_t)(t + at) * MLA_ROPE_DIM)[lane & 7] = o;
   }
 }
 
@@ -217,11 +254,20 @@ __device__ __forceinline__ void load_weights(uint32_t dst, const CUtensorMap *m,
   }
 }
 
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap *m, int32_t x, int32_t y, int32_t z, uint32_t src) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
-                   reinterpret_cast<uint64_t>(m)),
-               "r"(x), "r"(y), "r"(z), "r"(src)
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *m, int32_t x, int32_t y, int32_t z, uint32_t src,
+                                             uint64_t policy) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group.L2::cache_hint [%0, {%1, %2, %3}], [%4], %5;" ::
+                   "l"(reinterpret_cast<uint64_t>(m)),
+               "r"(x), "r"(y), "r"(z), "r"(src), "l"(policy)
                : "memory");
+}
+
+// Results leave L2 first (90 MB of them, 16 heads of 11,051 tokens: 36 us; with
+// the normal policy 44).
+__device__ __forceinline__ uint64_t policy_stream() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
 }
 
 template <bool kFp8, int kCluster>
@@ -239,11 +285,15 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
       mbar_init(smem_u32(&s.d_full[i]), 1);
       mbar_init(smem_u32(&s.d_empty[i]), kRows);
     }
-    mbar_init(smem_u32(&s.a_full), kRows);
+    mbar_init(smem_u32(&s.a_full), 2 * kRows);
     mbar_init(smem_u32(&s.fin), 1);
     s.abort = 0;
     fence_mbarrier_init_cluster();
   }
+  // Launched as a programmatic dependent: what is above may run while the
+  // kernel before this one ends, what is below reads and writes memory.
+  griddep_wait();
+  griddep_launch_dependents();
   if (blockIdx.x == 0)
     ragged::check_offsets(p.kv_offsets, p.batch, p.total_kv, threadIdx.x, kThreads, p.dev_status);
   if (warp == 0) {
@@ -263,41 +313,49 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
   const int64_t all = (int64_t)((rows_end + kCluster * kRows - 1) / (kCluster * kRows)) * per;
   const int64_t i0 = all * c / clusters, i1 = all * (c + 1) / clusters;
 
-  if (warp < 4) {
+  if (warp < kOutWarps) {
     // ------------------------------------------------ rows in, results out
-    const int r = warp * 32 + lane;
-    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+    const int side = warp >> 2;             // the group of four warps, and its result buffer
+    const int r = (warp & 3) * 32 + lane;   // row = TMEM lane
+    const bool leader = (warp & 3) == 0 && lane == 0;
+    const uint64_t hint = policy_stream();
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const int32_t rows_begin = ragged::cut(p.kv_offsets[0], p.total_kv);
-    int32_t group = -1, t0 = 0;
+    int32_t item = 0, t0 = 0;
     int64_t row = -1;
     bool whole = false;  // every row of the tile (that the tensors have) is a request's
     uint32_t n = 0;
-    bool ok = true;
-    for (int64_t i = i0; i < i1 && ok; ++i, ++n) {
-      const int32_t g = (int32_t)(i / per), item = (int32_t)(i % per);
-      if (g != group) {
-        // Every product of the previous group is complete: its results were
-        // read below.  The first item's CTAs also copy the rotary dims.
-        group = g;
-        t0 = (g * kCluster + (int32_t)rank) * kRows;
-        row = t0 < p.total_kv ? cache_row(p, t0 + r) : -1;
-        if (row == -2) report(p.dev_status, MLA_ERR_DEVICE_RANGE);
+    for (int64_t i = i0; i < i1; ++i, ++n) {
+      if (i == i0 || ++item == per) {
+        const int32_t group = (int32_t)(i / per);
+        item = (int32_t)(i % per);
+        t0 = (group * kCluster + (int32_t)rank) * kRows;
+        row = cache_row(p, t0 + r, rows_begin, rows_end);
+        if (row == -2 && side == 0) report(p.dev_status, MLA_ERR_DEVICE_RANGE);
         whole = t0 < p.total_kv && t0 >= rows_begin && min(t0 + kRows, p.total_kv) <= rows_end;
+        HalfRows<kFp8> rows;
+        rows.load(p, row, side, lane);
+        // the staging buffer is free once its last store has read it, the
+        // previous rows once the last product is complete
+        if (leader) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        named_barrier_sync(1 + side, kRows);
+        if (n > 0 && !warp_wait(s, p, s.d_full[(n - 1) & 1], ((n - 1) >> 1) & 1)) break;
         tc_fence_after();
-        load_row<kFp8>(p, row, t0 + r, item == 0, lanes);
+        rows.store(&s.out[side][0][0] + (warp & 3) * 8192, lanes + kColA + 128 * side, lane);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(smem_u32(&s.a_full));
+        if (item == 0 && side == 1) copy_rope<kFp8>(p, row, t0 + (warp & 3) * 32, lane);
       }
-      const uint32_t buf = n & 1;
-      if (!(ok = warp_wait(s, p, s.d_full[buf], (n >> 1) & 1))) break;
+      if ((n & 1) != (uint32_t)side) continue;  // the other group's
+      if (!warp_wait(s, p, s.d_full[side], (n >> 1) & 1)) break;
       tc_fence_after();
       uint32_t d[kDims];
 #pragma unroll
-      for (int k = 0; k < kDims; k += 32) tmem_ld32(lanes + kColD + 128 * buf + k, d + k);
+      for (int k = 0; k < kDims; k += 32) tmem_ld32(lanes + kColD + 128 * side + k, d + k);
       tmem_wait_ld();
       tc_fence_before();
-      mbar_arrive(smem_u32(&s.d_empty[buf]));
+      mbar_arrive(smem_u32(&s.d_empty[side]));
       const float by = kFp8 ? p.kv_scale : 1.f;
       uint4 o[kDims / 8];
 #pragma unroll
@@ -310,17 +368,17 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
       const int h = item >> 1;
       if (whole) {
         // the store that used this staging buffer two items ago has read it
-        if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-        named_barrier_sync(1, kRows);
+        if (leader) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        named_barrier_sync(1 + side, kRows);
 #pragma unroll
         for (int k = 0; k < kDims / 8; ++k)
-          *reinterpret_cast<uint4 *>(&s.out[buf][k >> 3][r * 128 + (((k & 7) ^ (r & 7)) << 4)]) = o[k];
+          *reinterpret_cast<uint4 *>(&s.out[side][k >> 3][r * 128 + (((k & 7) ^ (r & 7)) << 4)]) = o[k];
         fence_proxy_async_shared();
-        named_barrier_sync(1, kRows);
-        if (threadIdx.x == 0) {
+        named_barrier_sync(1 + side, kRows);
+        if (leader) {
           const CUtensorMap *m = item & 1 ? &maps.v : &maps.k_nope;
-          tma_store_3d(m, 0, h, t0, smem_u32(s.out[buf][0]));
-          tma_store_3d(m, 64, h, t0, smem_u32(s.out[buf][1]));
+          tma_store_3d(m, 0, h, t0, smem_u32(s.out[side][0]), hint);
+          tma_store_3d(m, 64, h, t0, smem_u32(s.out[side][1]), hint);
           asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         }
       } else if (row != -1) {
@@ -330,8 +388,8 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
         for (int k = 0; k < kDims / 8; ++k) dst[k] = o[k];
       }
     }
-    if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-  } else if (warp == 4) {
+    if (leader) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  } else if (warp == kOutWarps) {
     // ------------------------------------------------ weights
     if (elect_one_sync()) {
       prefetch_tmap(&maps.w_uk);
@@ -344,11 +402,12 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
       constexpr int kMine = kDims / kBox / kCluster;  // boxes of this CTA
       uint32_t n = 0;
       bool ok = true;
-      for (int64_t i = i0; i < i1 && ok; ++i) {
-        const int32_t item = (int32_t)(i % per), h = item >> 1;
+      uint32_t st = 0, ph = 1;
+      int32_t item = (int32_t)(i0 % per);
+      for (int64_t i = i0; i < i1 && ok; ++i, item = item + 1 == per ? 0 : item + 1) {
+        const int32_t h = item >> 1;
         for (int kc = 0; kc < kKChunks; ++kc, ++n) {
-          const uint32_t st = n % kStages;
-          if (!(ok = wait_or_abort(s, p, s.w_empty[st], ((n / kStages) & 1) ^ 1))) break;
+          if (!(ok = wait_or_abort(s, p, s.w_empty[st], ph))) break;
           const uint32_t bar = smem_u32(&s.w_full[st]);
           mbar_arrive_expect_tx(bar, kStage);
 #pragma unroll
@@ -360,6 +419,10 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
             else           // rows: output dims
               load_weights<kCluster>(dst, &maps.w_uk, kc * 64, h * kDims + at, bar, hint);
           }
+          if (++st == kStages) {
+            st = 0;
+            ph ^= 1;
+          }
         }
       }
       if (*(volatile int *)&s.abort)  // no copy may still be landing when the shared memory is given up
@@ -369,34 +432,44 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
   } else {
     // ------------------------------------------------ MMA issuer
     if (elect_one_sync()) {
-      const uint32_t id_k = idesc_bf16_f32(kRows, kDims, 0), id_v = idesc_bf16_f32(kRows, kDims, 1);
       const uint64_t d_k = smem_desc(smem_u32(s.w[0]), 16, 1024, kSwizzle128B);
       const uint64_t d_v = smem_desc(smem_u32(s.w[0]), kStage / 2, 1024, kSwizzle128B);
-      int32_t group = -1;
-      uint32_t n = 0, st_n = 0, loads = 0;
+      uint32_t n = 0, st = 0, ph = 0, loads = 0;  // results, the ring's place and phase, row tiles
+      // one item; keys and values differ in how K runs through a stage
+      auto product = [&](auto is_value) -> bool {
+        constexpr bool kValue = decltype(is_value)::value;
+        constexpr uint32_t id = idesc_bf16_f32(kRows, kDims, kValue);
+        constexpr uint64_t kStep = kValue ? 128 : 2;  // 16 of K: 16 rows, or 32 bytes
+        const uint32_t d = tmem + kColD + 128 * (n & 1);
+#pragma unroll
+        for (int kc = 0; kc < kKChunks; ++kc) {
+          if (!wait_or_abort(s, p, s.w_full[st], ph)) return false;
+          tc_fence_after();
+          const uint64_t b = (kValue ? d_v : d_k) + (uint64_t)(st * (kStage >> 4));
+          const uint32_t a = tmem + kColA + 32 * kc;
+          if (kc == 0) mma_ts(d, a, b, id, 0u);
+          else mma_ts_acc(d, a, b, id);
+#pragma unroll
+          for (int k = 1; k < 4; ++k) mma_ts_acc(d, a + 8 * k, b + kStep * k, id);
+          commit_all<kCluster>(smem_u32(&s.w_empty[st]));
+          if (++st == kStages) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+        return true;
+      };
+      int32_t left = 0;  // items of the current group
       bool ok = true;
-      for (int64_t i = i0; i < i1 && ok; ++i, ++n) {
-        const int32_t g = (int32_t)(i / per);
-        const bool value = i & 1;  // per is even
-        if (g != group) {
-          group = g;
+      for (int64_t i = i0; i < i1 && ok; ++i, ++n, --left) {
+        if (left == 0) {
+          left = per - (int32_t)(i % per);
           if (!(ok = wait_or_abort(s, p, s.a_full, loads++ & 1))) break;
         }
-        const uint32_t buf = n & 1;
-        if (!(ok = wait_or_abort(s, p, s.d_empty[buf], ((n >> 1) & 1) ^ 1))) break;
+        if (!(ok = wait_or_abort(s, p, s.d_empty[n & 1], ((n >> 1) & 1) ^ 1))) break;
         tc_fence_after();
-        for (int kc = 0; kc < kKChunks; ++kc, ++st_n) {
-          const uint32_t st = st_n % kStages;
-          if (!(ok = wait_or_abort(s, p, s.w_full[st], (st_n / kStages) & 1))) break;
-          tc_fence_after();
-          const uint64_t b = (value ? d_v : d_k) + (uint64_t)((st * kStage) >> 4);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_ts(tmem + kColD + 128 * buf, tmem + kColA + 32 * kc + 8 * k, b + (uint64_t)(value ? 128 * k : 2 * k),
-                   value ? id_v : id_k, (kc > 0 || k > 0) ? 1u : 0u);
-          commit_all<kCluster>(smem_u32(&s.w_empty[st]));
-        }
-        if (ok) mma_commit(smem_u32(&s.d_full[buf]));
+        ok = i & 1 ? product(std::true_type{}) : product(std::false_type{});  // per is even
+        if (ok) mma_commit(smem_u32(&s.d_full[n & 1]));
       }
       mma_commit(smem_u32(&s.fin));
       if (!mbar_wait(smem_u32(&s.fin), 0, nullptr, kWaitNs)) report(p.dev_status, MLA_ERR_DEVICE_TIMEOUT);
@@ -461,12 +534,14 @@ cudaError_t launch(const Params &p, cudaStream_t stream) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = sizeof(Smem) + 1024;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kCluster;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kCluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, expand_kernel<kFp8, kCluster>, maps, p);
 }
 

@@ -373,7 +373,7 @@ mla_status_t mla_decode_fp8_planned(const void *q, void *cache8, const void *kv_
  *                 place), and q_out may be the rotary dims of mla_decode's q.
  *   num_heads     1 to 128 (not looked at without a query)
  * Pointers to bf16 and fp32 data 16-byte aligned, to int64 data 8-byte.
- * num_tokens = 0 is a no-op; num_tokens < 2^31, block_size >= 1.
+ * num_tokens = 0 is a no-op; num_tokens < 2^27, block_size >= 1.
  *
  * mla_rope_append_fp8 — the same into an FP8 latent cache (uint8 [num_blocks,
  * block_size, 576], see below): each fp32 value x of the row is stored as the

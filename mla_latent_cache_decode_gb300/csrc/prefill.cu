@@ -834,13 +834,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     s.abort = 0;
     fence_mbarrier_init_cluster();
   }
-  if (blockIdx.x == 0) {
-    ragged::check_offsets(p.q_offsets, p.batch, p.total_q, threadIdx.x, kThreads, p.dev_status);
-    ragged::check_offsets(p.kv_offsets, p.batch, p.total_kv, threadIdx.x, kThreads, p.dev_status);
-  }
   if (warp == 0) {
     tmem_alloc(smem_u32(&s.tmem_base), kTmemCols);
     tmem_relinquish();
+  }
+  // Launched as a programmatic dependent: what is above may run while the
+  // kernel before this one ends, what is below reads and writes memory.
+  griddep_wait();
+  griddep_launch_dependents();
+  if (blockIdx.x == 0) {
+    ragged::check_offsets(p.q_offsets, p.batch, p.total_q, threadIdx.x, kThreads, p.dev_status);
+    ragged::check_offsets(p.kv_offsets, p.batch, p.total_kv, threadIdx.x, kThreads, p.dev_status);
   }
   __syncwarp();
   tc_fence_before();
@@ -974,6 +978,24 @@ cudaError_t prepare_device(int dev, int *sms) {
   return e;
 }
 
+// A launch as a programmatic dependent (every kernel here waits for the one
+// before it ahead of its first memory access).
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream,
+                   const A &...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 mla_status_t run(const Args &a, void *workspace, size_t workspace_bytes, void *stream) {
   set_error_detail("");
   if (a.batch < 0 || a.total_q < 0 || a.total_kv < 0 || a.total_q > INT32_MAX || a.total_kv > kMaxKv)
@@ -1034,23 +1056,11 @@ mla_status_t run(const Args &a, void *workspace, size_t workspace_bytes, void *s
   if (workspace && most <= blocks / 2) {  // see find_part
     p.partial = (float *)workspace;
     p.partial_lse = p.partial + (int64_t)blocks * 2 * kTile * kV;
-    prefill_kernel<<<blocks, kThreads, sizeof(Smem) + 1024, st>>>(maps, p);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return cuda_failed(e);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, join_kernel, p);
-    return e == cudaSuccess ? MLA_OK : cuda_failed(e);
+    e = launch(prefill_kernel, blocks, kThreads, sizeof(Smem) + 1024, st, maps, p);
+    if (e == cudaSuccess) e = launch(join_kernel, blocks, kJoinThreads, 0, st, p);
+  } else {
+    e = launch(prefill_kernel, (unsigned)most, kThreads, sizeof(Smem) + 1024, st, maps, p);
   }
-  prefill_kernel<<<(unsigned)most, kThreads, sizeof(Smem) + 1024, st>>>(maps, p);
-  e = cudaGetLastError();
   return e == cudaSuccess ? MLA_OK : cuda_failed(e);
 }
 

@@ -36,7 +36,7 @@ def append(lib, fp8=False, **kw):
 
 
 @pytest.mark.parametrize("bad, status", [
-    (dict(tokens=-1), 1), (dict(tokens=1 << 31), 1), (dict(block_size=0), 1), (dict(num_blocks=0), 1), (dict(max_position=0), 1),
+    (dict(tokens=-1), 1), (dict(tokens=1 << 27), 1), (dict(block_size=0), 1), (dict(num_blocks=0), 1), (dict(max_position=0), 1),
     (dict(interleaved=2), 1), (dict(weight=A, eps=float("nan")), 1), (dict(weight=A, eps=-1.0), 1), (dict(q=None), 1), (dict(qo=None), 1),
     (dict(heads=0), 2), (dict(heads=129), 2), (dict(kv=None), 1), (dict(positions=None), 1), (dict(cos_sin=None), 1), (dict(slots=None), 1),
     (dict(cache=None), 1), (dict(kv=A + 8), 1), (dict(cos_sin=A + 4), 1), (dict(cache=A + 8), 1), (dict(weight=A + 2), 1), (dict(q=A + 2), 1),

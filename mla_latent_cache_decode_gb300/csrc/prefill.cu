@@ -60,7 +60,8 @@ constexpr int64_t kMaxKv = 1 << 26;
 constexpr uint64_t kWaitNs = 3000000000ull;
 constexpr uint64_t kDrainNs = 10000000ull;
 constexpr float kRescale = 8.0f;  // log2
-constexpr int64_t kGroupBytes = 48 << 20;  // keys and values walked together, of 129 MB of L2
+constexpr int32_t kGroupKeys = (48 << 20) / (2 * (kNope + kV));  // key rows of all heads walked together: 48 MB of 129 MB of L2
+constexpr int kAskTiles = 4;               // key tiles ahead of an item's last load
 constexpr int kMinPart = 4;                // key tiles of a part, at least
 
 struct Strided {
@@ -74,7 +75,7 @@ struct Maps {
 
 struct Params {
   const int32_t *q_offsets, *kv_offsets;
-  int32_t batch, heads, total_q, total_kv, causal;
+  int32_t batch, heads, total_q, total_kv, causal, two_heads;
   float scale_log2;
   __nv_bfloat16 *out;
   float *lse;
@@ -84,13 +85,24 @@ struct Params {
 
 // One item: rows [q0, q0 + rows) of head h over key tiles [kt, kt + .) of key
 // rows [k0, k0 + nk).  Row r of the item sees keys [0, min(nk, see + r)).
-// More than 128 rows: query tile t holds rows 128 t .. and runs n[t] key tiles
-// from kt on (n[0] <= n[1]).  Up to 128 rows (shared): both query tiles hold
-// the same rows, tile t runs key tiles kt + t, kt + t + 2, ...: two chains of
-// softmax and MMA instead of one, joined in the epilogue.
+// Query tile t runs n[t] key tiles.
+enum Mode : int32_t {
+  // More than 128 rows: query tile t holds rows 128 t ..; both run the same key
+  // tiles (n[0] <= n[1]).
+  kTwoTiles,
+  // Up to 128 rows: both query tiles hold them, tile t runs key tiles kt + t,
+  // kt + t + 2, ...: two chains of softmax and MMA instead of one, joined in
+  // the epilogue.
+  kOddEven,
+  // Up to 128 rows, with items enough: query tile t holds head h + t, each with
+  // its own keys and values.
+  kTwoHeads,
+};
 struct Work {
-  int32_t h, q0, rows, k0, nk, see, kt, n[2], shared;
+  int32_t h, q0, rows, k0, nk, see, kt, n[2], mode;
   int32_t part, parts, slot, slot_step;  // parts > 1: a part of the keys, joined later
+  // key tiles loaded: of the only head, or of both in turn
+  __device__ __forceinline__ int32_t loads() const { return mode == kTwoTiles ? n[1] : n[0] + n[1]; }
 };
 
 struct __align__(1024) Smem {
@@ -99,11 +111,11 @@ struct __align__(1024) Smem {
   uint8_t v[kVSlots][kVChunks][kChunk];
   uint64_t q_full[2], q_empty[2], k_full[kKSlots], k_empty[kKSlots], v_full[kVSlots], v_empty[kVSlots];
   uint64_t s_full[2], p_full[2], o_full[2];
-  // a shared item: tile 1's maxima and sums, then both tiles' factors
+  // an odd-even item: tile 1's maxima and sums, then both tiles' factors
   float2 join[kTile];
   uint64_t join_sums, join_factors, join_end;
   uint64_t work_full[2], work_empty[2];
-  uint64_t fin, roles_done, claim_full;
+  uint64_t fin, roles_done, claim_full, near_end;
   uint4 claim;  // the answer of cluster launch control
   Work work[2];  // rows = 0: no more items
   uint32_t tmem_base;
@@ -170,23 +182,25 @@ __device__ __forceinline__ Request shuffle(const Request &r, int src) {
 
 // Up to 32 requests in the order of their contexts, longest first, so that
 // the longest items start first and short ones fill the end.
-__device__ __forceinline__ Request sorted(const Request &r, int lane) {
+__device__ __forceinline__ Request sorted(const Request &r, int32_t batch, int lane) {
+  if (batch <= 1) return r;
   int rank = 0, src = 0;
-#pragma unroll 1
+#pragma unroll
   for (int i = 0; i < 32; ++i) {
     const int32_t nk = __shfl_sync(0xffffffffu, r.nk, i);
     rank += nk > r.nk || (nk == r.nk && i < lane);
   }
-#pragma unroll 1
+#pragma unroll
   for (int i = 0; i < 32; ++i)
     if (__shfl_sync(0xffffffffu, rank, i) == lane) src = i;
   return shuffle(r, src);
 }
 
-__device__ __forceinline__ int64_t prefix(int64_t x, int lane) {  // inclusive
+template <typename T>
+__device__ __forceinline__ T prefix(T x, int lane) {  // inclusive
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    const T y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
   return x;
@@ -199,9 +213,10 @@ __device__ __forceinline__ int32_t key_tiles(const Params &p, const Request &r, 
 }
 
 // Tile `tile` (from the request's start) of head h, key tiles
-// [n part / parts, n (part + 1) / parts) of its n.
+// [n part / parts, n (part + 1) / parts) of its n; `two_heads`: up to 128 rows
+// are taken together with the next head's.
 __device__ __forceinline__ Work make_work(const Params &p, const Request &r, int32_t tile, int32_t h, int32_t part,
-                                          int32_t parts) {
+                                          int32_t parts, bool two_heads) {
   Work w = {};
   const int32_t first = tile * 2 * kTile;
   w.h = h;
@@ -215,37 +230,56 @@ __device__ __forceinline__ Work make_work(const Params &p, const Request &r, int
   const int32_t n = key_tiles(p, r, first, w.rows);
   w.kt = (int32_t)((int64_t)n * part / parts);
   const int32_t end = (int32_t)((int64_t)n * (part + 1) / parts);
-  w.shared = w.rows <= kTile;
-  if (w.shared) {
+  if (w.rows <= kTile && two_heads) {
+    w.mode = kTwoHeads;
+    w.n[0] = w.n[1] = end - w.kt;
+  } else if (w.rows <= kTile) {
+    w.mode = kOddEven;
     w.n[0] = (end - w.kt + 1) / 2;
     w.n[1] = (end - w.kt) / 2;
   } else {
+    w.mode = kTwoTiles;
     w.n[0] = max(min(key_tiles(p, r, first, kTile), end) - w.kt, 0);
     w.n[1] = end - w.kt;
   }
   return w;
 }
 
+// A request's last tile, when it has up to 128 rows and pairs of heads share
+// an item.
+__device__ __forceinline__ int32_t thin_tile(const Params &p, const Request &r) {
+  return p.two_heads && r.tiles > 0 && r.nq - (r.tiles - 1) * 2 * kTile <= kTile ? 1 : 0;
+}
+
 // Item `at` in the order: requests (up to 32: longest context first), groups of
 // heads whose keys and values fit L2 together, tiles from the request's last
 // (the longest when causal) to its first, heads of the group.  By one warp;
 // rows = 0 behind the last.
-__device__ __forceinline__ Work find_work(const Params &p, const Request &few, int64_t at, int lane) {
-  int64_t before = 0;
+__device__ __forceinline__ Work find_work(const Params &p, const Request &few, int32_t at, int lane) {
+  int32_t before = 0;
   for (int32_t b0 = 0; b0 < p.batch; b0 += 32) {
     const Request mine = p.batch <= 32 ? few : request(p, b0 + lane);
-    const int64_t items = (int64_t)mine.tiles * p.heads, upto = before + prefix(items, lane);
+    const int32_t thin = thin_tile(p, mine);
+    const int32_t items = (mine.tiles - thin) * p.heads + thin * ((p.heads + 1) / 2);
+    const int32_t upto = before + prefix(items, lane);
     const uint32_t hit = __ballot_sync(0xffffffffu, at >= upto - items && at < upto);
     if (hit) {
       const int src = __ffs(hit) - 1;
       const Request r = shuffle(mine, src);
-      const int64_t i = at - __shfl_sync(0xffffffffu, upto - items, src);
-      const int64_t head_bytes = (int64_t)r.nk * (kNope + kV) * 2 + 1;
-      const int32_t group = (int32_t)min((int64_t)p.heads, max((int64_t)1, kGroupBytes / head_bytes));
-      const int32_t first = (int32_t)(i / ((int64_t)r.tiles * group)) * group;
+      int32_t i = at - __shfl_sync(0xffffffffu, upto - items, src);
+      const int32_t rt = thin_tile(p, r);
+      // an even number of heads, or all
+      const int32_t group = min(p.heads, max(2, kGroupKeys / max(r.nk, 1) & ~1));
+      const int32_t of_group = (r.tiles - rt) * group + rt * ((group + 1) / 2);
+      const int32_t first = i / of_group * group;
       const int32_t heads = min(group, p.heads - first);
-      const int32_t in_group = (int32_t)(i - (int64_t)first * r.tiles);
-      return make_work(p, r, r.tiles - 1 - in_group / heads, first + in_group % heads, 0, 1);
+      i -= i / of_group * of_group;
+      if (rt && i < (heads + 1) / 2) {
+        const int32_t h = first + 2 * i;
+        return make_work(p, r, r.tiles - 1, h, 0, 1, h + 1 < p.heads);
+      }
+      i -= rt * ((heads + 1) / 2);
+      return make_work(p, r, r.tiles - 1 - rt - i / heads, first + i % heads, 0, 1, false);
     }
     before = __shfl_sync(0xffffffffu, upto, 31);
   }
@@ -287,7 +321,7 @@ __device__ __forceinline__ Work find_part(const Params &p, int64_t at, int32_t b
         const int32_t cut = (int32_t)max((int64_t)1, (n + most - 1) / most);
         if (at < first + (int64_t)cut * p.heads) {
           const int32_t i = (int32_t)(at - first);
-          Work w = make_work(p, r, t, i % p.heads, i / p.heads, cut);
+          Work w = make_work(p, r, t, i % p.heads, i / p.heads, cut, false);
           w.slot = (int32_t)at;
           w.slot_step = p.heads;
           return w;
@@ -449,7 +483,7 @@ __device__ __forceinline__ void softmax_role(Smem &s, const Params &p, int warp,
   const uint32_t s_addr = lanes + kColS + 128 * t;
   const bool wide = ((uintptr_t)p.out & 31) == 0;
   Items items;
-  // key tiles of this query tile, key tiles loaded, outputs of either query tile, shared items
+  // key tiles of this query tile, key tiles loaded, outputs of either query tile, odd-even items
   uint32_t g = 0, vg = 0, outs0 = 0, outs1 = 0, joins = 0;
   while (true) {
     if (!warp_wait(s, p, s.work_full[items.i & 1], (items.i >> 1) & 1)) return;
@@ -457,15 +491,15 @@ __device__ __forceinline__ void softmax_role(Smem &s, const Params &p, int warp,
     const Work &w = s.work[items.i & 1];
     if (w.rows == 0) return;
     const int n = t ? w.n[1] : w.n[0];
-    const int at = w.shared ? row : t * kTile + row;  // row of the item
+    const int at = w.mode == kTwoTiles ? t * kTile + row : row;  // row of the item
     float m = -INFINITY, l = 0.f;
     {
       // of this query tile's first key tile: the keys the row sees from there
       // on, the keys there are, and its number among all tiles loaded
-      const int key = (w.kt + (w.shared ? t : 0)) * kTile;
+      const int key = (w.kt + (w.mode == kOddEven ? t : 0)) * kTile;
       int lim = min(w.nk, p.causal ? w.see + at : w.nk) - key;
-      const int step = w.shared ? 2 : 1;
-      for (int j = 0; j < n; ++j, ++g, lim -= step * kTile) {
+      const int step = w.mode == kOddEven ? 2 * kTile : kTile;
+      for (int j = 0; j < n; ++j, ++g, lim -= step) {
         if (!warp_wait(s, p, s.s_full[t], g & 1)) return;
         tc_fence_after();
         softmax_tile(s_addr, s_addr + (kColO - kColS), p.scale_log2, __any_sync(0xffffffffu, lim < kTile), lim, j == 0, m,
@@ -474,9 +508,9 @@ __device__ __forceinline__ void softmax_role(Smem &s, const Params &p, int warp,
           // A last key tile's P V reads value rows up to a multiple of 16: those
           // behind the request's last key hold anything (0 * NaN = NaN), so they
           // are zeroed first, by both query tiles alike.
-          const int jt = w.shared ? 2 * j + t : j, valid = w.nk - (w.kt + jt) * kTile;
+          const int valid = w.nk - key - j * step;
           if (valid < kTile && (valid & 15)) {
-            const uint32_t vi = vg + jt;
+            const uint32_t vi = vg + (w.mode == kTwoTiles ? j : 2 * j + t);
             if (!warp_wait(s, p, s.v_full[vi % kVSlots], (vi / kVSlots) & 1)) return;
             const int pad = 16 - (valid & 15);
             for (int k = q4 * 32 + lane; k < pad * 16; k += 128) {
@@ -491,17 +525,17 @@ __device__ __forceinline__ void softmax_role(Smem &s, const Params &p, int warp,
         mbar_arrive(smem_u32(&s.p_full[t]));
       }
     }
-    vg += w.shared ? w.n[0] + w.n[1] : w.n[1];
+    vg += w.loads();
     // ---- epilogue: O / l
     const bool real = at < w.rows;
-    const int64_t out_row = ((int64_t)w.q0 + at) * p.heads + w.h;
+    const int64_t out_row = ((int64_t)w.q0 + at) * p.heads + w.h + (w.mode == kTwoHeads ? t : 0);
     __nv_bfloat16 *out = p.out + out_row * kV;
     float *partial = nullptr, *lse = p.lse ? p.lse + out_row : nullptr;
     if (w.parts > 1) {
       partial = p.partial + ((int64_t)w.slot * 2 * kTile + at) * kV;
       lse = p.partial_lse + (int64_t)w.slot * 2 * kTile + at;
     }
-    if (!w.shared) {
+    if (w.mode != kOddEven) {
       if (n > 0) {
         if (!warp_wait(s, p, s.o_full[t], (t ? outs1 : outs0) & 1)) return;
         tc_fence_after();
@@ -619,26 +653,28 @@ struct MmaRole {
     return true;
   }
 
-  template <int t, bool kShared>
-  __device__ __forceinline__ bool step(int j, int n, int total, int tail_keys) {
+  template <int t, Mode kMode>
+  __device__ __forceinline__ bool step(int j, int n, int loads, int tail_keys) {
     if (pend[t].on && !run_pv<t>()) return false;
     if (j >= n) return true;
-    if (j == 0 && (t == 0 || !kShared) && !wait_or_abort(s, p, s.q_full[t], q_used[t]++ & 1)) return false;
-    const int jt = kShared ? 2 * j + t : j;  // key tile of the item
-    if (!run_s<t, kShared ? 0 : t, kShared || t == 1>(kv + jt)) return false;
-    if (kShared ? jt == total - 1 : j == n - 1) mma_commit(smem_u32(&s.q_empty[kShared ? 0 : t]));
-    const int keys = tail_keys - jt * kTile;  // from this tile on
-    pend[t] = Pending{true, j == 0, j == n - 1, kShared || t == 1, kv + jt, keys >= kTile ? kTile / 16 : (keys + 15) >> 4};
+    constexpr bool kOwnTiles = kMode != kTwoTiles;        // key tiles of its own
+    constexpr int tq = kMode == kOddEven ? 0 : t;         // place of its Q
+    if (j == 0 && tq == t && !wait_or_abort(s, p, s.q_full[t], q_used[t]++ & 1)) return false;
+    const int jt = kOwnTiles ? 2 * j + t : j;             // among the item's loads
+    if (!run_s<t, tq, kOwnTiles || t == 1>(kv + jt)) return false;
+    if (kMode == kOddEven ? jt == loads - 1 : j == n - 1) mma_commit(smem_u32(&s.q_empty[tq]));
+    const int keys = tail_keys - (kMode == kOddEven ? jt : j) * kTile;  // from this tile on
+    pend[t] = Pending{true, j == 0, j == n - 1, kOwnTiles || t == 1, kv + jt, keys >= kTile ? kTile / 16 : (keys + 15) >> 4};
     return true;
   }
 
-  template <bool kShared>
-  __device__ __forceinline__ bool item(int n0, int n1, int tail_keys) {
-    const int rounds = max(n0, n1), total = kShared ? n0 + n1 : n1;
+  template <Mode kMode>
+  __device__ __forceinline__ bool item(int n0, int n1, int loads, int tail_keys) {
+    const int rounds = max(n0, n1);
 #pragma unroll 1
     for (int j = 0; j < rounds; ++j)
-      if (!step<0, kShared>(j, n0, total, tail_keys) || !step<1, kShared>(j, n1, total, tail_keys)) return false;
-    kv += total;
+      if (!step<0, kMode>(j, n0, loads, tail_keys) || !step<1, kMode>(j, n1, loads, tail_keys)) return false;
+    kv += loads;
     return true;
   }
 
@@ -648,13 +684,15 @@ struct MmaRole {
     while (ok && items.ready(s, p)) {
       const Work &w = s.work[items.i & 1];
       const int rows = w.rows, n0 = w.n[0], n1 = w.n[1], tail_keys = w.nk - w.kt * kTile;
-      const bool shared = w.shared;
+      const int mode = w.mode, loads = w.loads();
       items.done(s);
       if (max(n0, n1) == 0) {  // no key to see, or no more items: what is pending has no S to wait behind
         ok = (!pend[0].on || run_pv<0>()) && (!pend[1].on || run_pv<1>());
         if (rows == 0) break;
       } else {
-        ok = shared ? item<true>(n0, n1, tail_keys) : item<false>(n0, n1, tail_keys);
+        ok = mode == kTwoTiles  ? item<kTwoTiles>(n0, n1, loads, tail_keys)
+             : mode == kOddEven ? item<kOddEven>(n0, n1, loads, tail_keys)
+                                : item<kTwoHeads>(n0, n1, loads, tail_keys);
       }
     }
     // every MMA issued is finished before the tensor memory is given back
@@ -685,36 +723,36 @@ __device__ __forceinline__ void load_role(Smem &s, const Params &p, const Maps &
   const uint64_t hint = policy_evict_normal();
   bool ok = true;
   auto load_q = [&](const Work &w, int t) -> bool {
-    if ((t ? w.n[1] : w.n[0]) == 0 || (t == 1 && w.shared)) return true;
+    if ((t ? w.n[1] : w.n[0]) == 0 || (t == 1 && w.mode == kOddEven)) return true;
     if (!wait_or_abort(s, p, s.q_empty[t], (nq[t] & 1) ^ 1)) return false;
     const uint32_t bar = smem_u32(&s.q_full[t]);
     mbar_arrive_expect_tx(bar, kQChunks * kChunk);
-    const int32_t y = w.q0 + t * kTile;
-    tma_load_3d_hint(smem_u32(s.q[t][0]), &maps.q_nope, 0, w.h, y, bar, hint);
-    tma_load_3d_hint(smem_u32(s.q[t][1]), &maps.q_nope, 64, w.h, y, bar, hint);
-    tma_load_3d_hint(smem_u32(s.q[t][2]), &maps.q_pe, 0, w.h, y, bar, hint);
+    const int32_t y = w.q0 + (w.mode == kTwoTiles ? t * kTile : 0), h = w.h + (w.mode == kTwoHeads ? t : 0);
+    tma_load_3d_hint(smem_u32(s.q[t][0]), &maps.q_nope, 0, h, y, bar, hint);
+    tma_load_3d_hint(smem_u32(s.q[t][1]), &maps.q_nope, 64, h, y, bar, hint);
+    tma_load_3d_hint(smem_u32(s.q[t][2]), &maps.q_pe, 0, h, y, bar, hint);
     ++nq[t];
     return true;
   };
-  auto load_k = [&](const Work &w, int j) -> bool {
-    const int32_t y = w.k0 + (w.kt + j) * kTile;
+  // key rows from y on, of head h
+  auto load_k = [&](int32_t h, int32_t y) -> bool {
     for (int c = 0; c < kQChunks; ++c, ++nk) {
       const uint32_t slot = nk % kKSlots;
       if (!wait_or_abort(s, p, s.k_empty[slot], ((nk / kKSlots) & 1) ^ 1)) return false;
       const uint32_t bar = smem_u32(&s.k_full[slot]);
       mbar_arrive_expect_tx(bar, kChunk);
-      if (c < 2) tma_load_3d_hint(smem_u32(s.k[slot]), &maps.k_nope, 64 * c, w.h, y, bar, hint);
+      if (c < 2) tma_load_3d_hint(smem_u32(s.k[slot]), &maps.k_nope, 64 * c, h, y, bar, hint);
       else tma_load_3d_hint(smem_u32(s.k[slot]), &maps.k_pe, 0, 0, y, bar, hint);
     }
     return true;
   };
-  auto load_v = [&](const Work &w, int j) -> bool {
+  auto load_v = [&](int32_t h, int32_t y) -> bool {
     const uint32_t slot = nv % kVSlots;
     if (!wait_or_abort(s, p, s.v_empty[slot], ((nv / kVSlots) & 1) ^ 1)) return false;
     const uint32_t bar = smem_u32(&s.v_full[slot]);
     mbar_arrive_expect_tx(bar, kVChunks * kChunk);
     for (int c = 0; c < kVChunks; ++c)
-      tma_load_3d_hint(smem_u32(s.v[slot][c]), &maps.v, 64 * c, w.h, w.k0 + (w.kt + j) * kTile, bar, hint);
+      tma_load_3d_hint(smem_u32(s.v[slot][c]), &maps.v, 64 * c, h, y, bar, hint);
     ++nv;
     return true;
   };
@@ -727,10 +765,17 @@ __device__ __forceinline__ void load_role(Smem &s, const Params &p, const Maps &
     const Work w = items.get(s);
     items.done(s);
     if (w.rows == 0) break;
-    const int all = w.shared ? w.n[0] + w.n[1] : w.n[1];
+    const int loads = w.loads();
+    const bool heads = w.mode == kTwoHeads;
+    // Only now may the next item be claimed: a block that claims while its
+    // item has long to run would keep it from those that run dry.
+    const int ask = max(loads - kAskTiles, 0);
+    if (loads == 0) mbar_arrive(smem_u32(&s.near_end));
     ok = load_q(w, 0);
-    for (int j = 0; j < all && ok; ++j) {
-      ok = load_k(w, j) && (j > 0 || load_q(w, 1)) && load_v(w, j);
+    for (int j = 0; j < loads && ok; ++j) {
+      if (j == ask) mbar_arrive(smem_u32(&s.near_end));
+      const int32_t h = w.h + (heads ? j & 1 : 0), y = w.k0 + (w.kt + (heads ? j >> 1 : j)) * kTile;
+      ok = load_k(h, y) && (j > 0 || load_q(w, 1)) && load_v(h, y);
     }
   }
   if (*(volatile int *)&s.abort) {  // no copy may still be landing when the shared memory is given up
@@ -752,7 +797,7 @@ __device__ __forceinline__ void load_role(Smem &s, const Params &p, const Maps &
 struct Claims {
   uint32_t phase = 0;
   // By one warp: the next item's index, -1 when none is left (or on giving up).
-  __device__ __forceinline__ int64_t next(Smem &s, const Params &p, int lane) {
+  __device__ __forceinline__ int32_t next(Smem &s, const Params &p, int lane) {
     if (lane == 0) {
       fence_proxy_async_shared();  // the last answer has been read
       mbar_arrive_expect_tx(smem_u32(&s.claim_full), 16);
@@ -773,7 +818,7 @@ struct Claims {
         : "=r"(got), "=r"(x)
         : "l"(a0), "l"(a1));
     __syncwarp();
-    return got ? (int64_t)x : -1;
+    return got ? (int32_t)x : -1;
   }
 };
 
@@ -794,11 +839,12 @@ __device__ __forceinline__ void schedule_role(Smem &s, const Params &p, int lane
     return;
   }
   Request few = {};
-  if (p.batch <= 32) few = sorted(request(p, lane), lane);
+  if (p.batch <= 32) few = sorted(request(p, lane), p.batch, lane);
   Claims claims;
-  for (int64_t at = blockIdx.x; at >= 0; at = claims.next(s, p, lane)) {
+  for (int32_t at = blockIdx.x; at >= 0; at = claims.next(s, p, lane)) {
     const Work w = find_work(p, few, at, lane);
-    if (w.rows > 0 && !publish(w)) return;  // a block more than there are items brings none
+    if (w.rows == 0) continue;  // a block more than there are items brings none
+    if (!publish(w) || !warp_wait(s, p, s.near_end, (i - 1) & 1)) return;
   }
   (void)publish(Work{});
 }
@@ -829,6 +875,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     mbar_init(smem_u32(&s.join_factors), kTile);
     mbar_init(smem_u32(&s.join_end), 2 * kTile);
     mbar_init(smem_u32(&s.claim_full), 1);
+    mbar_init(smem_u32(&s.near_end), 1);
     mbar_init(smem_u32(&s.fin), 1);
     mbar_init(smem_u32(&s.roles_done), kThreads / 32);
     s.abort = 0;
@@ -842,10 +889,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   // kernel before this one ends, what is below reads and writes memory.
   griddep_wait();
   griddep_launch_dependents();
-  if (blockIdx.x == 0) {
-    ragged::check_offsets(p.q_offsets, p.batch, p.total_q, threadIdx.x, kThreads, p.dev_status);
-    ragged::check_offsets(p.kv_offsets, p.batch, p.total_kv, threadIdx.x, kThreads, p.dev_status);
-  }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
@@ -863,6 +906,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       if (elect_one_sync()) load_role(s, p, maps);
     } else if (warp == kSoftmaxWarps + 2) {
       schedule_role(s, p, lane);
+    } else if (blockIdx.x == 0) {
+      ragged::check_offsets(p.q_offsets, p.batch, p.total_q, lane, 32, p.dev_status);
+      ragged::check_offsets(p.kv_offsets, p.batch, p.total_kv, lane, 32, p.dev_status);
     }
   }
 
@@ -1048,6 +1094,7 @@ mla_status_t run(const Args &a, void *workspace, size_t workspace_bytes, void *s
   p.lse = a.lse;
   p.dev_status = a.dev_status;
   p.partial = p.partial_lse = nullptr;
+  p.two_heads = 0;
   // no more items than this, whatever the offsets say
   const int64_t most = (a.total_q / (2 * kTile) + a.batch) * (int64_t)a.heads;
   if (most > INT32_MAX) return invalid("more than 2^31 tiles of 256 queries and a head");
@@ -1059,6 +1106,8 @@ mla_status_t run(const Args &a, void *workspace, size_t workspace_bytes, void *s
     e = launch(prefill_kernel, blocks, kThreads, sizeof(Smem) + 1024, st, maps, p);
     if (e == cudaSuccess) e = launch(join_kernel, blocks, kJoinThreads, 0, st, p);
   } else {
+    // two rounds of items and more: halving their number costs no SM its work
+    p.two_heads = most >= 2 * sms;
     e = launch(prefill_kernel, (unsigned)most, kThreads, sizeof(Smem) + 1024, st, maps, p);
   }
   return e == cudaSuccess ? MLA_OK : cuda_failed(e);

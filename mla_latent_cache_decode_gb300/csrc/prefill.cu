@@ -51,7 +51,7 @@ constexpr int kSoftmaxWarps = 8;
 constexpr int kThreads = 32 * (kSoftmaxWarps + 4);  // the last warp completes a warpgroup
 // Registers a thread: 384 x 168 at launch; the softmax warpgroups, which hold
 // a row of S, take over what the third one gives up.
-constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
+constexpr int kSoftmaxRegs = 192, kOtherRegs = 120;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "register split");
 constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;  // tile t at + 128 t
 // The longest legal wait is for another role's whole item: 2^26 keys, at half
@@ -228,8 +228,11 @@ __device__ __forceinline__ Work make_work(const Params &p, const Request &r, int
   w.part = part;
   w.parts = parts;
   const int32_t n = key_tiles(p, r, first, w.rows);
-  w.kt = (int32_t)((int64_t)n * part / parts);
-  const int32_t end = (int32_t)((int64_t)n * (part + 1) / parts);
+  int32_t end = n;
+  if (parts > 1) {
+    w.kt = (int32_t)((int64_t)n * part / parts);
+    end = (int32_t)((int64_t)n * (part + 1) / parts);
+  }
   if (w.rows <= kTile && two_heads) {
     w.mode = kTwoHeads;
     w.n[0] = w.n[1] = end - w.kt;
@@ -370,25 +373,59 @@ __device__ __forceinline__ void add2(float &x, float &y, float a, float b) {  //
       : "f"(a), "f"(b));
 }
 
+// Columns c0 .. c0 + 31 of a row of S; keys from `lim` on are not seen.
+__device__ __forceinline__ void mask32(float *x, int c0, int lim) {
+#pragma unroll
+  for (int k = 0; k < 32; ++k) x[k] = c0 + k < lim ? x[k] : -INFINITY;
+}
+
+__device__ __forceinline__ void max32(const float *x, float (&mx)[4]) {
+#pragma unroll
+  for (int k = 0; k < 32; k += 2) mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], x[k], x[k + 1]);
+}
+
+// 32 weights 2^(x scale_log2 + nm) as bf16 into 16 columns of tensor memory,
+// their sum in fp32 into ps.
+__device__ __forceinline__ void weights32(const float *x, float scale_log2, float nm, float (&ps)[4], uint32_t p_addr) {
+  uint32_t pk[16];
+#pragma unroll
+  for (int k = 0; k < 32; k += 2) {
+    float a = x[k], b = x[k + 1];
+    fma2(a, b, scale_log2, nm);
+    a = ex2_approx(a);
+    b = ex2_approx(b);
+    add2(ps[k & 2], ps[(k & 2) + 1], a, b);
+    pk[k / 2] = pack2(a, b);
+  }
+  tmem_st16(p_addr, pk);
+}
+
 // One key tile of one row: S from tensor memory, its maximum and the sum of the
 // weights, and the weights back over S as bf16.  `lim`: keys of this tile that
-// the row sees (may be <= 0 or >= 128).
+// the row sees (may be <= 0 or >= 128).  The last 32 columns of S, which the
+// weights do not overwrite, are read twice: 96 values live at a time instead
+// of 128 leave the registers for the rest of the loop.
 __device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, float scale_log2, bool masked, int lim,
                                              bool first, float &m, float &l) {
-  float x[kTile];
+  float x[96];
   uint32_t *xr = reinterpret_cast<uint32_t *>(x);
-#pragma unroll
-  for (int c = 0; c < kTile; c += 32) tmem_ld32(s_addr + c, xr + c);
+  tmem_ld32(s_addr + 96, xr + 64);
+  tmem_ld32(s_addr, xr);
+  tmem_ld32(s_addr + 32, xr + 32);
   tmem_wait_ld();
   if (masked) {
-#pragma unroll
-    for (int k = 0; k < kTile; ++k) x[k] = k < lim ? x[k] : -INFINITY;
+    mask32(x + 64, 96, lim);
+    mask32(x, 0, lim);
+    mask32(x + 32, 32, lim);
   }
-  float mx[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) mx[k] = fmaxf(x[2 * k], x[2 * k + 1]);
-#pragma unroll
-  for (int k = 8; k < kTile; k += 2) mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], x[k], x[k + 1]);
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  max32(x + 64, mx);
+  tmem_ld32(s_addr + 64, xr + 64);
+  max32(x, mx);
+  max32(x + 32, mx);
+  tmem_wait_ld();
+  if (masked) mask32(x + 64, 64, lim);
+  max32(x + 64, mx);
   const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale_log2;
   const bool grow = top > m + kRescale || (m == -INFINITY && top > -INFINITY);
   if (__any_sync(0xffffffffu, grow)) {
@@ -397,32 +434,25 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, f
     l *= alpha;
     if (!first) {
 #pragma unroll 1
-      for (int c = 0; c < kV; c += 8) {
-        uint32_t o[8];
-        tmem_ld8(o_addr + c, o);
+      for (int c = 0; c < kV; c += 16) {
+        uint32_t o[16];
+        tmem_ld16(o_addr + c, o);
         tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-        tmem_st8(o_addr + c, o);
+        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+        tmem_st16(o_addr + c, o);
       }
     }
   }
   const float nm = m == -INFINITY ? 0.f : -m;  // a row that has seen nothing: every weight is 0
   float ps[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int c = 0; c < kTile; c += 32) {
-    uint32_t pk[16];
-#pragma unroll
-    for (int k = 0; k < 32; k += 2) {
-      float a = x[c + k], b = x[c + k + 1];
-      fma2(a, b, scale_log2, nm);
-      a = ex2_approx(a);
-      b = ex2_approx(b);
-      add2(ps[k & 2], ps[(k & 2) + 1], a, b);
-      pk[k / 2] = pack2(a, b);
-    }
-    tmem_st16(s_addr + c / 2, pk);
-  }
+  weights32(x, scale_log2, nm, ps, s_addr);
+  tmem_ld32(s_addr + 96, xr);
+  weights32(x + 32, scale_log2, nm, ps, s_addr + 16);
+  weights32(x + 64, scale_log2, nm, ps, s_addr + 32);
+  tmem_wait_ld();
+  if (masked) mask32(x, 96, lim);
+  weights32(x, scale_log2, nm, ps, s_addr + 48);
   l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
 }
 
@@ -756,11 +786,6 @@ __device__ __forceinline__ void load_role(Smem &s, const Params &p, const Maps &
     ++nv;
     return true;
   };
-  prefetch_tmap(&maps.q_nope);
-  prefetch_tmap(&maps.q_pe);
-  prefetch_tmap(&maps.k_nope);
-  prefetch_tmap(&maps.k_pe);
-  prefetch_tmap(&maps.v);
   while (ok && items.ready(s, p)) {
     const Work w = items.get(s);
     items.done(s);
@@ -884,6 +909,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   if (warp == 0) {
     tmem_alloc(smem_u32(&s.tmem_base), kTmemCols);
     tmem_relinquish();
+  }
+  if (threadIdx.x == 32 * (kSoftmaxWarps + 1)) {
+    prefetch_tmap(&maps.q_nope);
+    prefetch_tmap(&maps.q_pe);
+    prefetch_tmap(&maps.k_nope);
+    prefetch_tmap(&maps.k_pe);
+    prefetch_tmap(&maps.v);
   }
   // Launched as a programmatic dependent: what is above may run while the
   // kernel before this one ends, what is below reads and writes memory.

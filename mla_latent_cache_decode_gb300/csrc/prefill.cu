@@ -80,6 +80,7 @@ struct Params {
   __nv_bfloat16 *out;
   float *lse;
   float *partial, *partial_lse;  // split form: [blocks][256][128], [blocks][256]; else null
+  int4 *parts;                   // split form: two words a block, see join_kernel
   int32_t *dev_status;
 };
 
@@ -292,44 +293,45 @@ __device__ __forceinline__ Work find_work(const Params &p, const Request &few, i
 // Split form: few items on long contexts.  Every item is cut into parts of at
 // most `most` key tiles, such that the parts are no more than the blocks; part
 // `at` leaves its output in slot `at` of the workspace.  By one warp; rows = 0
-// behind the last.
-__device__ __forceinline__ Work find_part(const Params &p, int64_t at, int32_t blocks, int lane) {
-  int64_t items = 0, total = 0;
-  for (int32_t b = lane; b < p.batch; b += 32) {
-    const Request r = request(p, b);
-    items += r.tiles;
-    for (int32_t t = 0; t < r.tiles; ++t)
-      total += key_tiles(p, r, t * 2 * kTile, min(2 * kTile, r.nq - t * 2 * kTile));
-  }
-  items = __shfl_sync(0xffffffffu, prefix(items, lane), 31) * p.heads;
-  total = __shfl_sync(0xffffffffu, prefix(total, lane), 31) * p.heads;
-  // sum of ceil(n / most) <= total / most + items <= blocks (items <= blocks / 2)
-  const int64_t most = max((int64_t)kMinPart, (total + blocks - items - 1) / max((int64_t)1, blocks - items));
-  int64_t before = 0;
+// behind the last.  (At most half as many items as blocks, so everything here
+// counts in 32 bits and in few rounds of 32 requests.)
+__device__ __forceinline__ Work find_part(const Params &p, int32_t at, int32_t blocks, int lane) {
+  int32_t items = 0, total = 0;
+  Request mine = request(p, lane);
+  auto tiles_of = [&](const Request &r, int32_t t) {
+    return key_tiles(p, r, t * 2 * kTile, min(2 * kTile, r.nq - t * 2 * kTile));
+  };
   for (int32_t b0 = 0; b0 < p.batch; b0 += 32) {
-    const Request mine = request(p, b0 + lane);
-    int64_t parts = 0;
-    for (int32_t t = 0; t < mine.tiles; ++t) {
-      const int32_t n = key_tiles(p, mine, t * 2 * kTile, min(2 * kTile, mine.nq - t * 2 * kTile));
-      parts += max((int64_t)1, (n + most - 1) / most) * p.heads;
-    }
-    const int64_t upto = before + prefix(parts, lane);
+    const Request r = p.batch <= 32 ? mine : request(p, b0 + lane);
+    items += r.tiles;
+    for (int32_t t = 0; t < r.tiles; ++t) total += tiles_of(r, t);
+  }
+  items = __reduce_add_sync(0xffffffffu, items) * p.heads;
+  total = __reduce_add_sync(0xffffffffu, total) * p.heads;
+  // sum of ceil(n / most) <= total / most + items <= blocks
+  const int32_t spare = max(1, blocks - items), most = max(kMinPart, (total + spare - 1) / spare);
+  int32_t before = 0;
+  for (int32_t b0 = 0; b0 < p.batch; b0 += 32) {
+    if (p.batch > 32) mine = request(p, b0 + lane);
+    int32_t parts = 0;
+    for (int32_t t = 0; t < mine.tiles; ++t) parts += max(1, (tiles_of(mine, t) + most - 1) / most);
+    parts *= p.heads;
+    const int32_t upto = before + prefix(parts, lane);
     const uint32_t hit = __ballot_sync(0xffffffffu, at >= upto - parts && at < upto);
     if (hit) {
       const int src = __ffs(hit) - 1;
       const Request r = shuffle(mine, src);
-      int64_t first = __shfl_sync(0xffffffffu, upto - parts, src);
+      int32_t first = __shfl_sync(0xffffffffu, upto - parts, src);
       for (int32_t t = 0; t < r.tiles; ++t) {
-        const int32_t n = key_tiles(p, r, t * 2 * kTile, min(2 * kTile, r.nq - t * 2 * kTile));
-        const int32_t cut = (int32_t)max((int64_t)1, (n + most - 1) / most);
-        if (at < first + (int64_t)cut * p.heads) {
-          const int32_t i = (int32_t)(at - first);
+        const int32_t cut = max(1, (tiles_of(r, t) + most - 1) / most);
+        if (at < first + cut * p.heads) {
+          const int32_t i = at - first;
           Work w = make_work(p, r, t, i % p.heads, i / p.heads, cut, false);
-          w.slot = (int32_t)at;
+          w.slot = at;
           w.slot_step = p.heads;
           return w;
         }
-        first += (int64_t)cut * p.heads;
+        first += cut * p.heads;
       }
     }
     before = __shfl_sync(0xffffffffu, upto, 31);
@@ -616,6 +618,30 @@ __device__ __forceinline__ void softmax_role(Smem &s, const Params &p, int warp,
 
 // ---------------------------------------------------------------- MMA issuer
 
+// An operand's descriptor is 64 bits, of which only the address field in the
+// low word changes: the MMAs here take low words and one constant high word (a
+// stride of 1,024 bytes between groups of eight rows, 128-byte swizzle), which
+// halves the address arithmetic and the registers of the issue loop.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (kSwizzle128B << 29);
+__device__ __forceinline__ uint32_t desc_low(const void *p, uint32_t lbo_bytes) {
+  return (smem_u32(p) >> 4) | (lbo_bytes >> 4 << 16);
+}
+// D (+)= A B, A and B in shared memory; A in tensor memory.
+__device__ __forceinline__ void mma_ss_low(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t more) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %4, 0;\n mov.b64 a, {%1, %5};\n mov.b64 b, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "r"(more), "n"(kDescHigh)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_low(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t more) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %4, 0;\n mov.b64 b, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "r"(more), "n"(kDescHigh)
+      : "memory");
+}
+
 // P V of a query tile's latest key tile, issued once its softmax is done.
 struct Pending {
   bool on, first, last, free_v;
@@ -629,7 +655,7 @@ struct MmaRole {
   Smem &s;
   const Params &p;
   uint32_t tmem;
-  uint64_t d_q, d_k, d_v;  // descriptors of q[0][0], k[0], v[0]
+  uint32_t d_q, d_k, d_v;  // descriptors (low words) of q[0][0], k[0], v[0]
   Pending pend[2];
   uint32_t g[2], q_used[2];  // key tiles and items of each query tile
   uint32_t kv;               // key tiles of the items before
@@ -643,15 +669,16 @@ struct MmaRole {
       return false;
     tc_fence_after();
     constexpr uint32_t id = idesc_bf16_f32(kTile, kV, 1);
-    const uint64_t dv = d_v + (uint64_t)(slot * (kVChunks * kChunk >> 4));
+    const uint32_t dv = d_v + slot * (kVChunks * kChunk >> 4);
     const uint32_t d = tmem + kColO + 128 * t, pa = tmem + kColS + 128 * t;
     if (a.ksteps == kTile / 16) {
-      mma_ts(d, pa, dv, id, a.first ? 0u : 1u);
+      mma_ts_low(d, pa, dv, id, a.first ? 0u : 1u);
 #pragma unroll
-      for (int k = 1; k < kTile / 16; ++k) mma_ts_acc(d, pa + 8 * k, dv + (uint64_t)(128 * k), id);
+      for (int k = 1; k < kTile / 16; ++k) mma_ts_low(d, pa + 8 * k, dv + 128 * k, id, 1u);
     } else {
+#pragma unroll 1
       for (int k = 0; k < a.ksteps; ++k)
-        mma_ts(d, pa + 8 * k, dv + (uint64_t)(128 * k), id, (a.first && k == 0) ? 0u : 1u);
+        mma_ts_low(d, pa + 8 * k, dv + 128 * k, id, (a.first && k == 0) ? 0u : 1u);
     }
     if (a.free_v) mma_commit(smem_u32(&s.v_empty[slot]));
     if (a.last) mma_commit(smem_u32(&s.o_full[t]));
@@ -669,13 +696,9 @@ struct MmaRole {
       const uint32_t chunk = tile * kQChunks + c, slot = chunk % kKSlots;
       if (!wait_or_abort(s, p, s.k_full[slot], (chunk / kKSlots) & 1)) return false;
       tc_fence_after();
-      const uint64_t a = d_q + (uint64_t)((tq * kQChunks + c) * (kChunk >> 4));
-      const uint64_t b = d_k + (uint64_t)(slot * (kChunk >> 4));
+      const uint32_t a = d_q + (tq * kQChunks + c) * (kChunk >> 4), b = d_k + slot * (kChunk >> 4);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (c == 0 && k == 0) mma_ss(d, a, b, id, 0u);
-        else mma_ss_acc(d, a + 2 * k, b + 2 * k, id);
-      }
+      for (int k = 0; k < 4; ++k) mma_ss_low(d, a + 2 * k, b + 2 * k, id, (c > 0 || k > 0) ? 1u : 0u);
       if (kFreeK) mma_commit(smem_u32(&s.k_empty[slot]));
     }
     mma_commit(smem_u32(&s.s_full[t]));
@@ -735,9 +758,9 @@ __device__ __forceinline__ void mma_role(Smem &s, const Params &p, uint32_t tmem
   MmaRole r{s,
             p,
             tmem,
-            smem_desc(smem_u32(s.q[0][0]), 16, 1024, kSwizzle128B),
-            smem_desc(smem_u32(s.k[0]), 16, 1024, kSwizzle128B),
-            smem_desc(smem_u32(s.v[0][0]), kChunk, 1024, kSwizzle128B),
+            desc_low(s.q[0][0], 16),
+            desc_low(s.k[0], 16),
+            desc_low(s.v[0][0], kChunk),
             {},
             {0, 0},
             {0, 0},
@@ -861,6 +884,10 @@ __device__ __forceinline__ void schedule_role(Smem &s, const Params &p, int lane
   if (p.partial) {  // one part a block
     const Work w = find_part(p, blockIdx.x, gridDim.x, lane);
     if (w.rows == 0 || publish(w)) (void)publish(Work{});
+    if (lane == 0) {
+      p.parts[2 * blockIdx.x] = make_int4(w.rows, w.parts, w.part, w.q0);
+      p.parts[2 * blockIdx.x + 1] = make_int4(w.h, w.slot - w.part * w.slot_step, w.slot_step, 0);
+    }
     return;
   }
   Request few = {};
@@ -959,32 +986,41 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 
 // Split form: joins the parts of an item.  Block `at` takes every parts-th row
 // of the item that part `at` belongs to, a warp per row:
-//   out = sum_i 2^(lse_i - top) O_i / sum_i 2^(lse_i - top)
+//   out = sum_i e^(lse_i - top) O_i / sum_i e^(lse_i - top)
+// The attention kernel's block `at` left what to do: {rows, parts, part, first
+// row} and {head, first slot, slots from part to part}.
 constexpr int kJoinThreads = 256;
 
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p) {
   griddep_wait();
+  griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Work w = find_part(p, blockIdx.x, gridDim.x, lane);
-  if (w.rows == 0 || w.parts == 1) return;
-  const int64_t first = w.slot - (int64_t)w.part * w.slot_step;
-  for (int r = w.part + warp * w.parts; r < w.rows; r += kJoinThreads / 32 * w.parts) {
+  const int4 a = p.parts[2 * blockIdx.x], b = p.parts[2 * blockIdx.x + 1];
+  const int rows = a.x, parts = a.y, part = a.z, q0 = a.w, head = b.x, first = b.y, step = b.z;
+  if (rows == 0 || parts == 1) return;
+  for (int r = part + warp * parts; r < rows; r += kJoinThreads / 32 * parts) {
+    // lane i holds part i's log-sum-exp (parts come in groups of 32)
     float top = -INFINITY;
-    for (int i = 0; i < w.parts; ++i) top = fmaxf(top, p.partial_lse[(first + i * w.slot_step) * 2 * kTile + r]);
+    for (int i = lane; i < parts; i += 32) top = fmaxf(top, p.partial_lse[(int64_t)(first + i * step) * 2 * kTile + r]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float sum = 0.f;
-    for (int i = 0; i < w.parts && top > -INFINITY; ++i) {
-      const int64_t at = (first + i * w.slot_step) * 2 * kTile + r;
-      const float a = expf(p.partial_lse[at] - top);
-      const float4 x = reinterpret_cast<const float4 *>(p.partial + at * kV)[lane];
-      sum += a;
-      o.x += a * x.x;
-      o.y += a * x.y;
-      o.z += a * x.z;
-      o.w += a * x.w;
+    if (top > -INFINITY) {
+#pragma unroll 4
+      for (int i = 0; i < parts; ++i) {
+        const int64_t at = (int64_t)(first + i * step) * 2 * kTile + r;
+        const float f = expf(p.partial_lse[at] - top);
+        const float4 x = reinterpret_cast<const float4 *>(p.partial + at * kV)[lane];
+        sum += f;
+        o.x += f * x.x;
+        o.y += f * x.y;
+        o.z += f * x.z;
+        o.w += f * x.w;
+      }
     }
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    const int64_t row = ((int64_t)w.q0 + r) * p.heads + w.h;
+    const int64_t row = ((int64_t)q0 + r) * p.heads + head;
     reinterpret_cast<uint2 *>(p.out + row * kV)[lane] = make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv));
     if (p.lse && lane == 0) p.lse[row] = sum > 0.f ? top + logf(sum) : -INFINITY;
   }
@@ -1038,8 +1074,8 @@ bool encode(CUtensorMap *m, const Strided &s, int64_t tokens, int32_t heads, int
 }
 
 // The split form runs one part a block and at most one block an SM; a part
-// leaves 256 rows of 128 fp32 and their log-sum-exps.
-constexpr size_t kPartBytes = 2 * kTile * (kV + 1) * sizeof(float);
+// leaves 256 rows of 128 fp32 and their log-sum-exps, and what to join.
+constexpr size_t kPartBytes = 2 * kTile * (kV + 1) * sizeof(float) + 2 * sizeof(int4);
 constexpr size_t kWorkspaceBytes = 32u << 20;
 constexpr int kMaxParts = (int)(kWorkspaceBytes / kPartBytes);
 
@@ -1126,6 +1162,7 @@ mla_status_t run(const Args &a, void *workspace, size_t workspace_bytes, void *s
   p.lse = a.lse;
   p.dev_status = a.dev_status;
   p.partial = p.partial_lse = nullptr;
+  p.parts = nullptr;
   p.two_heads = 0;
   // no more items than this, whatever the offsets say
   const int64_t most = (a.total_q / (2 * kTile) + a.batch) * (int64_t)a.heads;
@@ -1135,6 +1172,7 @@ mla_status_t run(const Args &a, void *workspace, size_t workspace_bytes, void *s
   if (workspace && most <= blocks / 2) {  // see find_part
     p.partial = (float *)workspace;
     p.partial_lse = p.partial + (int64_t)blocks * 2 * kTile * kV;
+    p.parts = (int4 *)(p.partial_lse + (int64_t)blocks * 2 * kTile);
     e = launch(prefill_kernel, blocks, kThreads, sizeof(Smem) + 1024, st, maps, p);
     if (e == cudaSuccess) e = launch(join_kernel, blocks, kJoinThreads, 0, st, p);
   } else {

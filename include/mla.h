@@ -416,7 +416,7 @@ mla_status_t mla_rope_append_fp8(const void *kv, int64_t kv_stride, const int64_
  *                last are left as they are
  *   w_uk bf16 [num_heads, 128, 512]   w_uv bf16 [num_heads, 512, 128]
  *   k_nope, v    bf16 [total_kv, num_heads, 128]   k_pe bf16 [total_kv, 64]
- * num_heads 1 to 128 (else MLA_ERR_UNSUPPORTED); total_kv < 2^31 - 1024.  A
+ * num_heads 1 to 128 (else MLA_ERR_UNSUPPORTED); total_kv < 2^30.  A
  * token whose page lies
  * outside the table or the pool is reported as MLA_ERR_DEVICE_RANGE and its
  * rows are unspecified.

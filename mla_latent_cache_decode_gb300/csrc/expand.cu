@@ -46,9 +46,10 @@ constexpr int kRows = 128;              // output rows of a CTA
 constexpr int kDims = 128;              // key dims, value dims of a head
 constexpr int kKChunks = kVDim / 64;    // 64-dim chunks of the latent
 constexpr int kStage = kDims * 128;     // 128 output dims x 64 of K: 16 KB
-constexpr int kStages = 10;
+constexpr int kStages = 12;
 constexpr int kOutWarps = 8;            // rows in, results out: two groups of four warps
-constexpr int kThreads = 32 * (kOutWarps + 2);  // and one warp for the weights, one for the MMAs
+constexpr int kThreads = 32 * (kOutWarps + 3);  // and a warp each for weights, MMAs and rotary dims
+constexpr uint32_t kChange = 6;         // a change of rows, in items (see run_start)
 constexpr uint32_t kTmemCols = 512, kColA = 0, kColD = 256;
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr uint64_t kDrainNs = 10000000ull;
@@ -73,8 +74,8 @@ struct Params {
 
 struct __align__(1024) Smem {
   uint8_t w[kStages][kStage];
-  uint8_t out[2][2][kRows * 128];  // a result for each group: 64-dim halves of 128 rows, 128-byte swizzle
-  uint64_t w_full[kStages], w_empty[kStages], d_full[2], d_empty[2], a_full, fin;
+  uint8_t out[2][kRows * 128];  // half a result for each group: 64 dims of 128 rows, 128-byte swizzle
+  uint64_t w_full[kStages], w_empty[kStages], d_full[2], d_empty[2], group[2], a_full, fin;
   uint32_t tmem_base;
   int abort;
 };
@@ -124,27 +125,40 @@ __device__ __forceinline__ int64_t cache_row(const Params &p, int32_t t, int32_t
   return blk < 0 || row >= p.num_slots ? -2 : row;
 }
 
-// Half of 32 rows' latent dims (256 each) by a warp: from the cache, half a
-// warp per row and load so that every access is whole lines ...
+// Half of 32 rows' latent dims (256 each) by a warp: from the cache, a quarter
+// of a warp per row and load so that every access is a whole line ...
 template <bool kFp8>
 struct HalfRows {
-  static constexpr int kParts = kFp8 ? 1 : 2;  // of 256 bytes a row
-  uint4 v[kParts][16];
+  static constexpr int kParts = kFp8 ? 2 : 4;  // of 128 bytes a row
+  uint4 v[kParts][8];
 
   // `row`: the lane's own cache row (< 0: zeros)
   __device__ __forceinline__ void load(const Params &p, int64_t row, int half, int lane) {
-    const uint8_t *cache = static_cast<const uint8_t *>(p.cache) + half * kParts * 256 + (lane & 15) * 16;
+    const uint8_t *cache = static_cast<const uint8_t *>(p.cache) + half * kParts * 128 + (lane & 7) * 16;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int64_t r = __shfl_sync(0xffffffffu, row, 2 * i + (lane >> 4));
+    for (int i = 0; i < 8; ++i) {
+      const int64_t r = __shfl_sync(0xffffffffu, row, 4 * i + (lane >> 3));
 #pragma unroll
       for (int k = 0; k < kParts; ++k)
         v[k][i] = r < 0 ? make_uint4(0, 0, 0, 0)
-                        : *reinterpret_cast<const uint4 *>(cache + r * (kFp8 ? kRow : 2 * kRow) + k * 256);
+                        : *reinterpret_cast<const uint4 *>(cache + r * (kFp8 ? kRow : 2 * kRow) + k * 128);
     }
   }
 
-  // ... and through 8 KB of the warp's own shared memory (16-byte units
+  // (the same lines towards L2 only)
+  static __device__ __forceinline__ void prefetch(const Params &p, int64_t row, int half, int lane) {
+    constexpr int kLines = kFp8 ? 3 : 4;  // E4M3 rows start anywhere in a line
+    const uint8_t *cache = static_cast<const uint8_t *>(p.cache) + half * kParts * 128;
+#pragma unroll
+    for (int i = 0; i < kLines; ++i) {
+      const int64_t r = __shfl_sync(0xffffffffu, row, (lane + 32 * i) / kLines);
+      const int at = (lane + 32 * i) % kLines * 128;
+      if (r >= 0)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(cache + r * (kFp8 ? kRow : 2 * kRow) + min(at, kParts * 128 - 16)));
+    }
+  }
+
+  // ... and through 4 KB of the warp's own shared memory (16-byte units
   // swizzled by the row) into the tensor-memory lane of each row, E4M3 codes
   // as bf16.
   __device__ __forceinline__ void store(uint8_t *stage, uint32_t a_addr, int lane) const {
@@ -152,17 +166,17 @@ struct HalfRows {
     for (int k = 0; k < kParts; ++k) {
       __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int r = 2 * i + (lane >> 4);
-        *reinterpret_cast<uint4 *>(stage + r * 256 + (((lane & 15) ^ (r & 7)) << 4)) = v[k][i];
+      for (int i = 0; i < 8; ++i) {
+        const int r = 4 * i + (lane >> 3);
+        *reinterpret_cast<uint4 *>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4)) = v[k][i];
       }
       __syncwarp();
 #pragma unroll
-      for (int w0 = 0; w0 < 16; w0 += kFp8 ? 4 : 8) {  // 32 columns at a time
+      for (int w0 = 0; w0 < 8; w0 += kFp8 ? 4 : 8) {  // 32 columns at a time
         uint32_t a[32];
 #pragma unroll
         for (int w = 0; w < (kFp8 ? 4 : 8); ++w) {
-          const uint4 u = *reinterpret_cast<const uint4 *>(stage + lane * 256 + (((w0 + w) ^ (lane & 7)) << 4));
+          const uint4 u = *reinterpret_cast<const uint4 *>(stage + lane * 128 + (((w0 + w) ^ (lane & 7)) << 4));
           const uint32_t e[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -174,7 +188,7 @@ struct HalfRows {
             }
           }
         }
-        tmem_st32(a_addr + k * 64 + w0 * (kFp8 ? 8 : 4), a);
+        tmem_st32(a_addr + k * (kFp8 ? 64 : 32) + w0 * (kFp8 ? 8 : 4), a);
       }
     }
   }
@@ -185,14 +199,27 @@ struct HalfRows {
 template <bool kFp8>
 __device__ __forceinline__ void copy_rope(const Params &p, int64_t row, int32_t t, int lane) {
   const uint8_t *cache = static_cast<const uint8_t *>(p.cache) + kVDim * (kFp8 ? 1 : 2) + (lane & 7) * (kFp8 ? 8 : 16);
+  uint4 in[8];
+  int64_t r[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int at = 4 * i + (lane >> 3);
-    const int64_t r = __shfl_sync(0xffffffffu, row, at);
-    if (r < 0) continue;
-    uint4 o;
+    r[i] = __shfl_sync(0xffffffffu, row, 4 * i + (lane >> 3));
+    in[i] = make_uint4(0, 0, 0, 0);
+    if (r[i] < 0) continue;
     if (kFp8) {
-      const uint2 c = *reinterpret_cast<const uint2 *>(cache + r * kRow);
+      const uint2 c = *reinterpret_cast<const uint2 *>(cache + r[i] * kRow);
+      in[i].x = c.x;
+      in[i].y = c.y;
+    } else {
+      in[i] = *reinterpret_cast<const uint4 *>(cache + r[i] * 2 * kRow);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (r[i] < 0) continue;
+    uint4 o = in[i];
+    if (kFp8) {
+      const uint2 c = make_uint2(in[i].x, in[i].y);
       const uint32_t u[4] = {c.x & 0xffffu, c.x >> 16, c.y & 0xffffu, c.y >> 16};
       uint32_t e[4];
 #pragma unroll
@@ -202,10 +229,8 @@ __device__ __forceinline__ void copy_rope(const Params &p, int64_t row, int32_t 
         e[k] = pack2(f.x * p.kv_scale, f.y * p.kv_scale);
       }
       o = make_uint4(e[0], e[1], e[2], e[3]);
-    } else {
-      o = *reinterpret_cast<const uint4 *>(cache + r * 2 * kRow);
     }
-    reinterpret_cast<uint4 *>(p.k_pe + (int64_t)(t + at) * MLA_ROPE_DIM)[lane & 7] = o;
+    reinterpret_cast<uint4 *>(p.k_pe + (int64_t)(t + 4 * i + (lane >> 3)) * MLA_ROPE_DIM)[lane & 7] = o;
   }
 }
 
@@ -284,34 +309,46 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&s.d_full[i]), 1);
       mbar_init(smem_u32(&s.d_empty[i]), kRows);
+      mbar_init(smem_u32(&s.group[i]), kRows);
     }
     mbar_init(smem_u32(&s.a_full), 2 * kRows);
     mbar_init(smem_u32(&s.fin), 1);
     s.abort = 0;
     fence_mbarrier_init_cluster();
   }
-  // Launched as a programmatic dependent: what is above may run while the
-  // kernel before this one ends, what is below reads and writes memory.
-  griddep_wait();
-  griddep_launch_dependents();
-  if (blockIdx.x == 0)
-    ragged::check_offsets(p.kv_offsets, p.batch, p.total_kv, threadIdx.x, kThreads, p.dev_status);
   if (warp == 0) {
     tmem_alloc(smem_u32(&s.tmem_base), kTmemCols);
     tmem_relinquish();
   }
+  // Launched as a programmatic dependent: what is above may run while the
+  // kernel before this one ends, what is below reads and writes memory.
+  griddep_wait();
+  griddep_launch_dependents();
+  const int32_t rows_begin = ragged::cut(p.kv_offsets[0], p.total_kv), rows_end = ragged::cut(p.kv_offsets[p.batch], p.total_kv);
+  // This cluster's run of items [i0, i1): group i / per, head and kind i % per.
+  // The runs are equal in cost, in which a change of rows counts as kChange
+  // items (1,500 + 3,001 tokens of 128 heads took 107.6 us with 3, 103.8 with 8;
+  // 11,051 of 16 heads 41.0 with 3, 40.1 with 5, 42.1 with 8).  (Fewer than 2^30 rows in tiles of 128, 264 units each:
+  // 32 bits.)
+  const uint32_t clusters = gridDim.x / kCluster, c = blockIdx.x / kCluster, per = 2 * p.heads;
+  const uint32_t groups = (uint32_t)((rows_end + kCluster * kRows - 1) / (kCluster * kRows));
+  const uint32_t cost = groups == 0 ? 0 : groups * (per + kChange) - kChange;
+  auto run_start = [&](uint32_t k) -> uint32_t {  // of cluster k
+    const uint32_t at = cost / clusters * k + cost % clusters * k / clusters + kChange;
+    const uint32_t g = at / (per + kChange), in = at % (per + kChange);
+    return min(g * per + (in > kChange ? in - kChange : 0), groups * per);
+  };
+  const uint32_t i0 = run_start(c), i1 = run_start(c + 1);
+  // the first rows' places, while the barriers and the tensor memory are set up
+  int64_t first_row = -1;
+  if (warp < kOutWarps && i0 < i1)
+    first_row = cache_row(p, ((int32_t)(i0 / per) * kCluster + (int32_t)rank) * kRows + (warp & 3) * 32 + lane, rows_begin,
+                          rows_end);
   __syncwarp();
   tc_fence_before();
   cluster_sync<kCluster>();
   tc_fence_after();
   const uint32_t tmem = s.tmem_base;
-
-  // this cluster's run of items [i0, i1): group i / per, head and kind i % per
-  const int32_t clusters = gridDim.x / kCluster, c = blockIdx.x / kCluster;
-  const int32_t per = 2 * p.heads;
-  const int32_t rows_end = ragged::cut(p.kv_offsets[p.batch], p.total_kv);
-  const int64_t all = (int64_t)((rows_end + kCluster * kRows - 1) / (kCluster * kRows)) * per;
-  const int64_t i0 = all * c / clusters, i1 = all * (c + 1) / clusters;
 
   if (warp < kOutWarps) {
     // ------------------------------------------------ rows in, results out
@@ -320,35 +357,50 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
     const bool leader = (warp & 3) == 0 && lane == 0;
     const uint64_t hint = policy_stream();
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const int32_t rows_begin = ragged::cut(p.kv_offsets[0], p.total_kv);
-    int32_t item = 0, t0 = 0;
-    int64_t row = -1;
-    bool whole = false;  // every row of the tile (that the tensors have) is a request's
-    uint32_t n = 0;
-    for (int64_t i = i0; i < i1; ++i, ++n) {
-      if (i == i0 || ++item == per) {
-        const int32_t group = (int32_t)(i / per);
-        item = (int32_t)(i % per);
-        t0 = (group * kCluster + (int32_t)rank) * kRows;
-        row = cache_row(p, t0 + r, rows_begin, rows_end);
+    uint32_t syncs = 0;
+    // all four warps of the group are here (false: a wait gave up)
+    auto group_sync = [&]() -> bool {
+      mbar_arrive(smem_u32(&s.group[side]));
+      return warp_wait(s, p, s.group[side], syncs++ & 1);
+    };
+    // the tile of rows being multiplied: its first row, the lane's cache row,
+    // and whether every row of it (that the tensors have) is a request's
+    int32_t t0 = 0;
+    int64_t row = -1, next_row = -1;
+    bool whole = false;
+    uint32_t item = i0 % per;
+    // Item i of the run: its group's rows first, if they are new, then the
+    // result of the item before, so that at a change of rows the MMAs wait no
+    // longer than for them.
+    for (uint32_t i = i0, n = 0; i <= i1 && i0 < i1; ++i, ++n, item = item + 1 == per ? 0 : item + 1) {
+      const int32_t t = t0;
+      const int64_t own_row = row;
+      const bool store_whole = whole;
+      if (i < i1 && (n == 0 || item == 0)) {
+        t0 = ((int32_t)(i / per) * kCluster + (int32_t)rank) * kRows;
+        row = n == 0 ? first_row : next_row;
         if (row == -2 && side == 0) report(p.dev_status, MLA_ERR_DEVICE_RANGE);
         whole = t0 < p.total_kv && t0 >= rows_begin && min(t0 + kRows, p.total_kv) <= rows_end;
         HalfRows<kFp8> rows;
         rows.load(p, row, side, lane);
-        // the staging buffer is free once its last store has read it, the
-        // previous rows once the last product is complete
-        if (leader) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-        named_barrier_sync(1 + side, kRows);
-        if (n > 0 && !warp_wait(s, p, s.d_full[(n - 1) & 1], ((n - 1) >> 1) & 1)) break;
-        tc_fence_after();
-        rows.store(&s.out[side][0][0] + (warp & 3) * 8192, lanes + kColA + 128 * side, lane);
+        // the rows before are done with when the last product is complete, the
+        // staging buffer when its last store has read it
+        if (n > 0) {
+          if (leader) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          if (!group_sync() || !warp_wait(s, p, s.d_full[(n - 1) & 1], ((n - 1) >> 1) & 1)) break;
+          tc_fence_after();
+        }
+        rows.store(&s.out[side][0] + (warp & 3) * 4096, lanes + kColA + 128 * side, lane);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(smem_u32(&s.a_full));
-        if (item == 0 && side == 1) copy_rope<kFp8>(p, row, t0 + (warp & 3) * 32, lane);
+        if (i + per - item < i1) {  // the next group's rows towards L2 meanwhile
+          next_row = cache_row(p, t0 + kCluster * kRows + r, rows_begin, rows_end);
+          HalfRows<kFp8>::prefetch(p, next_row, side, lane);
+        }
       }
-      if ((n & 1) != (uint32_t)side) continue;  // the other group's
-      if (!warp_wait(s, p, s.d_full[side], (n >> 1) & 1)) break;
+      if (n == 0 || ((n - 1) & 1) != (uint32_t)side) continue;  // nothing yet, or the other group's
+      if (!warp_wait(s, p, s.d_full[side], ((n - 1) >> 1) & 1)) break;
       tc_fence_after();
       uint32_t d[kDims];
 #pragma unroll
@@ -357,36 +409,40 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
       tc_fence_before();
       mbar_arrive(smem_u32(&s.d_empty[side]));
       const float by = kFp8 ? p.kv_scale : 1.f;
-      uint4 o[kDims / 8];
+      const uint32_t done = (item == 0 ? per : item) - 1;  // the item before
+      const int h = (int)(done >> 1);
+      bool ok = true;
 #pragma unroll
-      for (int k = 0; k < kDims / 8; ++k) {
-        float x[8];
+      for (int half = 0; half < 2; ++half) {
+        uint4 o[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(d[8 * k + e]) * by;
-        o[k] = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
-      }
-      const int h = item >> 1;
-      if (whole) {
-        // the store that used this staging buffer two items ago has read it
-        if (leader) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-        named_barrier_sync(1 + side, kRows);
+        for (int k = 0; k < 8; ++k) {
+          float x[8];
 #pragma unroll
-        for (int k = 0; k < kDims / 8; ++k)
-          *reinterpret_cast<uint4 *>(&s.out[side][k >> 3][r * 128 + (((k & 7) ^ (r & 7)) << 4)]) = o[k];
-        fence_proxy_async_shared();
-        named_barrier_sync(1 + side, kRows);
-        if (leader) {
-          const CUtensorMap *m = item & 1 ? &maps.v : &maps.k_nope;
-          tma_store_3d(m, 0, h, t0, smem_u32(s.out[side][0]), hint);
-          tma_store_3d(m, 64, h, t0, smem_u32(s.out[side][1]), hint);
-          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(d[64 * half + 8 * k + e]) * by;
+          o[k] = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
         }
-      } else if (row != -1) {
-        uint4 *dst = reinterpret_cast<uint4 *>((item & 1 ? p.v : p.k_nope) +
-                                               ((int64_t)(t0 + r) * p.heads + h) * kDims);
+        if (store_whole) {
+          // the store that used the staging buffer before has read it
+          if (leader) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          if (!(ok = group_sync())) break;
 #pragma unroll
-        for (int k = 0; k < kDims / 8; ++k) dst[k] = o[k];
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<uint4 *>(&s.out[side][r * 128 + ((k ^ (r & 7)) << 4)]) = o[k];
+          fence_proxy_async_shared();
+          if (!(ok = group_sync())) break;
+          if (leader) {
+            tma_store_3d(done & 1 ? &maps.v : &maps.k_nope, 64 * half, h, t, smem_u32(s.out[side]), hint);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+        } else if (own_row != -1) {
+          uint4 *dst = reinterpret_cast<uint4 *>((done & 1 ? p.v : p.k_nope) +
+                                                 ((int64_t)(t + r) * p.heads + h) * kDims + 64 * half);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) dst[k] = o[k];
+        }
       }
+      if (!ok) break;
     }
     if (leader) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   } else if (warp == kOutWarps) {
@@ -403,9 +459,9 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
       uint32_t n = 0;
       bool ok = true;
       uint32_t st = 0, ph = 1;
-      int32_t item = (int32_t)(i0 % per);
-      for (int64_t i = i0; i < i1 && ok; ++i, item = item + 1 == per ? 0 : item + 1) {
-        const int32_t h = item >> 1;
+      uint32_t item = i0 % per;
+      for (uint32_t i = i0; i < i1 && ok; ++i, item = item + 1 == per ? 0 : item + 1) {
+        const int32_t h = (int32_t)(item >> 1);
         for (int kc = 0; kc < kKChunks; ++kc, ++n) {
           if (!(ok = wait_or_abort(s, p, s.w_empty[st], ph))) break;
           const uint32_t bar = smem_u32(&s.w_full[st]);
@@ -429,28 +485,25 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
         for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i)
           (void)mbar_wait(smem_u32(&s.w_full[i % kStages]), (i / kStages) & 1, nullptr, kDrainNs);
     }
-  } else {
+  } else if (warp == kOutWarps + 1) {
     // ------------------------------------------------ MMA issuer
     if (elect_one_sync()) {
-      const uint64_t d_k = smem_desc(smem_u32(s.w[0]), 16, 1024, kSwizzle128B);
-      const uint64_t d_v = smem_desc(smem_u32(s.w[0]), kStage / 2, 1024, kSwizzle128B);
+      const uint32_t d_k = desc_low(s.w[0], 16), d_v = desc_low(s.w[0], kStage / 2);
       uint32_t n = 0, st = 0, ph = 0, loads = 0;  // results, the ring's place and phase, row tiles
       // one item; keys and values differ in how K runs through a stage
       auto product = [&](auto is_value) -> bool {
         constexpr bool kValue = decltype(is_value)::value;
         constexpr uint32_t id = idesc_bf16_f32(kRows, kDims, kValue);
-        constexpr uint64_t kStep = kValue ? 128 : 2;  // 16 of K: 16 rows, or 32 bytes
+        constexpr uint32_t kStep = kValue ? 128 : 2;  // 16 of K: 16 rows, or 32 bytes
         const uint32_t d = tmem + kColD + 128 * (n & 1);
 #pragma unroll
         for (int kc = 0; kc < kKChunks; ++kc) {
           if (!wait_or_abort(s, p, s.w_full[st], ph)) return false;
           tc_fence_after();
-          const uint64_t b = (kValue ? d_v : d_k) + (uint64_t)(st * (kStage >> 4));
+          const uint32_t b = (kValue ? d_v : d_k) + st * (kStage >> 4);
           const uint32_t a = tmem + kColA + 32 * kc;
-          if (kc == 0) mma_ts(d, a, b, id, 0u);
-          else mma_ts_acc(d, a, b, id);
 #pragma unroll
-          for (int k = 1; k < 4; ++k) mma_ts_acc(d, a + 8 * k, b + kStep * k, id);
+          for (int k = 0; k < 4; ++k) mma_ts_low(d, a + 8 * k, b + kStep * k, id, (kc > 0 || k > 0) ? 1u : 0u);
           commit_all<kCluster>(smem_u32(&s.w_empty[st]));
           if (++st == kStages) {
             st = 0;
@@ -459,11 +512,11 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
         }
         return true;
       };
-      int32_t left = 0;  // items of the current group
+      uint32_t left = 0;  // items of the current group
       bool ok = true;
-      for (int64_t i = i0; i < i1 && ok; ++i, ++n, --left) {
+      for (uint32_t i = i0; i < i1 && ok; ++i, ++n, --left) {
         if (left == 0) {
-          left = per - (int32_t)(i % per);
+          left = per - i % per;
           if (!(ok = wait_or_abort(s, p, s.a_full, loads++ & 1))) break;
         }
         if (!(ok = wait_or_abort(s, p, s.d_empty[n & 1], ((n >> 1) & 1) ^ 1))) break;
@@ -474,6 +527,18 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
       mma_commit(smem_u32(&s.fin));
       if (!mbar_wait(smem_u32(&s.fin), 0, nullptr, kWaitNs)) report(p.dev_status, MLA_ERR_DEVICE_TIMEOUT);
     }
+  } else {
+    // ------------------------------------------------ rotary dims
+    // of the groups whose first item is in this run
+    for (uint32_t g = (i0 + per - 1) / per; g * per < i1; ++g) {
+      const int32_t t = ((int32_t)g * kCluster + (int32_t)rank) * kRows;
+      int64_t rows[kRows / 32];
+#pragma unroll
+      for (int q = 0; q < kRows / 32; ++q) rows[q] = cache_row(p, t + 32 * q + lane, rows_begin, rows_end);
+#pragma unroll
+      for (int q = 0; q < kRows / 32; ++q) copy_rope<kFp8>(p, rows[q], t + 32 * q, lane);
+    }
+    if (blockIdx.x == 0) ragged::check_offsets(p.kv_offsets, p.batch, p.total_kv, lane, 32, p.dev_status);
   }
   // no CTA leaves while another may still write into it or arrive at it
   __syncwarp();
@@ -547,8 +612,8 @@ cudaError_t launch(const Params &p, cudaStream_t stream) {
 
 mla_status_t run(Params p, int64_t num_blocks, int64_t total_kv, bool fp8, void *stream) {
   set_error_detail("");
-  if (p.batch < 0 || total_kv < 0 || total_kv > INT32_MAX - 1024)
-    return invalid("batch < 0, or total_kv outside [0, 2^31 - 1024)");
+  if (p.batch < 0 || total_kv < 0 || total_kv >= 1 << 30)
+    return invalid("batch < 0, or total_kv outside [0, 2^30)");
   p.total_kv = (int32_t)total_kv;
   if (p.block_size <= 0 || num_blocks <= 0 || num_blocks > INT32_MAX)
     return invalid("block_size and num_blocks must be > 0");

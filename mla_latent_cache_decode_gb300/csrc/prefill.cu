@@ -618,30 +618,6 @@ __device__ __forceinline__ void softmax_role(Smem &s, const Params &p, int warp,
 
 // ---------------------------------------------------------------- MMA issuer
 
-// An operand's descriptor is 64 bits, of which only the address field in the
-// low word changes: the MMAs here take low words and one constant high word (a
-// stride of 1,024 bytes between groups of eight rows, 128-byte swizzle), which
-// halves the address arithmetic and the registers of the issue loop.
-constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (kSwizzle128B << 29);
-__device__ __forceinline__ uint32_t desc_low(const void *p, uint32_t lbo_bytes) {
-  return (smem_u32(p) >> 4) | (lbo_bytes >> 4 << 16);
-}
-// D (+)= A B, A and B in shared memory; A in tensor memory.
-__device__ __forceinline__ void mma_ss_low(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t more) {
-  asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %4, 0;\n mov.b64 a, {%1, %5};\n mov.b64 b, {%2, %5};\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "r"(b), "r"(id), "r"(more), "n"(kDescHigh)
-      : "memory");
-}
-__device__ __forceinline__ void mma_ts_low(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t more) {
-  asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %4, 0;\n mov.b64 b, {%2, %5};\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "r"(b), "r"(id), "r"(more), "n"(kDescHigh)
-      : "memory");
-}
-
 // P V of a query tile's latest key tile, issued once its softmax is done.
 struct Pending {
   bool on, first, last, free_v;

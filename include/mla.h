@@ -463,7 +463,7 @@ mla_status_t mla_expand_kv_fp8(const void *cache8, int64_t num_blocks, int32_t b
  *                aligned, contents free: lets a call of few queries on long
  *                contexts spread the keys over the whole GPU.  Calls that
  *                share one must not overlap on the GPU
- * num_heads 1 to 128 (else MLA_ERR_UNSUPPORTED); total_q < 2^31, total_kv <=
+ * num_heads 1 to 128 (else MLA_ERR_UNSUPPORTED); total_q < 2^30, total_kv <=
  * 2^26.  The keys and values of a
  * request must be finite: a non-finite value row reaches, through a zero
  * weight, queries of its own request that do not see it.  What other rows

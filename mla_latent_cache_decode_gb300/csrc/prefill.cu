@@ -973,7 +973,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int4 a = p.parts[2 * blockIdx.x], b = p.parts[2 * blockIdx.x + 1];
   const int rows = a.x, parts = a.y, part = a.z, q0 = a.w, head = b.x, first = b.y, step = b.z;
-  if (rows == 0 || parts == 1) return;
+  // (offsets that overlap may ask for more parts than there are blocks)
+  if (rows == 0 || parts == 1 || first + (parts - 1) * step >= (int)gridDim.x) return;
   for (int r = part + warp * parts; r < rows; r += kJoinThreads / 32 * parts) {
     // lane i holds part i's log-sum-exp (parts come in groups of 32)
     float top = -INFINITY;
@@ -1088,8 +1089,8 @@ cudaError_t launch(void (*kernel)(P...), unsigned grid, unsigned threads, size_t
 
 mla_status_t run(const Args &a, void *workspace, size_t workspace_bytes, void *stream) {
   set_error_detail("");
-  if (a.batch < 0 || a.total_q < 0 || a.total_kv < 0 || a.total_q > INT32_MAX || a.total_kv > kMaxKv)
-    return invalid("batch < 0, total_q outside [0, 2^31) or total_kv outside [0, 2^26]");
+  if (a.batch < 0 || a.total_q < 0 || a.total_kv < 0 || a.total_q >= 1 << 30 || a.total_kv > kMaxKv)
+    return invalid("batch < 0, total_q outside [0, 2^30) or total_kv outside [0, 2^26]");
   if (a.heads < 1 || a.heads > kHeads) {
     set_error_detail("num_heads outside [1, 128]");
     return MLA_ERR_UNSUPPORTED;

@@ -372,6 +372,29 @@ def test_prefill_with_workspace(mla, q_lens, kv_lens, H, causal):
 
 
 @pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("q_lens,kv_lens,H", [([3, 100, 128, 129, 257, 40], [3, 350, 128, 129, 400, 20], 65), ([1] * 70, [5] * 70, 5),
+                                              ([200, 1, 64], [200, 130, 64], 128), ([90] * 40, [90, 300] * 20, 8)])
+def test_prefill_many_items(mla, q_lens, kv_lens, H, causal):
+    """Several items a block: heads in pairs (an odd head left over), more requests than a warp holds."""
+    c = prefill_case(np.random.default_rng(38), q_lens, kv_lens, H)
+    run_prefill(mla, c, causal=causal, ws=mla.make_prefill_workspace())
+    check_prefill(c, causal=causal)
+
+
+def test_prefill_overlapping_offsets_in_the_split_form(mla):
+    """Offsets that give every request all rows: more parts than blocks, reported, nothing out of place."""
+    c = prefill_case(np.random.default_rng(39), [4] * 30, [1000] * 30, 2)
+    ws, st = mla.make_prefill_workspace(), word()
+    bad = i32([0, 120] * 15 + [120])
+    mla.mla_prefill(c["qn"], c["qp"], c["kn"], c["kp"], c["v"], bad, i32([0, 30000] * 15 + [30000]), 0.07, c["out"], c["lse"], workspace=ws,
+                    dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st) == 5
+    run_prefill(mla, c, ws=ws)
+    check_prefill(c)
+
+
+@pytest.mark.parametrize("causal", [True, False])
 def test_prefill_rows_of_no_request_never_matter(mla, causal):
     """NaN in front of, behind and (as the neighbours' values) beside a request's rows."""
     c = prefill_case(np.random.default_rng(32), [100, 70, 140], [100, 131, 270], 2, q_start=5, kv_start=9, q_behind=77, kv_behind=300)
@@ -530,10 +553,11 @@ def test_prompt_then_decode(mla):
                         q_pe=q[..., 128:], q_pe_out=q_pe)
     Tk = sum(lens)
     k, v = (torch.empty(Tk, H, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
-    k_pe = torch.empty(Tk, 64, dtype=torch.bfloat16, device="cuda")
-    mla.mla_expand_kv(cache, i32(table), offsets(lens), w_uk, w_uv, k, v, k_pe)
+    k_pe, st = torch.empty(Tk, 64, dtype=torch.bfloat16, device="cuda"), word()
+    mla.mla_expand_kv(cache, i32(table), offsets(lens), w_uk, w_uv, k, v, k_pe, dev_status=st)
     out, lse = torch.empty(sum(new), H, 128, dtype=torch.bfloat16, device="cuda"), torch.empty(sum(new), H, device="cuda")
-    mla.mla_prefill(q[..., :128], q_pe, k, k_pe, v, offsets(new), offsets(lens), mi.SOFTMAX_SCALE, out, lse)
+    mla.mla_prefill(q[..., :128], q_pe, k, k_pe, v, offsets(new), offsets(lens), mi.SOFTMAX_SCALE, out, lse, dev_status=st)
+    assert int(st) == 0
     last = torch.tensor([new[0] - 1, sum(new) - 1], device="cuda")
     q_abs = torch.empty(2, H, 576, dtype=torch.bfloat16, device="cuda")
     mla.mla_absorb_q(q[last][..., :128].contiguous(), q_pe[last], w_uk, q_abs)

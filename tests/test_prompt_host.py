@@ -66,7 +66,7 @@ def expand(lib, fp8=False, **kw):
 
 
 @pytest.mark.parametrize("bad, status", [
-    (dict(batch=-1), 1), (dict(total=-1), 1), (dict(total=1 << 31), 1), (dict(block_size=0), 1), (dict(num_blocks=0), 1), (dict(width=0), 1),
+    (dict(batch=-1), 1), (dict(total=-1), 1), (dict(total=1 << 30), 1), (dict(block_size=0), 1), (dict(num_blocks=0), 1), (dict(width=0), 1),
     (dict(heads=0), 2), (dict(heads=129), 2), (dict(cache=None), 1), (dict(table=None), 1), (dict(offsets=None), 1), (dict(w_uk=None), 1),
     (dict(w_uv=None), 1), (dict(k=None), 1), (dict(v=None), 1), (dict(pe=None), 1), (dict(cache=A + 8), 1), (dict(w_uk=A + 2), 1),
     (dict(k=A + 8), 1), (dict(table=A + 2), 1), (dict(offsets=A + 1), 1)])
@@ -92,7 +92,7 @@ def prefill(lib, **kw):
 
 
 @pytest.mark.parametrize("bad, status", [
-    (dict(batch=-1), 1), (dict(tq=-1), 1), (dict(tk=-1), 1), (dict(tq=1 << 31), 1), (dict(tk=(1 << 26) + 1), 1), (dict(heads=0), 2),
+    (dict(batch=-1), 1), (dict(tq=-1), 1), (dict(tk=-1), 1), (dict(tq=1 << 30), 1), (dict(tk=(1 << 26) + 1), 1), (dict(heads=0), 2),
     (dict(heads=129), 2), (dict(causal=2), 1), (dict(scale=0.0), 1), (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1),
     (dict(scale=-1.0), 1), (dict(qn=None), 1), (dict(qp=None), 1), (dict(kn=None), 1), (dict(kp=None), 1), (dict(v=None), 1),
     (dict(qo=None), 1), (dict(ko=None), 1), (dict(out=None), 1), (dict(qn=A + 2), 1), (dict(kp=A + 8), 1), (dict(out=A + 8), 1),

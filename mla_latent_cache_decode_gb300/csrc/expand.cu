@@ -328,8 +328,8 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
   // This cluster's run of items [i0, i1): group i / per, head and kind i % per.
   // The runs are equal in cost, in which a change of rows counts as kChange
   // items (1,500 + 3,001 tokens of 128 heads took 107.6 us with 3, 103.8 with 8;
-  // 11,051 of 16 heads 41.0 with 3, 40.1 with 5, 42.1 with 8).  (Fewer than 2^30 rows in tiles of 128, 264 units each:
-  // 32 bits.)
+  // 11,051 of 16 heads 41.0 with 3, 40.1 with 5, 42.1 with 8).  32 bits hold the
+  // cost of all rows: less than 2^22 groups of 262 each.
   const uint32_t clusters = gridDim.x / kCluster, c = blockIdx.x / kCluster, per = 2 * p.heads;
   const uint32_t groups = (uint32_t)((rows_end + kCluster * kRows - 1) / (kCluster * kRows));
   const uint32_t cost = groups == 0 ? 0 : groups * (per + kChange) - kChange;
@@ -406,6 +406,8 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
 #pragma unroll
       for (int k = 0; k < kDims; k += 32) tmem_ld32(lanes + kColD + 128 * side + k, d + k);
       tmem_wait_ld();
+#pragma unroll
+      for (int k = 0; k < kDims; k += 32) tmem_loaded32(d + k);
       tc_fence_before();
       mbar_arrive(smem_u32(&s.d_empty[side]));
       const float by = kFp8 ? p.kv_scale : 1.f;

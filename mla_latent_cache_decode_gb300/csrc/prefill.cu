@@ -403,31 +403,52 @@ __device__ __forceinline__ void weights32(const float *x, float scale_log2, floa
 }
 
 // One key tile of one row: S from tensor memory, its maximum and the sum of the
-// weights, and the weights back over S as bf16.  `lim`: keys of this tile that
-// the row sees (may be <= 0 or >= 128).  The last 32 columns of S, which the
-// weights do not overwrite, are read twice: 96 values live at a time instead
-// of 128 leave the registers for the rest of the loop.
-__device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, float scale_log2, bool masked, int lim,
+// weights, and the weights back over S as bf16.  The row sees `lim` keys of the
+// tile (may be <= 0 or >= 128), the warp's rows at least `lo` and at most `hi`.
+//   kLong: straight-line code on registers.  The last chunk of S, which the
+//     weights do not overwrite, is read twice, so that 96 values live at a time
+//     leave the registers for the rest of the loop.
+//   else: loops over the four 32-key chunks, each read again for its weights, in
+//     a quarter of the code; chunks that no row sees are left out of the maximum.
+// The instruction cache decides: an item of few key tiles pays for its code, not
+// for its arithmetic (see use_long).
+template <bool kLong>
+__device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, float scale_log2, int lim, int lo, int hi,
                                              bool first, float &m, float &l) {
   float x[96];
   uint32_t *xr = reinterpret_cast<uint32_t *>(x);
-  tmem_ld32(s_addr + 96, xr + 64);
-  tmem_ld32(s_addr, xr);
-  tmem_ld32(s_addr + 32, xr + 32);
-  tmem_wait_ld();
-  if (masked) {
-    mask32(x + 64, 96, lim);
-    mask32(x, 0, lim);
-    mask32(x + 32, 32, lim);
-  }
   float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-  max32(x + 64, mx);
-  tmem_ld32(s_addr + 64, xr + 64);
-  max32(x, mx);
-  max32(x + 32, mx);
-  tmem_wait_ld();
-  if (masked) mask32(x + 64, 64, lim);
-  max32(x + 64, mx);
+  if (kLong) {
+    tmem_ld32(s_addr + 96, xr + 64);
+    tmem_ld32(s_addr, xr);
+    tmem_ld32(s_addr + 32, xr + 32);
+    tmem_wait_ld();
+    tmem_loaded32(xr);
+    tmem_loaded32(xr + 32);
+    tmem_loaded32(xr + 64);
+    if (lo < kTile) {
+      mask32(x + 64, 96, lim);
+      mask32(x, 0, lim);
+      mask32(x + 32, 32, lim);
+    }
+    max32(x + 64, mx);
+    tmem_ld32(s_addr + 64, xr + 64);
+    max32(x, mx);
+    max32(x + 32, mx);
+    tmem_wait_ld();
+    tmem_loaded32(xr + 64);
+    if (lo < kTile) mask32(x + 64, 64, lim);
+    max32(x + 64, mx);
+  } else {
+#pragma unroll 1
+    for (int c = 0; c < min(hi, kTile); c += 32) {
+      tmem_ld32(s_addr + c, xr);
+      tmem_wait_ld();
+      tmem_loaded32(xr);
+      if (lo < c + 32) mask32(x, 0, lim - c);
+      max32(x, mx);
+    }
+  }
   const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale_log2;
   const bool grow = top > m + kRescale || (m == -INFINITY && top > -INFINITY);
   if (__any_sync(0xffffffffu, grow)) {
@@ -440,6 +461,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, f
         uint32_t o[16];
         tmem_ld16(o_addr + c, o);
         tmem_wait_ld();
+        tmem_loaded16(o);
 #pragma unroll
         for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
         tmem_st16(o_addr + c, o);
@@ -448,13 +470,25 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, f
   }
   const float nm = m == -INFINITY ? 0.f : -m;  // a row that has seen nothing: every weight is 0
   float ps[4] = {0.f, 0.f, 0.f, 0.f};
-  weights32(x, scale_log2, nm, ps, s_addr);
-  tmem_ld32(s_addr + 96, xr);
-  weights32(x + 32, scale_log2, nm, ps, s_addr + 16);
-  weights32(x + 64, scale_log2, nm, ps, s_addr + 32);
-  tmem_wait_ld();
-  if (masked) mask32(x, 96, lim);
-  weights32(x, scale_log2, nm, ps, s_addr + 48);
+  if (kLong) {
+    weights32(x, scale_log2, nm, ps, s_addr);
+    tmem_ld32(s_addr + 96, xr);
+    weights32(x + 32, scale_log2, nm, ps, s_addr + 16);
+    weights32(x + 64, scale_log2, nm, ps, s_addr + 32);
+    tmem_wait_ld();
+    tmem_loaded32(xr);
+    if (lo < kTile) mask32(x, 96, lim);
+    weights32(x, scale_log2, nm, ps, s_addr + 48);
+  } else {
+#pragma unroll 1
+    for (int c = 0; c < kTile; c += 32) {
+      tmem_ld32(s_addr + c, xr);
+      tmem_wait_ld();
+      tmem_loaded32(xr);
+      if (lo < c + 32) mask32(x, 0, lim - c);
+      weights32(x, scale_log2, nm, ps, s_addr + c / 2);
+    }
+  }
   l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
 }
 
@@ -473,12 +507,32 @@ __device__ __forceinline__ void store16(__nv_bfloat16 *dst, const float *x, bool
   }
 }
 
+// A whole row of output: O / l.  Not inlined: the softmax loop around it needs
+// the registers.  A template, so that either kernel calls a copy of its own: with
+// one copy that both called, the kernel of the long form lost outputs.
+template <bool kLong>
+__device__ __noinline__ void store_out(uint32_t o, float inv, bool real, __nv_bfloat16 *out, bool wide) {
+#pragma unroll 1
+  for (int c = 0; c < kV; c += 32) {
+    float x[32];
+    uint32_t *xr = reinterpret_cast<uint32_t *>(x);
+    tmem_ld32(o + c, xr);
+    tmem_wait_ld();
+    tmem_loaded32(xr);
+    if (!real) continue;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) x[k] *= inv;
+    store16(out + c, x, wide);
+    store16(out + c + 16, x + 16, wide);
+  }
+}
+
 // Columns [c0, c1) of a row's output: a * O_a (+ b * O_b with `two`), to `out`
 // as bf16 or, for a part of the keys, to `partial` as fp32.  `any`: O holds
-// something.
-// (Not inlined: the softmax loop around it needs the registers.)
+// something.  Not inlined, and a template, like store_out.
+template <bool kLong>
 __device__ __noinline__ void store_row(uint32_t oa, float a, uint32_t ob, float b, bool two, bool any, int c0, int c1,
-                                          bool real, __nv_bfloat16 *out, bool wide, float *partial) {
+                                       bool real, __nv_bfloat16 *out, bool wide, float *partial) {
 #pragma unroll 1
   for (int c = c0; c < c1; c += 32) {
     float x[32];
@@ -486,6 +540,7 @@ __device__ __noinline__ void store_row(uint32_t oa, float a, uint32_t ob, float 
     if (any) {
       tmem_ld32(oa + c, xr);
       tmem_wait_ld();
+      tmem_loaded32(xr);
     }
 #pragma unroll
     for (int k = 0; k < 32; ++k) x[k] = a > 0.f ? x[k] * a : 0.f;
@@ -493,6 +548,7 @@ __device__ __noinline__ void store_row(uint32_t oa, float a, uint32_t ob, float 
       uint32_t y[32];
       tmem_ld32(ob + c, y);
       tmem_wait_ld();
+      tmem_loaded32(y);
 #pragma unroll
       for (int k = 0; k < 32; ++k) x[k] += b > 0.f ? __uint_as_float(y[k]) * b : 0.f;
     }
@@ -508,6 +564,7 @@ __device__ __noinline__ void store_row(uint32_t oa, float a, uint32_t ob, float 
   }
 }
 
+template <bool kLong>
 __device__ __forceinline__ void softmax_role(Smem &s, const Params &p, int warp, int lane, uint32_t tmem) {
   const int t = warp >> 2, q4 = warp & 3;
   const int row = q4 * 32 + lane;  // of the tile: TMEM lane
@@ -530,12 +587,12 @@ __device__ __forceinline__ void softmax_role(Smem &s, const Params &p, int warp,
       // on, the keys there are, and its number among all tiles loaded
       const int key = (w.kt + (w.mode == kOddEven ? t : 0)) * kTile;
       int lim = min(w.nk, p.causal ? w.see + at : w.nk) - key;
+      int lo = __reduce_min_sync(0xffffffffu, lim), hi = __reduce_max_sync(0xffffffffu, lim);
       const int step = w.mode == kOddEven ? 2 * kTile : kTile;
-      for (int j = 0; j < n; ++j, ++g, lim -= step) {
+      for (int j = 0; j < n; ++j, ++g, lim -= step, lo -= step, hi -= step) {
         if (!warp_wait(s, p, s.s_full[t], g & 1)) return;
         tc_fence_after();
-        softmax_tile(s_addr, s_addr + (kColO - kColS), p.scale_log2, __any_sync(0xffffffffu, lim < kTile), lim, j == 0, m,
-                     l);
+        softmax_tile<kLong>(s_addr, s_addr + (kColO - kColS), p.scale_log2, lim, lo, hi, j == 0, m, l);
         if (j == n - 1) {
           // A last key tile's P V reads value rows up to a multiple of 16: those
           // behind the request's last key hold anything (0 * NaN = NaN), so they
@@ -572,7 +629,10 @@ __device__ __forceinline__ void softmax_role(Smem &s, const Params &p, int warp,
         if (!warp_wait(s, p, s.o_full[t], (t ? outs1 : outs0) & 1)) return;
         tc_fence_after();
       }
-      store_row(s_addr + (kColO - kColS), l > 0.f ? 1.f / l : 0.f, 0, 0.f, false, n > 0, 0, kV, real, out, wide, partial);
+      if (n > 0 && !partial)
+        store_out<kLong>(s_addr + (kColO - kColS), l > 0.f ? 1.f / l : 0.f, real, out, wide);
+      else
+        store_row<kLong>(s_addr + (kColO - kColS), l > 0.f ? 1.f / l : 0.f, 0, 0.f, false, n > 0, 0, kV, real, out, wide, partial);
       if (real && lse) *lse = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
       tc_fence_before();
     } else {
@@ -601,7 +661,7 @@ __device__ __forceinline__ void softmax_role(Smem &s, const Params &p, int warp,
           (w.n[1] > 0 && !warp_wait(s, p, s.o_full[1], outs1 & 1)))
         return;
       tc_fence_after();
-      store_row(lanes + kColO, f.x, lanes + kColO + 128, f.y, w.n[1] > 0, w.n[0] > 0, 64 * t, 64 * t + 64, real, out,
+      store_row<kLong>(lanes + kColO, f.x, lanes + kColO + 128, f.y, w.n[1] > 0, w.n[0] > 0, 64 * t, 64 * t + 64, real, out,
                 wide, partial);
       tc_fence_before();
       // neither O nor the meeting place is reused before both have read it
@@ -877,6 +937,7 @@ __device__ __forceinline__ void schedule_role(Smem &s, const Params &p, int lane
   (void)publish(Work{});
 }
 
+template <bool kLong>
 __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ Maps maps, const Params p) {
   extern __shared__ uint8_t smem_raw[];
   Smem &s = *reinterpret_cast<Smem *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -932,7 +993,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 
   if (warp < kSoftmaxWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    softmax_role(s, p, warp, lane, tmem);
+    softmax_role<kLong>(s, p, warp, lane, tmem);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kSoftmaxWarps) {
@@ -1062,8 +1123,10 @@ cudaError_t prepare_device(int dev, int *sms) {
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   *sms = known[dev].load(std::memory_order_acquire);
   if (*sms > 0) return cudaSuccess;
-  cudaError_t e = cudaFuncSetAttribute(prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(prefill_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)sizeof(Smem) + 1024);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(prefill_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem) + 1024);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
   if (e == cudaSuccess) known[dev].store(*sms, std::memory_order_release);
   return e;
@@ -1086,6 +1149,13 @@ cudaError_t launch(void (*kernel)(P...), unsigned grid, unsigned threads, size_t
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
+
+// Which code the softmax runs, by the keys of a request in the mean (a causal
+// item sees about half of them).  Straight-line code against loops, in us, 128
+// heads: causal prompts of 1,024 tokens 54.1 / 51.2, 1,500 86.4 / 83.8, 2,048
+// 131.6 / 131.0, 8,192 1,640 / 1,710; every key visible 2,048 229 / 236; 700
+// tokens of 32 heads 51.9 / 53.0; prompts of 1, 17, 64 and 200 tokens 21.1 / 18.8.
+bool use_long(const Args &a) { return a.total_kv > (a.causal ? 2048 : 512) * (int64_t)a.batch; }
 
 mla_status_t run(const Args &a, void *workspace, size_t workspace_bytes, void *stream) {
   set_error_detail("");
@@ -1146,16 +1216,17 @@ mla_status_t run(const Args &a, void *workspace, size_t workspace_bytes, void *s
   if (most > INT32_MAX) return invalid("more than 2^31 tiles of 256 queries and a head");
   const cudaStream_t st = (cudaStream_t)stream;
   const int blocks = std::min(sms, kMaxParts);
+  const auto kernel = use_long(a) ? prefill_kernel<true> : prefill_kernel<false>;
   if (workspace && most <= blocks / 2) {  // see find_part
     p.partial = (float *)workspace;
     p.partial_lse = p.partial + (int64_t)blocks * 2 * kTile * kV;
     p.parts = (int4 *)(p.partial_lse + (int64_t)blocks * 2 * kTile);
-    e = launch(prefill_kernel, blocks, kThreads, sizeof(Smem) + 1024, st, maps, p);
+    e = launch(kernel, blocks, kThreads, sizeof(Smem) + 1024, st, maps, p);
     if (e == cudaSuccess) e = launch(join_kernel, blocks, kJoinThreads, 0, st, p);
   } else {
     // two rounds of items and more: halving their number costs no SM its work
     p.two_heads = most >= 2 * sms;
-    e = launch(prefill_kernel, (unsigned)most, kThreads, sizeof(Smem) + 1024, st, maps, p);
+    e = launch(kernel, (unsigned)most, kThreads, sizeof(Smem) + 1024, st, maps, p);
   }
   return e == cudaSuccess ? MLA_OK : cuda_failed(e);
 }

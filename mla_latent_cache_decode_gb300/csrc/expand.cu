@@ -32,7 +32,7 @@
 #include "common.cuh"
 #include "fp8.cuh"
 #include "ragged.cuh"
-#include "sm100.cuh"
+#include "sm100_issue.cuh"
 #include "tmap.h"
 #include "trace.h"
 

@@ -543,14 +543,14 @@ __device__ __noinline__ void store_row(uint32_t oa, float a, uint32_t ob, float 
       tmem_loaded32(xr);
     }
 #pragma unroll
-    for (int k = 0; k < 32; ++k) x[k] = a > 0.f ? x[k] * a : 0.f;
+    for (int k = 0; k < 32; ++k) x[k] = a != 0.f ? x[k] * a : 0.f;
     if (two) {
       uint32_t y[32];
       tmem_ld32(ob + c, y);
       tmem_wait_ld();
       tmem_loaded32(y);
 #pragma unroll
-      for (int k = 0; k < 32; ++k) x[k] += b > 0.f ? __uint_as_float(y[k]) * b : 0.f;
+      for (int k = 0; k < 32; ++k) x[k] += b != 0.f ? __uint_as_float(y[k]) * b : 0.f;
     }
     if (!real) continue;
     if (partial) {
@@ -615,7 +615,8 @@ __device__ __forceinline__ void softmax_role(Smem &s, const Params &p, int warp,
       }
     }
     vg += w.loads();
-    // ---- epilogue: O / l
+    // ---- epilogue: O / l.  A row that sees no key has l = 0; the NaN of a query
+    // that is not finite goes into its row of out and lse.
     const bool real = at < w.rows;
     const int64_t out_row = ((int64_t)w.q0 + at) * p.heads + w.h + (w.mode == kTwoHeads ? t : 0);
     __nv_bfloat16 *out = p.out + out_row * kV;
@@ -630,10 +631,11 @@ __device__ __forceinline__ void softmax_role(Smem &s, const Params &p, int warp,
         tc_fence_after();
       }
       if (n > 0 && !partial)
-        store_out<kLong>(s_addr + (kColO - kColS), l > 0.f ? 1.f / l : 0.f, real, out, wide);
+        store_out<kLong>(s_addr + (kColO - kColS), l != 0.f ? 1.f / l : 0.f, real, out, wide);
       else
-        store_row<kLong>(s_addr + (kColO - kColS), l > 0.f ? 1.f / l : 0.f, 0, 0.f, false, n > 0, 0, kV, real, out, wide, partial);
-      if (real && lse) *lse = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        store_row<kLong>(s_addr + (kColO - kColS), l != 0.f ? 1.f / l : 0.f, 0, 0.f, false, n > 0, 0, kV, real, out, wide,
+                         partial);
+      if (real && lse) *lse = l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
       tc_fence_before();
     } else {
       // tile 1 tells its maxima and sums, tile 0 answers with the factors of
@@ -648,14 +650,14 @@ __device__ __forceinline__ void softmax_role(Smem &s, const Params &p, int warp,
         if (!warp_wait(s, p, s.join_sums, joins & 1)) return;
         const float2 other = s.join[row];
         const float top = fmaxf(m, other.x);
-        f.x = l > 0.f ? ex2_approx(m - top) : 0.f;
-        f.y = other.y > 0.f ? ex2_approx(other.x - top) : 0.f;
-        const float sum = f.x * l + f.y * other.y, inv = sum > 0.f ? 1.f / sum : 0.f;
+        f.x = l != 0.f ? ex2_approx(m - top) : 0.f;
+        f.y = other.y != 0.f ? ex2_approx(other.x - top) : 0.f;
+        const float sum = f.x * l + f.y * other.y, inv = sum != 0.f ? 1.f / sum : 0.f;
         f.x *= inv;
         f.y *= inv;
         s.join[row] = f;
         mbar_arrive(smem_u32(&s.join_factors));
-        if (real && lse) *lse = sum > 0.f ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+        if (real && lse) *lse = sum != 0.f ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
       }
       if ((w.n[0] > 0 && !warp_wait(s, p, s.o_full[0], outs0 & 1)) ||
           (w.n[1] > 0 && !warp_wait(s, p, s.o_full[1], outs1 & 1)))
@@ -1039,12 +1041,17 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p) {
   for (int r = part + warp * parts; r < rows; r += kJoinThreads / 32 * parts) {
     // lane i holds part i's log-sum-exp (parts come in groups of 32)
     float top = -INFINITY;
-    for (int i = lane; i < parts; i += 32) top = fmaxf(top, p.partial_lse[(int64_t)(first + i * step) * 2 * kTile + r]);
+    bool any = false;  // a part saw a key, or is NaN
+    for (int i = lane; i < parts; i += 32) {
+      const float x = p.partial_lse[(int64_t)(first + i * step) * 2 * kTile + r];
+      top = fmaxf(top, x);
+      any |= x != -INFINITY;
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float sum = 0.f;
-    if (top > -INFINITY) {
+    if (__any_sync(0xffffffffu, any)) {
 #pragma unroll 4
       for (int i = 0; i < parts; ++i) {
         const int64_t at = (int64_t)(first + i * step) * 2 * kTile + r;
@@ -1057,10 +1064,10 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p) {
         o.w += f * x.w;
       }
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum != 0.f ? 1.f / sum : 0.f;
     const int64_t row = ((int64_t)q0 + r) * p.heads + head;
     reinterpret_cast<uint2 *>(p.out + row * kV)[lane] = make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv));
-    if (p.lse && lane == 0) p.lse[row] = sum > 0.f ? top + logf(sum) : -INFINITY;
+    if (p.lse && lane == 0) p.lse[row] = sum != 0.f ? top + logf(sum) : -INFINITY;
   }
 }
 

@@ -406,6 +406,23 @@ def test_prefill_rows_of_no_request_never_matter(mla, causal):
     check_prefill(c, causal=causal, only=(0, 2))
 
 
+@pytest.mark.parametrize("q_len,kv_len,H,split", [(200, 700, 2, False), (50, 700, 2, False), (50, 700, 2, True), (200, 2600, 2, True)])
+def test_prefill_query_that_is_not_finite(mla, q_len, kv_len, H, split):
+    """A query of NaN or infinity shows in its own rows of out and lse, and nowhere else."""
+    c = prefill_case(np.random.default_rng(41), [q_len], [kv_len], H)
+    c["qn"][17], c["qp"][33] = float("inf"), NAN
+    run_prefill(mla, c, ws=mla.make_prefill_workspace() if split else None)
+    for row in (17, 33):
+        assert torch.isnan(c["out"][row]).all() and torch.isnan(c["lse"][row]).all()
+    keep = [r for r in range(q_len) if r not in (17, 33)]
+    args = [f64(c[n]) for n in ("qn", "qp", "kn", "kp", "v")]
+    args[0][17], args[1][33] = 0, 0
+    out, lse, mag, size = op.attend(*args, float(np.float32(0.07)), True)
+    tol, lse_tol = attend_tol(out, lse, mag, size, kv_len)
+    assert_within(f64(c["out"])[keep], out[keep], tol[keep])
+    assert_within(f64(c["lse"])[keep], lse[keep], lse_tol[keep])
+
+
 def test_prefill_sharp_and_flat_scores(mla):
     """Scores of hundreds (one key takes all, maxima that keep rising) and of nearly nothing."""
     rng = np.random.default_rng(33)

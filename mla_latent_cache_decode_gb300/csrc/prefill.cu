@@ -258,10 +258,15 @@ __device__ __forceinline__ int32_t thin_tile(const Params &p, const Request &r) 
 // Item `at` in the order: requests (up to 32: longest context first), groups of
 // heads whose keys and values fit L2 together, tiles from the request's last
 // (the longest when causal) to its first, heads of the group.  By one warp;
-// rows = 0 behind the last.
-__device__ __forceinline__ Work find_work(const Params &p, const Request &few, int32_t at, int lane) {
-  int32_t before = 0;
-  for (int32_t b0 = 0; b0 < p.batch; b0 += 32) {
+// rows = 0 behind the last.  A walk over many requests resumes where the last
+// one ended: a block's items come in rising order.
+struct Walk {
+  int32_t b0, before;  // first of 32 requests, and the items of those before
+};
+__device__ __forceinline__ Work find_work(const Params &p, const Request &few, Walk &walk, int32_t at, int lane) {
+  if (at < walk.before) walk = Walk{0, 0};
+  int32_t &before = walk.before;
+  for (int32_t &b0 = walk.b0; b0 < p.batch; b0 += 32) {
     const Request mine = p.batch <= 32 ? few : request(p, b0 + lane);
     const int32_t thin = thin_tile(p, mine);
     const int32_t items = (mine.tiles - thin) * p.heads + thin * ((p.heads + 1) / 2);
@@ -930,9 +935,10 @@ __device__ __forceinline__ void schedule_role(Smem &s, const Params &p, int lane
   }
   Request few = {};
   if (p.batch <= 32) few = sorted(request(p, lane), p.batch, lane);
+  Walk walk = {0, 0};
   Claims claims;
   for (int32_t at = blockIdx.x; at >= 0; at = claims.next(s, p, lane)) {
-    const Work w = find_work(p, few, at, lane);
+    const Work w = find_work(p, few, walk, at, lane);
     if (w.rows == 0) continue;  // a block more than there are items brings none
     if (!publish(w) || !warp_wait(s, p, s.near_end, (i - 1) & 1)) return;
   }

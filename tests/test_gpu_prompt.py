@@ -406,6 +406,16 @@ def test_prefill_rows_of_no_request_never_matter(mla, causal):
     check_prefill(c, causal=causal, only=(0, 2))
 
 
+@pytest.mark.parametrize("q_len", [0, 1])
+def test_prefill_thousands_of_short_requests(mla, q_len):
+    """A block's items lie many groups of 32 requests apart (q_len 0: but the last request has none)."""
+    n = 3000
+    q_lens, kv_lens = [q_len] * (n - 1) + [3], [2] * (n - 1) + [70]
+    c = prefill_case(np.random.default_rng(42), q_lens, kv_lens, 3)
+    run_prefill(mla, c)
+    check_prefill(c)
+
+
 @pytest.mark.parametrize("q_len,kv_len,H,split", [(200, 700, 2, False), (50, 700, 2, False), (50, 700, 2, True), (200, 2600, 2, True)])
 def test_prefill_query_that_is_not_finite(mla, q_len, kv_len, H, split):
     """A query of NaN or infinity shows in its own rows of out and lse, and nowhere else."""

@@ -376,10 +376,12 @@ mla_status_t mla_decode_fp8_planned(const void *q, void *cache8, const void *kv_
  * num_tokens = 0 is a no-op; num_tokens < 2^27, block_size >= 1.
  *
  * mla_rope_append_fp8 — the same into an FP8 latent cache (uint8 [num_blocks,
- * block_size, 576], see below): each fp32 value x of the row is stored as the
- * E4M3 code nearest to x * fp32(1 / kv_scale), ties to even, saturating to
- * +-448; it is not rounded to bf16 on the way.  kv_scale and 1 / kv_scale must
- * be positive and finite.
+ * block_size, 576], see below): each value x of the row is stored as the E4M3
+ * code nearest to x * fp32(1 / kv_scale), ties to even, saturating to +-448.
+ * Neither x nor the product is rounded on the way (they are held to 2^-40 or
+ * better), but for an x that is an fp32 number: without a weight, or turned by
+ * no angle, a row has the codes that mla_cache_append_fp8 gives it.  kv_scale
+ * and 1 / kv_scale must be positive and finite.
  */
 mla_status_t mla_rope_append(const void *kv, int64_t kv_stride, const int64_t *positions,
                              const float *cos_sin, int64_t max_position,

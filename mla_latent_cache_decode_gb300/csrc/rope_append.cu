@@ -15,11 +15,21 @@
 // blocks.  A head is rotated by eight threads of 16 bytes (four of twice 16 for
 // pairs 32 apart): whole 128-byte lines, 64 bytes a thread in flight, the
 // cosines and sines kept over the job's heads.  The row's sum of squares is
-// taken in fp32 by warp shuffles.  Everything is computed in fp32 and rounded
-// once, to bf16 or to the nearest E4M3 code of x * (1 / kv_scale).
+// taken in fp32 by warp shuffles.  A bf16 row is computed in fp32 and rounded
+// once, to bf16.
 //
-// Measured at 8,191 tokens of 128 heads (290 MB): 44-45 us, 6.5 TB/s; of 16
-// heads (53 MB) 12.4 us.  Blocks of eight such jobs 47.5 us, jobs of 16 heads
+// An E4M3 row's codes are those of x * (1 / kv_scale) as if nothing had been
+// rounded before.  fp32 alone (off by at most 16 of its steps: 21 sums under a
+// root, the root, a reciprocal, three products) puts one value in a million,
+// next to the middle of two codes, on the wrong one, 6 to 12% off.  So a row
+// with a value within 32 steps of such a middle (one in 30) is computed again
+// in pairs of fp32, a value and what its rounding left off; the 64 rotary dims
+// always are.  In pairs throughout, 8,191 rows of one head took 13.4 us and of
+// 16 heads 16.9; so they take 8.5 and 12.5 (6.0 and 11.2
+// in fp32; of 128 heads 43.2 us either way).
+//
+// Measured at 8,191 tokens of 128 heads (290 MB), bf16: 44-45 us, 6.5 TB/s; of
+// 16 heads (53 MB) 11.7-12.4 us.  Blocks of eight such jobs 47.5 us, jobs of 16 heads
 // with pairs 32 apart 47.0 us, one block of 160 threads per token 16.4 us at
 // 16 heads.
 #include <cmath>
@@ -110,18 +120,112 @@ __device__ __forceinline__ void rotate_halves(float *x, float *y, const float *c
   }
 }
 
-// Stores eight elements of cache row `slot` from element e on.
-template <bool kFp8>
+// A value as the sum of two fp32: hi, rounded, and lo, what the rounding left
+// off.  (The _rn forms are never contracted or reordered.)
+struct Pair {
+  float hi, lo;
+};
+__device__ __forceinline__ Pair pair_add(Pair a, Pair b) {
+  const float t = __fadd_rn(a.hi, b.hi), u = __fsub_rn(t, a.hi);
+  const float e = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(t, u)), __fsub_rn(b.hi, u));
+  return Pair{t, __fadd_rn(e, __fadd_rn(a.lo, b.lo))};
+}
+__device__ __forceinline__ Pair pair_mul(Pair a, float b) {
+  const float t = __fmul_rn(a.hi, b);
+  return Pair{t, __fmaf_rn(a.lo, b, __fmaf_rn(a.hi, b, -t))};
+}
+// 1 / sqrt(m): one Newton step from the fp32 value, its residual 1 - m r^2 in pairs.
+__device__ __forceinline__ Pair pair_rsqrt(Pair m) {
+  const float r = 1.f / sqrtf(m.hi), rr = __fmul_rn(r, r), rest = __fmaf_rn(r, r, -rr);
+  const float e = __fmaf_rn(-m.hi, rr, 1.f) - m.hi * rest - m.lo * rr;
+  const float lo = 0.5f * r * e;
+  return Pair{r, isfinite(lo) ? lo : 0.f};
+}
+// In fp32, an inexact value as the odd one of its two neighbours: its rounding
+// to fewer bits is that of the exact value, a tie only where that is one.
+__device__ __forceinline__ float pair_to_odd(Pair a) {
+  const float hi = __fadd_rn(a.hi, a.lo), lo = __fsub_rn(a.lo, __fsub_rn(hi, a.hi));
+  const float side = hi * lo;  // > 0: hi is the neighbour nearer to zero
+  const int32_t bits = __float_as_int(hi);
+  if (!(fabsf(a.hi) < INFINITY)) return a.hi;
+  return __int_as_float(side > 0.f ? bits | 1 : side < 0.f ? (bits - 1) | 1 : bits);
+}
+
+// A value of the row scaled for its code.  One that fp32 holds exactly is scaled in
+// fp32, as mla_cache_append_fp8 scales it.
+__device__ __forceinline__ Pair scaled(Pair x, float by) {
+  Pair y = pair_mul(x, by);
+  if (x.lo == 0.f) y.lo = 0.f;
+  return y;
+}
+
+// Eight elements of a cache row from element e on.
 __device__ __forceinline__ void store8(const Params &p, int64_t slot, int e, const float *x) {
-  if (kFp8) {
-    uint32_t code[4];
+  *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.cache) + slot * kRow + e) = pack8(x);
+}
+__device__ __forceinline__ void store_codes8(const Params &p, int64_t slot, int e, const float *x) {
+  uint32_t code[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      code[i] = f32x2_to_e4m3x2(__fmul_rn(x[2 * i], p.inv_scale), __fmul_rn(x[2 * i + 1], p.inv_scale));
-    *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.cache) + slot * kRow + e) =
-        make_uint2(code[0] | (code[1] << 16), code[2] | (code[3] << 16));
+  for (int i = 0; i < 4; ++i) code[i] = f32x2_to_e4m3x2(x[2 * i], x[2 * i + 1]);
+  *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.cache) + slot * kRow + e) =
+      make_uint2(code[0] | (code[1] << 16), code[2] | (code[3] << 16));
+}
+
+// Whether x lies within 32 steps of fp32 of the middle between two codes: 20
+// bits below a code's last one.  Codes below 2^-6 are as far apart as those
+// above it.
+__device__ __forceinline__ bool near_middle(float x) {
+  const float a = fabsf(x);
+  return ((__float_as_uint(a < 0.015625f ? a + 0.015625f : a) + 0x80020u) & 0xfffffu) < 0x40u;
+}
+
+// The latent dims of an E4M3 row in pairs.  Not inlined: few rows come here.
+__device__ __noinline__ void store_latent_exactly(const Params &p, int64_t slot, int lane, const uint4 *row) {
+  float x0[8], x1[8], w0[8], w1[8];
+  unpack8(row[lane], x0);
+  unpack8(row[lane + 32], x1);
+  Pair part[8];  // (squares of bf16 are exact)
+#pragma unroll
+  for (int i = 0; i < 8; ++i) part[i] = pair_add(Pair{__fmul_rn(x0[i], x0[i]), 0.f}, Pair{__fmul_rn(x1[i], x1[i]), 0.f});
+#pragma unroll
+  for (int n = 4; n > 0; n >>= 1)
+#pragma unroll
+    for (int i = 0; i < n; ++i) part[i] = pair_add(part[i], part[i + n]);
+  Pair sum = part[0];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    sum = pair_add(sum, Pair{__shfl_xor_sync(0xffffffffu, sum.hi, o), __shfl_xor_sync(0xffffffffu, sum.lo, o)});
+  const Pair by = pair_mul(pair_rsqrt(pair_add(pair_mul(sum, 1.f / kVDim), Pair{p.eps, 0.f})), p.inv_scale);
+  const uint4 *weight = reinterpret_cast<const uint4 *>(p.norm_weight);
+  unpack8(__ldg(weight + lane), w0);
+  unpack8(__ldg(weight + lane + 32), w1);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x0[i] = pair_to_odd(pair_mul(pair_mul(by, w0[i]), x0[i]));
+    x1[i] = pair_to_odd(pair_mul(pair_mul(by, w1[i]), x1[i]));
+  }
+  store_codes8(p, slot, 8 * lane, x0);
+  store_codes8(p, slot, 256 + 8 * lane, x1);
+}
+
+// The rotary dims of an E4M3 row, pair `lane` of them: a c - b s and b c + a s,
+// always in pairs of fp32, because what cancels loses bits.
+template <bool kAdjacent>
+__device__ __forceinline__ void store_rotary_codes(const Params &p, int64_t slot, int lane, const __nv_bfloat16 *key,
+                                                   const float *angles) {
+  const int i = kAdjacent ? 2 * lane : lane, j = kAdjacent ? i + 1 : i + kHalf;
+  const float a = __bfloat162float(key[i]), b = __bfloat162float(key[j]);
+  const float c = __ldg(angles + lane), s = __ldg(angles + kHalf + lane);
+  auto turn = [&](float x, float y, float sine) -> Pair {
+    return scaled(pair_add(pair_mul(Pair{x, 0.f}, c), pair_mul(Pair{y, 0.f}, -sine)), p.inv_scale);
+  };
+  const uint32_t code = f32x2_to_e4m3x2(pair_to_odd(turn(a, b, s)), pair_to_odd(turn(b, a, -s)));
+  uint8_t *out = static_cast<uint8_t *>(p.cache) + slot * kRow + kVDim;
+  if (kAdjacent) {
+    *reinterpret_cast<uint16_t *>(out + i) = (uint16_t)code;
   } else {
-    *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.cache) + slot * kRow + e) = pack8(x);
+    out[i] = (uint8_t)code;
+    out[j] = (uint8_t)(code >> 8);
   }
 }
 
@@ -191,7 +295,9 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const Params p) {
   unpack8(row[lane], x0);
   unpack8(row[lane + 32], x1);
   constexpr int kRopeLanes = kAdjacent ? 8 : 4;
-  if (lane < kRopeLanes) {
+  if (kFp8) {
+    store_rotary_codes<kAdjacent>(p, slot, lane, reinterpret_cast<const __nv_bfloat16 *>(row + 64), angles);
+  } else if (lane < kRopeLanes) {
     unpack8(row[64 + lane], y0);
     if (!kAdjacent) unpack8(row[68 + lane], y1);
   }
@@ -212,18 +318,34 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const Params p) {
       x1[i] = x1[i] * r * w1[i];
     }
   }
-  store8<kFp8>(p, slot, 8 * lane, x0);
-  store8<kFp8>(p, slot, 256 + 8 * lane, x1);
+  if (kFp8) {
+    bool near = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x0[i] = __fmul_rn(x0[i], p.inv_scale);
+      x1[i] = __fmul_rn(x1[i], p.inv_scale);
+      near |= near_middle(x0[i]) || near_middle(x1[i]);
+    }
+    if (p.norm_weight && __any_sync(0xffffffffu, near)) {
+      store_latent_exactly(p, slot, lane, row);
+      return;
+    }
+    store_codes8(p, slot, 8 * lane, x0);
+    store_codes8(p, slot, 256 + 8 * lane, x1);
+    return;
+  }
+  store8(p, slot, 8 * lane, x0);
+  store8(p, slot, 256 + 8 * lane, x1);
   if (lane < kRopeLanes) {
     float c[8], s[8];
     load_angles<kAdjacent ? 4 : 8>(angles, (kAdjacent ? 4 : 8) * lane, c, s);
     if (kAdjacent) {
       rotate_adjacent(y0, c, s);
-      store8<kFp8>(p, slot, kVDim + 8 * lane, y0);
+      store8(p, slot, kVDim + 8 * lane, y0);
     } else {
       rotate_halves(y0, y1, c, s);
-      store8<kFp8>(p, slot, kVDim + 8 * lane, y0);
-      store8<kFp8>(p, slot, kVDim + kHalf + 8 * lane, y1);
+      store8(p, slot, kVDim + 8 * lane, y0);
+      store8(p, slot, kVDim + kHalf + 8 * lane, y1);
     }
   }
 }

@@ -111,6 +111,29 @@ def test_append_e4m3(mla, T, H, scale, interleaved):
     assert_within(f64(out), q, q_tol, "q")
 
 
+def e4m3_nearest(x):
+    """The E4M3 value nearest to x (fp64), ties to even."""
+    step = 2.0 ** (np.floor(np.log2(np.maximum(np.abs(x), 2.0 ** -6))) - 3)
+    return np.clip(np.round(x / step) * step, -448, 448)
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
+def test_append_e4m3_codes_are_those_of_the_exact_values(mla, interleaved):
+    """Next to the middle of two codes fp32 would take the wrong one of one value in a million."""
+    rng = np.random.default_rng(14)
+    T = 16000
+    c = append_case(rng, T, 1)
+    c["table"][0] = torch.cat([torch.ones(32), torch.zeros(32)]).cuda()
+    cache = torch.zeros(T // 64, 64, 576, dtype=torch.uint8, device="cuda")
+    mla.mla_rope_append_fp8(c["kv"], c["positions"], c["table"], torch.arange(T, device="cuda"), cache, kv_scale=0.037, norm_weight=c["weight"],
+                            interleaved=interleaved)
+    rows = append_ref(c, interleaved)[0]
+    rows *= float(np.float32(1) / np.float32(0.037))
+    turned = c["positions"].cpu().numpy() != 0  # (x itself is scaled in fp32)
+    got = cache.view(torch.float8_e4m3fn).double().cpu().numpy().reshape(T, 576)
+    assert np.array_equal(got[turned], e4m3_nearest(rows[turned]))
+
+
 def test_append_without_query_equals_finished_rows(mla):
     """No weight and position 0 (cos 1, sin 0): what mla_cache_append(_fp8) stores, bit for bit."""
     rng = np.random.default_rng(5)
@@ -181,8 +204,15 @@ def test_append_zero_rows_and_special_values(mla):
     cache = torch.zeros(1, 16, 576, dtype=torch.bfloat16, device="cuda")
     mla.mla_rope_append(c["kv"], c["positions"], c["table"], torch.arange(4, device="cuda"), cache, norm_weight=c["weight"])
     got = f64(cache)[0]
-    rows, tol, _, _ = append_ref(c, True)
+    with np.errstate(invalid="ignore"):
+        rows, tol, _, _ = append_ref(c, True)
     assert (got[1] == 0).all() and np.isnan(got[2]).any()
+    # E4M3: an infinity saturates, where the rotation or a row without a weight keeps it one
+    codes = torch.zeros(1, 16, 576, dtype=torch.uint8, device="cuda")
+    c["kv"][3], c["kv"][3, 7], c["kv"][3, 530] = 1, -float("inf"), float("inf")
+    mla.mla_rope_append_fp8(c["kv"], c["positions"], c["table"], torch.arange(len(c["kv"]), device="cuda"), codes, kv_scale=0.25)
+    val = codes.view(torch.float8_e4m3fn).float().cpu().numpy()[0]
+    assert val[3, 7] == -448 and (val[3, :7] == 4).all() and set(np.abs(val[3, 530:532])) == {448.0} and np.isnan(val[2, 520])
     assert_within(got[[0, 3]], rows[[0, 3]], (BF16 * np.abs(rows) + tol)[[0, 3]])
 
 

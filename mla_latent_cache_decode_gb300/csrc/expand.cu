@@ -12,8 +12,8 @@
 // cores from about 300 tokens on (below, by the 256 KB a head of weights).
 //
 // A CTA keeps 128 output rows: their 512 latent dims sit in tensor memory as
-// the A operand (256 columns), gathered from the pages once, one thread per
-// row (so any page size and request boundary will do, and E4M3 codes are
+// the A operand (256 columns), gathered from the pages once (each row looked up
+// by itself, so any page size and request boundary will do, and E4M3 codes are
 // widened to bf16, exactly, on the way), and every head's weights stream past
 // through a ring of 16 KB stages (128 output dims x 64 of K).  A from tensor
 // memory leaves shared memory's bandwidth to the weights.  A cluster of
@@ -25,6 +25,16 @@
 //
 // An item is one head's keys or values of a group of kCluster x 128 rows; the
 // items (group by group, head by head) are cut into equal runs, one a cluster.
+//
+// Measured: 8,192 tokens of 128 heads 182-201 us (1.48-1.37 PFLOP/s, 78-72% of
+// the measured bf16 rate; the slower in a row of calls, when the GPU's power
+// limit holds the clock near 1.9 GHz), 4,501 tokens from E4M3 104-109 us, 11,051
+// of 16 heads 40-42 us, 286 of 128 heads 21 us (53 MB: 8). The tensor cores are busy 71% of an SM's cycles; what is left are the start (a cluster's
+// rows are found and gathered and the first weights come from memory before the
+// first MMA) and the changes of rows. Clusters of four were slower, so were pairs
+// of CTAs that share each MMA, half of B in each (223 us against 200: half the
+// traffic into shared memory, which is not the bound), and more registers for
+// the output warps changed nothing (198 against 200, 42.0 against 42.0).
 #include <atomic>
 #include <cmath>
 #include <type_traits>

@@ -418,10 +418,9 @@ mla_status_t mla_rope_append_fp8(const void *kv, int64_t kv_stride, const int64_
  *                last are left as they are
  *   w_uk bf16 [num_heads, 128, 512]   w_uv bf16 [num_heads, 512, 128]
  *   k_nope, v    bf16 [total_kv, num_heads, 128]   k_pe bf16 [total_kv, 64]
- * num_heads 1 to 128 (else MLA_ERR_UNSUPPORTED); total_kv < 2^30.  A
- * token whose page lies
- * outside the table or the pool is reported as MLA_ERR_DEVICE_RANGE and its
- * rows are unspecified.
+ * num_heads 1 to 128 (else MLA_ERR_UNSUPPORTED); total_kv < 2^30.  A token
+ * whose page lies outside the table or the pool is reported as
+ * MLA_ERR_DEVICE_RANGE and its rows are unspecified.
  *
  * mla_expand_kv_fp8 — the same from an FP8 latent cache: the elements are
  * value(code) * kv_scale.  The products run on the codes' values and kv_scale
@@ -466,10 +465,14 @@ mla_status_t mla_expand_kv_fp8(const void *cache8, int64_t num_blocks, int32_t b
  *                contexts spread the keys over the whole GPU.  Calls that
  *                share one must not overlap on the GPU
  * num_heads 1 to 128 (else MLA_ERR_UNSUPPORTED); total_q < 2^30, total_kv <=
- * 2^26.  The keys and values of a
- * request must be finite: a non-finite value row reaches, through a zero
- * weight, queries of its own request that do not see it.  What other rows
- * hold never matters.
+ * 2^26.  The values of a request must be finite: a non-finite value row
+ * reaches, through a zero weight, queries of its own request that do not see
+ * it.  A key that is not finite reaches those that see it, a query its own row
+ * of out and lse (NaN).  What other rows hold never matters.
+ *
+ * Launch order: mla_rope_append, mla_expand_kv, mla_prefill and their FP8 forms
+ * are programmatic dependents of the kernel before them (see mla_decode): they
+ * wait for it to complete before they touch memory.
  */
 size_t mla_prefill_workspace_size(void);
 mla_status_t mla_prefill(const void *q_nope, int64_t q_nope_token_stride,

@@ -8,7 +8,8 @@ kernels; there is no other implementation to fall back to: the first call
 raises ImportError if the compiled library is missing.
 
 Functions carry the C names: mla_cache_append, mla_decode_plan, mla_decode,
-mla_decode_planned, mla_combine, mla_decode_workspace_size.
+mla_decode_planned, mla_combine, mla_decode_workspace_size; of the prompt side
+mla_rope_append, mla_expand_kv, mla_prefill.
 """
 from __future__ import annotations
 

@@ -29,12 +29,16 @@
 // Measured: 8,192 tokens of 128 heads 182-201 us (1.48-1.37 PFLOP/s, 78-72% of
 // the measured bf16 rate; the slower in a row of calls, when the GPU's power
 // limit holds the clock near 1.9 GHz), 4,501 tokens from E4M3 104-109 us, 11,051
-// of 16 heads 40-42 us, 286 of 128 heads 21 us (53 MB: 8). The tensor cores are busy 71% of an SM's cycles; what is left are the start (a cluster's
-// rows are found and gathered and the first weights come from memory before the
-// first MMA) and the changes of rows. Clusters of four were slower, so were pairs
-// of CTAs that share each MMA, half of B in each (223 us against 200: half the
-// traffic into shared memory, which is not the bound), and more registers for
-// the output warps changed nothing (198 against 200, 42.0 against 42.0).
+// of 16 heads 40-43 us, 286 of 128 heads 21-22 us (53 MB: 8).  The tensor cores
+// are busy 69% of an SM's cycles.  Without its weights' way in, the first takes
+// 141 us, without its results' way out 153, without both 131: each of the two
+// makes the MMAs wait somewhat, the weights by the latency that 192 KB in flight
+// have to cover (11 stages instead of 12: 185 us, and 45.7 instead of 43.0 with
+// 16 heads; stages of 32 KB: no change).  Slower were clusters of four; pairs of
+// CTAs that share each MMA, half of B in each (223 us against 200: at 128 columns
+// the shared MMA itself is slower, 173 us without weights); results stored from
+// registers instead of by TMA (259).  More registers for the output warps changed
+// nothing (198 against 200, 42.0 against 42.0).
 #include <atomic>
 #include <cmath>
 #include <type_traits>

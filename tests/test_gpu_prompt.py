@@ -463,6 +463,22 @@ def test_prefill_query_that_is_not_finite(mla, q_len, kv_len, H, split):
     assert_within(f64(c["lse"])[keep], lse[keep], lse_tol[keep])
 
 
+@pytest.mark.parametrize("q_len,split", [(300, False), (100, False), (100, True)])
+def test_prefill_key_that_is_not_finite_is_masked(mla, q_len, split):
+    """Causal: queries before such a key do not notice it, those that see it give NaN."""
+    c = prefill_case(np.random.default_rng(43), [q_len], [700], 2)
+    at = 700 - q_len + 40
+    c["kn"][at], c["kp"][at + 2] = NAN, float("inf")
+    run_prefill(mla, c, ws=mla.make_prefill_workspace() if split else None)
+    args = [f64(c[n]) for n in ("qn", "qp", "kn", "kp", "v")]
+    args[2][at], args[3][at + 2] = 0, 0
+    out, lse, mag, size = op.attend(*args, float(np.float32(0.07)), True)
+    tol, lse_tol = attend_tol(out, lse, mag, size, 700)
+    assert_within(f64(c["out"])[:40], out[:40], tol[:40])
+    assert_within(f64(c["lse"])[:40], lse[:40], lse_tol[:40])
+    assert torch.isnan(c["out"][40:]).all() and torch.isnan(c["lse"][40:]).all()
+
+
 def test_prefill_sharp_and_flat_scores(mla):
     """Scores of hundreds (one key takes all, maxima that keep rising) and of nearly nothing."""
     rng = np.random.default_rng(33)

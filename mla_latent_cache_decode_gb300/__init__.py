@@ -413,12 +413,12 @@ def _decode_fp8(fn, kv_new, q, cache8, block_table, seq_lens, softmax_scale, out
 
 
 def _strides(t, row):
-    """Element strides of t's outer dims; a dim of one entry, whose stride says
-    nothing, gets that of a dense tensor with rows of `row` elements."""
-    dense = [row]
-    for n in reversed(t.shape[1:-1]):
-        dense.insert(0, dense[0] * n)
-    return [d if n == 1 else st for n, st, d in zip(t.shape[:-1], t.stride(), dense)]
+    """Element strides of the outer dims of [tokens, row] or [tokens, heads, row]; a dim of one
+    entry, whose stride says nothing, gets that of a dense tensor."""
+    shape, st = t.shape, t.stride()
+    if len(shape) == 2:
+        return [st[0] if shape[0] != 1 else row]
+    return [st[0] if shape[0] != 1 else shape[1] * row, st[1] if shape[1] != 1 else row]
 
 
 def _refuse(t, dtype, shape, dev, name):
@@ -445,12 +445,9 @@ def _rows(t, dtype, shape, dev, name):
     """t's address and outer strides, once it holds rows of contiguous elements of this type and
     shape on the current device."""
     try:
-        if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
-            st = t.stride()
-            if st[-1] == 1:
-                if 1 in shape[:-1]:
-                    st = _strides(t, shape[-1])
-                return (t.data_ptr(), *st[:len(shape) - 1])
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == dev
+                and t.stride(-1) == 1):
+            return (t.data_ptr(), *_strides(t, shape[-1]))
     except AttributeError:
         pass
     _refuse(t, dtype, shape, dev, name)
@@ -458,12 +455,18 @@ def _rows(t, dtype, shape, dev, name):
 
 def _shape(t, ndim, name):
     """t's shape, once it is a tensor of ndim dims."""
+    try:
+        if t.dim() == ndim:
+            return t.shape
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
+    raise ValueError(f"{name}: need {ndim} dims, got {tuple(t.shape)}")
+
+
+def _stream_of(stream, dev):
+    """_stream for a call on tensors of the current device."""
     import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != ndim:
-        raise ValueError(f"{name}: need {ndim} dims, got {tuple(t.shape)}")
-    return t.shape
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def _current(t, name):
@@ -471,7 +474,7 @@ def _current(t, name):
     import torch
     if not t.is_cuda:
         raise ValueError(f"{name}: need a CUDA tensor, got one on {t.device}")
-    return torch.cuda.current_device()
+    return torch._C._cuda_getDevice()  # torch.cuda.current_device() without its check for a start
 
 
 def _status_word(dev_status, dev):
@@ -506,7 +509,7 @@ def _rope_append(fn, cache_dtype, scale, kv, positions, cos_sin, slot_mapping, c
               else _dense(norm_weight, bf16, (KV_LORA_RANK,), dev, "norm_weight"),
               eps, 1 if interleaved else 0, _dense(cache, cache_dtype, (NB, BS, ROW_DIM), dev, "cache"),
               NB, BS, *scale, *q_args, *out_args, heads, _status_word(dev_status, dev),
-              _stream(stream)))
+              _stream_of(stream, dev)))
 
 
 def mla_rope_append(kv, positions, cos_sin, slot_mapping, cache, norm_weight=None, eps=1e-6,
@@ -547,7 +550,7 @@ def _expand_kv(fn, cache_dtype, scale, cache, block_table, kv_offsets, w_uk, w_u
               _dense(w_uv, bf16, (H, KV_LORA_RANK, 128), dev, "w_uv"), H, *scale,
               _dense(k_nope, bf16, (T, H, 128), dev, "k_nope"), _dense(v, bf16, (T, H, 128), dev, "v"),
               _dense(k_pe, bf16, (T, ROPE_DIM), dev, "k_pe"), _status_word(dev_status, dev),
-              _stream(stream)))
+              _stream_of(stream, dev)))
     return k_nope, v, k_pe
 
 
@@ -604,7 +607,7 @@ def mla_prefill(q_nope, q_pe, k_nope, k_pe, v, q_offsets, kv_offsets, softmax_sc
         _dense(kv_offsets, i32, (B + 1,), dev, "kv_offsets"), B, Tq, Tk, H, 1 if causal else 0,
         softmax_scale, _dense(out, bf16, (Tq, H, 128), dev, "out"),
         None if lse is None else _dense(lse, torch.float32, (Tq, H), dev, "lse"), ws, nbytes or 0,
-        _status_word(dev_status, dev), _stream(stream)))
+        _status_word(dev_status, dev), _stream_of(stream, dev)))
     return out
 
 

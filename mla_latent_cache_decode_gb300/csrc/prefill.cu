@@ -439,12 +439,13 @@ __device__ __forceinline__ void weights32(const float *x, float scale_log2, floa
 //     weights do not overwrite, is read twice, so that 96 values live at a time
 //     leave the registers for the rest of the loop.
 //   else: loops over the four 32-key chunks, each read again for its weights, in
-//     a quarter of the code; chunks that no row sees are left out of the maximum.
+//     a quarter of the code; chunks that no row sees are left out of the maximum,
+//     those behind the request's last key (`keys` are there) altogether.
 // The instruction cache decides: an item of few key tiles pays for its code, not
 // for its arithmetic (see use_long).
 template <bool kLong>
-__device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, float scale_log2, int lim, int lo, int hi,
-                                             bool first, float &m, float &l) {
+__device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, float scale_log2, int keys, int lim, int lo,
+                                             int hi, bool first, float &m, float &l) {
   float x[96];
   uint32_t *xr = reinterpret_cast<uint32_t *>(x);
   float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -511,7 +512,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, f
     weights32(x, scale_log2, nm, ps, s_addr + 48);
   } else {
 #pragma unroll 1
-    for (int c = 0; c < kTile; c += 32) {
+    for (int c = 0; c < min(keys, kTile); c += 32) {
       tmem_ld32(s_addr + c, xr);
       tmem_wait_ld();
       tmem_loaded32(xr);
@@ -622,7 +623,7 @@ __device__ __forceinline__ void softmax_role(Smem &s, const Params &p, int warp,
       for (int j = 0; j < n; ++j, ++g, lim -= step, lo -= step, hi -= step) {
         if (!warp_wait(s, p, s.s_full[t], g & 1)) return;
         tc_fence_after();
-        softmax_tile<kLong>(s_addr, s_addr + (kColO - kColS), p.scale_log2, lim, lo, hi, j == 0, m, l);
+        softmax_tile<kLong>(s_addr, s_addr + (kColO - kColS), p.scale_log2, w.nk - key - j * step, lim, lo, hi, j == 0, m, l);
         if (j == n - 1) {
           // A last key tile's P V reads value rows up to a multiple of 16: those
           // behind the request's last key hold anything (0 * NaN = NaN), so they

@@ -926,7 +926,11 @@ struct Claims {
           "r"(smem_u32(&s.claim_full))
           : "memory");
     }
-    if (!warp_wait(s, p, s.claim_full, phase)) return -1;
+    if (!warp_wait(s, p, s.claim_full, phase)) {
+      // the answer must not still be landing when the shared memory is given up
+      (void)mbar_wait(smem_u32(&s.claim_full), phase, nullptr, kDrainNs);
+      return -1;
+    }
     phase ^= 1;
     uint64_t a0, a1;
     asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(a0), "=l"(a1) : "r"(smem_u32(&s.claim)) : "memory");
@@ -1195,7 +1199,8 @@ cudaError_t launch(void (*kernel)(P...), unsigned grid, unsigned threads, size_t
 // item sees about half of them).  Straight-line code against loops, in us, 128
 // heads: causal prompts of 1,024 tokens 54.1 / 51.2, 1,500 86.4 / 83.8, 2,048
 // 131.6 / 131.0, 8,192 1,640 / 1,710; every key visible 2,048 229 / 236; 700
-// tokens of 32 heads 51.9 / 53.0; prompts of 1, 17, 64 and 200 tokens 21.1 / 18.8.
+// tokens of 32 heads 51.9 / 53.0; prompts of 1, 17, 64 and 200 tokens 21.1 / 18.8
+// (17.5 since the loops end with the keys).
 bool use_long(const Args &a) { return a.total_kv > (a.causal ? 2048 : 512) * (int64_t)a.batch; }
 
 mla_status_t run(const Args &a, void *workspace, size_t workspace_bytes, void *stream) {

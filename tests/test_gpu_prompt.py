@@ -312,6 +312,17 @@ def test_expand_reports_pages_outside(mla, fp8):
     assert int(st) == 5
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_expand_thousands_of_short_requests(mla, fp8):
+    """More requests than are compared one by one, every fourth of them empty, the first and the last too."""
+    lens = [0, 1, 2, 3] * 400 + [0]
+    c = expand_case(np.random.default_rng(25), lens, 2, 2, fp8)
+    st = word()
+    run_expand(mla, c, 0.37 if fp8 else None, dev_status=st)
+    assert int(st) == 0
+    check_expand(c, 0.37 if fp8 else 1.0)
+
+
 def test_expand_offsets_beyond_the_rows_are_cut(mla):
     c = expand_case(np.random.default_rng(24), [40, 20], 2, 16)
     c["offsets"] = i32([-3, 40, 1000])

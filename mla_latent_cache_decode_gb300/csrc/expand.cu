@@ -61,6 +61,7 @@ constexpr int kDims = 128;              // key dims, value dims of a head
 constexpr int kKChunks = kVDim / 64;    // 64-dim chunks of the latent
 constexpr int kStage = kDims * 128;     // 128 output dims x 64 of K: 16 KB
 constexpr int kStages = 12;
+constexpr int kWarpStage = 4096;        // a warp's 64 dims of its 32 rows, 128-byte swizzle
 constexpr int kOutWarps = 8;            // rows in, results out: two groups of four warps
 constexpr int kThreads = 32 * (kOutWarps + 3);  // and a warp each for weights, MMAs and rotary dims
 constexpr uint32_t kChange = 6;         // a change of rows, in items (see run_start)
@@ -88,8 +89,8 @@ struct Params {
 
 struct __align__(1024) Smem {
   uint8_t w[kStages][kStage];
-  uint8_t out[2][kRows * 128];  // half a result for each group: 64 dims of 128 rows, 128-byte swizzle
-  uint64_t w_full[kStages], w_empty[kStages], d_full[2], d_empty[2], group[2], a_full, fin;
+  uint8_t out[2][4 * kWarpStage];
+  uint64_t w_full[kStages], w_empty[kStages], d_full[2], d_empty[2], a_full, fin;
   uint32_t tmem_base;
   int abort;
 };
@@ -323,7 +324,6 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&s.d_full[i]), 1);
       mbar_init(smem_u32(&s.d_empty[i]), kRows);
-      mbar_init(smem_u32(&s.group[i]), kRows);
     }
     mbar_init(smem_u32(&s.a_full), 2 * kRows);
     mbar_init(smem_u32(&s.fin), 1);
@@ -368,17 +368,16 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
     // ------------------------------------------------ rows in, results out
     const int side = warp >> 2;             // the group of four warps, and its result buffer
     const int r = (warp & 3) * 32 + lane;   // row = TMEM lane
-    const bool leader = (warp & 3) == 0 && lane == 0;
+    uint8_t *const stage = &s.out[side][0] + (warp & 3) * kWarpStage;
     const uint64_t hint = policy_stream();
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    uint32_t syncs = 0;
-    // all four warps of the group are here (false: a wait gave up)
-    auto group_sync = [&]() -> bool {
-      mbar_arrive(smem_u32(&s.group[side]));
-      return warp_wait(s, p, s.group[side], syncs++ & 1);
+    // what the staging buffer held has been read
+    auto stage_free = [&]() {
+      if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      __syncwarp();
     };
     // the tile of rows being multiplied: its first row, the lane's cache row,
-    // and whether every row of it (that the tensors have) is a request's
+    // and whether each of the warp's 32 (that the tensors have) is a request's
     int32_t t0 = 0;
     int64_t row = -1, next_row = -1;
     bool whole = false;
@@ -394,17 +393,18 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
         t0 = ((int32_t)(i / per) * kCluster + (int32_t)rank) * kRows;
         row = n == 0 ? first_row : next_row;
         if (row == -2 && side == 0) report(p.dev_status, MLA_ERR_DEVICE_RANGE);
-        whole = t0 < p.total_kv && t0 >= rows_begin && min(t0 + kRows, p.total_kv) <= rows_end;
+        const int32_t tw = t0 + (warp & 3) * 32;
+        whole = tw < p.total_kv && tw >= rows_begin && min(tw + 32, p.total_kv) <= rows_end;
         HalfRows<kFp8> rows;
         rows.load(p, row, side, lane);
         // the rows before are done with when the last product is complete, the
         // staging buffer when its last store has read it
         if (n > 0) {
-          if (leader) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-          if (!group_sync() || !warp_wait(s, p, s.d_full[(n - 1) & 1], ((n - 1) >> 1) & 1)) break;
+          stage_free();
+          if (!warp_wait(s, p, s.d_full[(n - 1) & 1], ((n - 1) >> 1) & 1)) break;
           tc_fence_after();
         }
-        rows.store(&s.out[side][0] + (warp & 3) * 4096, lanes + kColA + 128 * side, lane);
+        rows.store(stage, lanes + kColA + 128 * side, lane);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(smem_u32(&s.a_full));
@@ -427,7 +427,6 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
       const float by = kFp8 ? p.kv_scale : 1.f;
       const uint32_t done = (item == 0 ? per : item) - 1;  // the item before
       const int h = (int)(done >> 1);
-      bool ok = true;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         uint4 o[8];
@@ -439,16 +438,13 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
           o[k] = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
         }
         if (store_whole) {
-          // the store that used the staging buffer before has read it
-          if (leader) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-          if (!(ok = group_sync())) break;
+          stage_free();
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            *reinterpret_cast<uint4 *>(&s.out[side][r * 128 + ((k ^ (r & 7)) << 4)]) = o[k];
+          for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4 *>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) = o[k];
           fence_proxy_async_shared();
-          if (!(ok = group_sync())) break;
-          if (leader) {
-            tma_store_3d(done & 1 ? &maps.v : &maps.k_nope, 64 * half, h, t, smem_u32(s.out[side]), hint);
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(done & 1 ? &maps.v : &maps.k_nope, 64 * half, h, t + (warp & 3) * 32, smem_u32(stage), hint);
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           }
         } else if (own_row != -1) {
@@ -458,9 +454,8 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
           for (int k = 0; k < 8; ++k) dst[k] = o[k];
         }
       }
-      if (!ok) break;
     }
-    if (leader) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   } else if (warp == kOutWarps) {
     // ------------------------------------------------ weights
     if (elect_one_sync()) {
@@ -604,8 +599,8 @@ cudaError_t launch(const Params &p, cudaStream_t stream) {
   Maps maps;
   if (!encode(&maps.w_uk, p.w_uk, 2, kVDim, (uint64_t)p.heads * kDims, 1, kBox, 1) ||
       !encode(&maps.w_uv, p.w_uv, 2, kDims, (uint64_t)p.heads * kVDim, 1, kBox, 1) ||
-      !encode(&maps.k_nope, p.k_nope, 3, kDims, p.heads, p.total_kv, 1, kRows) ||
-      !encode(&maps.v, p.v, 3, kDims, p.heads, p.total_kv, 1, kRows))
+      !encode(&maps.k_nope, p.k_nope, 3, kDims, p.heads, p.total_kv, 1, 32) ||
+      !encode(&maps.v, p.v, 3, kDims, p.heads, p.total_kv, 1, 32))
     return cudaErrorInvalidValue;
   // one cluster per item at most, and as many as the SMs hold
   const int64_t items = ((int64_t)p.total_kv + kCluster * kRows - 1) / (kCluster * kRows) * 2 * p.heads;

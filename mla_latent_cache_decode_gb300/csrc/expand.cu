@@ -21,22 +21,28 @@
 // every stage and multicasts it, so L2 delivers a weight once per cluster.
 // Accumulators are double-buffered (2 x 128 columns); two groups of four warps
 // take turns to round them to bf16, stage them in shared memory and store them
-// by TMA (one group cannot keep up with the MMAs: 2,048 cycles a result).
+// by TMA, 32 rows a warp (one group cannot keep up with the MMAs: 2,048 cycles a result).
 //
 // An item is one head's keys or values of a group of kCluster x 128 rows; the
 // items (group by group, head by head) are cut into equal runs, one a cluster.
 //
-// Measured: 8,192 tokens of 128 heads 182-201 us (1.48-1.37 PFLOP/s, 78-72% of
+// Measured: 8,192 tokens of 128 heads 179-197 us (1.54-1.40 PFLOP/s, 81-73% of
 // the measured bf16 rate; the slower in a row of calls, when the GPU's power
-// limit holds the clock near 1.9 GHz), 4,501 tokens from E4M3 104-109 us, 11,051
-// of 16 heads 40-43 us, 286 of 128 heads 21-22 us (53 MB: 8).  The tensor cores
-// are busy 69% of an SM's cycles.  Without its weights' way in, the first takes
-// 141 us, without its results' way out 153, without both 131: each of the two
-// makes the MMAs wait somewhat, the weights by the latency that 192 KB in flight
-// have to cover (11 stages instead of 12: 185 us, and 45.7 instead of 43.0 with
-// 16 heads; stages of 32 KB: no change).  Slower were clusters of four; pairs of
-// CTAs that share each MMA, half of B in each (223 us against 200: at 128 columns
-// the shared MMA itself is slower, 173 us without weights); results stored from
+// limit holds the clock at 1.8-1.9 GHz), 4,501 tokens from E4M3 104-108 us,
+// 11,051 of 16 heads 40-41 us, 286 of 128 heads 20.5 us (53 MB: 8).  The tensor
+// cores are busy 72% of an SM's cycles.
+//
+// What its parts give, the first case at 182 us (results then staged by four
+// warps together; each warp for itself, without a barrier, 179 and 42.0 -> 40.9
+// with 16 heads): without its weights' way in 141, without its results' way out
+// 153, without both 131; staged but not stored 158, all stored to a few rows that
+// stay in L2 182.  Each way makes the MMAs wait somewhat, the weights by the
+// latency that 192 KB in flight have to cover (11 stages instead of 12: 185 us,
+// and 45.7 instead of 43.0 with 16 heads; 13 by halving the staging buffer, which
+// then waits more often: 200 against 194).  Stages of 32 KB and staging in
+// quarters of a row changed nothing.  Slower were clusters of four; pairs of CTAs
+// that share each MMA, half of B in each (223 us against 200: at 128 columns the
+// shared MMA itself is slower, 173 us without weights); results stored from
 // registers instead of by TMA (259).  More registers for the output warps changed
 // nothing (198 against 200, 42.0 against 42.0).
 #include <atomic>

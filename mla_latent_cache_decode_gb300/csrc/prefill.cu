@@ -41,7 +41,7 @@
 // The tensor cores are busy 74% of the cycles of a 4,096-token prompt; the rest
 // is the fill and the drain of each item (a claim, Q, the first S without a
 // softmax beside it, O's way out) and the GPU's power limit.  Short prompts are
-// bound by that latency: 4 prompts of 1 to 200 tokens 17.5 us, of which 6 are
+// bound by that latency: 4 prompts of 1 to 200 tokens 17.5-18 us, of which 6 are
 // bytes; 9 queries on 18,097 keys of 16 heads 38.7 us, 3.9 TB/s.
 //
 // What its parts gave, us (8,192 causal tokens of 128 heads; 3,992 queries of 16

@@ -16,35 +16,28 @@
 // by itself, so any page size and request boundary will do, and E4M3 codes are
 // widened to bf16, exactly, on the way), and every head's weights stream past
 // through a ring of 16 KB stages (128 output dims x 64 of K).  A from tensor
-// memory leaves shared memory's bandwidth to the weights.  A cluster of
-// CTAs holds neighbouring rows and walks the same heads: each loads a part of
-// every stage and multicasts it, so L2 delivers a weight once per cluster.
+// memory leaves shared memory's bandwidth to the weights.  Every CTA loads its
+// weights for itself, by plain TMA loads into its own shared memory: CTAs depend
+// on no other, and the weights may lie in any memory that the GPU can read.
 // Accumulators are double-buffered (2 x 128 columns); two groups of four warps
 // take turns to round them to bf16, stage them in shared memory and store them
 // by TMA, 32 rows a warp (one group cannot keep up with the MMAs: 2,048 cycles a result).
 //
-// An item is one head's keys or values of a group of kCluster x 128 rows; the
-// items (group by group, head by head) are cut into equal runs, one a cluster.
+// An item is one head's keys or values of a tile of 128 rows; the items (tile
+// by tile, head by head) are cut into equal runs, one a CTA.
 //
-// Measured: 8,192 tokens of 128 heads 179-197 us (1.54-1.40 PFLOP/s, 81-73% of
-// the measured bf16 rate; the slower in a row of calls, when the GPU's power
-// limit holds the clock at 1.8-1.9 GHz), 4,501 tokens from E4M3 104-108 us,
-// 11,051 of 16 heads 40-41 us, 286 of 128 heads 20.5 us (53 MB: 8).  The tensor
-// cores are busy 72% of an SM's cycles.
+// Measured: 8,192 tokens of 128 heads 207-212 us (1.33-1.30 PFLOP/s, 70-68% of
+// the measured bf16 rate), 4,501 tokens from E4M3 113-115 us, 11,051 of 16 heads
+// 42 us, 286 of 128 heads 18.9 us (53 MB: 8).
 //
-// What its parts give, the first case at 182 us (results then staged by four
-// warps together; each warp for itself, without a barrier, 179 and 42.0 -> 40.9
-// with 16 heads): without its weights' way in 141, without its results' way out
-// 153, without both 131; staged but not stored 158, all stored to a few rows that
-// stay in L2 182.  Each way makes the MMAs wait somewhat, the weights by the
-// latency that 192 KB in flight have to cover (11 stages instead of 12: 185 us,
-// and 45.7 instead of 43.0 with 16 heads; 13 by halving the staging buffer, which
-// then waits more often: 200 against 194).  Stages of 32 KB and staging in
-// quarters of a row changed nothing.  Slower were clusters of four; pairs of CTAs
-// that share each MMA, half of B in each (223 us against 200: at 128 columns the
-// shared MMA itself is slower, 173 us without weights); results stored from
-// registers instead of by TMA (259).  More registers for the output warps changed
-// nothing (198 against 200, 42.0 against 42.0).
+// What bounds it: the weights' way in and the results' way out, beside the MMAs'
+// own reads of the weights.  Of the first case's 212 us, 164 are left without
+// weights loaded, 170 without results stored, 148 without both (of 16 heads' 42:
+// 37, 37, 35).  At the MMAs' full rate an SM takes in 64 bytes of weights a cycle
+// from L2, and its shared memory passes 64 in, 64 to the MMAs and 32 of results
+// of the 128 that it can; latency is covered (11 stages instead of 12: 209 against
+// 212 us).  Results stored from registers instead of by TMA were slower (259 us
+// against 182 when this was tried).
 #include <atomic>
 #include <cmath>
 #include <type_traits>
@@ -70,7 +63,7 @@ constexpr int kStages = 12;
 constexpr int kWarpStage = 4096;        // a warp's 64 dims of its 32 rows, 128-byte swizzle
 constexpr int kOutWarps = 8;            // rows in, results out: two groups of four warps
 constexpr int kThreads = 32 * (kOutWarps + 3);  // and a warp each for weights, MMAs and rotary dims
-constexpr uint32_t kChange = 6;         // a change of rows, in items (see run_start)
+constexpr uint32_t kChange = 4;         // a change of rows, in items (see run_start)
 constexpr uint32_t kTmemCols = 512, kColA = 0, kColD = 256;
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr uint64_t kDrainNs = 10000000ull;
@@ -255,51 +248,6 @@ __device__ __forceinline__ void copy_rope(const Params &p, int64_t row, int32_t 
   }
 }
 
-template <int kCluster>
-__device__ __forceinline__ uint32_t cluster_rank() {
-  if (kCluster == 1) return 0;
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-
-template <int kCluster>
-__device__ __forceinline__ void cluster_sync() {
-  if (kCluster == 1) {
-    __syncthreads();
-  } else {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  }
-}
-
-// The barrier at this offset in every CTA of the cluster.
-template <int kCluster>
-__device__ __forceinline__ void commit_all(uint32_t bar) {
-  if (kCluster == 1) {
-    mma_commit(bar);
-  } else {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"((uint16_t)((1 << kCluster) - 1))
-        : "memory");
-  }
-}
-
-template <int kCluster>
-__device__ __forceinline__ void load_weights(uint32_t dst, const CUtensorMap *m, int32_t x, int32_t y, uint32_t bar,
-                                             uint64_t policy) {
-  if (kCluster == 1) {
-    tma_load_2d_hint(dst, m, x, y, bar, policy);
-  } else {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-        ".L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5, %6;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar), "h"((uint16_t)((1 << kCluster) - 1)),
-        "l"(policy)
-        : "memory");
-  }
-}
-
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap *m, int32_t x, int32_t y, int32_t z, uint32_t src,
                                              uint64_t policy) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group.L2::cache_hint [%0, {%1, %2, %3}], [%4], %5;" ::
@@ -316,16 +264,15 @@ __device__ __forceinline__ uint64_t policy_stream() {
   return p;
 }
 
-template <bool kFp8, int kCluster>
+template <bool kFp8>
 __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_constant__ Maps maps, const Params p) {
   extern __shared__ uint8_t smem_raw[];
   Smem &s = *reinterpret_cast<Smem *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank<kCluster>();
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(&s.w_full[i]), 1);
-      mbar_init(smem_u32(&s.w_empty[i]), kCluster);
+      mbar_init(smem_u32(&s.w_empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&s.d_full[i]), 1);
@@ -345,28 +292,26 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
   griddep_wait();
   griddep_launch_dependents();
   const int32_t rows_begin = ragged::cut(p.kv_offsets[0], p.total_kv), rows_end = ragged::cut(p.kv_offsets[p.batch], p.total_kv);
-  // This cluster's run of items [i0, i1): group i / per, head and kind i % per.
+  // This CTA's run of items [i0, i1): row tile i / per, head and kind i % per.
   // The runs are equal in cost, in which a change of rows counts as kChange
-  // items (1,500 + 3,001 tokens of 128 heads took 107.6 us with 3, 103.8 with 8;
-  // 11,051 of 16 heads 41.0 with 3, 40.1 with 5, 42.1 with 8).  32 bits hold the
-  // cost of all rows: less than 2^22 groups of 262 each.
-  const uint32_t clusters = gridDim.x / kCluster, c = blockIdx.x / kCluster, per = 2 * p.heads;
-  const uint32_t groups = (uint32_t)((rows_end + kCluster * kRows - 1) / (kCluster * kRows));
-  const uint32_t cost = groups == 0 ? 0 : groups * (per + kChange) - kChange;
-  auto run_start = [&](uint32_t k) -> uint32_t {  // of cluster k
-    const uint32_t at = cost / clusters * k + cost % clusters * k / clusters + kChange;
+  // items (11,051 tokens of 16 heads 41.7 us with 3, 42.1 with 4, 42.8 with 6, 44.5
+  // with 10; 286 of 128 heads 19.2, 18.8, 18.9, 20.0; large calls of 128 heads all
+  // the same).  32 bits hold the cost of all rows: at most 2^23 tiles of 260 each.
+  const uint32_t per = 2 * p.heads, tiles = (uint32_t)((rows_end + kRows - 1) / kRows);
+  const uint32_t cost = tiles == 0 ? 0 : tiles * (per + kChange) - kChange;
+  auto run_start = [&](uint32_t k) -> uint32_t {  // of CTA k
+    const uint32_t at = cost / gridDim.x * k + cost % gridDim.x * k / gridDim.x + kChange;
     const uint32_t g = at / (per + kChange), in = at % (per + kChange);
-    return min(g * per + (in > kChange ? in - kChange : 0), groups * per);
+    return min(g * per + (in > kChange ? in - kChange : 0), tiles * per);
   };
-  const uint32_t i0 = run_start(c), i1 = run_start(c + 1);
+  const uint32_t i0 = run_start(blockIdx.x), i1 = run_start(blockIdx.x + 1);
   // the first rows' places, while the barriers and the tensor memory are set up
   int64_t first_row = -1;
   if (warp < kOutWarps && i0 < i1)
-    first_row = cache_row(p, ((int32_t)(i0 / per) * kCluster + (int32_t)rank) * kRows + (warp & 3) * 32 + lane, rows_begin,
-                          rows_end);
+    first_row = cache_row(p, (int32_t)(i0 / per) * kRows + (warp & 3) * 32 + lane, rows_begin, rows_end);
   __syncwarp();
   tc_fence_before();
-  cluster_sync<kCluster>();
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s.tmem_base;
 
@@ -388,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
     int64_t row = -1, next_row = -1;
     bool whole = false;
     uint32_t item = i0 % per;
-    // Item i of the run: its group's rows first, if they are new, then the
+    // Item i of the run: its tile's rows first, if they are new, then the
     // result of the item before, so that at a change of rows the MMAs wait no
     // longer than for them.
     for (uint32_t i = i0, n = 0; i <= i1 && i0 < i1; ++i, ++n, item = item + 1 == per ? 0 : item + 1) {
@@ -396,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
       const int64_t own_row = row;
       const bool store_whole = whole;
       if (i < i1 && (n == 0 || item == 0)) {
-        t0 = ((int32_t)(i / per) * kCluster + (int32_t)rank) * kRows;
+        t0 = (int32_t)(i / per) * kRows;
         row = n == 0 ? first_row : next_row;
         if (row == -2 && side == 0) report(p.dev_status, MLA_ERR_DEVICE_RANGE);
         const int32_t tw = t0 + (warp & 3) * 32;
@@ -414,8 +359,8 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(smem_u32(&s.a_full));
-        if (i + per - item < i1) {  // the next group's rows towards L2 meanwhile
-          next_row = cache_row(p, t0 + kCluster * kRows + r, rows_begin, rows_end);
+        if (i + per - item < i1) {  // the next tile's rows towards L2 meanwhile
+          next_row = cache_row(p, t0 + kRows + r, rows_begin, rows_end);
           HalfRows<kFp8>::prefetch(p, next_row, side, lane);
         }
       }
@@ -470,9 +415,6 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
       prefetch_tmap(&maps.k_nope);
       prefetch_tmap(&maps.v);
       const uint64_t hint = policy_evict_normal();
-      // a stage is 128 rows of 128 bytes, loaded in boxes of kBox rows
-      constexpr int kBox = kCluster <= 2 ? 64 : 128 / kCluster;
-      constexpr int kMine = kDims / kBox / kCluster;  // boxes of this CTA
       uint32_t n = 0;
       bool ok = true;
       uint32_t st = 0, ph = 1;
@@ -483,14 +425,12 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
           if (!(ok = wait_or_abort(s, p, s.w_empty[st], ph))) break;
           const uint32_t bar = smem_u32(&s.w_full[st]);
           mbar_arrive_expect_tx(bar, kStage);
-#pragma unroll
-          for (int b = 0; b < kMine; ++b) {
-            const int at = ((int)rank * kMine + b) * kBox;  // first row of the stage
-            const uint32_t dst = smem_u32(s.w[st]) + at * 128;
-            if (item & 1)  // rows: 64 of K for output dims 0-63, then for 64-127
-              load_weights<kCluster>(dst, &maps.w_uv, 64 * (at / 64), h * kVDim + kc * 64 + at % 64, bar, hint);
-            else           // rows: output dims
-              load_weights<kCluster>(dst, &maps.w_uk, kc * 64, h * kDims + at, bar, hint);
+          const uint32_t dst = smem_u32(s.w[st]);
+          if (item & 1) {  // rows: 64 of K for output dims 0-63, then for 64-127
+            tma_load_2d_hint(dst, &maps.w_uv, 0, h * kVDim + kc * 64, bar, hint);
+            tma_load_2d_hint(dst + kStage / 2, &maps.w_uv, 64, h * kVDim + kc * 64, bar, hint);
+          } else {         // rows: output dims
+            tma_load_2d_hint(dst, &maps.w_uk, kc * 64, h * kDims, bar, hint);
           }
           if (++st == kStages) {
             st = 0;
@@ -521,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
           const uint32_t a = tmem + kColA + 32 * kc;
 #pragma unroll
           for (int k = 0; k < 4; ++k) mma_ts_low(d, a + 8 * k, b + kStep * k, id, (kc > 0 || k > 0) ? 1u : 0u);
-          commit_all<kCluster>(smem_u32(&s.w_empty[st]));
+          mma_commit(smem_u32(&s.w_empty[st]));
           if (++st == kStages) {
             st = 0;
             ph ^= 1;
@@ -529,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
         }
         return true;
       };
-      uint32_t left = 0;  // items of the current group
+      uint32_t left = 0;  // items of the current row tile
       bool ok = true;
       for (uint32_t i = i0; i < i1 && ok; ++i, ++n, --left) {
         if (left == 0) {
@@ -546,9 +486,9 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
     }
   } else {
     // ------------------------------------------------ rotary dims
-    // of the groups whose first item is in this run
+    // of the row tiles whose first item is in this run
     for (uint32_t g = (i0 + per - 1) / per; g * per < i1; ++g) {
-      const int32_t t = ((int32_t)g * kCluster + (int32_t)rank) * kRows;
+      const int32_t t = (int32_t)g * kRows;
       int64_t rows[kRows / 32];
 #pragma unroll
       for (int q = 0; q < kRows / 32; ++q) rows[q] = cache_row(p, t + 32 * q + lane, rows_begin, rows_end);
@@ -557,10 +497,9 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
     }
     if (blockIdx.x == 0) ragged::check_offsets(p.kv_offsets, p.batch, p.total_kv, lane, 32, p.dev_status);
   }
-  // no CTA leaves while another may still write into it or arrive at it
   __syncwarp();
   tc_fence_before();
-  cluster_sync<kCluster>();
+  __syncthreads();
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
@@ -586,7 +525,7 @@ bool encode(CUtensorMap *m, const void *base, int rank, uint64_t d0, uint64_t d1
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool kFp8, int kCluster>
+template <bool kFp8>
 cudaError_t launch(const Params &p, cudaStream_t stream) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -595,36 +534,31 @@ cudaError_t launch(const Params &p, cudaStream_t stream) {
   static std::atomic<int> known[64];
   int sms = known[dev].load(std::memory_order_acquire);
   if (sms == 0) {
-    e = cudaFuncSetAttribute(expand_kernel<kFp8, kCluster>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(expand_kernel<kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)sizeof(Smem) + 1024);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     known[dev].store(sms, std::memory_order_release);
   }
-  constexpr uint32_t kBox = kCluster <= 2 ? 64 : 128 / kCluster;
   Maps maps;
-  if (!encode(&maps.w_uk, p.w_uk, 2, kVDim, (uint64_t)p.heads * kDims, 1, kBox, 1) ||
-      !encode(&maps.w_uv, p.w_uv, 2, kDims, (uint64_t)p.heads * kVDim, 1, kBox, 1) ||
+  if (!encode(&maps.w_uk, p.w_uk, 2, kVDim, (uint64_t)p.heads * kDims, 1, kDims, 1) ||
+      !encode(&maps.w_uv, p.w_uv, 2, kDims, (uint64_t)p.heads * kVDim, 1, 64, 1) ||
       !encode(&maps.k_nope, p.k_nope, 3, kDims, p.heads, p.total_kv, 1, 32) ||
       !encode(&maps.v, p.v, 3, kDims, p.heads, p.total_kv, 1, 32))
     return cudaErrorInvalidValue;
-  // one cluster per item at most, and as many as the SMs hold
-  const int64_t items = ((int64_t)p.total_kv + kCluster * kRows - 1) / (kCluster * kRows) * 2 * p.heads;
-  const int64_t clusters = items < sms / kCluster ? items : sms / kCluster;
+  // as many CTAs as SMs, but no more than items
+  const int64_t items = ((int64_t)p.total_kv + kRows - 1) / kRows * 2 * p.heads;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(clusters * kCluster));
+  cfg.gridDim = dim3((unsigned)(items < sms ? items : sms));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = sizeof(Smem) + 1024;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = kCluster;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, expand_kernel<kFp8, kCluster>, maps, p);
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, expand_kernel<kFp8>, maps, p);
 }
 
 mla_status_t run(Params p, int64_t num_blocks, int64_t total_kv, bool fp8, void *stream) {
@@ -649,10 +583,7 @@ mla_status_t run(Params p, int64_t num_blocks, int64_t total_kv, bool fp8, void 
   if (!aligned(p.block_table, 4) || !aligned(p.kv_offsets, 4))
     return invalid("block_table and kv_offsets must be 4-byte aligned");
   p.num_slots = num_blocks * (int64_t)p.block_size;
-  // One tile of rows has no neighbour to share weights with.
-  const cudaStream_t st = (cudaStream_t)stream;
-  const cudaError_t e = p.total_kv <= kRows ? (fp8 ? launch<true, 1>(p, st) : launch<false, 1>(p, st))
-                                            : (fp8 ? launch<true, 2>(p, st) : launch<false, 2>(p, st));
+  const cudaError_t e = fp8 ? launch<true>(p, (cudaStream_t)stream) : launch<false>(p, (cudaStream_t)stream);
   if (e == cudaSuccess) return MLA_OK;
   set_error_detail(cudaGetErrorString(e));
   return MLA_ERR_CUDA;

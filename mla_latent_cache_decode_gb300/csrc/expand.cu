@@ -283,6 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
     s.abort = 0;
     fence_mbarrier_init_cluster();
   }
+  __syncwarp();
   if (warp == 0) {
     tmem_alloc(smem_u32(&s.tmem_base), kTmemCols);
     tmem_relinquish();

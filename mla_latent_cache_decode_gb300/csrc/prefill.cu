@@ -538,6 +538,11 @@ __device__ __forceinline__ void store16(__nv_bfloat16 *dst, const float *x, bool
   }
 }
 
+// A tcgen05 instruction is the whole warp's: every lane comes to it, and together.
+// Lanes without a row (the last of a tile) leave out the stores, not the loop, and
+// where lanes part (a store, a loop of unequal length) a __syncwarp joins them again
+// ahead of the next one.
+
 // A whole row of output: O / l.  Not inlined: the softmax loop around it needs
 // the registers.  A template, so that either kernel calls a copy of its own: with
 // one copy that both called, the kernel of the long form lost outputs.
@@ -547,14 +552,16 @@ __device__ __noinline__ void store_out(uint32_t o, float inv, bool real, __nv_bf
   for (int c = 0; c < kV; c += 32) {
     float x[32];
     uint32_t *xr = reinterpret_cast<uint32_t *>(x);
+    __syncwarp();
     tmem_ld32(o + c, xr);
     tmem_wait_ld();
     tmem_loaded32(xr);
-    if (!real) continue;
 #pragma unroll
     for (int k = 0; k < 32; ++k) x[k] *= inv;
-    store16(out + c, x, wide);
-    store16(out + c + 16, x + 16, wide);
+    if (real) {
+      store16(out + c, x, wide);
+      store16(out + c + 16, x + 16, wide);
+    }
   }
 }
 
@@ -568,6 +575,7 @@ __device__ __noinline__ void store_row(uint32_t oa, float a, uint32_t ob, float 
   for (int c = c0; c < c1; c += 32) {
     float x[32];
     uint32_t *xr = reinterpret_cast<uint32_t *>(x);
+    __syncwarp();
     if (any) {
       tmem_ld32(oa + c, xr);
       tmem_wait_ld();
@@ -583,12 +591,11 @@ __device__ __noinline__ void store_row(uint32_t oa, float a, uint32_t ob, float 
 #pragma unroll
       for (int k = 0; k < 32; ++k) x[k] += b != 0.f ? __uint_as_float(y[k]) * b : 0.f;
     }
-    if (!real) continue;
-    if (partial) {
+    if (real && partial) {
 #pragma unroll
       for (int k = 0; k < 32; k += 4)
         *reinterpret_cast<float4 *>(partial + c + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
-    } else {
+    } else if (real) {
       store16(out + c, x, wide);
       store16(out + c + 16, x + 16, wide);
     }
@@ -638,6 +645,7 @@ __device__ __forceinline__ void softmax_role(Smem &s, const Params &p, int warp,
               *reinterpret_cast<uint4 *>(&s.v[vi % kVSlots][c][r * 128 + (k & 7) * 16]) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_shared();
+            __syncwarp();
           }
         }
         tmem_wait_st();
@@ -1010,6 +1018,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     s.abort = 0;
     fence_mbarrier_init_cluster();
   }
+  __syncwarp();
   if (warp == 0) {
     tmem_alloc(smem_u32(&s.tmem_base), kTmemCols);
     tmem_relinquish();

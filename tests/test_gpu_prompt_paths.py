@@ -1,0 +1,95 @@
+"""The prompt side's kernels on the paths that only long contexts and many
+items take: mla_prefill's straight-line softmax with claimed items, pairs of
+heads and tiles that are not full, and mla_expand_kv over many changes of rows.
+Against the fp64 oracle, with the derived tolerances of prompt_helpers."""
+import numpy as np
+import pytest
+
+import oracle.prompt as op
+from prompt_helpers import assert_within, attend_tol, f64
+from test_gpu_prompt import bits, check_expand, expand_case, mla, prefill_case, run_expand, run_prefill, word  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+def check_heads(c, heads, causal, scale=0.07):
+    """check_prefill on some heads: every row of out and lse of each request."""
+    qn, qp, kn, v = (f64(c[n][:, heads]) for n in ("qn", "qp", "kn", "v"))
+    kp = f64(c["kp"])
+    got, got_lse = f64(c["out"][:, heads]), f64(c["lse"][:, heads])
+    q0 = k0 = 0
+    for nq, nk in zip(c["q_lens"], c["kv_lens"]):
+        q, k = slice(q0, q0 + nq), slice(k0, k0 + nk)
+        out, lse, mag, size = op.attend(qn[q], qp[q], kn[k], kp[k], v[k], float(np.float32(scale)), causal)
+        tol, lse_tol = attend_tol(out, lse, mag, size, nk)
+        empty = np.isneginf(lse)
+        assert_within(got[q], out, tol, f"out of {nq} queries on {nk} keys")
+        assert np.array_equal(np.isneginf(got_lse[q]), empty) and (got[q][empty] == 0).all()
+        assert_within(np.where(empty, 0, got_lse[q]), np.where(empty, 0, lse), lse_tol, f"lse of {nq} queries on {nk} keys")
+        q0, k0 = q0 + nq, k0 + nk
+
+
+# Tiles of up to 256 queries a request; the last with 1 to 128 rows runs odd and
+# even key tiles, or pairs of heads from 304 tiles and heads on.  Means above
+# 2,048 keys (causal) and 512 (not) run the straight-line softmax, those below the loops.
+SHAPES = [
+    ([300], [2600], 3),                                    # two tiles, then 44 rows
+    ([257, 129], [2500, 2100], 5),                         # a last tile of one row, 129 rows
+    ([90], [2700], 2), ([1], [2305], 1), ([33], [4100], 3),  # odd and even key tiles
+    ([300, 129], [2600, 2300], 64),                        # claimed items, two tiles
+    ([700, 40], [3000, 1700], 61),
+    ([40, 100, 127], [2500, 2100, 3001], 125),             # claimed pairs of heads, one left over
+    ([300, 1], [2200, 2100], 128),                         # two tiles and pairs of heads in one call
+    ([40, 100, 127], [300, 210, 1300], 125),               # the same with loops when causal
+    ([300, 129], [400, 135], 64),
+]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("q_lens,kv_lens,H", SHAPES)
+def test_prefill_long_without_workspace(mla, q_lens, kv_lens, H, causal):
+    c = prefill_case(np.random.default_rng(sum(q_lens) + H), q_lens, kv_lens, H)
+    run_prefill(mla, c, causal=causal)
+    check_heads(c, sorted({0, H // 2, H - 1, max(H - 2, 0)}), causal)
+    assert torch.isfinite(c["out"]).all() and torch.isfinite(c["lse"]).all()
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("q_lens,kv_lens,H", [([300, 129], [2600, 2300], 64), ([40, 100, 127], [2500, 2100, 3001], 125),
+                                              ([40, 100, 127], [300, 210, 1300], 125)])
+def test_prefill_claimed_items_repeat_bit_for_bit(mla, q_lens, kv_lens, H, causal):
+    """Which block claims an item changes from run to run; what comes out does not."""
+    c = prefill_case(np.random.default_rng(7), q_lens, kv_lens, H)
+    first = None
+    for _ in range(10):
+        c["out"].fill_(float("nan"))
+        run_prefill(mla, c, causal=causal)
+        got = (bits(c["out"]), bits(c["lse"]))
+        if first is None:
+            first = got
+        assert np.array_equal(got[0], first[0]) and np.array_equal(got[1], first[1])
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_prefill_long_rows_behind_a_request_never_matter(mla, causal):
+    """Straight-line softmax, claimed items: NaN behind every request's rows, key counts that
+    leave 1 to 15 rows of a step of 16."""
+    lens_q, lens_k, H = [130, 300, 65], [2113, 2575, 2305], 51
+    c = prefill_case(np.random.default_rng(8), lens_q, lens_k, H, q_behind=200, kv_behind=300)
+    run_prefill(mla, c, causal=causal)
+    rows = sum(lens_q)
+    assert torch.isnan(c["out"][rows:]).all() and torch.isnan(c["lse"][rows:]).all()
+    check_heads(c, [0, 25, 50], causal)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("lens,H", [([60001], 1), ([20000, 1, 0, 25003], 2)])
+def test_expand_many_changes_of_rows(mla, lens, H, fp8):
+    """Few heads on many rows: a block walks through several tiles of rows."""
+    c = expand_case(np.random.default_rng(9), lens, H, 64, fp8, behind=70)
+    st = word()
+    run_expand(mla, c, 0.37 if fp8 else None, dev_status=st)
+    assert int(st) == 0
+    check_expand(c, 0.37 if fp8 else 1.0)

@@ -523,19 +523,17 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, f
   l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
 }
 
-// 16 outputs of a row as 32 bytes; `wide`: the address is a multiple of 32.
-__device__ __forceinline__ void store16(__nv_bfloat16 *dst, const float *x, bool wide) {
+// 16 outputs of a row, 16 bytes a store.  No 32-byte stores: in a function that both
+// kernels below call, not inlined, they wrote only their first 4 or 8 bytes in one of
+// the two, written as PTX or as a 32-byte vector type (nvcc 13.0).  They took 65.2 us
+// where these take 66.9-67.7 (3,992 queries of 16 heads, every key visible), 38.8 / 39.2
+// (9 queries on 18,097 keys), the same elsewhere.
+__device__ __forceinline__ void store16(__nv_bfloat16 *dst, const float *x) {
   uint32_t u[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) u[k] = pack2(x[2 * k], x[2 * k + 1]);
-  if (wide) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(u[0]), "r"(u[1]),
-                 "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
-                 : "memory");
-  } else {
-    reinterpret_cast<uint4 *>(dst)[0] = make_uint4(u[0], u[1], u[2], u[3]);
-    reinterpret_cast<uint4 *>(dst)[1] = make_uint4(u[4], u[5], u[6], u[7]);
-  }
+  reinterpret_cast<uint4 *>(dst)[0] = make_uint4(u[0], u[1], u[2], u[3]);
+  reinterpret_cast<uint4 *>(dst)[1] = make_uint4(u[4], u[5], u[6], u[7]);
 }
 
 // A tcgen05 instruction is the whole warp's: every lane comes to it, and together.
@@ -544,10 +542,8 @@ __device__ __forceinline__ void store16(__nv_bfloat16 *dst, const float *x, bool
 // ahead of the next one.
 
 // A whole row of output: O / l.  Not inlined: the softmax loop around it needs
-// the registers.  A template, so that either kernel calls a copy of its own: with
-// one copy that both called, the kernel of the long form lost outputs.
-template <bool kLong>
-__device__ __noinline__ void store_out(uint32_t o, float inv, bool real, __nv_bfloat16 *out, bool wide) {
+// the registers.
+__device__ __noinline__ void store_out(uint32_t o, float inv, bool real, __nv_bfloat16 *out) {
 #pragma unroll 1
   for (int c = 0; c < kV; c += 32) {
     float x[32];
@@ -559,18 +555,17 @@ __device__ __noinline__ void store_out(uint32_t o, float inv, bool real, __nv_bf
 #pragma unroll
     for (int k = 0; k < 32; ++k) x[k] *= inv;
     if (real) {
-      store16(out + c, x, wide);
-      store16(out + c + 16, x + 16, wide);
+      store16(out + c, x);
+      store16(out + c + 16, x + 16);
     }
   }
 }
 
 // Columns [c0, c1) of a row's output: a * O_a (+ b * O_b with `two`), to `out`
 // as bf16 or, for a part of the keys, to `partial` as fp32.  `any`: O holds
-// something.  Not inlined, and a template, like store_out.
-template <bool kLong>
+// something.  Not inlined, like store_out.
 __device__ __noinline__ void store_row(uint32_t oa, float a, uint32_t ob, float b, bool two, bool any, int c0, int c1,
-                                       bool real, __nv_bfloat16 *out, bool wide, float *partial) {
+                                       bool real, __nv_bfloat16 *out, float *partial) {
 #pragma unroll 1
   for (int c = c0; c < c1; c += 32) {
     float x[32];
@@ -596,8 +591,8 @@ __device__ __noinline__ void store_row(uint32_t oa, float a, uint32_t ob, float 
       for (int k = 0; k < 32; k += 4)
         *reinterpret_cast<float4 *>(partial + c + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
     } else if (real) {
-      store16(out + c, x, wide);
-      store16(out + c + 16, x + 16, wide);
+      store16(out + c, x);
+      store16(out + c + 16, x + 16);
     }
   }
 }
@@ -608,7 +603,6 @@ __device__ __forceinline__ void softmax_role(Smem &s, const Params &p, int warp,
   const int row = q4 * 32 + lane;  // of the tile: TMEM lane
   const uint32_t lanes = tmem + ((uint32_t)(q4 * 32) << 16);
   const uint32_t s_addr = lanes + kColS + 128 * t;
-  const bool wide = ((uintptr_t)p.out & 31) == 0;
   Items items;
   // key tiles of this query tile, key tiles loaded, outputs of either query tile, odd-even items
   uint32_t g = 0, vg = 0, outs0 = 0, outs1 = 0, joins = 0;
@@ -670,10 +664,9 @@ __device__ __forceinline__ void softmax_role(Smem &s, const Params &p, int warp,
         tc_fence_after();
       }
       if (n > 0 && !partial)
-        store_out<kLong>(s_addr + (kColO - kColS), l != 0.f ? 1.f / l : 0.f, real, out, wide);
+        store_out(s_addr + (kColO - kColS), l != 0.f ? 1.f / l : 0.f, real, out);
       else
-        store_row<kLong>(s_addr + (kColO - kColS), l != 0.f ? 1.f / l : 0.f, 0, 0.f, false, n > 0, 0, kV, real, out, wide,
-                         partial);
+        store_row(s_addr + (kColO - kColS), l != 0.f ? 1.f / l : 0.f, 0, 0.f, false, n > 0, 0, kV, real, out, partial);
       if (real && lse) *lse = l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
       tc_fence_before();
     } else {
@@ -702,8 +695,8 @@ __device__ __forceinline__ void softmax_role(Smem &s, const Params &p, int warp,
           (w.n[1] > 0 && !warp_wait(s, p, s.o_full[1], outs1 & 1)))
         return;
       tc_fence_after();
-      store_row<kLong>(lanes + kColO, f.x, lanes + kColO + 128, f.y, w.n[1] > 0, w.n[0] > 0, 64 * t, 64 * t + 64, real, out,
-                wide, partial);
+      store_row(lanes + kColO, f.x, lanes + kColO + 128, f.y, w.n[1] > 0, w.n[0] > 0, 64 * t, 64 * t + 64, real, out,
+                partial);
       tc_fence_before();
       // neither O nor the meeting place is reused before both have read it
       mbar_arrive(smem_u32(&s.join_end));

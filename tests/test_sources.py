@@ -28,3 +28,12 @@ def test_the_search_sees_asm_statements():
     text = 'asm volatile(\n "cp.async.bulk.a"\n ".b [%0];" ::"r"(x) : "memory");'
     assert asm_texts(text)[0].startswith("cp.async.bulk.a.b [%0];")
     assert sum(len(asm_texts(open(p).read())) for p in SOURCES) > 40
+
+
+@pytest.mark.parametrize("path", SOURCES, ids=os.path.basename)
+def test_no_32_byte_stores(path):
+    """In a function that two kernels call, not inlined, nvcc 13.0 wrote only the first element of
+    such a store in one of them."""
+    with open(path) as f:
+        source = f.read()
+    assert not re.search(r"st\.global\.v8|_32a\b", re.sub(r"//[^\n]*", "", source)), path

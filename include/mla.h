@@ -467,8 +467,10 @@ mla_status_t mla_expand_kv_fp8(const void *cache8, int64_t num_blocks, int32_t b
  * num_heads 1 to 128 (else MLA_ERR_UNSUPPORTED); total_q < 2^30, total_kv <=
  * 2^26.  The values of a request must be finite: a non-finite value row
  * reaches, through a zero weight, queries of its own request that do not see
- * it.  A key that is not finite reaches those that see it, a query its own row
- * of out and lse (NaN).  What other rows hold never matters.
+ * it.  A key that is not finite reaches those that see it: they get NaN in out
+ * and lse, unless its score is -inf and others are not (a weight of 0).  A query
+ * that is not finite gets NaN in its own row of out and lse, unless it sees no
+ * key.  What other rows hold never matters.
  *
  * Launch order: mla_rope_append, mla_expand_kv, mla_prefill and their FP8 forms
  * are programmatic dependents of the kernel before them (see mla_decode): they

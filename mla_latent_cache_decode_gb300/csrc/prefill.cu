@@ -4,7 +4,8 @@
 //   s_ij = softmax_scale * (q_nope_i . k_nope_j + q_pe_i . k_pe_j)
 //   j visible to i: j < nk, and when causal also j <= nk - nq + i
 //   out_i = sum_j softmax(s_i)_j v_j,   lse_i = log sum_j exp(s_ij)
-// A row that sees no key gets out = 0 and lse = -inf.
+// A row that sees no key gets out = 0 and lse = -inf, one that sees keys but has
+// no score above -inf NaN in both.
 //
 // Work.  An item is up to 256 query rows of one request and head: two tiles (A,
 // B) of 128 rows that share every key and value tile of 128 rows.  Per key tile
@@ -648,9 +649,11 @@ __device__ __forceinline__ void softmax_role(Smem &s, const Params &p, int warp,
       }
     }
     vg += w.loads();
-    // ---- epilogue: O / l.  A row that sees no key has l = 0; the NaN of a query
-    // that is not finite goes into its row of out and lse.
+    // ---- epilogue: O / l.  A row that sees no key has l = 0, and so has one whose
+    // scores are all -inf (a key or query that is not finite): it becomes NaN, like
+    // those with a score of NaN or +inf.  (A part of the keys leaves that to the join.)
     const bool real = at < w.rows;
+    const bool nan = w.parts == 1 && (p.causal ? w.see + at : w.nk) > 0;  // if l = 0
     const int64_t out_row = ((int64_t)w.q0 + at) * p.heads + w.h + (w.mode == kTwoHeads ? t : 0);
     __nv_bfloat16 *out = p.out + out_row * kV;
     float *partial = nullptr, *lse = p.lse ? p.lse + out_row : nullptr;
@@ -664,10 +667,10 @@ __device__ __forceinline__ void softmax_role(Smem &s, const Params &p, int warp,
         tc_fence_after();
       }
       if (n > 0 && !partial)
-        store_out(s_addr + (kColO - kColS), l != 0.f ? 1.f / l : 0.f, real, out);
+        store_out(s_addr + (kColO - kColS), l != 0.f ? 1.f / l : nan ? NAN : 0.f, real, out);
       else
         store_row(s_addr + (kColO - kColS), l != 0.f ? 1.f / l : 0.f, 0, 0.f, false, n > 0, 0, kV, real, out, partial);
-      if (real && lse) *lse = l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+      if (real && lse) *lse = l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : nan ? NAN : -INFINITY;
       tc_fence_before();
     } else {
       // tile 1 tells its maxima and sums, tile 0 answers with the factors of
@@ -684,12 +687,12 @@ __device__ __forceinline__ void softmax_role(Smem &s, const Params &p, int warp,
         const float top = fmaxf(m, other.x);
         f.x = l != 0.f ? ex2_approx(m - top) : 0.f;
         f.y = other.y != 0.f ? ex2_approx(other.x - top) : 0.f;
-        const float sum = f.x * l + f.y * other.y, inv = sum != 0.f ? 1.f / sum : 0.f;
+        const float sum = f.x * l + f.y * other.y, inv = sum != 0.f ? 1.f / sum : nan ? NAN : 0.f;
         f.x *= inv;
         f.y *= inv;
         s.join[row] = f;
         mbar_arrive(smem_u32(&s.join_factors));
-        if (real && lse) *lse = sum != 0.f ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+        if (real && lse) *lse = sum != 0.f ? (top + log2f(sum)) * 0.69314718055994531f : nan ? NAN : -INFINITY;
       }
       if ((w.n[0] > 0 && !warp_wait(s, p, s.o_full[0], outs0 & 1)) ||
           (w.n[1] > 0 && !warp_wait(s, p, s.o_full[1], outs1 & 1)))
@@ -962,7 +965,7 @@ __device__ __forceinline__ void schedule_role(Smem &s, const Params &p, int lane
     if (w.rows == 0 || publish(w)) (void)publish(Work{});
     if (lane == 0) {
       p.parts[2 * blockIdx.x] = make_int4(w.rows, w.parts, w.part, w.q0);
-      p.parts[2 * blockIdx.x + 1] = make_int4(w.h, w.slot - w.part * w.slot_step, w.slot_step, 0);
+      p.parts[2 * blockIdx.x + 1] = make_int4(w.h, w.slot - w.part * w.slot_step, w.slot_step, w.see);
     }
     return;
   }
@@ -1067,7 +1070,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 // of the item that part `at` belongs to, a warp per row:
 //   out = sum_i e^(lse_i - top) O_i / sum_i e^(lse_i - top)
 // The attention kernel's block `at` left what to do: {rows, parts, part, first
-// row} and {head, first slot, slots from part to part}.
+// row} and {head, first slot, slots from part to part, keys the first row sees}.
 constexpr int kJoinThreads = 256;
 
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p) {
@@ -1075,7 +1078,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p) {
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int4 a = p.parts[2 * blockIdx.x], b = p.parts[2 * blockIdx.x + 1];
-  const int rows = a.x, parts = a.y, part = a.z, q0 = a.w, head = b.x, first = b.y, step = b.z;
+  const int rows = a.x, parts = a.y, part = a.z, q0 = a.w, head = b.x, first = b.y, step = b.z, see = b.w;
   // (offsets that overlap may ask for more parts than there are blocks)
   if (rows == 0 || parts == 1 || first + (parts - 1) * step >= (int)gridDim.x) return;
   for (int r = part + warp * parts; r < rows; r += kJoinThreads / 32 * parts) {
@@ -1104,10 +1107,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p) {
         o.w += f * x.w;
       }
     }
-    const float inv = sum != 0.f ? 1.f / sum : 0.f;
+    // (sum = 0: no part has a score above -inf; NaN if the row sees a key)
+    const bool nan = (p.causal ? see + r : see) > 0;
+    const float inv = sum != 0.f ? 1.f / sum : nan ? NAN : 0.f;
     const int64_t row = ((int64_t)q0 + r) * p.heads + head;
     reinterpret_cast<uint2 *>(p.out + row * kV)[lane] = make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv));
-    if (p.lse && lane == 0) p.lse[row] = sum != 0.f ? top + logf(sum) : -INFINITY;
+    if (p.lse && lane == 0) p.lse[row] = sum != 0.f ? top + logf(sum) : nan ? NAN : -INFINITY;
   }
 }
 

@@ -93,3 +93,61 @@ def test_expand_many_changes_of_rows(mla, lens, H, fp8):
     run_expand(mla, c, 0.37 if fp8 else None, dev_status=st)
     assert int(st) == 0
     check_expand(c, 0.37 if fp8 else 1.0)
+
+
+# ------------------------------------------------------------------- scores of -inf
+
+INF = float("inf")
+
+# every form of an item: two tiles, odd and even key tiles, pairs of heads (and one left over), keys
+# in parts; with loops and straight-line
+FORMS = [([300], [300], 2, False), ([300], [2600], 2, False), ([60], [60], 3, False), ([60], [2600], 3, False), ([1], [1], 1, False),
+         ([40, 100, 127], [60, 130, 130], 125, False), ([40, 100, 127], [2500, 2100, 3001], 125, False), ([5, 3], [2000, 900], 2, True),
+         ([140], [2500], 1, True), ([3], [9], 1, True)]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("q_lens,kv_lens,H,split", FORMS)
+def test_prefill_query_whose_scores_are_all_minus_infinity(mla, q_lens, kv_lens, H, split, causal):
+    """An infinite query dim against keys of the other sign: NaN, not the row of a query that sees nothing."""
+    c = prefill_case(np.random.default_rng(51), q_lens, kv_lens, H)
+    c["kn"][:, :, 9] = -c["kn"][:, :, 9].abs() - 1
+    starts = np.concatenate([[0], np.cumsum(q_lens)])
+    rows = sorted({int(r) for b, n in enumerate(q_lens) for r in (starts[b], starts[b] + n // 2, starts[b] + n - 1)})
+    keep = np.setdiff1d(np.arange(sum(q_lens)), rows)
+    run_prefill(mla, c, causal=causal, ws=mla.make_prefill_workspace() if split else None)
+    before = bits(c["out"][keep]), bits(c["lse"][keep])
+    c["qn"][rows, :, 9] = INF
+    run_prefill(mla, c, causal=causal, ws=mla.make_prefill_workspace() if split else None)
+    assert torch.isnan(c["out"][rows]).all() and torch.isnan(c["lse"][rows]).all()
+    assert np.array_equal(bits(c["out"][keep]), before[0]) and np.array_equal(bits(c["lse"][keep]), before[1])
+
+
+@pytest.mark.parametrize("q_len,H,split", [(300, 2, False), (60, 3, False), (100, 128, False), (60, 1, True)])
+def test_prefill_key_whose_scores_are_minus_infinity(mla, q_len, H, split):
+    """The first key of a causal prompt: its own query sees only it (NaN), for the others it has no weight."""
+    c = prefill_case(np.random.default_rng(52), [q_len] * 3, [q_len] * 3, H)
+    c["qn"][:, :, 7] = c["qn"][:, :, 7].abs() + 1
+    first = [0, q_len, 2 * q_len]
+    c["kn"][first, :, 7] = -INF
+    run_prefill(mla, c, ws=mla.make_prefill_workspace() if split else None)
+    assert torch.isnan(c["out"][first]).all() and torch.isnan(c["lse"][first]).all()
+    heads = sorted({0, H - 1})
+    qn, qp, kn, kp, v = (f64(c[n] if n == "kp" else c[n][:, heads]) for n in ("qn", "qp", "kn", "kp", "v"))
+    for a in first:
+        rows = slice(a + 1, a + q_len)
+        out, lse, mag, size = op.attend(qn[rows], qp[rows], kn[rows], kp[rows], v[rows], float(np.float32(0.07)), True)
+        tol, lse_tol = attend_tol(out, lse, mag, size, q_len)
+        assert_within(f64(c["out"][rows][:, heads]), out, tol)
+        assert_within(f64(c["lse"][rows][:, heads]), lse, lse_tol)
+
+
+@pytest.mark.parametrize("split", [False, True])
+def test_prefill_infinite_query_that_sees_no_key(mla, split):
+    """More queries than keys: rows in front of the first key stay 0 and -inf whatever the query holds."""
+    c = prefill_case(np.random.default_rng(53), [200, 30], [40, 3], 2)
+    c["qn"][:160], c["qp"][200:227] = INF, float("nan")
+    run_prefill(mla, c, ws=mla.make_prefill_workspace() if split else None)
+    for rows in (slice(0, 160), slice(200, 227)):
+        assert (c["out"][rows] == 0).all() and torch.isneginf(c["lse"][rows]).all()
+    assert torch.isfinite(c["out"][160:200]).all() and torch.isfinite(c["lse"][227:]).all()

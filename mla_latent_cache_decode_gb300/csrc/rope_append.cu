@@ -195,14 +195,15 @@ __device__ __noinline__ void store_latent_exactly(const Params &p, int64_t slot,
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     sum = pair_add(sum, Pair{__shfl_xor_sync(0xffffffffu, sum.hi, o), __shfl_xor_sync(0xffffffffu, sum.lo, o)});
-  const Pair by = pair_mul(pair_rsqrt(pair_add(pair_mul(sum, 1.f / kVDim), Pair{p.eps, 0.f})), p.inv_scale);
+  const Pair by = pair_rsqrt(pair_add(pair_mul(sum, 1.f / kVDim), Pair{p.eps, 0.f}));
   const uint4 *weight = reinterpret_cast<const uint4 *>(p.norm_weight);
   unpack8(__ldg(weight + lane), w0);
   unpack8(__ldg(weight + lane + 32), w1);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    x0[i] = pair_to_odd(pair_mul(pair_mul(by, w0[i]), x0[i]));
-    x1[i] = pair_to_odd(pair_mul(pair_mul(by, w1[i]), x1[i]));
+    // (the scale last, as in fp32: its product may overflow, but no zero becomes NaN)
+    x0[i] = pair_to_odd(pair_mul(pair_mul(pair_mul(by, w0[i]), x0[i]), p.inv_scale));
+    x1[i] = pair_to_odd(pair_mul(pair_mul(pair_mul(by, w1[i]), x1[i]), p.inv_scale));
   }
   store_codes8(p, slot, 8 * lane, x0);
   store_codes8(p, slot, 256 + 8 * lane, x1);

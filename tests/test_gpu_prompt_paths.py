@@ -151,3 +151,21 @@ def test_prefill_infinite_query_that_sees_no_key(mla, split):
     for rows in (slice(0, 160), slice(200, 227)):
         assert (c["out"][rows] == 0).all() and torch.isneginf(c["lse"][rows]).all()
     assert torch.isfinite(c["out"][160:200]).all() and torch.isfinite(c["lse"][227:]).all()
+
+
+# ------------------------------------------------------------------- append, smallest scale
+
+def test_append_e4m3_zeros_stay_zero_at_the_smallest_scales(mla):
+    """1 / kv_scale next to fp32's largest: everything but zero saturates, in rows that are computed
+    in pairs of fp32 (some 3% of them here) as in those that are not."""
+    rng = np.random.default_rng(54)
+    T = 4096
+    kv = torch.from_numpy((rng.standard_normal((T, 576)) * 0.1).astype(np.float32)).cuda().to(torch.bfloat16)
+    weight = torch.from_numpy((1 + 0.1 * rng.standard_normal(512)).astype(np.float32)).cuda().to(torch.bfloat16)
+    kv[:, 5], kv[::2, 300:340] = 0, 0
+    table = torch.cat([torch.ones(1, 32), torch.zeros(1, 32)], 1).cuda()
+    cache = torch.zeros(T // 64, 64, 576, dtype=torch.uint8, device="cuda")
+    mla.mla_rope_append_fp8(kv, torch.zeros(T, dtype=torch.int64, device="cuda"), table, torch.arange(T, device="cuda"), cache, kv_scale=1e-38,
+                            norm_weight=weight)
+    got = cache.view(torch.float8_e4m3fn).float().view(T, 576)
+    assert torch.equal(got, torch.sign(kv.float()) * 448)

@@ -353,7 +353,9 @@ mla_status_t mla_decode_fp8_planned(const void *q, void *cache8, const void *kv_
  *     cache row slot_mapping[t] = [c', k']
  *     q_out[t, h, :] = the same rotation of q_pe[t, h, :], for every head
  * all in fp32, rounded once to bf16.  Pair i is elements 2i and 2i + 1 when
- * interleaved is 1, elements i and i + 32 when it is 0.
+ * interleaved is 1, elements i and i + 32 when it is 0.  (The squares are fp32
+ * too: their sum overflows for latents of 2^59 and more, whose rows become zeros,
+ * and elements below 2^-63 hardly count in it.)
  *
  *   kv            bf16, row t at kv + t * kv_stride (elements; a multiple of 8, >= 576)
  *   positions     int64 [num_tokens]; outside [0, max_position): the token is

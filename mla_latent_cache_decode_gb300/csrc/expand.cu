@@ -26,18 +26,19 @@
 // An item is one head's keys or values of a tile of 128 rows; the items (tile
 // by tile, head by head) are cut into equal runs, one a CTA.
 //
-// Measured: 8,192 tokens of 128 heads 207-212 us (1.33-1.30 PFLOP/s, 70-68% of
-// the measured bf16 rate), 4,501 tokens from E4M3 113-115 us, 11,051 of 16 heads
-// 42 us, 286 of 128 heads 18.9 us (53 MB: 8).
+// Measured: 8,192 tokens of 128 heads 203-212 us (1.36-1.30 PFLOP/s, 71-68% of
+// the measured bf16 rate), 4,501 tokens from E4M3 110-115 us, 11,051 of 16 heads
+// 41-42 us, 286 of 128 heads 18.8 us (53 MB: 8).
 //
-// What bounds it: the weights' way in and the results' way out, beside the MMAs'
-// own reads of the weights.  Of the first case's 212 us, 164 are left without
-// weights loaded, 170 without results stored, 148 without both (of 16 heads' 42:
-// 37, 37, 35).  At the MMAs' full rate an SM takes in 64 bytes of weights a cycle
-// from L2, and its shared memory passes 64 in, 64 to the MMAs and 32 of results
-// of the 128 that it can; latency is covered (11 stages instead of 12: 209 against
-// 212 us).  Results stored from registers instead of by TMA were slower (259 us
-// against 182 when this was tried).
+// What bounds it: the tensor cores are busy 69% of an SM's cycles; in between they
+// wait for weights and for results' way out.  Of the first case's 212 us, 164 are
+// left without weights loaded, 170 without results stored, 148 without both (of 16
+// heads' 42: 37, 37, 35); part of what that gains is the clock, 1.82 GHz under the
+// power limit.  No path is at its limit by its counters (L2 51%, its way to the SMs
+// 48% at 11 TB/s, HBM 36%, the MMAs' reads of shared memory 31%), and a shorter
+// ring changes nothing (11 stages instead of 12: 209 against 212 us).  Results
+// stored from registers instead of by TMA were slower (259 us against 182 when this
+// was tried).
 #include <atomic>
 #include <cmath>
 #include <type_traits>

@@ -37,13 +37,14 @@
 // a step 2^-8 each, independent from key to key); their sum, the maxima and O
 // are fp32.
 //
-// What bounds it.  8,192 causal tokens of 128 heads, 1,745-1,780 us: 1.55-1.58
-// PFLOP/s, 81-83% of the measured bf16 rate; every key visible 1.72-1.85 PFLOP/s.
-// The tensor cores are busy 74% of the cycles of a 4,096-token prompt; the rest
+// What bounds it.  8,192 causal tokens of 128 heads, 1,736-1,796 us: 1.53-1.58
+// PFLOP/s, 80-83% of the measured bf16 rate; every key visible 1.72-1.85 PFLOP/s.
+// The tensor cores are busy 72% of the cycles of a 4,096-token prompt; the rest
 // is the fill and the drain of each item (a claim, Q, the first S without a
 // softmax beside it, O's way out) and the GPU's power limit.  Short prompts are
-// bound by that latency: 4 prompts of 1 to 200 tokens 17.5-18 us, of which 6 are
-// bytes; 9 queries on 18,097 keys of 16 heads 38.7 us, 3.9 TB/s.
+// bound by that latency: 4 prompts of 1 to 200 tokens 18 us, of which 6 are
+// bytes (18.0 in a captured graph too: the GPU's time, not the call's); 9 queries
+// on 18,097 keys of 16 heads 39.1 us (38.6 in a graph), 3.9 TB/s.
 //
 // What its parts gave, us (8,192 causal tokens of 128 heads; 3,992 queries of 16
 // heads in four prompts, every key visible): two tiles an item, blocks by number 3,421 / 166; claimed items, the

@@ -169,3 +169,52 @@ def test_append_e4m3_zeros_stay_zero_at_the_smallest_scales(mla):
                             norm_weight=weight)
     got = cache.view(torch.float8_e4m3fn).float().view(T, 576)
     assert torch.equal(got, torch.sign(kv.float()) * 448)
+
+
+# ------------------------------------------------------------------- several calls
+
+def several(mla):
+    """Split, straight-line and short calls, each with what it gives alone."""
+    rng = np.random.default_rng(55)
+    cases = [prefill_case(rng, *shape) for shape in (([5, 1, 3], [2000, 1097, 1600], 4), ([300, 40], [2600, 1900], 32), ([1, 17, 64, 200],) * 2 + (64,))]
+    ws = mla.make_prefill_workspace()
+    for c in cases:
+        run_prefill(mla, c, ws=ws)
+        c["alone"] = bits(c["out"]), bits(c["lse"])
+        c["out"].zero_()
+    return cases
+
+
+def call(mla, c, ws, stream=None):
+    mla.mla_prefill(c["qn"], c["qp"], c["kn"], c["kp"], c["v"], c["qo"], c["ko"], 0.07, c["out"], c["lse"], workspace=ws, stream=stream)
+
+
+def test_prefill_calls_at_once(mla):
+    """Three streams, a workspace each."""
+    cases = several(mla)
+    streams, ws = [torch.cuda.Stream() for _ in cases], [mla.make_prefill_workspace() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, s, w in zip(cases, streams, ws):
+            call(mla, c, w, s)
+    torch.cuda.synchronize()
+    for c in cases:
+        assert np.array_equal(bits(c["out"]), c["alone"][0]) and np.array_equal(bits(c["lse"]), c["alone"][1])
+
+
+def test_prefill_graphs_that_share_a_workspace(mla):
+    """Captured apart, replayed one after the other on one stream."""
+    cases, ws, graphs = several(mla), mla.make_prefill_workspace(), []
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for c in cases:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            call(mla, c, ws)
+        graphs.append(graph)
+    for _ in range(10):
+        for graph in graphs:
+            graph.replay()
+    torch.cuda.synchronize()
+    for c in cases:
+        assert np.array_equal(bits(c["out"]), c["alone"][0]) and np.array_equal(bits(c["lse"]), c["alone"][1])

@@ -381,9 +381,10 @@ mla_status_t mla_decode_fp8_planned(const void *q, void *cache8, const void *kv_
  * block_size, 576], see below): each value x of the row is stored as the E4M3
  * code nearest to x * fp32(1 / kv_scale), ties to even, saturating to +-448.
  * Neither x nor the product is rounded on the way (they are held to 2^-40 or
- * better), but for an x that is an fp32 number: without a weight, or turned by
- * no angle, a row has the codes that mla_cache_append_fp8 gives it.  kv_scale
- * and 1 / kv_scale must be positive and finite.
+ * better, of the larger term where a rotation's two cancel), but for an x that
+ * is an fp32 number: without a weight, or turned by no angle, a row has the codes
+ * that mla_cache_append_fp8 gives it.  kv_scale and 1 / kv_scale must be positive
+ * and finite.
  */
 mla_status_t mla_rope_append(const void *kv, int64_t kv_stride, const int64_t *positions,
                              const float *cos_sin, int64_t max_position,

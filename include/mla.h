@@ -492,6 +492,145 @@ mla_status_t mla_prefill(const void *q_nope, int64_t q_nope_token_stride,
                          int32_t *dev_status, void *stream);
 
 /*
+ * mla_decode_shared — mla_decode for a batch whose requests begin with the same
+ * tokens (a system prompt, a document asked about many times) and hold those
+ * tokens' pages in common.  The result is mla_decode's: the pages in common are
+ * read, and multiplied with the queries of as many requests as fill the tensor
+ * cores' rows, once for all of them.  With P = *shared_blocks * block_size and
+ * L = seq_lens[b], token t < min(P, L) of request b is in block
+ * shared_table[t / block_size], token t >= P in block block_table[b][t /
+ * block_size] (its entries in front of P / block_size are not read).
+ *
+ *   q, cache, num_blocks, block_size, block_table, max_blocks_per_seq, seq_lens,
+ *   softmax_scale, out, lse     as in mla_decode; 1 <= num_heads <= 128
+ *   shared_table   int32 [max_shared_blocks] (device); may be NULL if that is 0
+ *   shared_blocks  int32 [1] (device): how many of its entries are shared, 0 to
+ *                  max_shared_blocks (else reported as MLA_ERR_DEVICE_RANGE and
+ *                  clamped).  Read on the device, as seq_lens is: a captured
+ *                  call follows what they hold when it is replayed
+ *   workspace      >= mla_decode_shared_workspace_size(batch, num_heads) bytes,
+ *                  256-byte aligned, contents free.  Calls that share one must
+ *                  not overlap on the GPU
+ * A length below P is fine (the request then sees its first L tokens), as is 0:
+ * out = 0 and lse = -inf.  A length outside [0, max_blocks_per_seq * block_size]
+ * is clamped and reported.  An entry that leaves the pool is reported, and the
+ * results of the requests that see its tokens are unspecified; nothing is read
+ * out of place.  Rows that no request sees are never part of a result, whatever
+ * they hold; a row that is not finite reaches the requests that see it.
+ * block_size in {16, 32, 64, 128, 256}; max_blocks_per_seq * block_size and
+ * max_shared_blocks * block_size <= 2^30; batch <= 2^20.  Split results are
+ * merged as mla_decode's: bf16 with fp32 log-sum-exps.
+ */
+size_t mla_decode_shared_workspace_size(int32_t batch, int32_t num_heads);
+mla_status_t mla_decode_shared(const void *q, const void *cache, int64_t num_blocks,
+                               int32_t block_size, const int32_t *shared_table,
+                               const int32_t *shared_blocks, int32_t max_shared_blocks,
+                               const int32_t *block_table, int32_t max_blocks_per_seq,
+                               const int32_t *seq_lens, int32_t batch, int32_t num_heads,
+                               float softmax_scale, void *out, float *lse, void *workspace,
+                               size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/*
+ * Thinning out a full cache by what attention looks at: mla_attention_mass adds
+ * up the weights (every step, every layer, or as many as the caller likes),
+ * mla_evict_select chooses the tokens that stay, mla_cache_compact moves their
+ * rows to the front of each request's pages.  The pages behind are free then,
+ * the request decodes on with its new length, and what it appends goes behind
+ * the rows that stayed (at the positions that its tokens have in the text:
+ * mla_rope_append takes position and slot apart).
+ *
+ * mla_attention_mass — for every token t < seq_lens[b] of request b
+ *     mass[b, t] = decay * previous[b, t] + sum_h exp(softmax_scale * q[b, h] . row_t - lse[b, h])
+ * the sum of its softmax weights over the heads (fp32 sums; with the lse that
+ * mla_decode wrote for the same q, a request's add up to num_heads; a head's
+ * weight below 2^-126 counts as 0).
+ *   q, cache, num_blocks, block_size, block_table, max_blocks_per_seq, seq_lens
+ *                  as in mla_decode; 1 <= num_heads <= 128
+ *   lse            fp32 [batch, num_heads]; a head with -inf gives nothing
+ *   previous       fp32, row b at previous + b * previous_stride, or NULL: nothing
+ *                  is added.  May be mass itself (same stride)
+ *   decay          >= 0 and finite (1: a plain sum); not looked at without previous
+ *   mass           fp32, row b at mass + b * mass_stride, max_tokens wide; entries
+ *                  behind seq_lens[b] are left as they are
+ * A length outside [0, min(max_tokens, max_blocks_per_seq * block_size)] is clamped
+ * and reported as MLA_ERR_DEVICE_RANGE; the weights of a page outside the pool
+ * are unspecified, and it is reported.  Strides in elements, >= max_tokens.
+ * block_size in {16, 32, 64, 128, 256}; batch < 2^24.
+ *
+ * mla_attention_mass_fp8 — the same over an FP8 cache (rows value(code) * kv_scale).
+ * The products run on the codes and on q as the sum of two E4M3 numbers a dim,
+ * which is exact for dims of 2^-10 of their head's largest and more, and off by at
+ * most 2^-17 of the largest below.
+ *
+ * mla_evict_select — the tokens of each request that stay when it may keep
+ * max_keep.  With L = seq_lens[b]: all of them if L <= max_keep; else the first
+ * `sink`, the last `recent`, and of those between them the max_keep - sink -
+ * recent of the largest mass (the earlier token where masses are equal; -0 and +0
+ * are, and a NaN is below everything).
+ *   mass       as above, read only
+ *   sink, recent   >= 0, sink + recent <= max_keep
+ *   keep       int32 [batch, max_keep], written: the positions that stay,
+ *              ascending, then -1
+ *   new_lens   int32 [batch], written: how many, min(L, max_keep)
+ * A length outside [0, max_tokens] is clamped and reported.
+ * 1 <= max_keep; max_tokens <= 2^30.
+ *
+ * mla_cache_compact — in place, in every layer: row j of request b becomes what
+ * row keep[b][j] was, for j < n = new_lens[b]; rows at their place already are
+ * not written.  With mass (or NULL): mass[b, j] becomes mass[b, keep[b][j]] too,
+ * and mass[b, j] = 0 for n <= j < seq_lens[b].
+ *   cache        bf16 [num_layers, num_blocks, block_size, 576] (one layer's cache:
+ *                num_layers = 1); the same block_table for all layers
+ *   keep         int32 [batch, max_keep]: keep[b][0..n) strictly ascending, all
+ *                below seq_lens[b], as mla_evict_select leaves it
+ *   seq_lens     int32 [batch]: the lengths before
+ *   new_lens     int32 [batch]: n <= min(max_keep, seq_lens[b])
+ * Lengths outside are clamped, an entry of keep that does not ascend or is
+ * outside is left out (its target keeps what it holds, or what a valid entry
+ * puts there), and so is a block outside the pool; each is reported as
+ * MLA_ERR_DEVICE_RANGE.  A page that several requests share must be one whose
+ * rows stay at their place in all of them (sink >= the tokens in common).
+ * Any block_size >= 1 with max_blocks_per_seq * block_size <= 2^30.
+ *
+ * mla_cache_compact_fp8 — the same for an FP8 cache (uint8, codes moved as they are).
+ *
+ * Launch order: these calls and mla_decode_shared are programmatic dependents
+ * of the kernel before them (see mla_decode): they wait for it to complete
+ * before they touch memory.
+ */
+mla_status_t mla_attention_mass(const void *q, const void *cache, int64_t num_blocks,
+                                int32_t block_size, const int32_t *block_table,
+                                int32_t max_blocks_per_seq, const int32_t *seq_lens, int32_t batch,
+                                int32_t num_heads, float softmax_scale, const float *lse,
+                                const float *previous, int64_t previous_stride, float decay,
+                                float *mass, int64_t mass_stride, int32_t max_tokens,
+                                int32_t *dev_status, void *stream);
+mla_status_t mla_attention_mass_fp8(const void *q, const void *cache8, int64_t num_blocks,
+                                    int32_t block_size, const int32_t *block_table,
+                                    int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                                    int32_t batch, int32_t num_heads, float softmax_scale,
+                                    float kv_scale, const float *lse, const float *previous,
+                                    int64_t previous_stride, float decay, float *mass,
+                                    int64_t mass_stride, int32_t max_tokens, int32_t *dev_status,
+                                    void *stream);
+mla_status_t mla_evict_select(const float *mass, int64_t mass_stride, int32_t max_tokens,
+                              const int32_t *seq_lens, int32_t batch, int32_t sink, int32_t recent,
+                              int32_t *keep, int32_t max_keep, int32_t *new_lens,
+                              int32_t *dev_status, void *stream);
+mla_status_t mla_cache_compact(void *cache, int64_t num_layers, int64_t num_blocks,
+                               int32_t block_size, const int32_t *block_table,
+                               int32_t max_blocks_per_seq, int32_t batch, const int32_t *keep,
+                               int32_t max_keep, const int32_t *seq_lens, const int32_t *new_lens,
+                               float *mass, int64_t mass_stride, int32_t max_tokens,
+                               int32_t *dev_status, void *stream);
+mla_status_t mla_cache_compact_fp8(void *cache8, int64_t num_layers, int64_t num_blocks,
+                                   int32_t block_size, const int32_t *block_table,
+                                   int32_t max_blocks_per_seq, int32_t batch, const int32_t *keep,
+                                   int32_t max_keep, const int32_t *seq_lens,
+                                   const int32_t *new_lens, float *mass, int64_t mass_stride,
+                                   int32_t max_tokens, int32_t *dev_status, void *stream);
+
+/*
  * mla_decode_noalloc — mla_decode for callers that cannot allocate device
  * memory.  The pages have no counterpart to this entry point; it exists for
  * users of this library.

@@ -9,7 +9,8 @@ raises ImportError if the compiled library is missing.
 
 Functions carry the C names: mla_cache_append, mla_decode_plan, mla_decode,
 mla_decode_planned, mla_combine, mla_decode_workspace_size; of the prompt side
-mla_rope_append, mla_expand_kv, mla_prefill.
+mla_rope_append, mla_expand_kv, mla_prefill; for a full cache mla_decode_shared,
+mla_attention_mass, mla_evict_select, mla_cache_compact.
 """
 from __future__ import annotations
 
@@ -33,7 +34,10 @@ EXPORTED = ("mla_status_string", "mla_last_error_detail", "mla_abi_version", "ml
             "mla_decode_append_planned", "mla_place_requests", "mla_place_one", "mla_absorb_q",
             "mla_absorb_out", "mla_selftest_wait_timeout", "mla_cache_append_fp8",
             "mla_decode_fp8", "mla_decode_fp8_planned", "mla_rope_append", "mla_rope_append_fp8",
-            "mla_expand_kv", "mla_expand_kv_fp8", "mla_prefill_workspace_size", "mla_prefill")
+            "mla_expand_kv", "mla_expand_kv_fp8", "mla_prefill_workspace_size", "mla_prefill",
+            "mla_decode_shared_workspace_size", "mla_decode_shared", "mla_attention_mass",
+            "mla_attention_mass_fp8", "mla_evict_select", "mla_cache_compact",
+            "mla_cache_compact_fp8")
 
 
 class MlaError(RuntimeError):
@@ -111,6 +115,24 @@ def _load():
     lib.mla_prefill.argtypes = [P, i64, i64, P, i64, i64, P, i64, i64, P, i64, P, i64, i64, P, P,
                                 i32, i64, i64, i32, i32, f32, P, P, P, sz, P, P]
     lib.mla_prefill.restype = ctypes.c_int
+    lib.mla_decode_shared_workspace_size.argtypes = [i32, i32]
+    lib.mla_decode_shared_workspace_size.restype = sz
+    lib.mla_decode_shared.argtypes = [P, P, i64, i32, P, P, i32, P, i32, P, i32, i32, f32, P, P, P,
+                                      sz, P, P]
+    lib.mla_decode_shared.restype = ctypes.c_int
+    lib.mla_attention_mass.argtypes = [P, P, i64, i32, P, i32, P, i32, i32, f32, P, P, i64, f32, P,
+                                       i64, i32, P, P]
+    lib.mla_attention_mass.restype = ctypes.c_int
+    lib.mla_attention_mass_fp8.argtypes = [P, P, i64, i32, P, i32, P, i32, i32, f32, f32, P, P, i64,
+                                           f32, P, i64, i32, P, P]
+    lib.mla_attention_mass_fp8.restype = ctypes.c_int
+    lib.mla_evict_select.argtypes = [P, i64, i32, P, i32, i32, i32, P, i32, P, P, P]
+    lib.mla_evict_select.restype = ctypes.c_int
+    compact = [P, i64, i64, i32, P, i32, i32, P, i32, P, P, P, i64, i32, P, P]
+    lib.mla_cache_compact.argtypes = compact
+    lib.mla_cache_compact.restype = ctypes.c_int
+    lib.mla_cache_compact_fp8.argtypes = compact
+    lib.mla_cache_compact_fp8.restype = ctypes.c_int
     lib.mla_selftest_wait_timeout.argtypes = [ctypes.c_uint64, P, P, P]
     lib.mla_selftest_wait_timeout.restype = ctypes.c_int
     return lib
@@ -609,6 +631,140 @@ def mla_prefill(q_nope, q_pe, k_nope, k_pe, v, q_offsets, kv_offsets, softmax_sc
         None if lse is None else _dense(lse, torch.float32, (Tq, H), dev, "lse"), ws, nbytes or 0,
         _status_word(dev_status, dev), _stream_of(stream, dev)))
     return out
+
+
+def mla_decode_shared_workspace_size(batch: int, num_heads: int = NUM_HEADS) -> int:
+    return int(get_lib().mla_decode_shared_workspace_size(batch, num_heads))
+
+
+def make_shared_workspace(batch: int, num_heads: int = NUM_HEADS, device=None):
+    """A workspace tensor of the size mla_decode_shared needs on the current device."""
+    import torch
+    n = mla_decode_shared_workspace_size(batch, num_heads)
+    if n == 0:
+        raise MlaError(4, "cannot size the workspace (no CUDA device, or batch or num_heads out of range)")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def mla_decode_shared(q, cache, shared_table, shared_blocks, block_table, seq_lens, softmax_scale,
+                      out, lse=None, workspace=None, dev_status=None, stream=None):
+    """mla_decode for requests that begin with the same tokens: blocks shared_table[0 ..
+    shared_blocks[0]) (int32 [N], int32 [1]) hold the first tokens of every request, and
+    block_table the others (its entries in front of those are not read)."""
+    import torch
+    bf16, i32 = torch.bfloat16, torch.int32
+    B, H, _ = _shape(q, 3, "q")
+    dev = _current(q, "q")
+    NB, BS, _ = _shape(cache, 3, "cache")
+    N = _shape(shared_table, 1, "shared_table")[0]
+    M = _shape(block_table, 2, "block_table")[1]
+    if workspace is None:
+        workspace = make_shared_workspace(B, H)
+    nbytes = _shape(workspace, 1, "workspace")[0]
+    _check(get_lib().mla_decode_shared(
+        _dense(q, bf16, (B, H, ROW_DIM), dev, "q"), _dense(cache, bf16, (NB, BS, ROW_DIM), dev, "cache"),
+        NB, BS, _dense(shared_table, i32, (N,), dev, "shared_table"),
+        _dense(shared_blocks, i32, (1,), dev, "shared_blocks"), N,
+        _dense(block_table, i32, (B, M), dev, "block_table"), M,
+        _dense(seq_lens, i32, (B,), dev, "seq_lens"), B, H, softmax_scale,
+        _dense(out, bf16, (B, H, KV_LORA_RANK), dev, "out"),
+        None if lse is None else _dense(lse, torch.float32, (B, H), dev, "lse"),
+        _dense(workspace, torch.uint8, (nbytes,), dev, "workspace"), nbytes,
+        _status_word(dev_status, dev), _stream_of(stream, dev)))
+    return out
+
+
+def _attention_mass(fn, cache_dtype, scale, q, cache, block_table, seq_lens, softmax_scale, lse,
+                    mass, previous, decay, dev_status, stream):
+    import torch
+    i32, f32 = torch.int32, torch.float32
+    B, H, _ = _shape(q, 3, "q")
+    dev = _current(q, "q")
+    NB, BS, _ = _shape(cache, 3, "cache")
+    M = _shape(block_table, 2, "block_table")[1]
+    S = _shape(mass, 2, "mass")[1]
+    mass_args = _rows(mass, f32, (B, S), dev, "mass")
+    _check(fn(_dense(q, torch.bfloat16, (B, H, ROW_DIM), dev, "q"),
+              _dense(cache, cache_dtype, (NB, BS, ROW_DIM), dev, "cache"), NB, BS,
+              _dense(block_table, i32, (B, M), dev, "block_table"), M,
+              _dense(seq_lens, i32, (B,), dev, "seq_lens"), B, H, softmax_scale, *scale,
+              _dense(lse, f32, (B, H), dev, "lse"),
+              *((None, 0) if previous is None else _rows(previous, f32, (B, S), dev, "previous")),
+              decay, *mass_args, S, _status_word(dev_status, dev), _stream_of(stream, dev)))
+    return mass
+
+
+def mla_attention_mass(q, cache, block_table, seq_lens, softmax_scale, lse, mass, previous=None,
+                       decay=1.0, dev_status=None, stream=None):
+    """mass[b, t] = decay * previous[b, t] + the weight that q[b]'s heads give token t, summed over
+    heads (mass, previous fp32 [B, S], rows at any stride; previous may be mass, or None for
+    nothing; lse as mla_decode left it)."""
+    import torch
+    return _attention_mass(get_lib().mla_attention_mass, torch.bfloat16, (), q, cache, block_table,
+                           seq_lens, softmax_scale, lse, mass, previous, decay, dev_status, stream)
+
+
+def mla_attention_mass_fp8(q, cache8, block_table, seq_lens, softmax_scale, lse, mass,
+                           previous=None, decay=1.0, kv_scale=1.0, dev_status=None, stream=None):
+    """mla_attention_mass over an FP8 (E4M3) cache: row elements are value(code) * kv_scale."""
+    import torch
+    return _attention_mass(get_lib().mla_attention_mass_fp8, torch.uint8, (float(kv_scale),), q,
+                           cache8, block_table, seq_lens, softmax_scale, lse, mass, previous, decay,
+                           dev_status, stream)
+
+
+def mla_evict_select(mass, seq_lens, keep, new_lens, sink=0, recent=0, dev_status=None,
+                     stream=None):
+    """The tokens that stay when every request may keep K: keep int32 [B, K] gets their positions,
+    ascending (then -1), new_lens int32 [B] how many.  Of a longer request the first `sink`, the
+    last `recent`, and of the others those of the largest mass (fp32 [B, S])."""
+    import torch
+    i32 = torch.int32
+    B, S = _shape(mass, 2, "mass")
+    dev = _current(mass, "mass")
+    K = _shape(keep, 2, "keep")[1]
+    _check(get_lib().mla_evict_select(
+        *_rows(mass, torch.float32, (B, S), dev, "mass"), S,
+        _dense(seq_lens, i32, (B,), dev, "seq_lens"), B, sink, recent,
+        _dense(keep, i32, (B, K), dev, "keep"), K, _dense(new_lens, i32, (B,), dev, "new_lens"),
+        _status_word(dev_status, dev), _stream_of(stream, dev)))
+    return keep, new_lens
+
+
+def _cache_compact(fn, cache_dtype, cache, block_table, keep, seq_lens, new_lens, mass, dev_status,
+                   stream):
+    import torch
+    i32 = torch.int32
+    shape = cache.shape if isinstance(cache, torch.Tensor) and cache.dim() == 4 else (1, *_shape(cache, 3, "cache"))
+    layers, NB, BS, _ = shape
+    dev = _current(cache, "cache")
+    B, M = _shape(block_table, 2, "block_table")
+    K = _shape(keep, 2, "keep")[1]
+    S = 0 if mass is None else _shape(mass, 2, "mass")[1]
+    _check(fn(_dense(cache, cache_dtype, (*shape[4 - cache.dim():3], ROW_DIM), dev, "cache"), layers, NB, BS,
+              _dense(block_table, i32, (B, M), dev, "block_table"), M, B,
+              _dense(keep, i32, (B, K), dev, "keep"), K, _dense(seq_lens, i32, (B,), dev, "seq_lens"),
+              _dense(new_lens, i32, (B,), dev, "new_lens"),
+              *((None, 0) if mass is None else _rows(mass, torch.float32, (B, S), dev, "mass")), S,
+              _status_word(dev_status, dev), _stream_of(stream, dev)))
+
+
+def mla_cache_compact(cache, block_table, keep, seq_lens, new_lens, mass=None, dev_status=None,
+                      stream=None):
+    """In place: row j of request b becomes its row keep[b, j], j < new_lens[b], in cache
+    [NB, BS, 576] or in every layer of [layers, NB, BS, 576]; mass (fp32 [B, S]) alike, its
+    entries from new_lens[b] to seq_lens[b] (the lengths before) set to 0."""
+    import torch
+    _cache_compact(get_lib().mla_cache_compact, torch.bfloat16, cache, block_table, keep, seq_lens,
+                   new_lens, mass, dev_status, stream)
+
+
+def mla_cache_compact_fp8(cache8, block_table, keep, seq_lens, new_lens, mass=None,
+                          dev_status=None, stream=None):
+    """mla_cache_compact for an FP8 (E4M3) cache, uint8."""
+    import torch
+    _cache_compact(get_lib().mla_cache_compact_fp8, torch.uint8, cache8, block_table, keep,
+                   seq_lens, new_lens, mass, dev_status, stream)
 
 
 def place_requests(kv_tokens, ranks: int, capacity_tokens: int = 0):

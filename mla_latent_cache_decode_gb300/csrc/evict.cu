@@ -26,8 +26,8 @@
 #include <atomic>
 #include <cmath>
 
+#include "cluster.cuh"
 #include "common.cuh"
-#include "sm100.cuh"
 #include "trace.h"
 
 namespace mla {
@@ -37,20 +37,9 @@ namespace evict {
 
 using namespace sm100;
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 // What block `rank` of the cluster holds at this block's address p.
 __device__ __forceinline__ uint32_t remote_u32(const uint32_t *p, uint32_t rank) {
-  uint32_t a, v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
+  return cluster_load_u32(cluster_addr(smem_u32(p), rank));
 }
 
 // ---------------------------------------------------------------------------- select

@@ -1,11 +1,53 @@
 // Decode of a batch whose requests begin with the same tokens (sm_103a), see
-// mla_decode_shared.  A block takes a head of a request: each warp every eighth
-// token with a running maximum and sum, the warps' results joined at the end.
+// mla_decode_shared.
+//
+// What is computed: the absorbed-form decode of decode_tc.cu, softmax(scale
+// q . row) over 576 dims times the rows' first 512, for R = batch * heads query
+// rows.  A cached row is 1,152 bytes and 1,088 products a query row: 128 query
+// rows that meet it at once (16 heads of 8 requests as well as 128 heads of one)
+// need 278,528 flops for those bytes, about this GPU's ratio of the two rates.
+// So query rows are packed to 128 over the shared tokens, whatever request they
+// are of, and the tokens behind are each request's own (its heads, padded to 128).
+//
+// Work.  A chain is 128 query rows on a run of tokens: kind A, one for each 128
+// packed rows, on the shared tokens; kind B, one for each request, on its own.
+// (Packing that leaves as many chains as there are requests, 128 heads for one,
+// saves nothing: then there is no kind A and B runs over all tokens.  A request
+// shorter than the shared part is a B over what it sees.)  Chains are cut into
+// units of 256 tokens and the units dealt out to the pairs of SMs in order, in
+// runs of equal cost; every block works the deal out from the lengths, so that
+// there is no plan to keep.  A run's piece of a chain leaves a partial result
+// (normalised, bf16, with its log-sum-exp) and merge_kernel joins them; a whole
+// request in one piece is written at once.
+//
+// A pair of SMs shares each MMA (cta_group::2, M = 128: 64 rows in each SM,
+// 128 lanes hold two halves of N).  An SM's tensor memory then holds O of 64 rows
+// x 512 dims (256 columns) and two S of 64 x 256 tokens (128 columns each), which
+// no single-SM shape does without computing scores twice.
+//   S [128 x 256] = Q K^T   B operand: each block's 128 tokens x 576 dims
+//   O [128 x 512] += P V    B operand: all 256 tokens, each block's 256 dims
+// So a token's row comes into the pair's shared memory almost twice (278 KB a
+// tile and SM against 4,352 clk of MMAs: 64 bytes a clock).  Operands stream
+// through one ring of seven 16 KB slots in the order of use: K(0), K(1), V(0),
+// K(2), V(1), ...; nine items of K and eight of V, each 256 clk of MMAs.  The
+// softmax of tile t runs under P V(t-1) and Q K(t+1).
+//
+// Rows behind the last token of a chain.  Scores of their columns are masked, and
+// P V stops at the next multiple of 16 tokens; V rows up to there have to be
+// zeros (0 * NaN is NaN), which a tensor copy cannot write for rows that exist.
+// The last items of such a chain are copied by a warp's threads instead.
+//
+// Warp roles: 0 loads K and V, 1 issues the MMAs (first block of the pair), 2
+// loads Q, 3 owns the tensor memory, 4-7 run the softmax and write results
+// (thread = 64 rows x 2 halves of a tile's tokens, or of 256 dims).  Every wait is bounded; one that runs out reports
+// MLA_ERR_DEVICE_TIMEOUT and ends the block's other waits.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
+#include "cluster.cuh"
 #include "common.cuh"
-#include "sm100.cuh"
+#include "tmap.h"
 #include "trace.h"
 
 namespace mla {
@@ -15,79 +57,703 @@ namespace shared {
 
 using namespace sm100;
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kRows = 128;          // query rows of a chain
+constexpr int kHalf = kRows / 2;    // ... in each block of a pair
+constexpr int kTile = 256;          // tokens of a unit
+constexpr int kOwn = kTile / 2;     // ... whose scores' operand a block holds
+constexpr int kGroup = 64;          // tokens of an item of V
+constexpr int kChunks = kRow / 64;  // 9
+constexpr int kChunkBytes = kHalf * 128;  // 8 KB: 64 rows x 64 dims
+constexpr int kItemBytes = 16384;
+constexpr int kSlots = 7;
+constexpr int kThreads = 256;
+constexpr int kSoftmaxWarp0 = 4;
+constexpr uint32_t kColO = 0, kColS = 256, kCols = 512;
+constexpr int64_t kUnitCost = 4, kChainCost = 4;  // a chain's start: queries and first keys without MMAs under them
+constexpr int kMaxPairs = 256;
+constexpr uint64_t kWaitBudgetNs = 100000000ull;
+constexpr uint64_t kDrainBudgetNs = 10000000ull;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units, as in decode_tc.cu
+
+struct __align__(1024) Smem {
+  uint8_t ring[kSlots][kItemBytes];
+  uint8_t q[kChunks][kChunkBytes];
+  uint8_t p[kTile / 64][kChunkBytes];  // P: 64 rows x 64 tokens each
+  float max[2][2][kHalf];              // of a row's half of the tokens, by tile parity
+  float sum[2][kHalf];
+  // full, q_full, p_full and o_free count in the first block
+  uint64_t full[kSlots], empty[kSlots], q_full, q_free, s_full[2], p_full, pv_done, o_free, mma_end;
+  uint64_t max_full[2][2], sum_full[2];  // [tile parity][32 rows]: both halves' warps have written
+  int64_t start_cost, total_cost, warp_cost[kThreads / 32];
+  int32_t start_chain;
+  uint32_t tmem_base;
+  int abort;
+};
+static_assert(sizeof(Smem) + 1024 <= 232448, "shared memory");
+
+struct Maps {
+  CUtensorMap k;  // {576, rows}, box {64, min(block_size, 128)}
+  CUtensorMap v;  // {64, rows, 9}, box {64, 64, 2} (pages of 64 rows and more)
+  CUtensorMap q;  // {64, batch * heads, 9}, box {64, 64, 3}
+};
+
+// What a piece's result needs is kept by chain: its pieces are those of the pairs first to last, in
+// slots chain + pair (chains counted in their kind; pairs and chains both ascend, so slots do).
+struct Pieces {
+  int32_t first, last;
+};
 
 struct Params {
-  const __nv_bfloat16 *q, *cache;
+  const __nv_bfloat16 *cache;
   const int32_t *shared_table, *shared_blocks, *block_table, *seq_lens;
   __nv_bfloat16 *out;
   float *lse;
   int32_t *dev_status;
-  int32_t num_blocks, block_size, max_shared_blocks, max_blocks_per_seq, batch, heads;
-  float scale;
+  Pieces *pieces_a, *pieces_b;
+  __nv_bfloat16 *o_a, *o_b;  // [slot][row][512]
+  float *lse_a, *lse_b;      // [slot][row]
+  int32_t num_blocks, block_size, max_shared_blocks, max_blocks_per_seq, batch, heads, pairs;
+  float scale_log2;
 };
 
-__global__ void __launch_bounds__(kThreads) shared_kernel(const Params p) {
-  __shared__ float s_m[kWarps], s_l[kWarps], s_acc[kWarps][kVDim];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = blockIdx.x / p.heads, h = blockIdx.x % p.heads;
-  griddep_wait();
-  int32_t shared = *p.shared_blocks, L = p.seq_lens[b];
-  if (shared < 0 || shared > p.max_shared_blocks) {
-    report(p.dev_status, MLA_ERR_DEVICE_RANGE);
-    shared = min(max(shared, 0), p.max_shared_blocks);
-  }
-  if (L < 0 || L > p.max_blocks_per_seq * p.block_size) {
-    report(p.dev_status, MLA_ERR_DEVICE_RANGE);
-    L = min(max(L, 0), p.max_blocks_per_seq * p.block_size);
-  }
-  float q[18], acc[16], m = -INFINITY, l = 0.f;
-  const __nv_bfloat16 *qr = p.q + ((int64_t)b * p.heads + h) * kRow;
-#pragma unroll
-  for (int i = 0; i < 18; ++i) q[i] = __bfloat162float(qr[32 * i + lane]) * p.scale;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-  for (int32_t t = warp; t < L; t += kWarps) {
-    const int32_t page = t / p.block_size;
-    const int32_t blk = page < shared ? p.shared_table[page] : p.block_table[(int64_t)b * p.max_blocks_per_seq + page];
-    if (blk < 0 || blk >= p.num_blocks) {
-      report(p.dev_status, MLA_ERR_DEVICE_RANGE);
-      continue;
+// The chains of a call, from what the device holds.
+struct Chains {
+  int32_t shared;  // tokens in common
+  int32_t packed;  // chains of kind A, 0: none
+  __device__ Chains(const Params &p, bool speak) {
+    int32_t n = *p.shared_blocks;
+    if (n < 0 || n > p.max_shared_blocks) {
+      if (speak) report(p.dev_status, MLA_ERR_DEVICE_RANGE);
+      n = min(max(n, 0), p.max_shared_blocks);
     }
-    const __nv_bfloat16 *row = p.cache + ((int64_t)blk * p.block_size + t % p.block_size) * kRow;
-    float x[18], s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 18; ++i) {
-      x[i] = __bfloat162float(row[32 * i + lane]);
-      s += x[i] * q[i];
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (s == -INFINITY) continue;
-    const float top = fmaxf(m, s), keep = m == -INFINITY ? 0.f : expf(m - top), w = expf(s - top);
-    m = top;
-    l = l * keep + w;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = acc[i] * keep + w * x[i];
+    shared = n * p.block_size;
+    packed = (int32_t)(((int64_t)p.batch * p.heads + kRows - 1) / kRows);
+    if (packed >= p.batch || shared == 0) packed = 0;
   }
-  if (lane == 0) s_m[warp] = m, s_l[warp] = l;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) s_acc[warp][32 * i + lane] = acc[i];
-  __syncthreads();
-  float top = -INFINITY, total = 0.f;
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w]);
-  for (int d = tid; d < kVDim; d += kThreads) {
-    float o = 0.f;
-    total = 0.f;
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = s_m[w] == -INFINITY ? 0.f : expf(s_m[w] - top);
-      o += f * s_acc[w][d];
-      total += f * s_l[w];
-    }
-    p.out[((int64_t)b * p.heads + h) * kVDim + d] = __float2bfloat16_rn(total == 0.f ? 0.f : o / total);
+  __device__ int32_t length(const Params &p, int32_t b, bool speak) const {
+    const int32_t L = p.seq_lens[b], most = p.max_blocks_per_seq * p.block_size;
+    if (L >= 0 && L <= most) return L;
+    if (speak) report(p.dev_status, MLA_ERR_DEVICE_RANGE);
+    return L < 0 ? 0 : most;
   }
-  if (tid == 0 && p.lse) p.lse[(int64_t)b * p.heads + h] = total == 0.f ? -INFINITY : top + logf(total);
+  // The first token of request b's own chain.
+  __device__ int32_t from(int32_t L) const { return packed > 0 && L >= shared ? shared : 0; }
+  __device__ int32_t units(int32_t L) const { return (L - from(L) + kTile - 1) / kTile; }
+  __device__ int32_t units_a() const { return (shared + kTile - 1) / kTile; }
+  static __device__ int64_t cost(int32_t units) { return units > 0 ? kChainCost + kUnitCost * units : 0; }
+  __device__ int64_t cost_a() const { return packed * cost(units_a()); }
+};
+
+// Pair w's share of cost C over n pairs is [bound(w), bound(w + 1)); a unit belongs where its place,
+// its chain's start and kChainCost and kUnitCost for each unit before it, lies.
+__device__ __forceinline__ int64_t bound(int64_t C, int32_t n, int32_t w) { return (w * C + n - 1) / n; }
+// No pair's share is shorter than a unit, so that a chain has no hole between its first and last pair.
+__device__ __forceinline__ int32_t pairs_for(int64_t C, int32_t pairs) {
+  return (int32_t)min((int64_t)pairs, max((int64_t)1, C / kUnitCost));
 }
+__device__ __forceinline__ Pieces pieces_of(int64_t start, int32_t units, int64_t C, int32_t n) {
+  Pieces r;
+  r.first = (int32_t)((start + kChainCost) * n / C);
+  r.last = (int32_t)((start + kChainCost + kUnitCost * (units - 1)) * n / C);
+  return r;
+}
+
+// A pair's pieces in order.
+struct Walk {
+  const Params &p;
+  const Chains &ch;
+  int64_t x0, x1, at;  // the pair's share, the next chain's start
+  int32_t next_chain;
+  // the current piece: kind, chain, tokens [t0, t1), all of the chain
+  bool packed, whole;
+  int32_t chain, t0, t1;
+  __device__ Walk(const Params &params, const Chains &c, const Smem &s, int32_t pair) : p(params), ch(c) {
+    const int64_t C = s.total_cost;
+    const int32_t n = pairs_for(C, p.pairs);
+    x0 = pair < n ? bound(C, n, pair) : C;
+    x1 = pair < n ? bound(C, n, pair + 1) : C;
+    at = s.start_cost;
+    next_chain = s.start_chain;
+  }
+  __device__ bool next() {
+    const int32_t all = ch.packed + p.batch;
+    while (next_chain < all && at < x1) {
+      packed = next_chain < ch.packed;
+      chain = packed ? next_chain : next_chain - ch.packed;
+      const int32_t end = packed ? ch.shared : ch.length(p, chain, false);
+      const int32_t first = packed ? 0 : ch.from(end);
+      const int32_t units = (end - first + kTile - 1) / kTile;
+      ++next_chain;
+      if (units <= 0) continue;
+      const int64_t place = at + kChainCost;
+      at = place + kUnitCost * units;
+      const int64_t k0 = x0 <= place ? 0 : (x0 - place + kUnitCost - 1) / kUnitCost;
+      const int64_t k1 = x1 <= place ? 0 : min((int64_t)units, (x1 - place + kUnitCost - 1) / kUnitCost);
+      if (k0 >= k1) continue;
+      t0 = first + (int32_t)k0 * kTile;
+      t1 = min(end, first + (int32_t)k1 * kTile);
+      whole = !packed && first == 0 && t0 == 0 && t1 == end;
+      return true;
+    }
+    return false;
+  }
+  // The packed query row of the piece's first.
+  __device__ int32_t row() const { return packed ? chain * kRows : chain * p.heads; }
+};
+
+__device__ __forceinline__ int groups_of(int n) { return (n + kGroup - 1) / kGroup; }
+
+__device__ __forceinline__ void set_abort(Smem &s, int32_t *dev_status) {
+  s.abort = 1;
+  report(dev_status, MLA_ERR_DEVICE_TIMEOUT);
+}
+
+// Every lane polls, then the warp agrees.
+__device__ __forceinline__ bool warp_wait(Smem &s, uint64_t *bar, uint32_t parity, int32_t *dev_status) {
+  const bool ok = mbar_wait_cluster(smem_u32(bar), parity, &s.abort, kWaitBudgetNs);
+  if (__all_sync(0xffffffffu, ok)) return true;
+  if ((threadIdx.x & 31) == 0) set_abort(s, dev_status);
+  return false;
+}
+
+// The pool's row of token t (the first of a run inside one page), 0 if its block is none (reported).
+__device__ __forceinline__ int32_t pool_row(const Params &p, const Walk &w, int32_t t) {
+  const int32_t page = t / p.block_size;
+  const int32_t blk = t < w.ch.shared ? p.shared_table[page] : p.block_table[(int64_t)w.chain * p.max_blocks_per_seq + page];
+  if (blk < 0 || blk >= p.num_blocks) {
+    report(p.dev_status, MLA_ERR_DEVICE_RANGE);
+    return 0;
+  }
+  return blk * p.block_size + (t - page * p.block_size);
+}
+
+__global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_constant__ Maps maps, const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  Smem &s = *reinterpret_cast<Smem *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank();
+  const int32_t pair = (int32_t)cluster_id();
+  const bool first_block = rank == 0;
+
+  if (tid == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(smem_u32(&s.full[i]), 2);
+      mbar_init(smem_u32(&s.empty[i]), 1);
+    }
+    mbar_init(smem_u32(&s.q_full), 2);
+    mbar_init(smem_u32(&s.q_free), 1);
+    mbar_init(smem_u32(&s.s_full[0]), 1);
+    mbar_init(smem_u32(&s.s_full[1]), 1);
+    mbar_init(smem_u32(&s.p_full), 8);
+    mbar_init(smem_u32(&s.pv_done), 1);
+    mbar_init(smem_u32(&s.o_free), 8);
+    mbar_init(smem_u32(&s.mma_end), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&s.max_full[0][i]), 2);
+      mbar_init(smem_u32(&s.max_full[1][i]), 2);
+      mbar_init(smem_u32(&s.sum_full[i]), 2);
+    }
+    s.abort = 0;
+    fence_mbarrier_init_cluster();
+    prefetch_tmap(&maps.k);
+    prefetch_tmap(&maps.v);
+    prefetch_tmap(&maps.q);
+  }
+  if (warp == 3) {
+    tmem_alloc_pair(smem_u32(&s.tmem_base), kCols);
+    tmem_relinquish_pair();
+  }
+  griddep_wait();
+  griddep_launch_dependents();  // the merge waits for this grid's end, on the SMs' free threads
+
+  // ---------------------------------------------------------------- the deal
+  const bool speaker = blockIdx.x == 0;
+  const Chains ch(p, speaker && tid == 0);
+  {
+    int64_t base = ch.cost_a();
+    for (int turn = 0; turn < 2; ++turn) {  // the total, then where this pair's share starts
+      int64_t before = ch.cost_a();
+      const int64_t C = base;
+      const int32_t n = pairs_for(C, p.pairs);
+      const int64_t x0 = turn && pair < n ? bound(C, n, pair) : 0;
+      if (turn) {
+        if (tid == 0) {
+          s.total_cost = C;
+          s.start_chain = ch.packed + p.batch;  // nothing
+          s.start_cost = C;
+          if (ch.packed > 0 && x0 < before && pair < n) {
+            const int64_t each = ch.cost(ch.units_a());
+            s.start_chain = (int32_t)(x0 / each);
+            s.start_cost = s.start_chain * each;
+          }
+        }
+        if (speaker)
+          for (int32_t i = tid; i < ch.packed; i += kThreads)
+            p.pieces_a[i] = pieces_of(i * ch.cost(ch.units_a()), ch.units_a(), C, n);
+        __syncthreads();
+      }
+      for (int32_t b0 = 0; b0 < p.batch; b0 += kThreads) {
+        const int32_t b = b0 + tid;
+        const int32_t units = b < p.batch ? ch.units(ch.length(p, b, speaker && turn)) : 0;
+        const int64_t mine = ch.cost(units);
+        int64_t incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += y;
+        }
+        if (lane == 31) s.warp_cost[warp] = incl;
+        __syncthreads();
+        int64_t all = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+          if (w < warp) incl += s.warp_cost[w];
+          all += s.warp_cost[w];
+        }
+        if (turn && mine > 0) {
+          const int64_t start = before + incl - mine;
+          if (speaker) p.pieces_b[b] = pieces_of(start, units, C, n);
+          if (pair < n && start <= x0 && x0 < start + mine) {
+            s.start_chain = ch.packed + b;
+            s.start_cost = start;
+          }
+        }
+        before += all;
+        __syncthreads();
+      }
+      base = before;
+    }
+  }
+  tc_fence_before();
+  cluster_sync();  // barriers and tensor memory are ready in both blocks
+  tc_fence_after();
+  const uint32_t tmem = s.tmem_base;
+  const int BS = p.block_size;
+  Walk walk(p, ch, s, pair);
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- K and V
+    // Lane i < 16 knows the pool row of tokens 16 i .. 16 i + 15 of a tile.
+    uint32_t it = 0;
+    bool ok = true;
+    const int k_rows = min(BS, kOwn), v_rows = min(BS, kGroup);
+    // The two items with zeros are copied by the warp's threads, and handed over when the next load
+    // would have to wait (it may be for these two) or there is none.
+    bool open_items = false;
+    uint32_t open_at = 0;
+    auto hand_over = [&]() {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0)
+        for (int j = 0; j < 2; ++j) mbar_arrive_cluster(cluster_addr(smem_u32(&s.full[(open_at + j) % kSlots]), 0));
+      open_items = false;
+    };
+    auto acquire = [&]() {  // the slot of item `it`
+      uint64_t *bar = &s.empty[it % kSlots];
+      const uint32_t parity = ((it / kSlots) & 1u) ^ 1u;
+      if (open_items) {
+        if (__all_sync(0xffffffffu, mbar_try_wait_cluster(smem_u32(bar), parity))) return true;
+        hand_over();
+      }
+      return warp_wait(s, bar, parity, p.dev_status);
+    };
+    while (ok && walk.next()) {
+      auto rows_at = [&](int32_t tt) { return lane < 16 && tt + 16 * lane < walk.t1 ? pool_row(p, walk, tt + 16 * lane) : 0; };
+      int32_t y_v = 0, y_k = rows_at(walk.t0);
+      const int32_t tiles = (walk.t1 - walk.t0 + kTile - 1) / kTile;
+      for (int32_t t = 0; ok && t <= tiles; ++t) {
+        // K of tile t, then V of tile t - 1
+        if (t < tiles) {
+          const int32_t tt = walk.t0 + t * kTile, n = min(kTile, walk.t1 - tt);
+          const int32_t own = min(max(n - (int)rank * kOwn, 0), kOwn);
+          const int32_t boxes = (own + k_rows - 1) / k_rows;
+          const int32_t other = min(max(n - (1 - (int)rank) * kOwn, 0), kOwn);
+          const uint32_t bytes = (uint32_t)((boxes + (other + k_rows - 1) / k_rows) * k_rows * 128);
+          for (int c = 0; c < kChunks; ++c, ++it) {
+            const int sl = it % kSlots;
+            if (!(ok = acquire())) break;
+            const uint32_t bar = cluster_addr(smem_u32(&s.full[sl]), 0);
+            if (lane == 0) {
+              if (first_block) mbar_arrive_expect_tx(smem_u32(&s.full[sl]), bytes);
+              else mbar_arrive_cluster(bar);
+            }
+            for (int i = 0; i < boxes; ++i) {
+              const int32_t y = __shfl_sync(0xffffffffu, y_k, ((int)rank * kOwn + i * k_rows) / 16);
+              if (lane == 0) tma_load_2d_pair(smem_u32(s.ring[sl]) + i * k_rows * 128, &maps.k, 64 * c, y, bar);
+            }
+          }
+        }
+        const int32_t y_next = t + 1 < tiles ? rows_at(walk.t0 + (t + 1) * kTile) : 0;
+        if (ok && t > 0) {
+          const int32_t tt = walk.t0 + (t - 1) * kTile, n = min(kTile, walk.t1 - tt);
+          for (int g = 0; ok && g < groups_of(n); ++g) {
+            const int32_t cnt = min(kGroup, n - g * kGroup);
+            if (cnt & 15) {
+              // the chain's last tokens: rows up to the next multiple of 16 are zeros
+              for (int j = 0; j < 2; ++j, ++it) {
+                if (!(ok = acquire())) break;
+                const uint32_t ring = smem_u32(s.ring[it % kSlots]);
+                const int dim0 = 64 * (4 * j + 2 * (int)rank);
+                for (int u = lane; u < ((cnt + 15) & ~15) * 16; u += 32) {
+                  const int r = u >> 4, c = u & 15;  // 16 bytes c of row r's 256
+                  const int64_t y = r < cnt ? pool_row(p, walk, tt + g * kGroup + r) : 0;
+                  const uint32_t dst = ring + (c >> 3) * kChunkBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+                  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(p.cache + y * kRow + dim0 + 8 * c),
+                               "r"(r < cnt ? 16 : 0)
+                               : "memory");
+                }
+              }
+              open_items = ok;
+              open_at = it - 2;
+              break;
+            }
+            const int32_t boxes = (cnt + v_rows - 1) / v_rows;
+            const uint32_t bytes = (uint32_t)(2 * 2 * boxes * v_rows * 128);  // two chunks, two blocks
+            for (int j = 0; j < 2; ++j, ++it) {
+              const int sl = it % kSlots;
+              if (!(ok = acquire())) break;
+              const uint32_t bar = cluster_addr(smem_u32(&s.full[sl]), 0);
+              if (lane == 0) {
+                if (first_block) mbar_arrive_expect_tx(smem_u32(&s.full[sl]), bytes);
+                else mbar_arrive_cluster(bar);
+              }
+              const int chunk = 4 * j + 2 * (int)rank;
+              for (int i = 0; i < boxes; ++i) {
+                const int32_t y = __shfl_sync(0xffffffffu, y_v, (g * kGroup + i * v_rows) / 16);
+                if (lane == 0) {
+                  const uint32_t dst = smem_u32(s.ring[sl]) + i * v_rows * 128;
+                  if (BS >= kGroup) {
+                    tma_load_3d_pair(dst, &maps.v, 0, y, chunk, bar);
+                  } else {
+                    tma_load_2d_pair(dst, &maps.k, 64 * chunk, y, bar);
+                    tma_load_2d_pair(dst + kChunkBytes, &maps.k, 64 * (chunk + 1), y, bar);
+                  }
+                }
+              }
+            }
+          }
+        }
+        y_v = y_k;
+        y_k = y_next;
+      }
+    }
+    if (open_items) hand_over();
+    if (s.abort && first_block) {  // let the loads in flight land in both blocks
+      for (uint32_t i = it > kSlots ? it - kSlots : 0; i < it; ++i)
+        (void)mbar_wait_cluster(smem_u32(&s.full[i % kSlots]), (i / kSlots) & 1u, nullptr, kDrainBudgetNs);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMAs
+    if (first_block && elect_one_sync()) {
+      const uint32_t id_s = idesc_bf16_f32(kRows, kTile, 0), id_o = idesc_bf16_f32(kRows, 256, 1);
+      const uint64_t d_q = smem_desc(smem_u32(s.q[0]), 16, 1024, kSwizzle128B);
+      const uint64_t d_p = smem_desc(smem_u32(s.p[0]), 16, 1024, kSwizzle128B);
+      const uint64_t d_k = smem_desc(smem_u32(s.ring[0]), 16, 1024, kSwizzle128B);
+      const uint64_t d_v = smem_desc(smem_u32(s.ring[0]), kChunkBytes, 1024, kSwizzle128B);
+      uint32_t it = 0, g = 0, piece = 0;  // ring items, tiles whose K / V came
+      bool ok = true;
+      auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (!mbar_wait_cluster(smem_u32(bar), parity, &s.abort, kWaitBudgetNs)) {
+          set_abort(s, p.dev_status);
+          ok = false;
+        }
+        return ok;
+      };
+      while (ok && walk.next()) {
+        if (!wait(&s.q_full, piece & 1u)) break;
+        const int32_t tiles = (walk.t1 - walk.t0 + kTile - 1) / kTile;
+        for (int32_t t = 0; ok && t <= tiles; ++t) {
+          if (t < tiles) {
+            // this S was read by the softmax of tile g - 2, whose P V has been issued
+            const uint32_t d = tmem + kColS + 128 * ((g + t) & 1u);
+            for (int c = 0; ok && c < kChunks; ++c, ++it) {
+              const int sl = it % kSlots;
+              if (!wait(&s.full[sl], (it / kSlots) & 1u)) break;
+              tc_fence_after();
+              const uint64_t a = d_q + (uint64_t)(c * kChunkBytes >> 4), b = d_k + (uint64_t)(sl * kItemBytes >> 4);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) mma_ss_pair(d, a + 2 * k, b + 2 * k, id_s, (c | k) ? 1u : 0u);
+              mma_commit_pair(smem_u32(&s.empty[sl]));
+            }
+            if (!ok) break;
+            mma_commit_pair(smem_u32(&s.s_full[(g + t) & 1u]));
+            if (t + 1 == tiles) mma_commit_pair(smem_u32(&s.q_free));
+          }
+          if (t > 0) {
+            const uint32_t gt = g + t - 1;
+            if (!wait(&s.p_full, gt & 1u)) break;
+            if (t == 1 && piece > 0 && !wait(&s.o_free, (piece - 1) & 1u)) break;  // the last piece's O is out
+            tc_fence_after();
+            const int32_t n = min(kTile, walk.t1 - (walk.t0 + (t - 1) * kTile));
+            for (int gr = 0; ok && gr < groups_of(n); ++gr) {
+              const int steps = (min(kGroup, n - gr * kGroup) + 15) >> 4;
+              for (int j = 0; ok && j < 2; ++j, ++it) {
+                const int sl = it % kSlots;
+                if (!wait(&s.full[sl], (it / kSlots) & 1u)) break;
+                tc_fence_after();
+                const uint64_t a = d_p + (uint64_t)(gr * kChunkBytes >> 4), b = d_v + (uint64_t)(sl * kItemBytes >> 4);
+                for (int k = 0; k < steps; ++k)
+                  mma_ss_pair(tmem + kColO + 128 * j, a + 2 * k, b + 128 * k, id_o, (t > 1 || gr > 0 || k > 0) ? 1u : 0u);
+                mma_commit_pair(smem_u32(&s.empty[sl]));
+              }
+            }
+            if (!ok) break;
+            mma_commit_pair(smem_u32(&s.pv_done));
+          }
+        }
+        g += tiles;
+        ++piece;
+      }
+      mma_commit_pair(smem_u32(&s.mma_end));
+      if (!mbar_wait_cluster(smem_u32(&s.mma_end), 0, nullptr, kWaitBudgetNs)) report(p.dev_status, MLA_ERR_DEVICE_TIMEOUT);
+    }
+  } else if (warp == 2) {
+    // ---------------------------------------------------------------- Q
+    uint32_t piece = 0;
+    const uint32_t bar = cluster_addr(smem_u32(&s.q_full), 0);
+    while (walk.next()) {
+      if (piece > 0 && !warp_wait(s, &s.q_free, (piece - 1) & 1u, p.dev_status)) break;
+      if (lane == 0) {
+        if (first_block) mbar_arrive_expect_tx(smem_u32(&s.q_full), 2 * kChunks * kChunkBytes);
+        else mbar_arrive_cluster(bar);
+        for (int c = 0; c < kChunks; c += 3) tma_load_3d_pair(smem_u32(s.q[c]), &maps.q, 0, walk.row() + (int)rank * kHalf, c, bar);
+      }
+      ++piece;
+    }
+    if (s.abort && first_block && piece > 0)
+      (void)mbar_wait_cluster(smem_u32(&s.q_full), (piece - 1) & 1u, nullptr, kDrainBudgetNs);
+  } else if (warp >= kSoftmaxWarp0) {
+    // ---------------------------------------------------------------- softmax, results
+    const int quarter = warp - kSoftmaxWarp0, half = quarter >> 1;  // of the tile's tokens; of 256 dims
+    const int r = (quarter & 1) * 32 + lane;                        // this block's row
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t p_bar = cluster_addr(smem_u32(&s.p_full), 0), o_bar = cluster_addr(smem_u32(&s.o_free), 0);
+    const float c = p.scale_log2;
+    uint32_t g = 0, piece = 0;
+    bool ok = true;
+    while (ok && walk.next()) {
+      float m_used = -INFINITY, l = 0.f;
+      for (int32_t tt = walk.t0; tt < walk.t1; tt += kTile, ++g) {
+        const int32_t mine = min(max(walk.t1 - tt - half * kOwn, 0), kOwn);  // real tokens of this half
+        if (!warp_wait(s, &s.s_full[g & 1u], (g >> 1) & 1u, p.dev_status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t src = lanes + kColS + 128 * (g & 1u);
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t x[32];
+          tmem_ld32(src + 32 * i, x);
+          tmem_wait_ld();
+          if (mine >= 32 * (i + 1)) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) top = fmaxf(top, __uint_as_float(x[k]));
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) top = 32 * i + k < mine ? fmaxf(top, __uint_as_float(x[k])) : top;
+          }
+        }
+        s.max[g & 1u][half][r] = top;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s.max_full[g & 1u][quarter & 1]));
+        if (!warp_wait(s, &s.max_full[g & 1u][quarter & 1], (g >> 1) & 1u, p.dev_status)) {
+          ok = false;
+          break;
+        }
+        top = fmaxf(top, s.max[g & 1u][half ^ 1][r]) * c;
+        float alpha = 1.f;
+        if (top > m_used + kRescaleThreshold || tt == walk.t0) {
+          alpha = ex2_approx(m_used - top);  // (0 at first; NaN if both are -inf, where nothing is summed yet)
+          if (m_used == -INFINITY) alpha = 0.f;
+          m_used = top;
+        }
+        const float shift = m_used == -INFINITY ? 0.f : m_used;
+        uint32_t w[64];
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t x[32];
+          tmem_ld32(src + 32 * i, x);
+          tmem_wait_ld();
+          float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            float a = ex2_approx(fmaf(__uint_as_float(x[2 * k]), c, -shift)), b = ex2_approx(fmaf(__uint_as_float(x[2 * k + 1]), c, -shift));
+            if (mine < 32 * (i + 1)) {
+              if (32 * i + 2 * k >= mine) a = 0.f;
+              if (32 * i + 2 * k + 1 >= mine) b = 0.f;
+            }
+            s0 += a;
+            s1 += b;
+            __nv_bfloat162 two = __floats2bfloat162_rn(a, b);
+            w[16 * i + k] = *reinterpret_cast<uint32_t *>(&two);
+          }
+          sum += s0 + s1;
+        }
+        l = l * alpha + sum;
+        // P and O are free once the P V of the tile before is done
+        if (g > 0 && !warp_wait(s, &s.pv_done, (g - 1) & 1u, p.dev_status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (tt > walk.t0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+          for (int i = 0; i < 8; ++i) {
+            uint32_t o[32];
+            tmem_ld32(lanes + kColO + 32 * i, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+            tmem_st32(lanes + kColO + 32 * i, o);
+          }
+          tmem_wait_st();
+        }
+#pragma unroll
+        for (int u = 0; u < 16; ++u)
+          *reinterpret_cast<uint4 *>(s.p[2 * half + (u >> 3)] + r * 128 + (((u & 7) ^ (r & 7)) << 4)) =
+              make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+        fence_proxy_async_shared();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(p_bar);
+      }
+      if (!ok) break;
+      // ---- O / l
+      s.sum[half][r] = l;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&s.sum_full[quarter & 1]));
+      if (!warp_wait(s, &s.sum_full[quarter & 1], piece & 1u, p.dev_status) || !warp_wait(s, &s.pv_done, (g - 1) & 1u, p.dev_status)) break;
+      ++piece;
+      l += s.sum[half ^ 1][r];
+      tc_fence_after();
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float lse = l == 0.f ? -INFINITY : (m_used + log2f(l)) * 0.69314718055994531f;
+      const int row = (int)rank * kHalf + r;  // of the chain
+      __nv_bfloat16 *dst;
+      float *lse_dst;
+      if (walk.packed) {
+        const int64_t at = ((int64_t)walk.chain + pair) * kRows + row;
+        dst = p.o_a + at * kVDim;
+        lse_dst = p.lse_a + at;
+      } else if (walk.whole) {
+        const int64_t at = (int64_t)walk.chain * p.heads + row;
+        dst = p.out + at * kVDim;
+        lse_dst = p.lse ? p.lse + at : nullptr;
+      } else {
+        const int64_t at = ((int64_t)walk.chain + pair) * p.heads + row;
+        dst = p.o_b + at * kVDim;
+        lse_dst = p.lse_b + at;
+      }
+      const bool real = walk.packed || row < p.heads;
+#pragma unroll 1
+      for (int i = 0; i < 8; ++i) {
+        uint32_t o[32];
+        tmem_ld32(lanes + kColO + 32 * i, o);
+        tmem_wait_ld();
+        uint4 v[4];
+        uint32_t *vw = reinterpret_cast<uint32_t *>(v);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          __nv_bfloat162 two = __floats2bfloat162_rn(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+          vw[k] = *reinterpret_cast<uint32_t *>(&two);
+        }
+        if (real) {
+          uint4 *to = reinterpret_cast<uint4 *>(dst + 256 * (i >> 2) + 128 * half + 32 * (i & 3));
+#pragma unroll
+          for (int k = 0; k < 4; ++k) to[k] = v[k];
+        }
+      }
+      if (real && half == 0 && lse_dst) *lse_dst = lse;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(o_bar);
+    }
+  }
+
+  // ---------------------------------------------------------------- the end
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();  // nobody arrives at a block that has left
+  tc_fence_after();
+  if (warp == 3) tmem_dealloc_pair(tmem, kCols);
+}
+
+// ---------------------------------------------------------------------------- merge
+
+// A warp joins the pieces of a query row: those of its packed chain on the shared tokens and those of
+// its request's own.  out = sum_i e^(lse_i - M) o_i / sum_i e^(lse_i - M), in fp32.
+constexpr int kMergeThreads = 256, kMergeFlight = 4;
+
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
+  griddep_wait();
+  if (row >= (int64_t)p.batch * p.heads) return;
+  const int32_t b = (int32_t)(row / p.heads), h = (int32_t)(row % p.heads);
+  const Chains ch(p, false);
+  const int32_t L = ch.length(p, b, false);
+  const Pieces none = {0, -1};
+  const Pieces own = ch.units(L) > 0 ? p.pieces_b[b] : none;
+  const Pieces com = ch.packed > 0 && L >= ch.shared ? p.pieces_a[row / kRows] : none;
+  const int na = com.last - com.first + 1, nb = own.last - own.first + 1;
+  if (ch.from(L) == 0 && nb == 1) return;  // written at once
+  const int64_t a0 = (row / kRows + com.first) * kRows + row % kRows;
+  const int64_t b0 = ((int64_t)b + own.first) * p.heads + h;
+  float m = -INFINITY, z = 0.f, acc[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) acc[k] = 0.f;
+  for (int i0 = 0; i0 < na + nb; i0 += kMergeFlight) {
+    float l[kMergeFlight];
+    uint4 x[kMergeFlight][2];
+#pragma unroll
+    for (int u = 0; u < kMergeFlight; ++u) {
+      const int i = min(i0 + u, na + nb - 1);
+      const int64_t at = i < na ? a0 + (int64_t)i * kRows : b0 + (int64_t)(i - na) * p.heads;
+      l[u] = i0 + u < na + nb ? (i < na ? p.lse_a : p.lse_b)[at] : -INFINITY;
+      const uint4 *src = reinterpret_cast<const uint4 *>((i < na ? p.o_a : p.o_b) + at * kVDim);
+      x[u][0] = src[lane];
+      x[u][1] = src[32 + lane];
+    }
+    float top = m;
+#pragma unroll
+    for (int u = 0; u < kMergeFlight; ++u) top = fmaxf(top, l[u]);
+    const float keep = m == -INFINITY ? 0.f : ex2_approx((m - top) * 1.4426950408889634f);
+    m = top;
+    z *= keep;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) acc[k] *= keep;
+#pragma unroll
+    for (int u = 0; u < kMergeFlight; ++u) {
+      const float w = l[u] == -INFINITY ? 0.f : ex2_approx((l[u] - (m == -INFINITY ? 0.f : m)) * 1.4426950408889634f);
+      z += w;
+      const uint32_t v[8] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w, x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
+      if (w != 0.f) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          acc[2 * k] += w * __uint_as_float(v[k] << 16);
+          acc[2 * k + 1] += w * __uint_as_float(v[k] & 0xffff0000u);
+        }
+      }
+    }
+  }
+  const float inv = z == 0.f ? 0.f : 1.f / z;
+  uint4 o[2];
+  uint32_t *ow = reinterpret_cast<uint32_t *>(o);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    __nv_bfloat162 two = __floats2bfloat162_rn(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+    ow[k] = *reinterpret_cast<uint32_t *>(&two);
+  }
+  uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * kVDim);
+  dst[lane] = o[0];
+  dst[32 + lane] = o[1];
+  if (lane == 0 && p.lse) p.lse[row] = z == 0.f ? -INFINITY : m + logf(z);
+}
+
+// ---------------------------------------------------------------------------- host
 
 mla_status_t invalid(const char *why) {
   set_error_detail(why);
@@ -95,6 +761,57 @@ mla_status_t invalid(const char *why) {
 }
 
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+mla_status_t status_of(cudaError_t e) {
+  if (e == cudaSuccess) return MLA_OK;
+  set_error_detail(cudaGetErrorString(e));
+  return MLA_ERR_CUDA;
+}
+
+// Pairs of SMs of the current device that run at once, 0 if it cannot be asked.
+int pairs_current() {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = known[dev].load(std::memory_order_acquire);
+  if (n > 0) return n;
+  const int smem = (int)sizeof(Smem) + 1024;
+  if (cudaFuncSetAttribute(shared_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return 0;
+  int sms = 0;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(sms / 2 * 2);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, shared_kernel, &cfg) != cudaSuccess || n < 1) return 0;
+  n = std::min(n, kMaxPairs);
+  known[dev].store(n, std::memory_order_release);
+  return n;
+}
+
+struct Layout {
+  size_t pieces_a, pieces_b, lse_a, lse_b, o_a, o_b, total;
+};
+
+Layout layout(int64_t batch, int64_t heads, int64_t pairs) {
+  const int64_t packed = (batch * heads + kRows - 1) / kRows;
+  Layout l;
+  size_t o = 0;
+  l.pieces_a = o; o = align256(o + sizeof(Pieces) * packed);
+  l.pieces_b = o; o = align256(o + sizeof(Pieces) * batch);
+  l.lse_a = o;    o = align256(o + sizeof(float) * (packed + pairs) * kRows);
+  l.lse_b = o;    o = align256(o + sizeof(float) * (batch + pairs) * heads);
+  l.o_a = o;      o = align256(o + sizeof(__nv_bfloat16) * (packed + pairs) * kRows * kVDim);
+  l.o_b = o;      o = align256(o + sizeof(__nv_bfloat16) * (batch + pairs) * heads * kVDim);
+  l.total = o;
+  return l;
+}
 
 }  // namespace shared
 }  // namespace mla
@@ -104,8 +821,9 @@ using namespace mla;
 extern "C" {
 
 size_t mla_decode_shared_workspace_size(int32_t batch, int32_t num_heads) {
-  if (batch < 0 || num_heads < 1 || num_heads > kHeads) return 0;
-  return 256;
+  if (batch < 0 || batch > 1 << 20 || num_heads < 1 || num_heads > kHeads) return 0;
+  const int pairs = shared::pairs_current();
+  return pairs > 0 ? shared::layout(batch, num_heads, pairs).total : 0;
 }
 
 mla_status_t mla_decode_shared(const void *q, const void *cache, int64_t num_blocks, int32_t block_size, const int32_t *shared_table,
@@ -127,8 +845,8 @@ mla_status_t mla_decode_shared(const void *q, const void *cache, int64_t num_blo
     return MLA_ERR_UNSUPPORTED;
   }
   if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.f)) return invalid("softmax_scale must be positive and finite");
-  if (num_blocks <= 0 || num_blocks > INT32_MAX || max_blocks_per_seq <= 0 || (int64_t)max_blocks_per_seq * block_size > 1 << 30 ||
-      (int64_t)max_shared_blocks * block_size > 1 << 30)
+  if (num_blocks <= 0 || num_blocks * block_size > INT32_MAX || max_blocks_per_seq <= 0 ||
+      (int64_t)max_blocks_per_seq * block_size > 1 << 30 || (int64_t)max_shared_blocks * block_size > 1 << 30)
     return invalid("num_blocks, max_blocks_per_seq or max_shared_blocks out of range");
   if (batch > 1 << 20) return invalid("batch > 2^20");
   if (batch == 0) return MLA_OK;
@@ -138,13 +856,22 @@ mla_status_t mla_decode_shared(const void *q, const void *cache, int64_t num_blo
   if (!aligned(shared_table, 4) || !aligned(shared_blocks, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(lse, 4))
     return invalid("shared_table, shared_blocks, block_table, seq_lens and lse must be 4-byte aligned");
   if (!aligned(workspace, 256)) return invalid("workspace must be 256-byte aligned");
-  const size_t need = mla_decode_shared_workspace_size(batch, num_heads);
-  if (workspace_bytes < need) {
+  const int pairs = pairs_current();
+  if (pairs < 1) return status_of(cudaErrorInvalidDevice);
+  const Layout l = layout(batch, num_heads, pairs);
+  if (workspace_bytes < l.total) {
     set_error_detail("workspace is smaller than mla_decode_shared_workspace_size()");
     return MLA_ERR_WORKSPACE_TOO_SMALL;
   }
+  Maps maps;
+  const int64_t rows = num_blocks * block_size;
+  if (!tmap::encode_2d(&maps.k, cache, rows, (uint32_t)std::min(block_size, kOwn)) || !tmap::encode_3d(&maps.v, cache, rows, kGroup, 2) ||
+      !tmap::encode_3d(&maps.q, q, (int64_t)batch * num_heads, kHalf, 3)) {
+    set_error_detail("cannot describe q or the cache to TMA");
+    return MLA_ERR_CUDA;
+  }
+  char *ws = (char *)workspace;
   Params p;
-  p.q = (const __nv_bfloat16 *)q;
   p.cache = (const __nv_bfloat16 *)cache;
   p.shared_table = shared_table;
   p.shared_blocks = shared_blocks;
@@ -153,18 +880,41 @@ mla_status_t mla_decode_shared(const void *q, const void *cache, int64_t num_blo
   p.out = (__nv_bfloat16 *)out;
   p.lse = lse;
   p.dev_status = dev_status;
+  p.pieces_a = (Pieces *)(ws + l.pieces_a);
+  p.pieces_b = (Pieces *)(ws + l.pieces_b);
+  p.lse_a = (float *)(ws + l.lse_a);
+  p.lse_b = (float *)(ws + l.lse_b);
+  p.o_a = (__nv_bfloat16 *)(ws + l.o_a);
+  p.o_b = (__nv_bfloat16 *)(ws + l.o_b);
   p.num_blocks = (int32_t)num_blocks;
   p.block_size = block_size;
   p.max_shared_blocks = max_shared_blocks;
   p.max_blocks_per_seq = max_blocks_per_seq;
   p.batch = batch;
   p.heads = num_heads;
-  p.scale = softmax_scale;
-  shared_kernel<<<batch * num_heads, kThreads, 0, (cudaStream_t)stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) return MLA_OK;
-  set_error_detail(cudaGetErrorString(e));
-  return MLA_ERR_CUDA;
+  p.pairs = pairs;
+  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * pairs);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = sizeof(Smem) + 1024;
+  cfg.stream = (cudaStream_t)stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, shared_kernel, maps, p);
+  if (e != cudaSuccess) return status_of(e);
+  const int64_t warps = kMergeThreads / 32;
+  cfg.gridDim = dim3((unsigned)(((int64_t)batch * num_heads + warps - 1) / warps));
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.dynamicSmemBytes = 0;
+  cfg.numAttrs = 1;
+  return status_of(cudaLaunchKernelEx(&cfg, merge_kernel, p));
 }
 
 }  // extern "C"

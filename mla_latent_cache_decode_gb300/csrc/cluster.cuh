@@ -3,7 +3,7 @@
 // another block's shared memory.
 #pragma once
 
-#include "sm100.cuh"
+#include "sm100_issue.cuh"
 
 namespace mla {
 namespace sm100 {
@@ -35,31 +35,12 @@ __device__ __forceinline__ uint32_t cluster_load_u32(uint32_t addr) {
 }
 // Arrives at a barrier of any block of the cluster, given by its cluster_addr.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+// The same after writes that the other block's MMAs read.
+__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
-// mbar_wait for barriers that other blocks arrive at.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, const volatile int *abort, uint64_t budget_ns) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
-  const uint64_t t0 = globaltimer();
-  for (uint32_t it = 1;; ++it) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    if ((it & 255u) == 0) {
-      if (abort && *abort) return false;
-      if (globaltimer() - t0 > budget_ns) return false;
-    }
-  }
-}
-
 // ------------------------------------------------------------------ loads of a pair
 
 // Box into this block's shared memory; the bytes count at a barrier of either
@@ -90,12 +71,13 @@ __device__ __forceinline__ void tmem_relinquish_pair() {
 __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
-// D (+)= A B, A's rows and B's columns half in each block's shared memory, at the same addresses.
-__device__ __forceinline__ void mma_ss_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+// D (+)= A B, A's rows and B's columns half in each block's shared memory, at the same addresses;
+// descriptors by their low words (sm100_issue.cuh).
+__device__ __forceinline__ void mma_ss_pair_low(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t more) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %4, 0;\n mov.b64 a, {%1, %5};\n mov.b64 b, {%2, %5};\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "r"(more), "n"(kDescHigh)
       : "memory");
 }
 // Arrives at the barrier at this address in both blocks when every MMA issued before has completed.

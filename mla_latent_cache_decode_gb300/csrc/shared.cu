@@ -65,9 +65,9 @@ constexpr int kGroup = 64;          // tokens of an item of V
 constexpr int kChunks = kRow / 64;  // 9
 constexpr int kChunkBytes = kHalf * 128;  // 8 KB: 64 rows x 64 dims
 constexpr int kItemBytes = 16384;
-constexpr int kSlots = 7;
-constexpr int kThreads = 256;
-constexpr int kSoftmaxWarp0 = 4;
+constexpr int kSlotsK = 4, kSlotsV = 3;
+constexpr int kThreads = 384;
+constexpr int kSoftmaxWarp0 = 4, kSoftmaxWarps = 8;
 constexpr uint32_t kColO = 0, kColS = 256, kCols = 512;
 constexpr int64_t kUnitCost = 4, kChainCost = 4;  // a chain's start: queries and first keys without MMAs under them
 constexpr int kMaxPairs = 256;
@@ -76,14 +76,21 @@ constexpr uint64_t kDrainBudgetNs = 10000000ull;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units, as in decode_tc.cu
 
 struct __align__(1024) Smem {
-  uint8_t ring[kSlots][kItemBytes];
+  uint8_t k[kSlotsK][kItemBytes];
+  uint8_t v[kSlotsV][kItemBytes];
   uint8_t q[kChunks][kChunkBytes];
   uint8_t p[kTile / 64][kChunkBytes];  // P: 64 rows x 64 tokens each
-  float max[2][2][kHalf];              // of a row's half of the tokens, by tile parity
-  float sum[2][kHalf];
-  // full, q_full, p_full and o_free count in the first block
-  uint64_t full[kSlots], empty[kSlots], q_full, q_free, s_full[2], p_full, pv_done, o_free, mma_end;
-  uint64_t max_full[2][2], sum_full[2];  // [tile parity][32 rows]: both halves' warps have written
+  float max[2][kHalf][4];              // of a row's quarters of the tokens, by tile parity
+  float sum[kHalf][4];
+  // Loads (k_full, v_full, q_full) and what the MMAs wait for (s_free, p_full, o_free, tail_full) count
+  // in the first block, whose loaders announce the bytes of both blocks' loads; the others in each.
+  // P is handed over and freed by halves (128 tokens), so that a tile's is written while the P V of
+  // the tile before still runs.
+  uint64_t k_full[kSlotsK], k_empty[kSlotsK], v_full[kSlotsV], v_empty[kSlotsV], q_full, q_free;
+  uint64_t s_full[2], s_free[2], p_full[2], p_free[2], pv_done[2], o_free, mma_end;  // (s, pv_done: by tile parity; p: by half)
+  uint64_t tail_full;                    // the other block has filled its items with zeros
+  uint64_t p_here[2];                    // the other block: its P is written, to be said to the first
+  uint64_t max_full[2][2], sum_full[2];  // [tile parity][32 rows]: their four warps have written
   int64_t start_cost, total_cost, warp_cost[kThreads / 32];
   int32_t start_chain;
   uint32_t tmem_base;
@@ -112,7 +119,7 @@ struct Params {
   Pieces *pieces_a, *pieces_b;
   __nv_bfloat16 *o_a, *o_b;  // [slot][row][512]
   float *lse_a, *lse_b;      // [slot][row]
-  int32_t num_blocks, block_size, max_shared_blocks, max_blocks_per_seq, batch, heads, pairs;
+  int32_t num_blocks, block_size, page_log2, max_shared_blocks, max_blocks_per_seq, batch, heads, pairs;
   float scale_log2;
 };
 
@@ -210,23 +217,27 @@ __device__ __forceinline__ void set_abort(Smem &s, int32_t *dev_status) {
 
 // Every lane polls, then the warp agrees.
 __device__ __forceinline__ bool warp_wait(Smem &s, uint64_t *bar, uint32_t parity, int32_t *dev_status) {
-  const bool ok = mbar_wait_cluster(smem_u32(bar), parity, &s.abort, kWaitBudgetNs);
+  const bool ok = mbar_wait(smem_u32(bar), parity, &s.abort, kWaitBudgetNs);
   if (__all_sync(0xffffffffu, ok)) return true;
   if ((threadIdx.x & 31) == 0) set_abort(s, dev_status);
   return false;
 }
 
-// The pool's row of token t (the first of a run inside one page), 0 if its block is none (reported).
-__device__ __forceinline__ int32_t pool_row(const Params &p, const Walk &w, int32_t t) {
-  const int32_t page = t / p.block_size;
-  const int32_t blk = t < w.ch.shared ? p.shared_table[page] : p.block_table[(int64_t)w.chain * p.max_blocks_per_seq + page];
+// The block of token t, and the pool's row of t in it: 0 if it is none (reported).
+__device__ __forceinline__ int32_t block_of(const Params &p, const Walk &w, int32_t t) {
+  const int32_t page = t >> p.page_log2;
+  return t < w.ch.shared ? p.shared_table[page] : p.block_table[(int64_t)w.chain * p.max_blocks_per_seq + page];
+}
+__device__ __forceinline__ int32_t pool_row(const Params &p, int32_t blk, int32_t t) {
   if (blk < 0 || blk >= p.num_blocks) {
     report(p.dev_status, MLA_ERR_DEVICE_RANGE);
     return 0;
   }
-  return blk * p.block_size + (t - page * p.block_size);
+  return (blk << p.page_log2) + (t & (p.block_size - 1));
 }
 
+// kBox: rows of a box of K, min(block_size, 128).
+template <int kBox>
 __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_constant__ Maps maps, const Params p) {
   extern __shared__ uint8_t smem_raw[];
   Smem &s = *reinterpret_cast<Smem *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -236,23 +247,25 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
   const bool first_block = rank == 0;
 
   if (tid == 0) {
-    for (int i = 0; i < kSlots; ++i) {
-      mbar_init(smem_u32(&s.full[i]), 2);
-      mbar_init(smem_u32(&s.empty[i]), 1);
-    }
-    mbar_init(smem_u32(&s.q_full), 2);
-    mbar_init(smem_u32(&s.q_free), 1);
-    mbar_init(smem_u32(&s.s_full[0]), 1);
-    mbar_init(smem_u32(&s.s_full[1]), 1);
-    mbar_init(smem_u32(&s.p_full), 8);
-    mbar_init(smem_u32(&s.pv_done), 1);
-    mbar_init(smem_u32(&s.o_free), 8);
-    mbar_init(smem_u32(&s.mma_end), 1);
+    auto init = [](uint64_t *bar, int count) { mbar_init(smem_u32(bar), count); };
+    for (int i = 0; i < kSlotsK; ++i) init(&s.k_full[i], 1), init(&s.k_empty[i], 1);
+    for (int i = 0; i < kSlotsV; ++i) init(&s.v_full[i], 1), init(&s.v_empty[i], 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&s.max_full[0][i]), 2);
-      mbar_init(smem_u32(&s.max_full[1][i]), 2);
-      mbar_init(smem_u32(&s.sum_full[i]), 2);
+      init(&s.s_full[i], 1);
+      init(&s.s_free[i], 2 * kSoftmaxWarps);
+      init(&s.max_full[0][i], 4);
+      init(&s.max_full[1][i], 4);
+      init(&s.sum_full[i], 4);
+      init(&s.p_full[i], 5);
+      init(&s.p_here[i], 4);
+      init(&s.p_free[i], 1);
+      init(&s.pv_done[i], 1);
     }
+    init(&s.q_full, 1);
+    init(&s.q_free, 1);
+    init(&s.o_free, 2 * kSoftmaxWarps);
+    init(&s.mma_end, 2);
+    init(&s.tail_full, 1);
     s.abort = 0;
     fence_mbarrier_init_cluster();
     prefetch_tmap(&maps.k);
@@ -327,307 +340,326 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
   cluster_sync();  // barriers and tensor memory are ready in both blocks
   tc_fence_after();
   const uint32_t tmem = s.tmem_base;
-  const int BS = p.block_size;
   Walk walk(p, ch, s, pair);
 
+  // The issuing roles are one thread each.
+  auto wait = [&](uint64_t *bar, uint32_t parity) {
+    if (mbar_wait(smem_u32(bar), parity, &s.abort, kWaitBudgetNs)) return true;
+    set_abort(s, p.dev_status);
+    return false;
+  };
+
   if (warp == 0) {
-    // ---------------------------------------------------------------- K and V
-    // Lane i < 16 knows the pool row of tokens 16 i .. 16 i + 15 of a tile.
-    uint32_t it = 0;
-    bool ok = true;
-    const int k_rows = min(BS, kOwn), v_rows = min(BS, kGroup);
-    // The two items with zeros are copied by the warp's threads, and handed over when the next load
-    // would have to wait (it may be for these two) or there is none.
-    bool open_items = false;
-    uint32_t open_at = 0;
-    auto hand_over = [&]() {
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      fence_proxy_async_shared();
-      __syncwarp();
-      if (lane == 0)
-        for (int j = 0; j < 2; ++j) mbar_arrive_cluster(cluster_addr(smem_u32(&s.full[(open_at + j) % kSlots]), 0));
-      open_items = false;
-    };
-    auto acquire = [&]() {  // the slot of item `it`
-      uint64_t *bar = &s.empty[it % kSlots];
-      const uint32_t parity = ((it / kSlots) & 1u) ^ 1u;
-      if (open_items) {
-        if (__all_sync(0xffffffffu, mbar_try_wait_cluster(smem_u32(bar), parity))) return true;
-        hand_over();
-      }
-      return warp_wait(s, bar, parity, p.dev_status);
-    };
-    while (ok && walk.next()) {
-      auto rows_at = [&](int32_t tt) { return lane < 16 && tt + 16 * lane < walk.t1 ? pool_row(p, walk, tt + 16 * lane) : 0; };
-      int32_t y_v = 0, y_k = rows_at(walk.t0);
-      const int32_t tiles = (walk.t1 - walk.t0 + kTile - 1) / kTile;
-      for (int32_t t = 0; ok && t <= tiles; ++t) {
-        // K of tile t, then V of tile t - 1
-        if (t < tiles) {
-          const int32_t tt = walk.t0 + t * kTile, n = min(kTile, walk.t1 - tt);
-          const int32_t own = min(max(n - (int)rank * kOwn, 0), kOwn);
-          const int32_t boxes = (own + k_rows - 1) / k_rows;
-          const int32_t other = min(max(n - (1 - (int)rank) * kOwn, 0), kOwn);
-          const uint32_t bytes = (uint32_t)((boxes + (other + k_rows - 1) / k_rows) * k_rows * 128);
-          for (int c = 0; c < kChunks; ++c, ++it) {
-            const int sl = it % kSlots;
-            if (!(ok = acquire())) break;
-            const uint32_t bar = cluster_addr(smem_u32(&s.full[sl]), 0);
-            if (lane == 0) {
-              if (first_block) mbar_arrive_expect_tx(smem_u32(&s.full[sl]), bytes);
-              else mbar_arrive_cluster(bar);
-            }
-            for (int i = 0; i < boxes; ++i) {
-              const int32_t y = __shfl_sync(0xffffffffu, y_k, ((int)rank * kOwn + i * k_rows) / 16);
-              if (lane == 0) tma_load_2d_pair(smem_u32(s.ring[sl]) + i * k_rows * 128, &maps.k, 64 * c, y, bar);
-            }
-          }
-        }
-        const int32_t y_next = t + 1 < tiles ? rows_at(walk.t0 + (t + 1) * kTile) : 0;
-        if (ok && t > 0) {
-          const int32_t tt = walk.t0 + (t - 1) * kTile, n = min(kTile, walk.t1 - tt);
-          for (int g = 0; ok && g < groups_of(n); ++g) {
-            const int32_t cnt = min(kGroup, n - g * kGroup);
-            if (cnt & 15) {
-              // the chain's last tokens: rows up to the next multiple of 16 are zeros
-              for (int j = 0; j < 2; ++j, ++it) {
-                if (!(ok = acquire())) break;
-                const uint32_t ring = smem_u32(s.ring[it % kSlots]);
-                const int dim0 = 64 * (4 * j + 2 * (int)rank);
-                for (int u = lane; u < ((cnt + 15) & ~15) * 16; u += 32) {
-                  const int r = u >> 4, c = u & 15;  // 16 bytes c of row r's 256
-                  const int64_t y = r < cnt ? pool_row(p, walk, tt + g * kGroup + r) : 0;
-                  const uint32_t dst = ring + (c >> 3) * kChunkBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-                  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(p.cache + y * kRow + dim0 + 8 * c),
-                               "r"(r < cnt ? 16 : 0)
-                               : "memory");
-                }
-              }
-              open_items = ok;
-              open_at = it - 2;
-              break;
-            }
-            const int32_t boxes = (cnt + v_rows - 1) / v_rows;
-            const uint32_t bytes = (uint32_t)(2 * 2 * boxes * v_rows * 128);  // two chunks, two blocks
-            for (int j = 0; j < 2; ++j, ++it) {
-              const int sl = it % kSlots;
-              if (!(ok = acquire())) break;
-              const uint32_t bar = cluster_addr(smem_u32(&s.full[sl]), 0);
-              if (lane == 0) {
-                if (first_block) mbar_arrive_expect_tx(smem_u32(&s.full[sl]), bytes);
-                else mbar_arrive_cluster(bar);
-              }
-              const int chunk = 4 * j + 2 * (int)rank;
-              for (int i = 0; i < boxes; ++i) {
-                const int32_t y = __shfl_sync(0xffffffffu, y_v, (g * kGroup + i * v_rows) / 16);
-                if (lane == 0) {
-                  const uint32_t dst = smem_u32(s.ring[sl]) + i * v_rows * 128;
-                  if (BS >= kGroup) {
-                    tma_load_3d_pair(dst, &maps.v, 0, y, chunk, bar);
-                  } else {
-                    tma_load_2d_pair(dst, &maps.k, 64 * chunk, y, bar);
-                    tma_load_2d_pair(dst + kChunkBytes, &maps.k, 64 * (chunk + 1), y, bar);
-                  }
-                }
-              }
-            }
-          }
-        }
-        y_v = y_k;
-        y_k = y_next;
-      }
-    }
-    if (open_items) hand_over();
-    if (s.abort && first_block) {  // let the loads in flight land in both blocks
-      for (uint32_t i = it > kSlots ? it - kSlots : 0; i < it; ++i)
-        (void)mbar_wait_cluster(smem_u32(&s.full[i % kSlots]), (i / kSlots) & 1u, nullptr, kDrainBudgetNs);
-    }
-  } else if (warp == 1) {
-    // ---------------------------------------------------------------- MMAs
-    if (first_block && elect_one_sync()) {
-      const uint32_t id_s = idesc_bf16_f32(kRows, kTile, 0), id_o = idesc_bf16_f32(kRows, 256, 1);
-      const uint64_t d_q = smem_desc(smem_u32(s.q[0]), 16, 1024, kSwizzle128B);
-      const uint64_t d_p = smem_desc(smem_u32(s.p[0]), 16, 1024, kSwizzle128B);
-      const uint64_t d_k = smem_desc(smem_u32(s.ring[0]), 16, 1024, kSwizzle128B);
-      const uint64_t d_v = smem_desc(smem_u32(s.ring[0]), kChunkBytes, 1024, kSwizzle128B);
-      uint32_t it = 0, g = 0, piece = 0;  // ring items, tiles whose K / V came
+    // ---------------------------------------------------------------- Q and K
+    if (elect_one_sync()) {
+      constexpr int kBoxes = kOwn / kBox;
+      const uint32_t q_bar = cluster_addr(smem_u32(&s.q_full), 0), k_bar = cluster_addr(smem_u32(&s.k_full[0]), 0);
+      uint32_t sl = 0, turn = 1, items = 0, piece = 0;
       bool ok = true;
-      auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (!mbar_wait_cluster(smem_u32(bar), parity, &s.abort, kWaitBudgetNs)) {
-          set_abort(s, p.dev_status);
-          ok = false;
-        }
-        return ok;
-      };
       while (ok && walk.next()) {
-        if (!wait(&s.q_full, piece & 1u)) break;
-        const int32_t tiles = (walk.t1 - walk.t0 + kTile - 1) / kTile;
-        for (int32_t t = 0; ok && t <= tiles; ++t) {
-          if (t < tiles) {
-            // this S was read by the softmax of tile g - 2, whose P V has been issued
-            const uint32_t d = tmem + kColS + 128 * ((g + t) & 1u);
-            for (int c = 0; ok && c < kChunks; ++c, ++it) {
-              const int sl = it % kSlots;
-              if (!wait(&s.full[sl], (it / kSlots) & 1u)) break;
-              tc_fence_after();
-              const uint64_t a = d_q + (uint64_t)(c * kChunkBytes >> 4), b = d_k + (uint64_t)(sl * kItemBytes >> 4);
+        int32_t blk[kBoxes];  // read a tile ahead
+        auto look_up = [&](int32_t tt) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) mma_ss_pair(d, a + 2 * k, b + 2 * k, id_s, (c | k) ? 1u : 0u);
-              mma_commit_pair(smem_u32(&s.empty[sl]));
-            }
-            if (!ok) break;
-            mma_commit_pair(smem_u32(&s.s_full[(g + t) & 1u]));
-            if (t + 1 == tiles) mma_commit_pair(smem_u32(&s.q_free));
+          for (int i = 0; i < kBoxes; ++i) {
+            const int32_t at = tt + (int)rank * kOwn + i * kBox;
+            blk[i] = at < walk.t1 ? block_of(p, walk, at) : 0;
           }
-          if (t > 0) {
-            const uint32_t gt = g + t - 1;
-            if (!wait(&s.p_full, gt & 1u)) break;
-            if (t == 1 && piece > 0 && !wait(&s.o_free, (piece - 1) & 1u)) break;  // the last piece's O is out
-            tc_fence_after();
-            const int32_t n = min(kTile, walk.t1 - (walk.t0 + (t - 1) * kTile));
-            for (int gr = 0; ok && gr < groups_of(n); ++gr) {
-              const int steps = (min(kGroup, n - gr * kGroup) + 15) >> 4;
-              for (int j = 0; ok && j < 2; ++j, ++it) {
-                const int sl = it % kSlots;
-                if (!wait(&s.full[sl], (it / kSlots) & 1u)) break;
-                tc_fence_after();
-                const uint64_t a = d_p + (uint64_t)(gr * kChunkBytes >> 4), b = d_v + (uint64_t)(sl * kItemBytes >> 4);
-                for (int k = 0; k < steps; ++k)
-                  mma_ss_pair(tmem + kColO + 128 * j, a + 2 * k, b + 128 * k, id_o, (t > 1 || gr > 0 || k > 0) ? 1u : 0u);
-                mma_commit_pair(smem_u32(&s.empty[sl]));
-              }
-            }
-            if (!ok) break;
-            mma_commit_pair(smem_u32(&s.pv_done));
+        };
+        look_up(walk.t0);
+        if (piece > 0 && !(ok = wait(&s.q_free, (piece - 1) & 1u))) break;
+        ++piece;
+        if (first_block) mbar_arrive_expect_tx(smem_u32(&s.q_full), 2 * kChunks * kChunkBytes);
+        for (int c = 0; c < kChunks; c += 3) tma_load_3d_pair(smem_u32(s.q[c]), &maps.q, 0, walk.row() + (int)rank * kHalf, c, q_bar);
+        for (int32_t tt = walk.t0; ok && tt < walk.t1; tt += kTile) {
+          const int32_t n = min(kTile, walk.t1 - tt);
+          const int32_t boxes = (min(max(n - (int)rank * kOwn, 0), kOwn) + kBox - 1) / kBox;
+          const int32_t others = (min(max(n - (1 - (int)rank) * kOwn, 0), kOwn) + kBox - 1) / kBox;
+          const uint32_t bytes = (uint32_t)((boxes + others) * kBox * 128);
+          int32_t y[kBoxes];
+#pragma unroll
+          for (int i = 0; i < kBoxes; ++i) y[i] = i < boxes ? pool_row(p, blk[i], tt + (int)rank * kOwn + i * kBox) : 0;
+          if (tt + kTile < walk.t1) look_up(tt + kTile);
+          for (int c = 0; c < kChunks; ++c) {
+            if (!(ok = wait(&s.k_empty[sl], turn))) break;
+            if (first_block) mbar_arrive_expect_tx(smem_u32(&s.k_full[sl]), bytes);
+            const uint32_t dst = smem_u32(s.k[0]) + sl * kItemBytes, bar = k_bar + 8 * sl;
+#pragma unroll
+            for (int i = 0; i < kBoxes; ++i)
+              if (i < boxes) tma_load_2d_pair(dst + i * kBox * 128, &maps.k, 64 * c, y[i], bar);
+            ++items;
+            if (++sl == kSlotsK) sl = 0, turn ^= 1u;
           }
         }
-        g += tiles;
-        ++piece;
       }
-      mma_commit_pair(smem_u32(&s.mma_end));
-      if (!mbar_wait_cluster(smem_u32(&s.mma_end), 0, nullptr, kWaitBudgetNs)) report(p.dev_status, MLA_ERR_DEVICE_TIMEOUT);
+      if (s.abort && first_block) {  // let the loads in flight land in both blocks
+        for (uint32_t i = items > kSlotsK ? items - kSlotsK : 0; i < items; ++i)
+          (void)mbar_wait(smem_u32(&s.k_full[i % kSlotsK]), (i / kSlotsK) & 1u, nullptr, kDrainBudgetNs);
+        if (piece > 0) (void)mbar_wait(smem_u32(&s.q_full), (piece - 1) & 1u, nullptr, kDrainBudgetNs);
+      }
     }
   } else if (warp == 2) {
-    // ---------------------------------------------------------------- Q
-    uint32_t piece = 0;
-    const uint32_t bar = cluster_addr(smem_u32(&s.q_full), 0);
-    while (walk.next()) {
-      if (piece > 0 && !warp_wait(s, &s.q_free, (piece - 1) & 1u, p.dev_status)) break;
-      if (lane == 0) {
-        if (first_block) mbar_arrive_expect_tx(smem_u32(&s.q_full), 2 * kChunks * kChunkBytes);
-        else mbar_arrive_cluster(bar);
-        for (int c = 0; c < kChunks; c += 3) tma_load_3d_pair(smem_u32(s.q[c]), &maps.q, 0, walk.row() + (int)rank * kHalf, c, bar);
+    // ---------------------------------------------------------------- V
+    constexpr int kBoxV = kBox < kGroup ? kBox : kGroup, kBoxes = kGroup / kBoxV;
+    const uint32_t v_bar = cluster_addr(smem_u32(&s.v_full[0]), 0), tail_bar = cluster_addr(smem_u32(&s.tail_full), 0);
+    uint32_t sl = 0, turn = 1, items = 0;
+    auto advance = [&]() {
+      ++items;
+      if (++sl == kSlotsV) sl = 0, turn ^= 1u;
+    };
+    bool ok = true;
+    while (ok && walk.next()) {
+      int32_t blk[kBoxes];
+      auto look_up = [&](int32_t tt) {
+#pragma unroll
+        for (int i = 0; i < kBoxes; ++i) blk[i] = tt + i * kBoxV < walk.t1 ? block_of(p, walk, tt + i * kBoxV) : 0;
+      };
+      look_up(walk.t0);
+      for (int32_t tt = walk.t0; ok && tt < walk.t1; tt += kGroup) {
+        const int cnt = min(kGroup, walk.t1 - tt), boxes = (cnt + kBoxV - 1) / kBoxV;
+        if (cnt & 15) {
+          // the chain's last tokens: the warp's threads copy, with zeros up to the next multiple of 16
+          const uint32_t slots[2] = {sl, sl + 1 == kSlotsV ? 0 : sl + 1};
+          for (int j = 0; ok && j < 2; ++j) {
+            if (!(ok = warp_wait(s, &s.v_empty[sl], turn, p.dev_status))) break;
+            const uint32_t ring = smem_u32(s.v[sl]);
+            const int dim0 = 64 * (4 * j + 2 * (int)rank);
+            for (int u = lane; u < ((cnt + 15) & ~15) * 16; u += 32) {
+              const int r = u >> 4, c = u & 15;  // 16 bytes c of row r's 256
+              const int64_t y = r < cnt ? pool_row(p, block_of(p, walk, tt + r), tt + r) : 0;
+              const uint32_t dst = ring + (c >> 3) * kChunkBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(p.cache + y * kRow + dim0 + 8 * c),
+                           "r"(r < cnt ? 16 : 0)
+                           : "memory");
+            }
+            advance();
+          }
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (ok && lane == 0) {
+            if (first_block) {
+              mbar_arrive(smem_u32(&s.v_full[slots[0]]));
+              mbar_arrive(smem_u32(&s.v_full[slots[1]]));
+            } else {
+              mbar_arrive_release_cluster(tail_bar);
+            }
+          }
+          break;
+        }
+        const uint32_t bytes = (uint32_t)(2 * 2 * boxes * kBoxV * 128);  // two chunks, two blocks
+        int32_t y[kBoxes];
+#pragma unroll
+        for (int i = 0; i < kBoxes; ++i) y[i] = i < boxes ? pool_row(p, blk[i], tt + i * kBoxV) : 0;
+        if (tt + kGroup < walk.t1) look_up(tt + kGroup);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if (!(ok = warp_wait(s, &s.v_empty[sl], turn, p.dev_status))) break;
+          if (elect_one_sync()) {
+            if (first_block) mbar_arrive_expect_tx(smem_u32(&s.v_full[sl]), bytes);
+            const int chunk = 4 * j + 2 * (int)rank;
+            const uint32_t dst = smem_u32(s.v[0]) + sl * kItemBytes, bar = v_bar + 8 * sl;
+            if (kBox >= kGroup) {
+              tma_load_3d_pair(dst, &maps.v, 0, y[0], chunk, bar);
+            } else {
+#pragma unroll
+              for (int i = 0; i < kBoxes; ++i) {
+                if (i >= boxes) break;
+                tma_load_2d_pair(dst + i * kBoxV * 128, &maps.k, 64 * chunk, y[i], bar);
+                tma_load_2d_pair(dst + kChunkBytes + i * kBoxV * 128, &maps.k, 64 * (chunk + 1), y[i], bar);
+              }
+            }
+          }
+          __syncwarp();
+          advance();
+        }
       }
-      ++piece;
     }
-    if (s.abort && first_block && piece > 0)
-      (void)mbar_wait_cluster(smem_u32(&s.q_full), (piece - 1) & 1u, nullptr, kDrainBudgetNs);
-  } else if (warp >= kSoftmaxWarp0) {
+    if (s.abort && first_block && lane == 0)
+      for (uint32_t i = items > kSlotsV ? items - kSlotsV : 0; i < items; ++i)
+        (void)mbar_wait(smem_u32(&s.v_full[i % kSlotsV]), (i / kSlotsV) & 1u, nullptr, kDrainBudgetNs);
+  } else if (warp == 1) {
+    if (elect_one_sync()) {
+      if (first_block) {
+        // -------------------------------------------------------------- S = Q K^T
+        constexpr uint32_t id = idesc_bf16_f32(kRows, kTile, 0);
+        const uint32_t a0 = desc_low(s.q[0], 16), b0 = desc_low(s.k[0], 16);
+        uint32_t sl = 0, turn = 0, g = 0, piece = 0;
+        bool ok = true;
+        while (ok && walk.next()) {
+          if (!(ok = wait(&s.q_full, piece++ & 1u))) break;
+          for (int32_t tt = walk.t0; ok && tt < walk.t1; tt += kTile, ++g) {
+            if (g >= 2 && !(ok = wait(&s.s_free[g & 1u], ((g >> 1) - 1) & 1u))) break;
+            const uint32_t d = tmem + kColS + 128 * (g & 1u);
+            for (int c = 0; c < kChunks; ++c) {
+              if (!(ok = wait(&s.k_full[sl], turn))) break;
+              tc_fence_after();
+              const uint32_t a = a0 + c * (kChunkBytes >> 4), b = b0 + sl * (kItemBytes >> 4);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) mma_ss_pair_low(d, a + 2 * k, b + 2 * k, id, (c | k) ? 1u : 0u);
+              mma_commit_pair(smem_u32(&s.k_empty[sl]));
+              if (++sl == kSlotsK) sl = 0, turn ^= 1u;
+            }
+            mma_commit_pair(smem_u32(&s.s_full[g & 1u]));
+          }
+          mma_commit_pair(smem_u32(&s.q_free));
+        }
+        mma_commit_pair(smem_u32(&s.mma_end));
+        if (!mbar_wait(smem_u32(&s.mma_end), 0, nullptr, kWaitBudgetNs)) report(p.dev_status, MLA_ERR_DEVICE_TIMEOUT);
+      } else {
+        // The other block's P, said to the first when both warps of a half have written it.
+        const uint32_t bar = cluster_addr(smem_u32(&s.p_full[0]), 0);
+        uint32_t g = 0;
+        bool ok = true;
+        while (ok && walk.next())
+          for (int32_t tt = walk.t0; ok && tt < walk.t1; tt += kTile, ++g)
+            for (int h = 0; ok && h < 2; ++h)
+              if ((ok = wait(&s.p_here[h], g & 1u))) mbar_arrive_release_cluster(bar + 8 * h);
+      }
+    }
+  } else if (warp == 3) {
+    // ---------------------------------------------------------------- O += P V
+    if (first_block && elect_one_sync()) {
+      constexpr uint32_t id = idesc_bf16_f32(kRows, 256, 1);
+      const uint32_t a0 = desc_low(s.p[0], 16), b0 = desc_low(s.v[0], kChunkBytes);
+      uint32_t sl = 0, turn = 0, g = 0, piece = 0, tails = 0;
+      bool ok = true;
+      while (ok && walk.next()) {
+        if (piece > 0 && !(ok = wait(&s.o_free, (piece - 1) & 1u))) break;  // the last piece's O is out
+        ++piece;
+        uint32_t more = 0;
+        for (int32_t tt = walk.t0; ok && tt < walk.t1; tt += kTile, ++g) {
+          const int32_t n = min(kTile, walk.t1 - tt);
+          if (!(ok = wait(&s.s_free[g & 1u], (g >> 1) & 1u))) break;  // O is at this tile's scale
+          for (int h = 0; h < 2; ++h) {
+            if (!(ok = wait(&s.p_full[h], g & 1u))) break;
+            for (int gr = 2 * h; ok && gr < min(2 * h + 2, groups_of(n)); ++gr) {
+              const int cnt = min(kGroup, n - gr * kGroup), steps = (cnt + 15) >> 4;
+              if ((cnt & 15) && !(ok = wait(&s.tail_full, tails++ & 1u))) break;
+              for (int j = 0; j < 2; ++j) {
+                if (!(ok = wait(&s.v_full[sl], turn))) break;
+                tc_fence_after();
+                const uint32_t a = a0 + gr * (kChunkBytes >> 4), b = b0 + sl * (kItemBytes >> 4);
+                const uint32_t d = tmem + kColO + 128 * j;
+                if (steps == 4) {
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) mma_ss_pair_low(d, a + 2 * k, b + 128 * k, id, k > 0 ? 1u : more);
+                } else {
+                  for (int k = 0; k < steps; ++k) mma_ss_pair_low(d, a + 2 * k, b + 128 * k, id, k > 0 ? 1u : more);
+                }
+                mma_commit_pair(smem_u32(&s.v_empty[sl]));
+                if (++sl == kSlotsV) sl = 0, turn ^= 1u;
+              }
+              more = 1;
+            }
+            if (!ok) break;
+            mma_commit_pair(smem_u32(&s.p_free[h]));
+          }
+          if (ok) mma_commit_pair(smem_u32(&s.pv_done[g & 1u]));
+        }
+      }
+      mma_commit_pair(smem_u32(&s.mma_end));
+      if (!mbar_wait(smem_u32(&s.mma_end), 0, nullptr, kWaitBudgetNs)) report(p.dev_status, MLA_ERR_DEVICE_TIMEOUT);
+    }
+  } else {
     // ---------------------------------------------------------------- softmax, results
-    const int quarter = warp - kSoftmaxWarp0, half = quarter >> 1;  // of the tile's tokens; of 256 dims
-    const int r = (quarter & 1) * 32 + lane;                        // this block's row
-    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
-    const uint32_t p_bar = cluster_addr(smem_u32(&s.p_full), 0), o_bar = cluster_addr(smem_u32(&s.o_free), 0);
+    // Thread = a row and a quarter of the tile's tokens (64), or of the 512 dims: tensor memory's lanes
+    // hold 64 rows x the two halves of N, and two warps share a lane's columns.
+    const int quad = warp & 3, half = quad >> 1, part = (warp - kSoftmaxWarp0) >> 2;
+    const int rows32 = quad & 1, r = rows32 * 32 + lane;  // this block's row
+    const int place = 2 * half + part;                    // which 64 tokens
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+    const uint32_t s_bar = cluster_addr(smem_u32(&s.s_free[0]), 0), o_bar = cluster_addr(smem_u32(&s.o_free), 0);
+    const uint32_t p_bar = smem_u32(first_block ? &s.p_full[half] : &s.p_here[half]);
     const float c = p.scale_log2;
     uint32_t g = 0, piece = 0;
     bool ok = true;
     while (ok && walk.next()) {
       float m_used = -INFINITY, l = 0.f;
       for (int32_t tt = walk.t0; tt < walk.t1; tt += kTile, ++g) {
-        const int32_t mine = min(max(walk.t1 - tt - half * kOwn, 0), kOwn);  // real tokens of this half
-        if (!warp_wait(s, &s.s_full[g & 1u], (g >> 1) & 1u, p.dev_status)) {
-          ok = false;
-          break;
-        }
+        const int32_t mine = walk.t1 - tt - place * 64;  // real tokens of this quarter, if below 64
+        if (!(ok = warp_wait(s, &s.s_full[g & 1u], (g >> 1) & 1u, p.dev_status))) break;
         tc_fence_after();
-        const uint32_t src = lanes + kColS + 128 * (g & 1u);
-        float top = -INFINITY;
+        uint32_t x[64];
+        const uint32_t src = lanes + kColS + 128 * (g & 1u) + 64 * part;
+        tmem_ld32(src, x);
+        tmem_ld32(src + 32, x + 32);
+        tmem_wait_ld();
+        tmem_loaded32(x);
+        tmem_loaded32(x + 32);
+        tc_fence_before();
+        if (mine < 64) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t x[32];
-          tmem_ld32(src + 32 * i, x);
-          tmem_wait_ld();
-          if (mine >= 32 * (i + 1)) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) top = fmaxf(top, __uint_as_float(x[k]));
-          } else {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) top = 32 * i + k < mine ? fmaxf(top, __uint_as_float(x[k])) : top;
-          }
+          for (int k = 0; k < 64; ++k)
+            if (k >= mine) x[k] = 0xff800000u;  // -inf
         }
-        s.max[g & 1u][half][r] = top;
+        float t0 = __uint_as_float(x[0]), t1 = __uint_as_float(x[1]);
+#pragma unroll
+        for (int k = 2; k < 64; k += 2) {
+          t0 = fmaxf(t0, __uint_as_float(x[k]));
+          t1 = fmaxf(t1, __uint_as_float(x[k + 1]));
+        }
+        s.max[g & 1u][r][place] = fmaxf(t0, t1);
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&s.max_full[g & 1u][quarter & 1]));
-        if (!warp_wait(s, &s.max_full[g & 1u][quarter & 1], (g >> 1) & 1u, p.dev_status)) {
-          ok = false;
-          break;
-        }
-        top = fmaxf(top, s.max[g & 1u][half ^ 1][r]) * c;
+        if (lane == 0) mbar_arrive(smem_u32(&s.max_full[g & 1u][rows32]));
+        if (!(ok = warp_wait(s, &s.max_full[g & 1u][rows32], (g >> 1) & 1u, p.dev_status))) break;
+        const float4 four = *reinterpret_cast<const float4 *>(s.max[g & 1u][r]);
+        const float top = fmaxf(fmaxf(four.x, four.y), fmaxf(four.z, four.w)) * c;
         float alpha = 1.f;
         if (top > m_used + kRescaleThreshold || tt == walk.t0) {
-          alpha = ex2_approx(m_used - top);  // (0 at first; NaN if both are -inf, where nothing is summed yet)
-          if (m_used == -INFINITY) alpha = 0.f;
+          alpha = m_used == -INFINITY ? 0.f : ex2_approx(m_used - top);
           m_used = top;
         }
         const float shift = m_used == -INFINITY ? 0.f : m_used;
-        uint32_t w[64];
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t x[32];
-          tmem_ld32(src + 32 * i, x);
-          tmem_wait_ld();
-          float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            float a = ex2_approx(fmaf(__uint_as_float(x[2 * k]), c, -shift)), b = ex2_approx(fmaf(__uint_as_float(x[2 * k + 1]), c, -shift));
-            if (mine < 32 * (i + 1)) {
-              if (32 * i + 2 * k >= mine) a = 0.f;
-              if (32 * i + 2 * k + 1 >= mine) b = 0.f;
-            }
-            s0 += a;
-            s1 += b;
-            __nv_bfloat162 two = __floats2bfloat162_rn(a, b);
-            w[16 * i + k] = *reinterpret_cast<uint32_t *>(&two);
-          }
-          sum += s0 + s1;
-        }
-        l = l * alpha + sum;
-        // P and O are free once the P V of the tile before is done
-        if (g > 0 && !warp_wait(s, &s.pv_done, (g - 1) & 1u, p.dev_status)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
         if (tt > walk.t0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+          // O is free once the P V of the tile before is done
+          if (!(ok = warp_wait(s, &s.pv_done[(g - 1) & 1u], ((g - 1) >> 1) & 1u, p.dev_status))) break;
+          tc_fence_after();
 #pragma unroll 1
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < 4; ++i) {
             uint32_t o[32];
-            tmem_ld32(lanes + kColO + 32 * i, o);
+            tmem_ld32(lanes + kColO + 128 * part + 32 * i, o);
             tmem_wait_ld();
+            tmem_loaded32(o);
 #pragma unroll
             for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-            tmem_st32(lanes + kColO + 32 * i, o);
+            tmem_st32(lanes + kColO + 128 * part + 32 * i, o);
           }
           tmem_wait_st();
+          tc_fence_before();
         }
-#pragma unroll
-        for (int u = 0; u < 16; ++u)
-          *reinterpret_cast<uint4 *>(s.p[2 * half + (u >> 3)] + r * 128 + (((u & 7) ^ (r & 7)) << 4)) =
-              make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
-        fence_proxy_async_shared();
-        tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(p_bar);
+        if (lane == 0) mbar_arrive_cluster(s_bar + 8 * (g & 1u));  // S is read, O at this tile's scale
+        uint32_t w[32];
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const float a = ex2_approx(fmaf(__uint_as_float(x[2 * k]), c, -shift)), b = ex2_approx(fmaf(__uint_as_float(x[2 * k + 1]), c, -shift));
+          s0 += a;
+          s1 += b;
+          __nv_bfloat162 two = __floats2bfloat162_rn(a, b);
+          w[k] = *reinterpret_cast<uint32_t *>(&two);
+        }
+        l = l * alpha + (s0 + s1);
+        // this half of P was last read by the P V of the tile before
+        if (g > 0 && !(ok = warp_wait(s, &s.p_free[half], (g - 1) & 1u, p.dev_status))) break;
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          *reinterpret_cast<uint4 *>(s.p[place] + r * 128 + ((u ^ (r & 7)) << 4)) = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_bar);
       }
       if (!ok) break;
       // ---- O / l
-      s.sum[half][r] = l;
+      s.sum[r][place] = l;
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&s.sum_full[quarter & 1]));
-      if (!warp_wait(s, &s.sum_full[quarter & 1], piece & 1u, p.dev_status) || !warp_wait(s, &s.pv_done, (g - 1) & 1u, p.dev_status)) break;
+      if (lane == 0) mbar_arrive(smem_u32(&s.sum_full[rows32]));
+      if (!warp_wait(s, &s.sum_full[rows32], piece & 1u, p.dev_status) ||
+          !warp_wait(s, &s.pv_done[(g - 1) & 1u], ((g - 1) >> 1) & 1u, p.dev_status))
+        break;
       ++piece;
-      l += s.sum[half ^ 1][r];
+      const float4 four = *reinterpret_cast<const float4 *>(s.sum[r]);
+      l = (four.x + four.y) + (four.z + four.w);
       tc_fence_after();
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const float lse = l == 0.f ? -INFINITY : (m_used + log2f(l)) * 0.69314718055994531f;
@@ -649,10 +681,11 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
       }
       const bool real = walk.packed || row < p.heads;
 #pragma unroll 1
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 4; ++i) {
         uint32_t o[32];
-        tmem_ld32(lanes + kColO + 32 * i, o);
+        tmem_ld32(lanes + kColO + 128 * part + 32 * i, o);
         tmem_wait_ld();
+        tmem_loaded32(o);
         uint4 v[4];
         uint32_t *vw = reinterpret_cast<uint32_t *>(v);
 #pragma unroll
@@ -661,12 +694,12 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
           vw[k] = *reinterpret_cast<uint32_t *>(&two);
         }
         if (real) {
-          uint4 *to = reinterpret_cast<uint4 *>(dst + 256 * (i >> 2) + 128 * half + 32 * (i & 3));
+          uint4 *to = reinterpret_cast<uint4 *>(dst + 256 * part + 128 * half + 32 * i);
 #pragma unroll
           for (int k = 0; k < 4; ++k) to[k] = v[k];
         }
       }
-      if (real && half == 0 && lse_dst) *lse_dst = lse;
+      if (real && place == 0 && lse_dst) *lse_dst = lse;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(o_bar);
@@ -776,7 +809,11 @@ int pairs_current() {
   int n = known[dev].load(std::memory_order_acquire);
   if (n > 0) return n;
   const int smem = (int)sizeof(Smem) + 1024;
-  if (cudaFuncSetAttribute(shared_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return 0;
+  if (cudaFuncSetAttribute(shared_kernel<16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+      cudaFuncSetAttribute(shared_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+      cudaFuncSetAttribute(shared_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+      cudaFuncSetAttribute(shared_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return 0;
   int sms = 0;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
   cudaLaunchConfig_t cfg = {};
@@ -789,7 +826,7 @@ int pairs_current() {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, shared_kernel, &cfg) != cudaSuccess || n < 1) return 0;
+  if (cudaOccupancyMaxActiveClusters(&n, shared_kernel<128>, &cfg) != cudaSuccess || n < 1) return 0;
   n = std::min(n, kMaxPairs);
   known[dev].store(n, std::memory_order_release);
   return n;
@@ -888,6 +925,7 @@ mla_status_t mla_decode_shared(const void *q, const void *cache, int64_t num_blo
   p.o_b = (__nv_bfloat16 *)(ws + l.o_b);
   p.num_blocks = (int32_t)num_blocks;
   p.block_size = block_size;
+  for (p.page_log2 = 4; 1 << p.page_log2 < block_size;) ++p.page_log2;
   p.max_shared_blocks = max_shared_blocks;
   p.max_blocks_per_seq = max_blocks_per_seq;
   p.batch = batch;
@@ -907,7 +945,10 @@ mla_status_t mla_decode_shared(const void *q, const void *cache, int64_t num_blo
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, shared_kernel, maps, p);
+  cudaError_t e = block_size == 16   ? cudaLaunchKernelEx(&cfg, shared_kernel<16>, maps, p)
+                  : block_size == 32 ? cudaLaunchKernelEx(&cfg, shared_kernel<32>, maps, p)
+                  : block_size == 64 ? cudaLaunchKernelEx(&cfg, shared_kernel<64>, maps, p)
+                                     : cudaLaunchKernelEx(&cfg, shared_kernel<128>, maps, p);
   if (e != cudaSuccess) return status_of(e);
   const int64_t warps = kMergeThreads / 32;
   cfg.gridDim = dim3((unsigned)(((int64_t)batch * num_heads + warps - 1) / warps));

@@ -65,6 +65,9 @@ constexpr int kGroup = 64;          // tokens of an item of V
 constexpr int kChunks = kRow / 64;  // 9
 constexpr int kChunkBytes = kHalf * 128;  // 8 KB: 64 rows x 64 dims
 constexpr int kItemBytes = 16384;
+// Queries of few heads (kind B, up to kFew): 16 rows a chunk.  Their MMAs read 64 rows from each chunk's
+// start on, the rest being what follows: rows of no query, whose results nobody reads.
+constexpr int kFew = 16, kFewChunkBytes = kFew * 128, kFewBytes = 32768;
 constexpr int kSlotsK = 4, kSlotsV = 3;
 constexpr int kThreads = 384;
 constexpr int kSoftmaxWarp0 = 4, kSoftmaxWarps = 8;
@@ -86,7 +89,7 @@ struct __align__(1024) Smem {
   // in the first block, whose loaders announce the bytes of both blocks' loads; the others in each.
   // P is handed over and freed by halves (128 tokens), so that a tile's is written while the P V of
   // the tile before still runs.
-  uint64_t k_full[kSlotsK], k_empty[kSlotsK], v_full[kSlotsV], v_empty[kSlotsV], q_full, q_free;
+  uint64_t k_full[kSlotsK], k_empty[kSlotsK], v_full[kSlotsV], v_empty[kSlotsV], q_full[2], q_free[2];
   uint64_t s_full[2], s_free[2], p_full[2], p_free[2], pv_done[2], o_free, mma_end;  // (s, pv_done: by tile parity; p: by half)
   uint64_t tail_full;                    // the other block has filled its items with zeros
   uint64_t p_here[2];                    // the other block: its P is written, to be said to the first
@@ -96,12 +99,15 @@ struct __align__(1024) Smem {
   uint32_t tmem_base;
   int abort;
 };
+static_assert(kChunks * kFewChunkBytes <= kFewBytes && kFewBytes + (kChunks - 1) * kFewChunkBytes + kChunkBytes <= kChunks * kChunkBytes,
+              "two sets of few heads' queries, and what is read behind them, lie in q");
 static_assert(sizeof(Smem) + 1024 <= 232448, "shared memory");
 
 struct Maps {
   CUtensorMap k;  // {576, rows}, box {64, min(block_size, 128)}
   CUtensorMap v;  // {64, rows, 9}, box {64, 64, 2} (pages of 64 rows and more)
   CUtensorMap q;  // {64, batch * heads, 9}, box {64, 64, 3}
+  CUtensorMap q_few;  // the same, box {64, kFew, 9}
 };
 
 // What a piece's result needs is kept by chain: its pieces are those of the pairs first to last, in
@@ -204,6 +210,7 @@ struct Walk {
     }
     return false;
   }
+  __device__ bool few() const { return !packed && p.heads <= kFew; }
   // The packed query row of the piece's first.
   __device__ int32_t row() const { return packed ? chain * kRows : chain * p.heads; }
 };
@@ -259,10 +266,10 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
       init(&s.p_full[i], 5);
       init(&s.p_here[i], 4);
       init(&s.p_free[i], 1);
+      init(&s.q_full[i], 1);
+      init(&s.q_free[i], 1);
       init(&s.pv_done[i], 1);
     }
-    init(&s.q_full, 1);
-    init(&s.q_free, 1);
     init(&s.o_free, 2 * kSoftmaxWarps);
     init(&s.mma_end, 2);
     init(&s.tail_full, 1);
@@ -271,6 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
     prefetch_tmap(&maps.k);
     prefetch_tmap(&maps.v);
     prefetch_tmap(&maps.q);
+    prefetch_tmap(&maps.q_few);
   }
   if (warp == 3) {
     tmem_alloc_pair(smem_u32(&s.tmem_base), kCols);
@@ -353,31 +361,45 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
     // ---------------------------------------------------------------- Q and K
     if (elect_one_sync()) {
       constexpr int kBoxes = kOwn / kBox;
-      const uint32_t q_bar = cluster_addr(smem_u32(&s.q_full), 0), k_bar = cluster_addr(smem_u32(&s.k_full[0]), 0);
+      const uint32_t q_bar = cluster_addr(smem_u32(&s.q_full[0]), 0), k_bar = cluster_addr(smem_u32(&s.k_full[0]), 0);
       uint32_t sl = 0, turn = 1, items = 0, piece = 0;
-      bool ok = true;
+      bool ok = true, was_few = false;
       while (ok && walk.next()) {
         int32_t blk[kBoxes];  // read a tile ahead
         auto look_up = [&](int32_t tt) {
 #pragma unroll
           for (int i = 0; i < kBoxes; ++i) {
-            const int32_t at = tt + (int)rank * kOwn + i * kBox;
+            const int32_t own = tt + (int)rank * kOwn, at = (own < walk.t1 ? own : tt) + i * kBox;
             blk[i] = at < walk.t1 ? block_of(p, walk, at) : 0;
           }
         };
         look_up(walk.t0);
-        if (piece > 0 && !(ok = wait(&s.q_free, (piece - 1) & 1u))) break;
+        // the last piece's queries stay where they are read while these come, if neither takes all the room
+        if (piece >= 2 && !(ok = wait(&s.q_free[piece & 1u], ((piece >> 1) - 1) & 1u))) break;
+        const bool few = walk.few(), beside = few && was_few;
+        if (piece >= 1 && !beside && !(ok = wait(&s.q_free[(piece - 1) & 1u], ((piece - 1) >> 1) & 1u))) break;
+        was_few = few;
+        const uint32_t bar = q_bar + 8 * (piece & 1u);
+        if (few) {
+          if (first_block) {
+            mbar_arrive_expect_tx(smem_u32(&s.q_full[piece & 1u]), kChunks * kFewChunkBytes);
+            tma_load_3d_pair(smem_u32(s.q[0]) + (piece & 1u) * kFewBytes, &maps.q_few, 0, walk.row(), 0, bar);
+          }
+        } else {
+          if (first_block) mbar_arrive_expect_tx(smem_u32(&s.q_full[piece & 1u]), 2 * kChunks * kChunkBytes);
+          for (int c = 0; c < kChunks; c += 3) tma_load_3d_pair(smem_u32(s.q[c]), &maps.q, 0, walk.row() + (int)rank * kHalf, c, bar);
+        }
         ++piece;
-        if (first_block) mbar_arrive_expect_tx(smem_u32(&s.q_full), 2 * kChunks * kChunkBytes);
-        for (int c = 0; c < kChunks; c += 3) tma_load_3d_pair(smem_u32(s.q[c]), &maps.q, 0, walk.row() + (int)rank * kHalf, c, q_bar);
         for (int32_t tt = walk.t0; ok && tt < walk.t1; tt += kTile) {
           const int32_t n = min(kTile, walk.t1 - tt);
-          const int32_t boxes = (min(max(n - (int)rank * kOwn, 0), kOwn) + kBox - 1) / kBox;
-          const int32_t others = (min(max(n - (1 - (int)rank) * kOwn, 0), kOwn) + kBox - 1) / kBox;
-          const uint32_t bytes = (uint32_t)((boxes + others) * kBox * 128);
+          // Both blocks load at least a box of every item, so that neither falls behind the ring's rounds
+          // (the second one the tile's first tokens where it has none of its own: masked columns).
+          const int32_t tokens = min(max(n - (int)rank * kOwn, 0), kOwn), others = min(max(n - (1 - (int)rank) * kOwn, 0), kOwn);
+          const int32_t boxes = max(1, (tokens + kBox - 1) / kBox);
+          const uint32_t bytes = (uint32_t)((boxes + max(1, (others + kBox - 1) / kBox)) * kBox * 128);
           int32_t y[kBoxes];
 #pragma unroll
-          for (int i = 0; i < kBoxes; ++i) y[i] = i < boxes ? pool_row(p, blk[i], tt + (int)rank * kOwn + i * kBox) : 0;
+          for (int i = 0; i < kBoxes; ++i) y[i] = i < boxes ? pool_row(p, blk[i], (tokens > 0 ? tt + (int)rank * kOwn : tt) + i * kBox) : 0;
           if (tt + kTile < walk.t1) look_up(tt + kTile);
           for (int c = 0; c < kChunks; ++c) {
             if (!(ok = wait(&s.k_empty[sl], turn))) break;
@@ -394,7 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
       if (s.abort && first_block) {  // let the loads in flight land in both blocks
         for (uint32_t i = items > kSlotsK ? items - kSlotsK : 0; i < items; ++i)
           (void)mbar_wait(smem_u32(&s.k_full[i % kSlotsK]), (i / kSlotsK) & 1u, nullptr, kDrainBudgetNs);
-        if (piece > 0) (void)mbar_wait(smem_u32(&s.q_full), (piece - 1) & 1u, nullptr, kDrainBudgetNs);
+        for (uint32_t i = piece > 2 ? piece - 2 : 0; i < piece; ++i)
+          (void)mbar_wait(smem_u32(&s.q_full[i & 1u]), (i >> 1) & 1u, nullptr, kDrainBudgetNs);
       }
     }
   } else if (warp == 2) {
@@ -486,14 +509,16 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
         uint32_t sl = 0, turn = 0, g = 0, piece = 0;
         bool ok = true;
         while (ok && walk.next()) {
-          if (!(ok = wait(&s.q_full, piece++ & 1u))) break;
+          if (!(ok = wait(&s.q_full[piece & 1u], (piece >> 1) & 1u))) break;
+          const uint32_t chunk = (walk.few() ? kFewChunkBytes : kChunkBytes) >> 4;
+          const uint32_t q0 = a0 + (walk.few() ? (piece & 1u) * (kFewBytes >> 4) : 0);
           for (int32_t tt = walk.t0; ok && tt < walk.t1; tt += kTile, ++g) {
             if (g >= 2 && !(ok = wait(&s.s_free[g & 1u], ((g >> 1) - 1) & 1u))) break;
             const uint32_t d = tmem + kColS + 128 * (g & 1u);
             for (int c = 0; c < kChunks; ++c) {
               if (!(ok = wait(&s.k_full[sl], turn))) break;
               tc_fence_after();
-              const uint32_t a = a0 + c * (kChunkBytes >> 4), b = b0 + sl * (kItemBytes >> 4);
+              const uint32_t a = q0 + c * chunk, b = b0 + sl * (kItemBytes >> 4);
 #pragma unroll
               for (int k = 0; k < 4; ++k) mma_ss_pair_low(d, a + 2 * k, b + 2 * k, id, (c | k) ? 1u : 0u);
               mma_commit_pair(smem_u32(&s.k_empty[sl]));
@@ -501,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
             }
             mma_commit_pair(smem_u32(&s.s_full[g & 1u]));
           }
-          mma_commit_pair(smem_u32(&s.q_free));
+          mma_commit_pair(smem_u32(&s.q_free[piece++ & 1u]));
         }
         mma_commit_pair(smem_u32(&s.mma_end));
         if (!mbar_wait(smem_u32(&s.mma_end), 0, nullptr, kWaitBudgetNs)) report(p.dev_status, MLA_ERR_DEVICE_TIMEOUT);
@@ -571,14 +596,24 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
     const uint32_t s_bar = cluster_addr(smem_u32(&s.s_free[0]), 0), o_bar = cluster_addr(smem_u32(&s.o_free), 0);
     const uint32_t p_bar = smem_u32(first_block ? &s.p_full[half] : &s.p_here[half]);
     const float c = p.scale_log2;
-    uint32_t g = 0, piece = 0;
+    uint32_t g = 0, tops = 0, sums = 0;  // tiles, and those with a maximum and pieces with a sum of this warp's
     bool ok = true;
     while (ok && walk.next()) {
       float m_used = -INFINITY, l = 0.f;
+      // this warp's rows that are queries; one without any only hands on
+      const int real_rows = min(32, (walk.packed ? kRows : p.heads) - (int)rank * kHalf - rows32 * 32);
       for (int32_t tt = walk.t0; tt < walk.t1; tt += kTile, ++g) {
         const int32_t mine = walk.t1 - tt - place * 64;  // real tokens of this quarter, if below 64
         if (!(ok = warp_wait(s, &s.s_full[g & 1u], (g >> 1) & 1u, p.dev_status))) break;
         tc_fence_after();
+        if (real_rows <= 0) {
+          if (g > 0 && !(ok = warp_wait(s, &s.p_free[half], (g - 1) & 1u, p.dev_status))) break;
+          if (lane == 0) {
+            mbar_arrive_cluster(s_bar + 8 * (g & 1u));
+            mbar_arrive(p_bar);
+          }
+          continue;
+        }
         uint32_t x[64];
         const uint32_t src = lanes + kColS + 128 * (g & 1u) + 64 * part;
         tmem_ld32(src, x);
@@ -598,11 +633,12 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
           t0 = fmaxf(t0, __uint_as_float(x[k]));
           t1 = fmaxf(t1, __uint_as_float(x[k + 1]));
         }
-        s.max[g & 1u][r][place] = fmaxf(t0, t1);
+        s.max[tops & 1u][r][place] = fmaxf(t0, t1);
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&s.max_full[g & 1u][rows32]));
-        if (!(ok = warp_wait(s, &s.max_full[g & 1u][rows32], (g >> 1) & 1u, p.dev_status))) break;
-        const float4 four = *reinterpret_cast<const float4 *>(s.max[g & 1u][r]);
+        if (lane == 0) mbar_arrive(smem_u32(&s.max_full[tops & 1u][rows32]));
+        if (!(ok = warp_wait(s, &s.max_full[tops & 1u][rows32], (tops >> 1) & 1u, p.dev_status))) break;
+        const float4 four = *reinterpret_cast<const float4 *>(s.max[tops & 1u][r]);
+        ++tops;
         const float top = fmaxf(fmaxf(four.x, four.y), fmaxf(four.z, four.w)) * c;
         float alpha = 1.f;
         if (top > m_used + kRescaleThreshold || tt == walk.t0) {
@@ -651,55 +687,67 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
       }
       if (!ok) break;
       // ---- O / l
-      s.sum[r][place] = l;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&s.sum_full[rows32]));
-      if (!warp_wait(s, &s.sum_full[rows32], piece & 1u, p.dev_status) ||
-          !warp_wait(s, &s.pv_done[(g - 1) & 1u], ((g - 1) >> 1) & 1u, p.dev_status))
-        break;
-      ++piece;
-      const float4 four = *reinterpret_cast<const float4 *>(s.sum[r]);
-      l = (four.x + four.y) + (four.z + four.w);
+      if (real_rows > 0) {
+        s.sum[r][place] = l;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s.sum_full[rows32]));
+        if (!warp_wait(s, &s.sum_full[rows32], sums++ & 1u, p.dev_status)) break;
+        const float4 four = *reinterpret_cast<const float4 *>(s.sum[r]);
+        l = (four.x + four.y) + (four.z + four.w);
+      }
+      if (!warp_wait(s, &s.pv_done[(g - 1) & 1u], ((g - 1) >> 1) & 1u, p.dev_status)) break;
       tc_fence_after();
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const float lse = l == 0.f ? -INFINITY : (m_used + log2f(l)) * 0.69314718055994531f;
-      const int row = (int)rank * kHalf + r;  // of the chain
-      __nv_bfloat16 *dst;
-      float *lse_dst;
-      if (walk.packed) {
-        const int64_t at = ((int64_t)walk.chain + pair) * kRows + row;
-        dst = p.o_a + at * kVDim;
-        lse_dst = p.lse_a + at;
-      } else if (walk.whole) {
-        const int64_t at = (int64_t)walk.chain * p.heads + row;
-        dst = p.out + at * kVDim;
-        lse_dst = p.lse ? p.lse + at : nullptr;
-      } else {
-        const int64_t at = ((int64_t)walk.chain + pair) * p.heads + row;
-        dst = p.o_b + at * kVDim;
-        lse_dst = p.lse_b + at;
-      }
-      const bool real = walk.packed || row < p.heads;
+      if (real_rows > 0) {
+        const int row0 = (int)rank * kHalf + rows32 * 32;  // of the chain
+        __nv_bfloat16 *dst;
+        float *lse_dst;
+        if (walk.packed) {
+          const int64_t at = ((int64_t)walk.chain + pair) * kRows + row0;
+          dst = p.o_a + at * kVDim;
+          lse_dst = p.lse_a + at;
+        } else if (walk.whole) {
+          const int64_t at = (int64_t)walk.chain * p.heads + row0;
+          dst = p.out + at * kVDim;
+          lse_dst = p.lse ? p.lse + at : nullptr;
+        } else {
+          const int64_t at = ((int64_t)walk.chain + pair) * p.heads + row0;
+          dst = p.o_b + at * kVDim;
+          lse_dst = p.lse_b + at;
+        }
+        dst += 256 * part + 128 * half + 8 * (lane & 7);
+        // 64 dims at a time by way of this warp's part of P, so that 8 threads store a row's 128 bytes
+        uint8_t *stage = s.p[place] + rows32 * 32 * 128;
 #pragma unroll 1
-      for (int i = 0; i < 4; ++i) {
-        uint32_t o[32];
-        tmem_ld32(lanes + kColO + 128 * part + 32 * i, o);
-        tmem_wait_ld();
-        tmem_loaded32(o);
-        uint4 v[4];
-        uint32_t *vw = reinterpret_cast<uint32_t *>(v);
+        for (int i = 0; i < 2; ++i) {
+          uint32_t o[64];
+          tmem_ld32(lanes + kColO + 128 * part + 64 * i, o);
+          tmem_ld32(lanes + kColO + 128 * part + 64 * i + 32, o + 32);
+          tmem_wait_ld();
+          tmem_loaded32(o);
+          tmem_loaded32(o + 32);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          __nv_bfloat162 two = __floats2bfloat162_rn(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
-          vw[k] = *reinterpret_cast<uint32_t *>(&two);
-        }
-        if (real) {
-          uint4 *to = reinterpret_cast<uint4 *>(dst + 256 * part + 128 * half + 32 * i);
+          for (int k = 0; k < 32; ++k) {
+            __nv_bfloat162 two = __floats2bfloat162_rn(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+            o[k] = *reinterpret_cast<uint32_t *>(&two);
+          }
+          __syncwarp();
 #pragma unroll
-          for (int k = 0; k < 4; ++k) to[k] = v[k];
+          for (int u = 0; u < 8; ++u)
+            *reinterpret_cast<uint4 *>(stage + lane * 128 + ((u ^ (lane & 7)) << 4)) = make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int rr = 4 * k + (lane >> 3);
+            if (rr < real_rows)
+              *reinterpret_cast<uint4 *>(dst + (int64_t)rr * kVDim + 64 * i) =
+                  *reinterpret_cast<const uint4 *>(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+          }
         }
+        __syncwarp();
+        if (lane < real_rows && place == 0 && lse_dst) lse_dst[lane] = lse;
       }
-      if (real && place == 0 && lse_dst) *lse_dst = lse;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(o_bar);
@@ -903,7 +951,8 @@ mla_status_t mla_decode_shared(const void *q, const void *cache, int64_t num_blo
   Maps maps;
   const int64_t rows = num_blocks * block_size;
   if (!tmap::encode_2d(&maps.k, cache, rows, (uint32_t)std::min(block_size, kOwn)) || !tmap::encode_3d(&maps.v, cache, rows, kGroup, 2) ||
-      !tmap::encode_3d(&maps.q, q, (int64_t)batch * num_heads, kHalf, 3)) {
+      !tmap::encode_3d(&maps.q, q, (int64_t)batch * num_heads, kHalf, 3) ||
+      !tmap::encode_3d(&maps.q_few, q, (int64_t)batch * num_heads, kFew, kChunks)) {
     set_error_detail("cannot describe q or the cache to TMA");
     return MLA_ERR_CUDA;
   }

@@ -439,21 +439,23 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
       look_up(walk.t0);
       for (int32_t tt = walk.t0; ok && tt < walk.t1; tt += kGroup) {
         const int cnt = min(kGroup, walk.t1 - tt), boxes = (cnt + kBoxV - 1) / kBoxV;
+        int32_t y[kBoxes];
+#pragma unroll
+        for (int i = 0; i < kBoxes; ++i) y[i] = i < boxes ? pool_row(p, blk[i], tt + i * kBoxV) : 0;
         if (cnt & 15) {
           // the chain's last tokens: the warp's threads copy, with zeros up to the next multiple of 16
           const uint32_t slots[2] = {sl, sl + 1 == kSlotsV ? 0 : sl + 1};
+          const int rows = (cnt + 15) & ~15, r0 = lane >> 4, c = lane & 15;  // 16 bytes c of a row's 256, every other row
           for (int j = 0; ok && j < 2; ++j) {
             if (!(ok = warp_wait(s, &s.v_empty[sl], turn, p.dev_status))) break;
-            const uint32_t ring = smem_u32(s.v[sl]);
-            const int dim0 = 64 * (4 * j + 2 * (int)rank);
-            for (int u = lane; u < ((cnt + 15) & ~15) * 16; u += 32) {
-              const int r = u >> 4, c = u & 15;  // 16 bytes c of row r's 256
-              const int64_t y = r < cnt ? pool_row(p, block_of(p, walk, tt + r), tt + r) : 0;
-              const uint32_t dst = ring + (c >> 3) * kChunkBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(p.cache + y * kRow + dim0 + 8 * c),
-                           "r"(r < cnt ? 16 : 0)
-                           : "memory");
-            }
+            const uint32_t ring = smem_u32(s.v[sl]) + (c >> 3) * kChunkBytes;
+            const __nv_bfloat16 *src = p.cache + 64 * (4 * j + 2 * (int)rank) + 8 * c;
+#pragma unroll
+            for (int i = 0; i < kBoxes; ++i)
+              for (int r = i * kBoxV + r0; r < min(rows, (i + 1) * kBoxV); r += 2)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ring + r * 128 + (((c & 7) ^ (r & 7)) << 4)),
+                             "l"(src + (r < cnt ? (int64_t)y[i] + (r - i * kBoxV) : 0) * kRow), "r"(r < cnt ? 16 : 0)
+                             : "memory");
             advance();
           }
           asm volatile("cp.async.wait_all;" ::: "memory");
@@ -470,9 +472,6 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
           break;
         }
         const uint32_t bytes = (uint32_t)(2 * 2 * boxes * kBoxV * 128);  // two chunks, two blocks
-        int32_t y[kBoxes];
-#pragma unroll
-        for (int i = 0; i < kBoxes; ++i) y[i] = i < boxes ? pool_row(p, blk[i], tt + i * kBoxV) : 0;
         if (tt + kGroup < walk.t1) look_up(tt + kGroup);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {

@@ -59,7 +59,7 @@ using namespace sm100;
 
 constexpr int kRows = 128;          // query rows of a chain
 constexpr int kHalf = kRows / 2;    // ... in each block of a pair
-constexpr int kTile = 256;          // tokens of a unit
+constexpr int kTile = 256;          // tokens of a tile
 constexpr int kOwn = kTile / 2;     // ... whose scores' operand a block holds
 constexpr int kGroup = 64;          // tokens of an item of V
 constexpr int kChunks = kRow / 64;  // 9
@@ -72,7 +72,7 @@ constexpr int kSlotsK = 4, kSlotsV = 3;
 constexpr int kThreads = 384;
 constexpr int kSoftmaxWarp0 = 4, kSoftmaxWarps = 8;
 constexpr uint32_t kColO = 0, kColS = 256, kCols = 512;
-constexpr int64_t kUnitCost = 4, kChainCost = 4;  // a chain's start: queries and first keys without MMAs under them
+constexpr int64_t kUnitCost = 2, kChainCost = 16;  // a chain's start: queries and first keys without MMAs under them
 constexpr int kMaxPairs = 256;
 constexpr uint64_t kWaitBudgetNs = 100000000ull;
 constexpr uint64_t kDrainBudgetNs = 10000000ull;
@@ -94,7 +94,7 @@ struct __align__(1024) Smem {
   uint64_t tail_full;                    // the other block has filled its items with zeros
   uint64_t p_here[2];                    // the other block: its P is written, to be said to the first
   uint64_t max_full[2][2], sum_full[2];  // [tile parity][32 rows]: their four warps have written
-  int64_t start_cost, total_cost, warp_cost[kThreads / 32];
+  int64_t total, start_cost, share[2], warp_cost[kThreads / 32];  // of all chains; where the first starts; this pair's
   int32_t start_chain;
   uint32_t tmem_base;
   int abort;
@@ -133,69 +133,69 @@ struct Params {
 struct Chains {
   int32_t shared;  // tokens in common
   int32_t packed;  // chains of kind A, 0: none
-  __device__ Chains(const Params &p, bool speak) {
-    int32_t n = *p.shared_blocks;
-    if (n < 0 || n > p.max_shared_blocks) {
+  int32_t longest;
+  int32_t unit;    // tokens that chains are dealt out by: 64, or the rows of a box where that is more
+  __device__ Chains(const Params &p, int32_t shared_blocks, bool speak) {
+    if (shared_blocks < 0 || shared_blocks > p.max_shared_blocks) {
       if (speak) report(p.dev_status, MLA_ERR_DEVICE_RANGE);
-      n = min(max(n, 0), p.max_shared_blocks);
+      shared_blocks = min(max(shared_blocks, 0), p.max_shared_blocks);
     }
-    shared = n * p.block_size;
+    shared = shared_blocks << p.page_log2;
     packed = (int32_t)(((int64_t)p.batch * p.heads + kRows - 1) / kRows);
     if (packed >= p.batch || shared == 0) packed = 0;
+    longest = p.max_blocks_per_seq << p.page_log2;
+    unit = p.block_size >= kOwn ? kOwn : kGroup;
   }
-  __device__ int32_t length(const Params &p, int32_t b, bool speak) const {
-    const int32_t L = p.seq_lens[b], most = p.max_blocks_per_seq * p.block_size;
-    if (L >= 0 && L <= most) return L;
-    if (speak) report(p.dev_status, MLA_ERR_DEVICE_RANGE);
-    return L < 0 ? 0 : most;
-  }
-  // The first token of request b's own chain.
+  __device__ int32_t length(int32_t L) const { return min(max(L, 0), longest); }
+  // The first token of the own chain of a request of L tokens.
   __device__ int32_t from(int32_t L) const { return packed > 0 && L >= shared ? shared : 0; }
-  __device__ int32_t units(int32_t L) const { return (L - from(L) + kTile - 1) / kTile; }
-  __device__ int32_t units_a() const { return (shared + kTile - 1) / kTile; }
+  __device__ int32_t units(int32_t L) const { return (L - from(L) + unit - 1) / unit; }
+  __device__ int32_t units_a() const { return (shared + unit - 1) / unit; }
   static __device__ int64_t cost(int32_t units) { return units > 0 ? kChainCost + kUnitCost * units : 0; }
   __device__ int64_t cost_a() const { return packed * cost(units_a()); }
 };
 
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {  // of numbers that are mostly small
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // Pair w's share of cost C over n pairs is [bound(w), bound(w + 1)); a unit belongs where its place,
 // its chain's start and kChainCost and kUnitCost for each unit before it, lies.
-__device__ __forceinline__ int64_t bound(int64_t C, int32_t n, int32_t w) { return (w * C + n - 1) / n; }
+__device__ __forceinline__ int64_t bound(int64_t C, int32_t n, int32_t w) { return quotient(w * C + n - 1, n); }
 // No pair's share is shorter than a unit, so that a chain has no hole between its first and last pair.
 __device__ __forceinline__ int32_t pairs_for(int64_t C, int32_t pairs) {
   return (int32_t)min((int64_t)pairs, max((int64_t)1, C / kUnitCost));
 }
 __device__ __forceinline__ Pieces pieces_of(int64_t start, int32_t units, int64_t C, int32_t n) {
   Pieces r;
-  r.first = (int32_t)((start + kChainCost) * n / C);
-  r.last = (int32_t)((start + kChainCost + kUnitCost * (units - 1)) * n / C);
+  r.first = (int32_t)quotient((start + kChainCost) * n, C);
+  r.last = (int32_t)quotient((start + kChainCost + kUnitCost * (units - 1)) * n, C);
   return r;
 }
 
 // A pair's pieces in order.
 struct Walk {
-  const Params &p;
-  const Chains &ch;
+  const Params *p;
+  const Chains *ch;
   int64_t x0, x1, at;  // the pair's share, the next chain's start
   int32_t next_chain;
   // the current piece: kind, chain, tokens [t0, t1), all of the chain
   bool packed, whole;
   int32_t chain, t0, t1;
-  __device__ Walk(const Params &params, const Chains &c, const Smem &s, int32_t pair) : p(params), ch(c) {
-    const int64_t C = s.total_cost;
-    const int32_t n = pairs_for(C, p.pairs);
-    x0 = pair < n ? bound(C, n, pair) : C;
-    x1 = pair < n ? bound(C, n, pair + 1) : C;
+  __device__ Walk(const Params &params, const Chains &c, const Smem &s) : p(&params), ch(&c) {
+    x0 = s.share[0];
+    x1 = s.share[1];
     at = s.start_cost;
     next_chain = s.start_chain;
   }
   __device__ bool next() {
-    const int32_t all = ch.packed + p.batch;
+    const int32_t all = ch->packed + p->batch;
     while (next_chain < all && at < x1) {
-      packed = next_chain < ch.packed;
-      chain = packed ? next_chain : next_chain - ch.packed;
-      const int32_t end = packed ? ch.shared : ch.length(p, chain, false);
-      const int32_t first = packed ? 0 : ch.from(end);
-      const int32_t units = (end - first + kTile - 1) / kTile;
+      packed = next_chain < ch->packed;
+      chain = packed ? next_chain : next_chain - ch->packed;
+      const int32_t end = packed ? ch->shared : ch->length(p->seq_lens[chain]);
+      const int32_t first = packed ? 0 : ch->from(end);
+      const int32_t unit = ch->unit, units = (end - first + unit - 1) / unit;
       ++next_chain;
       if (units <= 0) continue;
       const int64_t place = at + kChainCost;
@@ -203,17 +203,36 @@ struct Walk {
       const int64_t k0 = x0 <= place ? 0 : (x0 - place + kUnitCost - 1) / kUnitCost;
       const int64_t k1 = x1 <= place ? 0 : min((int64_t)units, (x1 - place + kUnitCost - 1) / kUnitCost);
       if (k0 >= k1) continue;
-      t0 = first + (int32_t)k0 * kTile;
-      t1 = min(end, first + (int32_t)k1 * kTile);
+      t0 = first + (int32_t)k0 * unit;
+      t1 = min(end, first + (int32_t)k1 * unit);
       whole = !packed && first == 0 && t0 == 0 && t1 == end;
       return true;
     }
     return false;
   }
-  __device__ bool few() const { return !packed && p.heads <= kFew; }
+  __device__ bool few() const { return !packed && p->heads <= kFew; }
   // The packed query row of the piece's first.
-  __device__ int32_t row() const { return packed ? chain * kRows : chain * p.heads; }
+  __device__ int32_t row() const { return packed ? chain * kRows : chain * p->heads; }
 };
+
+// The chains' pieces, for the merge; by a warp.
+__device__ void write_pieces(const Params &p, const Chains &ch, int64_t C) {
+  const int lane = threadIdx.x & 31;
+  const int32_t n = pairs_for(C, p.pairs);
+  for (int32_t i = lane; i < ch.packed; i += 32) p.pieces_a[i] = pieces_of(i * ch.cost(ch.units_a()), ch.units_a(), C, n);
+  int64_t before = ch.cost_a();
+  for (int32_t b0 = 0; b0 < p.batch; b0 += 32) {
+    const int32_t units = b0 + lane < p.batch ? ch.units(ch.length(p.seq_lens[b0 + lane])) : 0;
+    int64_t incl = ch.cost(units);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (units > 0) p.pieces_b[b0 + lane] = pieces_of(before + incl - ch.cost(units), units, C, n);
+    before += __shfl_sync(0xffffffffu, incl, 31);
+  }
+}
 
 __device__ __forceinline__ int groups_of(int n) { return (n + kGroup - 1) / kGroup; }
 
@@ -233,7 +252,7 @@ __device__ __forceinline__ bool warp_wait(Smem &s, uint64_t *bar, uint32_t parit
 // The block of token t, and the pool's row of t in it: 0 if it is none (reported).
 __device__ __forceinline__ int32_t block_of(const Params &p, const Walk &w, int32_t t) {
   const int32_t page = t >> p.page_log2;
-  return t < w.ch.shared ? p.shared_table[page] : p.block_table[(int64_t)w.chain * p.max_blocks_per_seq + page];
+  return t < w.ch->shared ? p.shared_table[page] : p.block_table[(int64_t)w.chain * p.max_blocks_per_seq + page];
 }
 __device__ __forceinline__ int32_t pool_row(const Params &p, int32_t blk, int32_t t) {
   if (blk < 0 || blk >= p.num_blocks) {
@@ -288,67 +307,67 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
   griddep_launch_dependents();  // the merge waits for this grid's end, on the SMs' free threads
 
   // ---------------------------------------------------------------- the deal
-  const bool speaker = blockIdx.x == 0;
-  const Chains ch(p, speaker && tid == 0);
+  const int32_t shared_blocks = *p.shared_blocks, my_length = tid < p.batch ? p.seq_lens[tid] : 0;
+  const Chains ch(p, shared_blocks, blockIdx.x == 0 && tid == 0);
   {
-    int64_t base = ch.cost_a();
-    for (int turn = 0; turn < 2; ++turn) {  // the total, then where this pair's share starts
-      int64_t before = ch.cost_a();
-      const int64_t C = base;
-      const int32_t n = pairs_for(C, p.pairs);
-      const int64_t x0 = turn && pair < n ? bound(C, n, pair) : 0;
-      if (turn) {
-        if (tid == 0) {
-          s.total_cost = C;
-          s.start_chain = ch.packed + p.batch;  // nothing
-          s.start_cost = C;
-          if (ch.packed > 0 && x0 < before && pair < n) {
-            const int64_t each = ch.cost(ch.units_a());
-            s.start_chain = (int32_t)(x0 / each);
-            s.start_cost = s.start_chain * each;
-          }
-        }
-        if (speaker)
-          for (int32_t i = tid; i < ch.packed; i += kThreads)
-            p.pieces_a[i] = pieces_of(i * ch.cost(ch.units_a()), ch.units_a(), C, n);
-        __syncthreads();
-      }
-      for (int32_t b0 = 0; b0 < p.batch; b0 += kThreads) {
-        const int32_t b = b0 + tid;
-        const int32_t units = b < p.batch ? ch.units(ch.length(p, b, speaker && turn)) : 0;
-        const int64_t mine = ch.cost(units);
-        int64_t incl = mine;
+    // costs of a block's worth of requests, and the sum over those before each
+    int64_t before = ch.cost_a(), mine = 0, start = 0;
+    auto sum_up = [&](int32_t b0, int32_t L) {
+      if (blockIdx.x == 0 && L != ch.length(L)) report(p.dev_status, MLA_ERR_DEVICE_RANGE);
+      mine = b0 + tid < p.batch ? ch.cost(ch.units(ch.length(L))) : 0;
+      int64_t incl = mine;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += y;
-        }
-        if (lane == 31) s.warp_cost[warp] = incl;
-        __syncthreads();
-        int64_t all = 0;
-        for (int w = 0; w < kThreads / 32; ++w) {
-          if (w < warp) incl += s.warp_cost[w];
-          all += s.warp_cost[w];
-        }
-        if (turn && mine > 0) {
-          const int64_t start = before + incl - mine;
-          if (speaker) p.pieces_b[b] = pieces_of(start, units, C, n);
-          if (pair < n && start <= x0 && x0 < start + mine) {
-            s.start_chain = ch.packed + b;
-            s.start_cost = start;
-          }
-        }
-        before += all;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (lane == 31) s.warp_cost[warp] = incl;
+      __syncthreads();
+      start = before + incl - mine;
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) start += s.warp_cost[w];
+        before += s.warp_cost[w];
+      }
+    };
+    sum_up(0, my_length);
+    for (int32_t b0 = kThreads; b0 < p.batch; b0 += kThreads) {
+      __syncthreads();
+      sum_up(b0, b0 + tid < p.batch ? p.seq_lens[b0 + tid] : 0);
+    }
+    const int64_t C = before, each = ch.cost(ch.units_a());
+    const int32_t n = pairs_for(C, p.pairs);
+    const int64_t x0 = pair < n ? bound(C, n, pair) : C;
+    if (tid == 0) {
+      s.total = C;
+      s.share[0] = x0;
+      s.share[1] = pair < n ? bound(C, n, pair + 1) : C;
+      const bool in_a = ch.packed > 0 && x0 < ch.cost_a();
+      s.start_chain = in_a ? (int32_t)quotient(x0, each) : ch.packed + p.batch;
+      s.start_cost = in_a ? s.start_chain * each : C;
+    }
+    __syncthreads();
+    auto find = [&](int32_t b0) {
+      if (mine > 0 && start <= x0 && x0 < start + mine) {
+        s.start_chain = ch.packed + b0 + tid;
+        s.start_cost = start;
+      }
+    };
+    if (p.batch <= kThreads) {
+      find(0);
+    } else {
+      before = ch.cost_a();
+      for (int32_t b0 = 0; b0 < p.batch; b0 += kThreads) {
+        sum_up(b0, b0 + tid < p.batch ? p.seq_lens[b0 + tid] : 0);
+        find(b0);
         __syncthreads();
       }
-      base = before;
     }
   }
   tc_fence_before();
   cluster_sync();  // barriers and tensor memory are ready in both blocks
   tc_fence_after();
   const uint32_t tmem = s.tmem_base;
-  Walk walk(p, ch, s, pair);
+  Walk walk(p, ch, s);
 
   // The issuing roles are one thread each.
   auto wait = [&](uint64_t *bar, uint32_t parity) {
@@ -363,17 +382,29 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
       constexpr int kBoxes = kOwn / kBox;
       const uint32_t q_bar = cluster_addr(smem_u32(&s.q_full[0]), 0), k_bar = cluster_addr(smem_u32(&s.k_full[0]), 0);
       uint32_t sl = 0, turn = 1, items = 0, piece = 0;
-      bool ok = true, was_few = false;
-      while (ok && walk.next()) {
-        int32_t blk[kBoxes];  // read a tile ahead
-        auto look_up = [&](int32_t tt) {
+      bool ok = true, was_few = false, have = walk.next();
+      // This block's tokens of a tile (both blocks load at least a box of every item, so that neither falls
+      // behind the rings' rounds: where the second has none of its own, the tile's first, for masked columns).
+      auto own_of = [&](const Walk &w, int32_t tt) { return tt + (int)rank * kOwn < w.t1 ? tt + (int)rank * kOwn : tt; };
+      auto boxes_of = [](int32_t tokens) { return max(1, (min(tokens, kOwn) + kBox - 1) / kBox); };
+      int32_t blk[kBoxes], y[kBoxes];
+      auto look_up = [&](const Walk &w, int32_t tt) {
+        const int32_t own = own_of(w, tt);
 #pragma unroll
-          for (int i = 0; i < kBoxes; ++i) {
-            const int32_t own = tt + (int)rank * kOwn, at = (own < walk.t1 ? own : tt) + i * kBox;
-            blk[i] = at < walk.t1 ? block_of(p, walk, at) : 0;
-          }
-        };
-        look_up(walk.t0);
+        for (int i = 0; i < kBoxes; ++i) blk[i] = own + i * kBox < w.t1 ? block_of(p, w, own + i * kBox) : 0;
+      };
+      auto settle = [&](const Walk &w, int32_t tt) {
+        const int32_t own = own_of(w, tt);
+#pragma unroll
+        for (int i = 0; i < kBoxes; ++i) y[i] = own + i * kBox < w.t1 ? pool_row(p, blk[i], own + i * kBox) : 0;
+      };
+      if (have) {
+        look_up(walk, walk.t0);
+        settle(walk, walk.t0);
+      }
+      while (ok && have) {
+        Walk ahead = walk;
+        const bool more = ahead.next();
         // the last piece's queries stay where they are read while these come, if neither takes all the room
         if (piece >= 2 && !(ok = wait(&s.q_free[piece & 1u], ((piece >> 1) - 1) & 1u))) break;
         const bool few = walk.few(), beside = few && was_few;
@@ -392,26 +423,29 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
         ++piece;
         for (int32_t tt = walk.t0; ok && tt < walk.t1; tt += kTile) {
           const int32_t n = min(kTile, walk.t1 - tt);
-          // Both blocks load at least a box of every item, so that neither falls behind the ring's rounds
-          // (the second one the tile's first tokens where it has none of its own: masked columns).
-          const int32_t tokens = min(max(n - (int)rank * kOwn, 0), kOwn), others = min(max(n - (1 - (int)rank) * kOwn, 0), kOwn);
-          const int32_t boxes = max(1, (tokens + kBox - 1) / kBox);
-          const uint32_t bytes = (uint32_t)((boxes + max(1, (others + kBox - 1) / kBox)) * kBox * 128);
-          int32_t y[kBoxes];
-#pragma unroll
-          for (int i = 0; i < kBoxes; ++i) y[i] = i < boxes ? pool_row(p, blk[i], (tokens > 0 ? tt + (int)rank * kOwn : tt) + i * kBox) : 0;
-          if (tt + kTile < walk.t1) look_up(tt + kTile);
+          const int32_t boxes = boxes_of(rank == 0 || n <= kOwn ? n : n - kOwn);
+          const int32_t others = boxes_of(rank == 1 || n <= kOwn ? n : n - kOwn);
+          const uint32_t bytes = (uint32_t)((boxes + others) * kBox * 128);
+          // what comes next: its table entries are read while this tile's loads are issued ...
+          const bool last = tt + kTile >= walk.t1;
+          if (!last) look_up(walk, tt + kTile);
+          else if (more) look_up(ahead, ahead.t0);
           for (int c = 0; c < kChunks; ++c) {
             if (!(ok = wait(&s.k_empty[sl], turn))) break;
             if (first_block) mbar_arrive_expect_tx(smem_u32(&s.k_full[sl]), bytes);
-            const uint32_t dst = smem_u32(s.k[0]) + sl * kItemBytes, bar = k_bar + 8 * sl;
+            const uint32_t dst = smem_u32(s.k[0]) + sl * kItemBytes, full = k_bar + 8 * sl;
 #pragma unroll
             for (int i = 0; i < kBoxes; ++i)
-              if (i < boxes) tma_load_2d_pair(dst + i * kBox * 128, &maps.k, 64 * c, y[i], bar);
+              if (i < boxes) tma_load_2d_pair(dst + i * kBox * 128, &maps.k, 64 * c, y[i], full);
             ++items;
             if (++sl == kSlotsK) sl = 0, turn ^= 1u;
           }
+          // ... and looked at when they are
+          if (!last) settle(walk, tt + kTile);
+          else if (more) settle(ahead, ahead.t0);
         }
+        walk = ahead;
+        have = more;
       }
       if (s.abort && first_block) {  // let the loads in flight land in both blocks
         for (uint32_t i = items > kSlotsK ? items - kSlotsK : 0; i < items; ++i)
@@ -583,6 +617,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
       }
       mma_commit_pair(smem_u32(&s.mma_end));
       if (!mbar_wait(smem_u32(&s.mma_end), 0, nullptr, kWaitBudgetNs)) report(p.dev_status, MLA_ERR_DEVICE_TIMEOUT);
+    } else if (!first_block) {
+      if (pair == 0) write_pieces(p, ch, s.total);
     }
   } else {
     // ---------------------------------------------------------------- softmax, results
@@ -773,11 +809,13 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p) {
   griddep_wait();
   if (row >= (int64_t)p.batch * p.heads) return;
   const int32_t b = (int32_t)(row / p.heads), h = (int32_t)(row % p.heads);
-  const Chains ch(p, false);
-  const int32_t L = ch.length(p, b, false);
-  const Pieces none = {0, -1};
-  const Pieces own = ch.units(L) > 0 ? p.pieces_b[b] : none;
-  const Pieces com = ch.packed > 0 && L >= ch.shared ? p.pieces_a[row / kRows] : none;
+  // all at once: what is not there is not looked at
+  const int32_t shared_blocks = *p.shared_blocks, length = p.seq_lens[b];
+  const Pieces all_own = p.pieces_b[b], all_com = p.pieces_a[row / kRows], none = {0, -1};
+  const Chains ch(p, shared_blocks, false);
+  const int32_t L = ch.length(length);
+  const Pieces own = ch.units(L) > 0 ? all_own : none;
+  const Pieces com = ch.packed > 0 && L >= ch.shared ? all_com : none;
   const int na = com.last - com.first + 1, nb = own.last - own.first + 1;
   if (ch.from(L) == 0 && nb == 1) return;  // written at once
   const int64_t a0 = (row / kRows + com.first) * kRows + row % kRows;
@@ -873,7 +911,7 @@ int pairs_current() {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, shared_kernel<128>, &cfg) != cudaSuccess || n < 1) return 0;
+  if (cudaOccupancyMaxActiveClusters(&n, shared_kernel<64>, &cfg) != cudaSuccess || n < 1) return 0;
   n = std::min(n, kMaxPairs);
   known[dev].store(n, std::memory_order_release);
   return n;
@@ -949,7 +987,8 @@ mla_status_t mla_decode_shared(const void *q, const void *cache, int64_t num_blo
   }
   Maps maps;
   const int64_t rows = num_blocks * block_size;
-  if (!tmap::encode_2d(&maps.k, cache, rows, (uint32_t)std::min(block_size, kOwn)) || !tmap::encode_3d(&maps.v, cache, rows, kGroup, 2) ||
+  if (!tmap::encode_2d(&maps.k, cache, rows, (uint32_t)std::min(block_size, kOwn)) ||
+      !tmap::encode_3d(&maps.v, cache, rows, kGroup, 2) ||
       !tmap::encode_3d(&maps.q, q, (int64_t)batch * num_heads, kHalf, 3) ||
       !tmap::encode_3d(&maps.q_few, q, (int64_t)batch * num_heads, kFew, kChunks)) {
     set_error_detail("cannot describe q or the cache to TMA");

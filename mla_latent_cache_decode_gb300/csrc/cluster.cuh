@@ -80,6 +80,19 @@ __device__ __forceinline__ void mma_ss_pair_low(uint32_t d, uint32_t a, uint32_t
       "r"(a), "r"(b), "r"(id), "r"(more), "n"(kDescHigh)
       : "memory");
 }
+__device__ __forceinline__ void mma_ss_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t more) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(more)
+      : "memory");
+}
+// The same of 8-bit numbers.
+__device__ __forceinline__ void mma_ss_pair_fp8(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t more) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(more)
+      : "memory");
+}
 // Arrives at the barrier at this address in both blocks when every MMA issued before has completed.
 __device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
   asm volatile(

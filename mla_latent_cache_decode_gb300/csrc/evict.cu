@@ -206,31 +206,35 @@ struct CompactParams {
   int32_t batch, layers, num_blocks, block_size, max_blocks_per_seq, budget, max_tokens, blocks;
 };
 
-// Where token t of the request lies in the pool, or -1 (and reported).
-__device__ __forceinline__ int64_t slot_of(const CompactParams &p, const int32_t *table, int32_t t) {
-  const int32_t page = t / p.block_size, blk = table[page];
-  if (blk < 0 || blk >= p.num_blocks) {
-    report(p.dev_status, MLA_ERR_DEVICE_RANGE);
-    return -1;
-  }
-  return (int64_t)blk * p.block_size + (t - page * p.block_size);
-}
-
 // The source of token j, or -1: it stays where it is, or its entry is no ascending one of the
 // request's (reported).
 __device__ __forceinline__ int32_t source_of(const CompactParams &p, const int32_t *keep, int32_t j, int32_t L) {
-  const int32_t t = keep[j];
-  if (t < j || t >= L || (j > 0 && keep[j - 1] >= t)) {
+  const int32_t t = keep[j], before = j > 0 ? keep[j - 1] : -1;
+  if (t < j || t >= L || before >= t) {
     report(p.dev_status, MLA_ERR_DEVICE_RANGE);
     return -1;
   }
   return t == j ? -1 : t;
 }
 
+// Pool rows of token j's source and target, or -1: nothing to move (a block outside the pool is reported).
+__device__ __forceinline__ int2 rows_of(const CompactParams &p, const int32_t *table, const int32_t *keep, int32_t j, int32_t L) {
+  const int32_t t = source_of(p, keep, j, L);
+  if (t < 0) return make_int2(-1, -1);
+  const int32_t from_page = t / p.block_size, to_page = j / p.block_size;
+  const int32_t from = table[from_page], to = table[to_page];
+  if (from < 0 || from >= p.num_blocks || to < 0 || to >= p.num_blocks) {
+    report(p.dev_status, MLA_ERR_DEVICE_RANGE);
+    return make_int2(-1, -1);
+  }
+  return make_int2(from * p.block_size + (t - from_page * p.block_size), to * p.block_size + (j - to_page * p.block_size));
+}
+
 // kLanes units of 16 bytes make a slice of a row: 8 (bf16) or 4 (E4M3).
 template <int kLanes>
 __global__ void __launch_bounds__(kMoveThreads) compact_kernel(const CompactParams p) {
-  constexpr int kRows = kMoveThreads / kLanes;  // rows of one unit a thread
+  constexpr int kPass = kMoveThreads / kLanes, kRows = kPass * kMoveUnits;  // rows of one unit a thread; of a phase
+  __shared__ int2 s_rows[2][kRows];  // sources and targets of a phase's rows
   const int tid = threadIdx.x, nb = p.blocks;
   const int rank = nb > 1 ? (int)cluster_rank() : 0;
   const int64_t job = blockIdx.x / nb;
@@ -240,7 +244,7 @@ __global__ void __launch_bounds__(kMoveThreads) compact_kernel(const CompactPara
   griddep_wait();
   int32_t L = p.seq_lens[b], n = p.new_lens[b];
   const int64_t pages = (int64_t)p.max_blocks_per_seq * p.block_size;
-  const int32_t most = p.mass ? (int32_t)min(pages, (int64_t)p.max_tokens) : (int32_t)min(pages, (int64_t)INT32_MAX);
+  const int32_t most = p.mass ? (int32_t)min(pages, (int64_t)p.max_tokens) : (int32_t)pages;
   if (L < 0 || L > most || n < 0 || n > min(L, p.budget)) {
     if (tid == 0) report(p.dev_status, MLA_ERR_DEVICE_RANGE);
     L = min(max(L, 0), most);
@@ -273,28 +277,32 @@ __global__ void __launch_bounds__(kMoveThreads) compact_kernel(const CompactPara
     return;
   }
   const int slice = (int)(job % kSlices), layer = (int)(job / kSlices / p.batch);
-  constexpr int kRowBytes = kSlices * kLanes * 16;
+  constexpr int64_t kRowBytes = kSlices * kLanes * 16;
   uint8_t *cache = p.cache + (int64_t)layer * p.layer_bytes + (slice * kLanes + tid % kLanes) * 16;
   const int32_t *table = p.block_table + (int64_t)b * p.max_blocks_per_seq;
-  for (int64_t base = 0; base < n; base += (int64_t)nb * kRows * kMoveUnits) {
+  auto look_up = [&](int64_t base, int2 *to) {
+    for (int r = tid; r < kRows; r += kMoveThreads) {
+      const int64_t j = base + (int64_t)rank * kRows + r;
+      to[r] = j < n ? rows_of(p, table, keep, (int32_t)j, L) : make_int2(-1, -1);
+    }
+  };
+  look_up(0, s_rows[0]);
+  __syncthreads();
+  int turn = 0;
+  for (int64_t base = 0; base < n; base += (int64_t)nb * kRows, turn ^= 1) {
     uint4 x[kMoveUnits];
-    bool put[kMoveUnits];
-    const int64_t j0 = base + (int64_t)rank * kRows * kMoveUnits + tid / kLanes;
+    int32_t to[kMoveUnits];
 #pragma unroll
     for (int u = 0; u < kMoveUnits; ++u) {
-      const int64_t j = j0 + u * kRows;
-      const int32_t t = j < n ? source_of(p, keep, (int32_t)j, L) : -1;
-      const int64_t from = t >= 0 ? slot_of(p, table, t) : -1;
-      put[u] = from >= 0;
-      if (put[u]) x[u] = __ldcg(reinterpret_cast<const uint4 *>(cache + from * kRowBytes));
+      const int2 row = s_rows[turn][u * kPass + tid / kLanes];
+      to[u] = row.y;
+      if (row.y >= 0) x[u] = __ldcg(reinterpret_cast<const uint4 *>(cache + row.x * kRowBytes));
     }
+    look_up(base + (int64_t)nb * kRows, s_rows[turn ^ 1]);  // the next phase's, while these load
     meet();
 #pragma unroll
-    for (int u = 0; u < kMoveUnits; ++u) {
-      if (!put[u]) continue;
-      const int64_t to = slot_of(p, table, (int32_t)(j0 + u * kRows));
-      if (to >= 0) *reinterpret_cast<uint4 *>(cache + to * kRowBytes) = x[u];
-    }
+    for (int u = 0; u < kMoveUnits; ++u)
+      if (to[u] >= 0) *reinterpret_cast<uint4 *>(cache + to[u] * kRowBytes) = x[u];
   }
 }
 
@@ -349,10 +357,10 @@ cudaError_t allow_select_smem() {
   return e;
 }
 
-// Blocks of a request's cluster: what its longest part asks for, as long as the SMs are not full.
-int cluster_for(int64_t wanted, int64_t clusters, int sms) {
+// Blocks of a cluster: what its longest part asks for, as long as there are fewer blocks than `enough`.
+int cluster_for(int64_t wanted, int64_t clusters, int64_t enough) {
   int c = 1;
-  while (c < 8 && c < wanted && clusters * c < sms) c *= 2;
+  while (c < 8 && c < wanted && clusters * c < enough) c *= 2;
   return c;
 }
 
@@ -360,8 +368,9 @@ mla_status_t run_compact(CompactParams p, int64_t num_blocks, int row_bytes, int
   set_error_detail("");
   if (p.batch < 0 || p.budget < 0) return invalid("batch < 0 or max_keep < 0");
   if (layers < 0 || layers > INT32_MAX) return invalid("num_layers outside [0, 2^31)");
-  if (p.block_size <= 0 || num_blocks <= 0 || num_blocks > INT32_MAX || p.max_blocks_per_seq <= 0)
-    return invalid("block_size, num_blocks and max_blocks_per_seq must be > 0, num_blocks below 2^31");
+  if (p.block_size <= 0 || num_blocks <= 0 || num_blocks > INT32_MAX || num_blocks * p.block_size > INT32_MAX ||
+      p.max_blocks_per_seq <= 0)
+    return invalid("block_size, num_blocks and max_blocks_per_seq must be > 0, num_blocks * block_size below 2^31");
   if ((int64_t)p.max_blocks_per_seq * p.block_size > INT32_MAX / 2) return invalid("max_blocks_per_seq * block_size > 2^30");
   if (p.batch == 0) return MLA_OK;
   if (!p.block_table || !p.seq_lens || !p.new_lens || (p.budget > 0 && !p.keep) || (layers > 0 && !p.cache)) return invalid("null pointer");
@@ -380,7 +389,7 @@ mla_status_t run_compact(CompactParams p, int64_t num_blocks, int row_bytes, int
   if (e != cudaSuccess) return status_of(e);
   const int lanes = row_bytes / kSlices / 16;
   const int64_t rows = std::min<int64_t>(p.budget, (int64_t)p.max_blocks_per_seq * p.block_size);
-  p.blocks = cluster_for((rows + kMoveUnits * kMoveThreads / lanes - 1) / (kMoveUnits * kMoveThreads / lanes), jobs, sms);
+  p.blocks = cluster_for((rows + kMoveUnits * kMoveThreads / lanes - 1) / (kMoveUnits * kMoveThreads / lanes), jobs, 4 * (int64_t)sms);
   if (jobs * p.blocks > INT32_MAX) return invalid("batch * num_layers too large");
   e = lanes == 8 ? launch(compact_kernel<8>, jobs * p.blocks, kMoveThreads, 0, p.blocks, (cudaStream_t)stream, p)
                  : launch(compact_kernel<4>, jobs * p.blocks, kMoveThreads, 0, p.blocks, (cudaStream_t)stream, p);

@@ -102,8 +102,16 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
   const float *mass = p.mass + (int64_t)b * p.mass_stride;
   const int32_t lo = p.sink, hi = L - p.recent;  // the tokens that are asked about
   auto key_at = [&](int32_t t) { return held ? s.keys[t - first] : key_of(mass[t]); };
-  if (held)
-    for (int32_t t = first + tid; t < last; t += kSelThreads) s.keys[t - first] = key_of(mass[t]);
+  if (held) {
+    for (int32_t t0 = first + tid; t0 < last; t0 += 16 * kSelThreads) {
+      float x[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = t0 + i * kSelThreads < last ? mass[t0 + i * kSelThreads] : 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (t0 + i * kSelThreads < last) s.keys[t0 + i * kSelThreads - first] = key_of(x[i]);
+    }
+  }
   __syncthreads();
   uint32_t known = 0, need = (uint32_t)(K - p.sink - p.recent);
   const int shifts[4] = {21, 10, 0, 0};
@@ -190,8 +198,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
 // ---------------------------------------------------------------------------- compact
 
 constexpr int kSlices = 9;
-constexpr int kMoveThreads = 256;
-constexpr int kMoveUnits = 8;  // 16-byte (4-byte: a weight) units that a thread holds in a phase
+constexpr int kMoveThreads = 256, kMoveBlocks = 6;
+constexpr int kMoveUnits = 4;  // 16-byte (4-byte: a weight) units that a thread holds in a phase
 
 struct CompactParams {
   uint8_t *cache;
@@ -232,7 +240,8 @@ __device__ __forceinline__ int2 rows_of(const CompactParams &p, const int32_t *t
 
 // kLanes units of 16 bytes make a slice of a row: 8 (bf16) or 4 (E4M3).
 template <int kLanes>
-__global__ void __launch_bounds__(kMoveThreads) compact_kernel(const CompactParams p) {
+__global__ void __launch_bounds__(kMoveThreads, kMoveBlocks) compact_kernel(const CompactParams p) {
+  static_assert(kMoveThreads % kLanes == 0, "whole rows");
   constexpr int kPass = kMoveThreads / kLanes, kRows = kPass * kMoveUnits;  // rows of one unit a thread; of a phase
   __shared__ int2 s_rows[2][kRows];  // sources and targets of a phase's rows
   const int tid = threadIdx.x, nb = p.blocks;
@@ -391,8 +400,8 @@ mla_status_t run_compact(CompactParams p, int64_t num_blocks, int row_bytes, int
   const int64_t rows = std::min<int64_t>(p.budget, (int64_t)p.max_blocks_per_seq * p.block_size);
   p.blocks = cluster_for((rows + kMoveUnits * kMoveThreads / lanes - 1) / (kMoveUnits * kMoveThreads / lanes), jobs, 4 * (int64_t)sms);
   if (jobs * p.blocks > INT32_MAX) return invalid("batch * num_layers too large");
-  e = lanes == 8 ? launch(compact_kernel<8>, jobs * p.blocks, kMoveThreads, 0, p.blocks, (cudaStream_t)stream, p)
-                 : launch(compact_kernel<4>, jobs * p.blocks, kMoveThreads, 0, p.blocks, (cudaStream_t)stream, p);
+  e = row_bytes == kRow * 2 ? launch(compact_kernel<kRow * 2 / 16 / kSlices>, jobs * p.blocks, kMoveThreads, 0, p.blocks, (cudaStream_t)stream, p)
+                            : launch(compact_kernel<kRow / 16 / kSlices>, jobs * p.blocks, kMoveThreads, 0, p.blocks, (cudaStream_t)stream, p);
   return status_of(e);
 }
 

@@ -64,6 +64,7 @@ struct SelectSmem {
   uint32_t warp_more[kSelWarps], warp_same[kSelWarps];
   uint32_t totals[2];  // of this block: tokens that stay without asking, tokens of weight T
   uint32_t found, above;
+  uint32_t bins[kBins / 2], bins_total;  // of a cluster's block: its share of the bins, over all blocks
   uint32_t keys[kSelKeys];
 };
 
@@ -72,6 +73,21 @@ __device__ __forceinline__ uint32_t key_of(float x) {
   if (x != x) return 0u;
   const uint32_t u = __float_as_uint(x + 0.0f);  // -0 + 0 = +0
   return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// Of a number of each thread, the sum over the threads before.
+__device__ __forceinline__ uint32_t sum_before(SelectSmem &s, uint32_t mine) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  __syncthreads();  // the last call's sums are read
+  if (lane == 31) s.warp_sum[warp] = incl;
+  __syncthreads();
+  return incl - mine + __reduce_add_sync(0xffffffffu, lane < warp ? s.warp_sum[lane] : 0);
 }
 
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p) {
@@ -124,30 +140,45 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
       const uint32_t k = key_at(t);
       if (pass == 0 || (k >> above_shift) == known) atomicAdd(&hist[(k >> shift) & mask], 1u);
     }
-    if (nb > 1) cluster_sync(); else __syncthreads();
-    // bins from the top down, two a thread: the one that holds the need-th largest
-    uint32_t n0 = 0, n1 = 0;
-    const int bin = kBins - 1 - 2 * tid;
-    for (int r = 0; r < nb; ++r) {
-      n0 += nb > 1 ? remote_u32(&hist[bin], r) : hist[bin];
-      n1 += nb > 1 ? remote_u32(&hist[bin - 1], r) : hist[bin - 1];
-    }
-    uint32_t incl = n0 + n1;
+    // the bin, from the top down, that holds the need-th largest
+    if (nb == 1) {
+      __syncthreads();
+      const int bin = kBins - 1 - 2 * tid;
+      const uint32_t n0 = hist[bin], n1 = hist[bin - 1], excl = sum_before(s, n0 + n1);
+      if (excl < need && need <= excl + n0 + n1) {
+        const bool second = excl + n0 < need;
+        s.found = (uint32_t)(second ? bin - 1 : bin);
+        s.above = second ? excl + n0 : excl;
+      }
+    } else {
+      // each block adds up its share of the bins over the blocks, and says what they hold together
+      cluster_sync();
+      const int per = kBins / nb, bin = kBins - 1 - (rank * per + tid);
+      uint32_t n[8], sum = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    if (lane == 31) s.warp_sum[warp] = incl;
-    __syncthreads();
-    uint32_t before = lane < warp ? s.warp_sum[lane] : 0;
-    before = __reduce_add_sync(0xffffffffu, before);
-    incl += before;
-    const uint32_t excl = incl - n0 - n1;
-    if (excl < need && need <= incl) {
-      const bool second = excl + n0 < need;
-      s.found = (uint32_t)(second ? bin - 1 : bin);
-      s.above = second ? excl + n0 : excl;
+      for (int r = 0; r < 8; ++r) n[r] = tid < per && r < nb ? remote_u32(&hist[bin], r) : 0;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) sum += n[r];
+      if (tid < per) s.bins[tid] = sum;
+      const uint32_t before = sum_before(s, sum);
+      if (tid == kSelThreads - 1) s.bins_total = before + sum;
+      cluster_sync();
+      uint32_t total[8], above = 0;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) total[r] = r < nb ? remote_u32(&s.bins_total, r) : 0;
+      int owner = 0;  // of the bin; the shares lie from the top down in order of rank
+#pragma unroll
+      for (int r = 0; r < 7; ++r) {
+        if (owner == r && above + total[r] < need) {
+          above += total[r];
+          owner = r + 1;
+        }
+      }
+      const uint32_t mine = tid < per ? remote_u32(&s.bins[tid], owner) : 0, excl = above + sum_before(s, mine);
+      if (excl < need && need <= excl + mine) {
+        s.found = (uint32_t)(kBins - 1 - (owner * per + tid));
+        s.above = excl;
+      }
     }
     __syncthreads();
     known = pass == 0 ? s.found : (known << (pass == 2 ? 10 : 11)) | s.found;

@@ -26,8 +26,8 @@
 // Work: a chain is a request's tokens in units of 128, the units dealt out to the
 // pairs in order in runs of equal cost; every block works out the deal (as in
 // shared.cu).  Warp roles: 0 loads rows, 1 issues the MMAs (first block of the
-// pair), 2 loads bf16 queries, 3 owns the tensor memory, 4-7 weigh (thread = 64
-// tokens x 2 halves of the heads) and split E4M3 queries.  Every wait is bounded;
+// pair), 2 loads bf16 queries, 3 owns the tensor memory, 4-11 weigh (thread = 64
+// tokens x 4 quarters of the heads) and split queries for E4M3.  Every wait is bounded;
 // one that runs out reports MLA_ERR_DEVICE_TIMEOUT and ends the block's others.
 #include <algorithm>
 #include <atomic>
@@ -51,7 +51,7 @@ using namespace sm100;
 constexpr int kTile = 128;          // tokens of a unit: 64 in each block of the pair
 constexpr int kOwn = kTile / 2;
 constexpr int kChunks = kRow / 64;  // 9
-constexpr int kThreads = 256, kWeighWarp0 = 4;
+constexpr int kThreads = 384, kWeighWarp0 = 4, kWeighWarps = 8;
 constexpr int kItemChunks = 3;      // chunks of an item of the ring
 constexpr int kMaxSlots = 12;
 constexpr int kBuffers = 2;         // of S, by tile
@@ -65,8 +65,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 struct Control {
   // full, q_full and s_free count in the first block; the others in each
   uint64_t full[kMaxSlots], empty[kMaxSlots], q_full, q_free, s_full[kBuffers], s_free[kBuffers], sum_full[2][2], head_full, mma_end;
-  float lse[2][kHeads + 16], factor[2][kHeads + 16];  // by chain parity: lse and scale for 2^x
-  float sum[2][kOwn];                       // the second half's heads, by tile parity
+  float lse[2][kHeads + 32], factor[2][kHeads + 32];  // by chain parity: lse and scale for 2^x
+  float sum[2][kOwn][4];                    // of a token's heads, by quarters, by tile parity
   int64_t start_cost, share[2], warp_cost[kThreads / 32];
   int32_t start_chain;
   uint32_t tmem_base;
@@ -177,13 +177,13 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
     for (int i = 0; i < p.slots; ++i) init(&s.full[i], 1), init(&s.empty[i], 1);
     for (int i = 0; i < 2; ++i) {
       init(&s.s_full[i], 1);
-      init(&s.s_free[i], 8);
-      init(&s.sum_full[i][0], 1);
-      init(&s.sum_full[i][1], 1);
+      init(&s.s_free[i], 2 * kWeighWarps);
+      init(&s.sum_full[i][0], 4);
+      init(&s.sum_full[i][1], 4);
     }
-    init(&s.q_full, kFp8 ? 8 : 1);
+    init(&s.q_full, kFp8 ? 2 * kWeighWarps : 1);
     init(&s.q_free, 1);
-    init(&s.head_full, 4);
+    init(&s.head_full, kWeighWarps);
     init(&s.mma_end, 1);
     s.abort = 0;
     fence_mbarrier_init_cluster();
@@ -372,68 +372,78 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
     }
   } else if (warp >= kWeighWarp0) {
     // ---------------------------------------------------------------- weights
-    const int quad = warp - kWeighWarp0, half = quad >> 1, rows32 = quad & 1;
+    // Thread = a token and a quarter of the heads: half a block's.
+    const int quad = warp & 3, half = quad >> 1, rows32 = quad & 1, part = (warp - kWeighWarp0) >> 2;
     const int r = rows32 * 32 + lane, thread = tid - 32 * kWeighWarp0;
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     const uint32_t s_bar = cluster_addr(smem_u32(&s.s_free[0]), 0), q_bar = cluster_addr(smem_u32(&s.q_full), 0);
     const int real = min(max(p.heads - half * p.head_stride, 0), p.head_stride);
+    const int split = (real / 2 + 15) / 16 * 16, i_from = part == 0 ? 0 : split, i_to = part == 0 ? min(split, real) : real;
     uint32_t g = 0, piece = 0;
     bool ok = true;
     while (ok && walk.next()) {
       const uint32_t turn = piece & 1u;
       // every head's lse and scale, for 2^x; nothing from a head with -inf
-      for (int h = thread; h < p.heads; h += 128) {
+      for (int h = thread; h < p.heads; h += 32 * kWeighWarps) {
         const float l = p.lse[(int64_t)walk.b * p.heads + h];
         s.lse[turn][h] = l == -INFINITY ? INFINITY : l * kLog2e;
       }
       if (kFp8) {
-        // the queries as sums of two E4M3 numbers: both blocks find every head's scale, each splits its own;
-        // four threads a head
+        // the queries as sums of two E4M3 numbers: both blocks find every head's scale, each splits its own
+        // heads; a warp takes four at a time.  (Columns of no head hold what they held.)
         if (piece > 0 && !(ok = warp_wait(s, &s.q_free, (piece - 1) & 1u, p.dev_status))) break;
-        const int quarter = thread & 3;
-        for (int i0 = 0; i0 < 2 * p.half_heads; i0 += 32) {
-          const int block = i0 + (thread >> 2) >= p.half_heads, i = i0 + (thread >> 2) - block * p.half_heads;
-          const int h = block * p.head_stride + i;
-          const bool is = i < p.head_stride && h < p.heads;
-          const uint4 *src = reinterpret_cast<const uint4 *>(p.q + ((int64_t)walk.b * p.heads + (is ? h : 0)) * kRow) + quarter * 18;
-          float top = 0.f;
-#pragma unroll 6
-          for (int u = 0; u < 18; ++u) {
-            const uint4 w = src[u];
-            const uint32_t w4[4] = {w.x, w.y, w.z, w.w};
+        for (int h0 = 4 * (warp - kWeighWarp0); h0 < p.heads; h0 += 4 * kWeighWarps) {
+          uint4 w[4][3];  // dims 8 x .. 8 x + 7 for x = lane, lane + 32, lane + 64
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w4[k] << 16)), fabsf(__uint_as_float(w4[k] & 0xffff0000u))));
-          }
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          // 2^e with top * 2^e in (224, 448]; a head of zeros, or of none but what is not finite, stays as it is
-          int e = 0;
-          if (top > 0.f && top < INFINITY) {
-            e = 8 - ilogbf(top);
-            if (ldexpf(top, e) > 448.f) --e;
-          }
-          if (is && quarter == 0) s.factor[turn][h] = ldexpf(p.scale_log2, -e);
-          if (block != (int)rank || i >= p.half_heads) continue;
-#pragma unroll 2
-          for (int u = 0; u < 18; ++u) {
-            const uint4 w = src[u];
-            const uint32_t w4[4] = {w.x, w.y, w.z, w.w};
-            uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+          for (int m = 0; m < 4; ++m) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(p.q + ((int64_t)walk.b * p.heads + min(h0 + m, p.heads - 1)) * kRow);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float x0 = is ? ldexpf(__uint_as_float(w4[k] << 16), e) : 0.f, x1 = is ? ldexpf(__uint_as_float(w4[k] & 0xffff0000u), e) : 0.f;
-              const uint32_t c = f32x2_to_e4m3x2(x0, x1), back = e4m3x2_to_f16x2(c);
-              const __half2 h2 = *reinterpret_cast<const __half2 *>(&back);
-              const uint32_t d = f32x2_to_e4m3x2(x0 - __low2float(h2), x1 - __high2float(h2));
-              hi[k >> 1] |= c << 16 * (k & 1);
-              lo[k >> 1] |= d << 16 * (k & 1);
+            for (int v = 0; v < 3; ++v) w[m][v] = lane + 32 * v < kRow / 8 ? src[lane + 32 * v] : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll 1
+          for (int m = 0; m < 4; ++m) {
+            const int h = h0 + m;
+            if (h >= p.heads) break;
+            uint32_t u[12];
+#pragma unroll
+            for (int v = 0; v < 3; ++v) u[4 * v] = w[0][v].x, u[4 * v + 1] = w[0][v].y, u[4 * v + 2] = w[0][v].z, u[4 * v + 3] = w[0][v].w;
+#pragma unroll
+            for (int v = 0; v < 3; ++v) w[0][v] = w[1][v], w[1][v] = w[2][v], w[2][v] = w[3][v];
+            float top = 0.f;
+#pragma unroll
+            for (int k = 0; k < 12; ++k) top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[k] << 16)), fabsf(__uint_as_float(u[k] & 0xffff0000u))));
+            // magnitudes as whole numbers of the same order
+            top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+            // 2^e with top * 2^e in (224, 448], in two factors that are fp32 numbers; a head of zeros, or of
+            // nothing above 2^-100, is scaled as if it had that
+            int e = 135 - max((int)(__float_as_uint(top) >> 23), 27);
+            const float up0 = __uint_as_float((uint32_t)(127 + e / 2) << 23);
+            if (top * up0 * __uint_as_float((uint32_t)(127 + e - e / 2) << 23) > 448.f) --e;
+            const float up1 = __uint_as_float((uint32_t)(127 + e / 2) << 23), up2 = __uint_as_float((uint32_t)(127 + e - e / 2) << 23);
+            if (lane == 0) s.factor[turn][h] = ldexpf(p.scale_log2, -e);
+            const int i = h - (int)rank * p.head_stride, j = p.half_heads + i;
+            if (i < 0 || i >= p.head_stride) continue;
+#pragma unroll
+            for (int v = 0; v < 3; ++v) {
+              uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                float x0 = __uint_as_float(u[4 * v + k] << 16) * up1 * up2, x1 = __uint_as_float(u[4 * v + k] & 0xffff0000u) * up1 * up2;
+                x0 += x0 - x0, x1 += x1 - x1;  // an infinity, which E4M3 has not, becomes a NaN
+                const uint32_t c = f32x2_to_e4m3x2(x0, x1), back = e4m3x2_to_f16x2(c);
+                const __half2 h2 = *reinterpret_cast<const __half2 *>(&back);
+                const uint32_t d = f32x2_to_e4m3x2(x0 - __low2float(h2), x1 - __high2float(h2));
+                hi[k >> 1] |= c << 16 * (k & 1);
+                lo[k >> 1] |= d << 16 * (k & 1);
+              }
+              // chunk x / 8, in which 16-byte units are exchanged by the row (64-byte swizzle)
+              const int x = lane + 32 * v, unit = (x >> 1) & 3;
+              if (x < kRow / 8) {
+                uint8_t *at = queries + (x >> 3) * cols * 64 + (x & 1) * 8;
+                *reinterpret_cast<uint2 *>(at + i * 64 + ((unit ^ ((i >> 1) & 3)) << 4)) = make_uint2(hi[0], hi[1]);
+                *reinterpret_cast<uint2 *>(at + j * 64 + ((unit ^ ((j >> 1) & 3)) << 4)) = make_uint2(lo[0], lo[1]);
+              }
             }
-            // dims 8 x .. 8 x + 7: chunk x / 8, in which 16-byte units are exchanged by the row (64-byte swizzle)
-            const int x = quarter * 18 + u, unit = (x >> 1) & 3, j = p.half_heads + i;
-            uint8_t *at = queries + (x >> 3) * cols * 64 + (x & 1) * 8;
-            *reinterpret_cast<uint2 *>(at + i * 64 + ((unit ^ ((i >> 1) & 3)) << 4)) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2 *>(at + j * 64 + ((unit ^ ((j >> 1) & 3)) << 4)) = make_uint2(lo[0], lo[1]);
           }
         }
         fence_proxy_async_shared();
@@ -448,40 +458,46 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
       const float c = p.scale_log2;
       for (int32_t tt = walk.t0; tt < walk.t1; tt += kTile, ++g) {
         const int32_t t = tt + (int)rank * kOwn + r;
-        const bool mine = half == 0 && t < walk.t1;
+        const bool mine = half == 0 && part == 0 && t < walk.t1;
         const float before = mine && p.previous ? p.previous[(int64_t)walk.b * p.previous_stride + t] : 0.f;
         if (!(ok = warp_wait(s, &s.s_full[g & 1u], (g >> 1) & 1u, p.dev_status))) break;
         tc_fence_after();
         const uint32_t src = lanes + 128 * (g & 1u);
         float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll 1
-        for (int i = 0; i < real; i += 16) {
-          uint32_t x[16], y[16];
+        for (int i = i_from; i < i_to; i += 32) {
+          uint32_t x[32], y[kFp8 ? 32 : 1];
           tmem_ld16(src + i, x);
           if (kFp8) tmem_ld16(src + p.half_heads + i, y);
+          const bool wide = i + 16 < i_to;
+          if (wide) {
+            tmem_ld16(src + i + 16, x + 16);
+            if (kFp8) tmem_ld16(src + p.half_heads + i + 16, y + 16 * kFp8);
+          }
           tmem_wait_ld();
-          tmem_loaded16(x);
-          if (kFp8) tmem_loaded16(y);
 #pragma unroll
-          for (int k = 0; k < 16; k += 2) {
-            float a = __uint_as_float(x[k]), b = __uint_as_float(x[k + 1]);
-            if (kFp8) a += __uint_as_float(y[k]), b += __uint_as_float(y[k + 1]);
-            a = ex2_approx(fmaf(a, kFp8 ? factor[i + k] : c, -lse[i + k]));
-            b = ex2_approx(fmaf(b, kFp8 ? factor[i + k + 1] : c, -lse[i + k + 1]));
-            if (i + k < real) sum0 += a;
-            if (i + k + 1 < real) sum1 += b;
+          for (int j = 0; j < 2; ++j) {
+            if (j == 1 && !wide) break;
+            tmem_loaded16(x + 16 * j);
+            if (kFp8) tmem_loaded16(y + 16 * kFp8 * j);
+#pragma unroll
+            for (int k = 16 * j; k < 16 * j + 16; k += 2) {
+              float a = __uint_as_float(x[k]), b = __uint_as_float(x[k + 1]);
+              if (kFp8) a += __uint_as_float(y[k * kFp8]), b += __uint_as_float(y[(k + 1) * kFp8]);
+              a = ex2_approx(fmaf(a, kFp8 ? factor[i + k] : c, -lse[i + k]));
+              b = ex2_approx(fmaf(b, kFp8 ? factor[i + k + 1] : c, -lse[i + k + 1]));
+              if (i + k < i_to) sum0 += a;
+              if (i + k + 1 < i_to) sum1 += b;
+            }
           }
         }
-        float sum = sum0 + sum1;
-        if (half == 1) {
-          s.sum[g & 1u][r] = sum;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&s.sum_full[g & 1u][rows32]));
-        } else {
-          if (!(ok = warp_wait(s, &s.sum_full[g & 1u][rows32], (g >> 1) & 1u, p.dev_status))) break;
-          sum += s.sum[g & 1u][r];
-        }
-        // S and the other half's sums are read
+        s.sum[g & 1u][r][2 * half + part] = sum0 + sum1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s.sum_full[g & 1u][rows32]));
+        if (!(ok = warp_wait(s, &s.sum_full[g & 1u][rows32], (g >> 1) & 1u, p.dev_status))) break;
+        const float4 four = *reinterpret_cast<const float4 *>(s.sum[g & 1u][r]);
+        const float sum = (four.x + four.y) + (four.z + four.w);
+        // S is read, and nobody needs this tile's sums
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(s_bar + 8 * (g & 1u));

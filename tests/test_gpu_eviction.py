@@ -82,6 +82,17 @@ def test_shared_many_requests(mla, heads, batch):
     check_shared(c)
 
 
+@pytest.mark.parametrize("heads,batch", [(1, 1500), (16, 385), (128, 386)])
+def test_shared_more_requests_than_threads(mla, heads, batch):
+    """Lengths are summed up a block's threads at a time; empty requests and short ones among them."""
+    rng = np.random.default_rng(batch)
+    lens = [int(n) for n in rng.choice([0, 1, 33, 64, 65, 90], batch)]
+    c = shared_case(rng, heads, 32, 2, lens)
+    run_shared(mla, c)
+    assert int(c["status"]) == 0
+    check_shared(c)
+
+
 @pytest.mark.parametrize("heads", [16, 128])
 def test_shared_nothing_in_common(mla, heads):
     c = shared_case(np.random.default_rng(8), heads, 64, 0, [300, 1, 64, 0, 999])
@@ -208,6 +219,43 @@ def test_mass_against_definition(mla, heads, page, lens, fp8):
     check_mass(c, 0.0, None)
     run_mass(mla, c, previous=c["previous"], decay=0.75)
     check_mass(c, 0.75, f64(c["previous"]))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("heads,batch", [(2, 1200), (40, 390)])
+def test_mass_more_requests_than_threads(mla, heads, batch, fp8):
+    rng = np.random.default_rng(batch)
+    c = mass_case(rng, heads, 16, [int(n) for n in rng.choice([0, 1, 33, 64, 65, 130], batch)], fp8)
+    run_mass(mla, c)
+    assert int(c["status"]) == 0
+    check_mass(c, 0.0, None)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("heads", [3, 40])
+def test_mass_long(mla, heads, fp8):
+    """More tiles than the rings' rounds and S's buffers, on every pair of SMs."""
+    c = mass_case(np.random.default_rng(28), heads, 64, [30001, 700, 5000], fp8)
+    run_mass(mla, c)
+    assert int(c["status"]) == 0
+    check_mass(c, 0.0, None)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_mass_rows_and_queries_that_are_not_finite(mla, fp8):
+    """A token's weight is its own row's affair; a head's query is every token's of its request."""
+    c = mass_case(np.random.default_rng(29), 16, 32, [200, 100, 90], fp8)
+    run_mass(mla, c)
+    clean = f64(c["mass"])
+    if fp8:
+        c["cache"][int(c["table"][0][2]), 7, 3] = 0x7F  # token 71: a NaN
+    else:
+        c["cache"][int(c["table"][0][2]), 7, 3] = float("nan")
+    c["q"][2, 5, 100] = float("inf")
+    run_mass(mla, c)
+    got = f64(c["mass"])
+    assert np.isnan(got[0, 71]) and np.array_equal(np.delete(got[0], 71), np.delete(clean[0], 71)) and np.array_equal(got[1], clean[1])
+    assert not np.isfinite(got[2, :90]).any() or not fp8
 
 
 @pytest.mark.parametrize("fp8", [False, True])

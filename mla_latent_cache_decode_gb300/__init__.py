@@ -467,9 +467,10 @@ def _rows(t, dtype, shape, dev, name):
     """t's address and outer strides, once it holds rows of contiguous elements of this type and
     shape on the current device."""
     try:
-        if (t.dtype is dtype and t.shape == shape and t.get_device() == dev
-                and t.stride(-1) == 1):
-            return (t.data_ptr(), *_strides(t, shape[-1]))
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+            strides = t.stride()
+            if strides[-1] == 1:
+                return (t.data_ptr(), *(_strides(t, shape[-1]) if 1 in shape[:-1] else strides[:-1]))
     except AttributeError:
         pass
     _refuse(t, dtype, shape, dev, name)

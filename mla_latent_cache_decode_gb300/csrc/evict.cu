@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
   int32_t *keep = p.keep + (int64_t)b * K;
   if (tid == 0 && rank == 0) p.new_lens[b] = min(L, K);
   if (L <= K) {  // (the same for every block of the cluster)
-    for (int j = rank * kSelThreads + tid; j < K; j += nb * kSelThreads) keep[j] = j < L ? j : -1;
+    for (int64_t j = rank * kSelThreads + tid; j < K; j += nb * kSelThreads) keep[j] = j < L ? (int32_t)j : -1;
     return;
   }
   // this block's tokens, and each warp's

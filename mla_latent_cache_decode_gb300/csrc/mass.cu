@@ -194,6 +194,9 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
     tmem_alloc_pair(smem_u32(&s.tmem_base), kCols);
     tmem_relinquish_pair();
   }
+  __syncwarp();
+  tc_fence_before();
+  cluster_arrive();  // barriers and tensor memory, to both blocks
   griddep_wait();
   griddep_launch_dependents();
 
@@ -248,8 +251,8 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
       }
     }
   }
-  tc_fence_before();
-  cluster_sync();  // barriers, the deal and tensor memory are ready in both blocks
+  __syncthreads();
+  cluster_wait();
   tc_fence_after();
   const uint32_t tmem = s.tmem_base;
   Walk walk(p, s);

@@ -101,6 +101,7 @@ struct __align__(1024) Smem {
 };
 static_assert(kChunks * kFewChunkBytes <= kFewBytes && kFewBytes + (kChunks - 1) * kFewChunkBytes + kChunkBytes <= kChunks * kChunkBytes,
               "two sets of few heads' queries, and what is read behind them, lie in q");
+static_assert(kSlotsV < 4, "two items with zeros have to be read before two more are filled: tail_full holds one round");
 static_assert(sizeof(Smem) + 1024 <= 232448, "shared memory");
 
 struct Maps {
@@ -303,6 +304,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
     tmem_alloc_pair(smem_u32(&s.tmem_base), kCols);
     tmem_relinquish_pair();
   }
+  __syncwarp();
+  tc_fence_before();
+  cluster_arrive();  // barriers and tensor memory, to both blocks
   griddep_wait();
   griddep_launch_dependents();  // the merge waits for this grid's end, on the SMs' free threads
 
@@ -363,8 +367,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
       }
     }
   }
-  tc_fence_before();
-  cluster_sync();  // barriers and tensor memory are ready in both blocks
+  __syncthreads();
+  cluster_wait();
   tc_fence_after();
   const uint32_t tmem = s.tmem_base;
   Walk walk(p, ch, s);

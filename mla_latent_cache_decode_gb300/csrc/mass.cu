@@ -60,12 +60,15 @@ constexpr int64_t kUnitCost = 2, kChainCost = 3;
 constexpr int kMaxPairs = 256;
 constexpr uint64_t kWaitBudgetNs = 100000000ull;
 constexpr uint64_t kDrainBudgetNs = 10000000ull;
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr double kLog2eExact = 1.4426950408889634074;
+constexpr float kLog2e = (float)kLog2eExact, kLog2eRest = (float)(kLog2eExact - (double)kLog2e);
 
 struct Control {
   // full, q_full and s_free count in the first block; the others in each
   uint64_t full[kMaxSlots], empty[kMaxSlots], q_full, q_free, s_full[kBuffers], s_free[kBuffers], sum_full[2][2], head_full, mma_end;
-  float lse[2][kHeads + 32], factor[2][kHeads + 32];  // by chain parity: lse and scale for 2^x
+  // By chain parity: lse and scale for 2^x, each as a number and what its rounding left (an exponent of 40
+  // rounded to 24 bits is off by as much as all of a weight's other errors).
+  float lse[2][kHeads + 32], lse_rest[2][kHeads + 32], factor[2][kHeads + 32], factor_rest[2][kHeads + 32];
   float sum[2][kOwn][4];                    // of a token's heads, by quarters, by tile parity
   int64_t start_cost, share[2], warp_cost[kThreads / 32];
   int32_t start_chain;
@@ -92,7 +95,7 @@ struct Params {
   int32_t head_stride;  // heads of the first block
   int32_t half_heads;   // columns for a block's heads, a multiple of 16
   int32_t slots;
-  float scale_log2, decay;
+  float scale_log2, scale_rest, decay;  // scale * log2(e) is the sum of the two
 };
 
 template <bool kFp8>
@@ -389,7 +392,9 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
       // every head's lse and scale, for 2^x; nothing from a head with -inf
       for (int h = thread; h < p.heads; h += 32 * kWeighWarps) {
         const float l = p.lse[(int64_t)walk.b * p.heads + h];
-        s.lse[turn][h] = l == -INFINITY ? INFINITY : l * kLog2e;
+        const float x = l * kLog2e;
+        s.lse[turn][h] = l == -INFINITY ? INFINITY : x;
+        s.lse_rest[turn][h] = fabsf(x) < INFINITY ? fmaf(l, kLog2e, -x) + l * kLog2eRest : 0.f;
       }
       if (kFp8) {
         // the queries as sums of two E4M3 numbers: both blocks find every head's scale, each splits its own
@@ -423,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
             const float up0 = __uint_as_float((uint32_t)(127 + e / 2) << 23);
             if (top * up0 * __uint_as_float((uint32_t)(127 + e - e / 2) << 23) > 448.f) --e;
             const float up1 = __uint_as_float((uint32_t)(127 + e / 2) << 23), up2 = __uint_as_float((uint32_t)(127 + e - e / 2) << 23);
-            if (lane == 0) s.factor[turn][h] = ldexpf(p.scale_log2, -e);
+            if (lane == 0) s.factor[turn][h] = ldexpf(p.scale_log2, -e), s.factor_rest[turn][h] = ldexpf(p.scale_rest, -e);
             const int i = h - (int)rank * p.head_stride, j = p.half_heads + i;
             if (i < 0 || i >= p.head_stride) continue;
 #pragma unroll
@@ -457,8 +462,12 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
       if (lane == 0) mbar_arrive(smem_u32(&s.head_full));
       if (!(ok = warp_wait(s, &s.head_full, turn, p.dev_status))) break;
       ++piece;
-      const float *lse = &s.lse[turn][half * p.head_stride], *factor = &s.factor[turn][half * p.head_stride];
-      const float c = p.scale_log2;
+      const int at = half * p.head_stride;
+      const float *lse = &s.lse[turn][at], *lse_rest = &s.lse_rest[turn][at], *factor = &s.factor[turn][at], *factor_rest = &s.factor_rest[turn][at];
+      auto weight = [&](float x, int h) {
+        const float c = kFp8 ? factor[h] : p.scale_log2, rest = kFp8 ? factor_rest[h] : p.scale_rest;
+        return ex2_approx(fmaf(x, c, -lse[h]) + fmaf(x, rest, -lse_rest[h]));
+      };
       for (int32_t tt = walk.t0; tt < walk.t1; tt += kTile, ++g) {
         const int32_t t = tt + (int)rank * kOwn + r;
         const bool mine = half == 0 && part == 0 && t < walk.t1;
@@ -487,8 +496,8 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
             for (int k = 16 * j; k < 16 * j + 16; k += 2) {
               float a = __uint_as_float(x[k]), b = __uint_as_float(x[k + 1]);
               if (kFp8) a += __uint_as_float(y[k * kFp8]), b += __uint_as_float(y[(k + 1) * kFp8]);
-              a = ex2_approx(fmaf(a, kFp8 ? factor[i + k] : c, -lse[i + k]));
-              b = ex2_approx(fmaf(b, kFp8 ? factor[i + k + 1] : c, -lse[i + k + 1]));
+              a = weight(a, i + k);
+              b = weight(b, i + k + 1);
               if (i + k < i_to) sum0 += a;
               if (i + k + 1 < i_to) sum1 += b;
             }
@@ -652,7 +661,9 @@ mla_status_t run(const Args &a, void *stream) {
   p.longest = (int32_t)std::min<int64_t>(a.max_tokens, (int64_t)a.max_blocks_per_seq * a.block_size);
   p.head_stride = (a.heads + 1) / 2;
   p.half_heads = (p.head_stride + 15) / 16 * 16;
-  p.scale_log2 = a.scale * a.kv_scale * kLog2e;
+  const double scale = (double)a.scale * a.kv_scale * kLog2eExact;
+  p.scale_log2 = (float)scale;
+  p.scale_rest = (float)(scale - (double)p.scale_log2);
   p.decay = a.decay;
   Maps maps;
   if (!encode(a.cache, a.num_blocks * a.block_size, a.fp8, std::min(a.block_size, kOwn), 1, &maps.k) ||

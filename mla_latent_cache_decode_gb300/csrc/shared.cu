@@ -45,6 +45,8 @@
 #include <atomic>
 #include <cmath>
 
+#include <cuda_fp16.h>
+
 #include "cluster.cuh"
 #include "common.cuh"
 #include "tmap.h"
@@ -124,7 +126,8 @@ struct Params {
   float *lse;
   int32_t *dev_status;
   Pieces *pieces_a, *pieces_b;
-  __nv_bfloat16 *o_a, *o_b;  // [slot][row][512]
+  __half *o_a, *o_b;         // [slot][row][512], in units of
+  float *unit_a, *unit_b;    // [slot][8][row], one for 64 dims
   float *lse_a, *lse_b;      // [slot][row]
   int32_t num_blocks, block_size, page_log2, max_shared_blocks, max_blocks_per_seq, batch, heads, pairs;
   float scale_log2;
@@ -740,20 +743,19 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
       const float lse = l == 0.f ? -INFINITY : (m_used + log2f(l)) * 0.69314718055994531f;
       if (real_rows > 0) {
         const int row0 = (int)rank * kHalf + rows32 * 32;  // of the chain
-        __nv_bfloat16 *dst;
-        float *lse_dst;
-        if (walk.packed) {
-          const int64_t at = ((int64_t)walk.chain + pair) * kRows + row0;
-          dst = p.o_a + at * kVDim;
-          lse_dst = p.lse_a + at;
-        } else if (walk.whole) {
+        const bool whole = walk.whole;
+        const int unit_rows = walk.packed ? kRows : p.heads;
+        uint16_t *dst;  // bf16 of a whole request, f16 of a piece
+        float *lse_dst, *unit_dst = nullptr;
+        if (whole) {
           const int64_t at = (int64_t)walk.chain * p.heads + row0;
-          dst = p.out + at * kVDim;
+          dst = (uint16_t *)p.out + at * kVDim;
           lse_dst = p.lse ? p.lse + at : nullptr;
         } else {
-          const int64_t at = ((int64_t)walk.chain + pair) * p.heads + row0;
-          dst = p.o_b + at * kVDim;
-          lse_dst = p.lse_b + at;
+          const int64_t slot = ((int64_t)walk.chain + pair) * unit_rows;
+          dst = (uint16_t *)(walk.packed ? p.o_a : p.o_b) + (slot + row0) * kVDim;
+          lse_dst = (walk.packed ? p.lse_a : p.lse_b) + slot + row0;
+          unit_dst = (walk.packed ? p.unit_a : p.unit_b) + slot * 8 + (4 * part + 2 * half) * unit_rows + row0 + lane;
         }
         dst += 256 * part + 128 * half + 8 * (lane & 7);
         // 64 dims at a time by way of this warp's part of P, so that 8 threads store a row's 128 bytes
@@ -766,10 +768,30 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
           tmem_wait_ld();
           tmem_loaded32(o);
           tmem_loaded32(o + 32);
+          if (whole) {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            __nv_bfloat162 two = __floats2bfloat162_rn(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
-            o[k] = *reinterpret_cast<uint32_t *>(&two);
+            for (int k = 0; k < 32; ++k) {
+              __nv_bfloat162 two = __floats2bfloat162_rn(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+              o[k] = *reinterpret_cast<uint32_t *>(&two);
+            }
+          } else {
+            // f16 in units of a power of two that takes the largest of the 64 to [2^14, 2^15): a rounding of
+            // 2^-12 of it at most, where bf16's 2^-9 of each was as large as all other errors of `out` together
+            float top0 = 0.f, top1 = 0.f;
+#pragma unroll
+            for (int k = 0; k < 64; k += 2) {
+              top0 = fmaxf(top0, fabsf(__uint_as_float(o[k])));
+              top1 = fmaxf(top1, fabsf(__uint_as_float(o[k + 1])));
+            }
+            const float top = fmaxf(top0, top1) * inv;
+            const uint32_t e = top < INFINITY ? max(__float_as_uint(top) >> 23, 15u) : 141u;  // (141: as they are)
+            const float by = inv * __uint_as_float((268u - e) << 23);
+            if (lane < real_rows) unit_dst[i * unit_rows] = __uint_as_float((e - 14u) << 23);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              __half2 two = __floats2half2_rn(__uint_as_float(o[2 * k]) * by, __uint_as_float(o[2 * k + 1]) * by);
+              o[k] = *reinterpret_cast<uint32_t *>(&two);
+            }
           }
           __syncwarp();
 #pragma unroll
@@ -828,14 +850,19 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p) {
 #pragma unroll
   for (int k = 0; k < 16; ++k) acc[k] = 0.f;
   for (int i0 = 0; i0 < na + nb; i0 += kMergeFlight) {
-    float l[kMergeFlight];
+    float l[kMergeFlight], unit[kMergeFlight][2];
     uint4 x[kMergeFlight][2];
 #pragma unroll
     for (int u = 0; u < kMergeFlight; ++u) {
       const int i = min(i0 + u, na + nb - 1);
-      const int64_t at = i < na ? a0 + (int64_t)i * kRows : b0 + (int64_t)(i - na) * p.heads;
-      l[u] = i0 + u < na + nb ? (i < na ? p.lse_a : p.lse_b)[at] : -INFINITY;
-      const uint4 *src = reinterpret_cast<const uint4 *>((i < na ? p.o_a : p.o_b) + at * kVDim);
+      const bool in_a = i < na;
+      const int rows = in_a ? kRows : p.heads, r = in_a ? (int)(row % kRows) : h;
+      const int64_t at = in_a ? a0 + (int64_t)i * kRows : b0 + (int64_t)(i - na) * p.heads;
+      l[u] = i0 + u < na + nb ? (in_a ? p.lse_a : p.lse_b)[at] : -INFINITY;
+      const float *units = (in_a ? p.unit_a : p.unit_b) + (at - r) * 8 + (lane >> 3) * rows + r;
+      unit[u][0] = units[0];
+      unit[u][1] = units[4 * rows];
+      const uint4 *src = reinterpret_cast<const uint4 *>((in_a ? p.o_a : p.o_b) + at * kVDim);
       x[u][0] = src[lane];
       x[u][1] = src[32 + lane];
     }
@@ -855,8 +882,10 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p) {
       if (w != 0.f) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          acc[2 * k] += w * __uint_as_float(v[k] << 16);
-          acc[2 * k + 1] += w * __uint_as_float(v[k] & 0xffff0000u);
+          const float2 two = __half22float2(*reinterpret_cast<const __half2 *>(&v[k]));
+          const float f = w * unit[u][k >> 2];
+          acc[2 * k] += f * two.x;
+          acc[2 * k + 1] += f * two.y;
         }
       }
     }
@@ -922,7 +951,7 @@ int pairs_current() {
 }
 
 struct Layout {
-  size_t pieces_a, pieces_b, lse_a, lse_b, o_a, o_b, total;
+  size_t pieces_a, pieces_b, lse_a, lse_b, unit_a, unit_b, o_a, o_b, total;
 };
 
 Layout layout(int64_t batch, int64_t heads, int64_t pairs) {
@@ -933,8 +962,10 @@ Layout layout(int64_t batch, int64_t heads, int64_t pairs) {
   l.pieces_b = o; o = align256(o + sizeof(Pieces) * batch);
   l.lse_a = o;    o = align256(o + sizeof(float) * (packed + pairs) * kRows);
   l.lse_b = o;    o = align256(o + sizeof(float) * (batch + pairs) * heads);
-  l.o_a = o;      o = align256(o + sizeof(__nv_bfloat16) * (packed + pairs) * kRows * kVDim);
-  l.o_b = o;      o = align256(o + sizeof(__nv_bfloat16) * (batch + pairs) * heads * kVDim);
+  l.unit_a = o;   o = align256(o + sizeof(float) * (packed + pairs) * kRows * 8);
+  l.unit_b = o;   o = align256(o + sizeof(float) * (batch + pairs) * heads * 8);
+  l.o_a = o;      o = align256(o + sizeof(__half) * (packed + pairs) * kRows * kVDim);
+  l.o_b = o;      o = align256(o + sizeof(__half) * (batch + pairs) * heads * kVDim);
   l.total = o;
   return l;
 }
@@ -1012,8 +1043,10 @@ mla_status_t mla_decode_shared(const void *q, const void *cache, int64_t num_blo
   p.pieces_b = (Pieces *)(ws + l.pieces_b);
   p.lse_a = (float *)(ws + l.lse_a);
   p.lse_b = (float *)(ws + l.lse_b);
-  p.o_a = (__nv_bfloat16 *)(ws + l.o_a);
-  p.o_b = (__nv_bfloat16 *)(ws + l.o_b);
+  p.unit_a = (float *)(ws + l.unit_a);
+  p.unit_b = (float *)(ws + l.unit_b);
+  p.o_a = (__half *)(ws + l.o_a);
+  p.o_b = (__half *)(ws + l.o_b);
   p.num_blocks = (int32_t)num_blocks;
   p.block_size = block_size;
   for (p.page_log2 = 4; 1 << p.page_log2 < block_size;) ++p.page_log2;

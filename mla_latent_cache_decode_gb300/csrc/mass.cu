@@ -55,7 +55,6 @@ constexpr int kThreads = 384, kWeighWarp0 = 4, kWeighWarps = 8;
 constexpr int kItemChunks = 3;      // chunks of an item of the ring
 constexpr int kMaxSlots = 12;
 constexpr int kBuffers = 2;         // of S, by tile
-constexpr uint32_t kCols = 256;
 constexpr int64_t kUnitCost = 2, kChainCost = 3;
 constexpr int kMaxPairs = 256;
 constexpr uint64_t kWaitBudgetNs = 100000000ull;
@@ -104,6 +103,10 @@ struct Sizes {
   static constexpr int kChunkBytes = kOwn * kChunkRow;
   static constexpr int kItemBytes = kItemChunks * kChunkBytes;
   static constexpr int kParts = kFp8 ? 2 : 1;             // columns of a head
+  // The tensor cores cut each sum to 24 bits: 36 steps of it were most of a weight's error.  The bf16 form
+  // has room for a sum of its own for each third of the dims, added in registers (E4M3: 18 steps, one sum).
+  static constexpr int kSums = kFp8 ? 1 : kChunks / kItemChunks;
+  static constexpr uint32_t kBuffer = kFp8 ? 128 : 256, kCols = kBuffers * kBuffer;
 };
 
 // Dynamic shared memory: the ring, the queries (chunk after chunk, this block's columns as rows), Control.
@@ -194,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
     if (!kFp8) prefetch_tmap(&maps.q);
   }
   if (warp == 3) {
-    tmem_alloc_pair(smem_u32(&s.tmem_base), kCols);
+    tmem_alloc_pair(smem_u32(&s.tmem_base), Z::kCols);
     tmem_relinquish_pair();
   }
   __syncwarp();
@@ -338,19 +341,21 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
         if (!(ok = wait(&s.q_full, piece++ & 1u))) break;
         for (int32_t tt = walk.t0; ok && tt < walk.t1; tt += kTile, ++g) {
           if (g >= kBuffers && !(ok = wait(&s.s_free[g & 1u], ((g >> 1) - 1) & 1u))) break;
-          const uint32_t d = tmem + 128 * (g & 1u);
+          const uint32_t buffer = tmem + Z::kBuffer * (g & 1u);
 #pragma unroll 1
           for (int c = 0; c < kChunks; c += kItemChunks) {
             if (!(ok = wait(&s.full[sl], turn))) break;
             tc_fence_after();
             const uint64_t a = a0 + (uint64_t)(sl * (Z::kItemBytes >> 4)), b = b0 + (uint64_t)(c * b_chunk);
+            const uint32_t d = buffer + (Z::kSums > 1 ? c / kItemChunks * cols : 0);
+            const bool fresh = Z::kSums > 1 || c == 0;
 #pragma unroll
             for (int k = 0; k < kItemChunks; ++k)
 #pragma unroll
               for (int st = 0; st < Z::kChunkRow / 32; ++st) {
                 const uint64_t ak = a + (uint64_t)((k * Z::kChunkBytes + 32 * st) >> 4), bk = b + (uint64_t)(k * b_chunk + 2 * st);
-                if (kFp8) mma_ss_pair_fp8(d, ak, bk, id, (c | k | st) ? 1u : 0u);
-                else mma_ss_pair(d, ak, bk, id, (c | k | st) ? 1u : 0u);
+                if (kFp8) mma_ss_pair_fp8(d, ak, bk, id, fresh && (k | st) == 0 ? 0u : 1u);
+                else mma_ss_pair(d, ak, bk, id, fresh && (k | st) == 0 ? 0u : 1u);
               }
             mma_commit_pair(smem_u32(&s.empty[sl]));
             if (++sl == (uint32_t)p.slots) sl = 0, turn ^= 1u;
@@ -474,33 +479,27 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
         const float before = mine && p.previous ? p.previous[(int64_t)walk.b * p.previous_stride + t] : 0.f;
         if (!(ok = warp_wait(s, &s.s_full[g & 1u], (g >> 1) & 1u, p.dev_status))) break;
         tc_fence_after();
-        const uint32_t src = lanes + 128 * (g & 1u);
+        const uint32_t src = lanes + Z::kBuffer * (g & 1u);
         float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll 1
-        for (int i = i_from; i < i_to; i += 32) {
-          uint32_t x[32], y[kFp8 ? 32 : 1];
-          tmem_ld16(src + i, x);
-          if (kFp8) tmem_ld16(src + p.half_heads + i, y);
-          const bool wide = i + 16 < i_to;
-          if (wide) {
-            tmem_ld16(src + i + 16, x + 16);
-            if (kFp8) tmem_ld16(src + p.half_heads + i + 16, y + 16 * kFp8);
-          }
+        for (int i = i_from; i < i_to; i += 16) {
+          // what adds up to a score: hi and lo, or the thirds of the dims
+          constexpr int kTerms = kFp8 ? 2 : Z::kSums;
+          uint32_t x[kTerms][16];
+#pragma unroll
+          for (int j = 0; j < kTerms; ++j) tmem_ld16(src + j * (kFp8 ? p.half_heads : cols) + i, x[j]);
           tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            if (j == 1 && !wide) break;
-            tmem_loaded16(x + 16 * j);
-            if (kFp8) tmem_loaded16(y + 16 * kFp8 * j);
+          for (int j = 0; j < kTerms; ++j) tmem_loaded16(x[j]);
 #pragma unroll
-            for (int k = 16 * j; k < 16 * j + 16; k += 2) {
-              float a = __uint_as_float(x[k]), b = __uint_as_float(x[k + 1]);
-              if (kFp8) a += __uint_as_float(y[k * kFp8]), b += __uint_as_float(y[(k + 1) * kFp8]);
-              a = weight(a, i + k);
-              b = weight(b, i + k + 1);
-              if (i + k < i_to) sum0 += a;
-              if (i + k + 1 < i_to) sum1 += b;
-            }
+          for (int k = 0; k < 16; k += 2) {
+            float a = __uint_as_float(x[0][k]), b = __uint_as_float(x[0][k + 1]);
+#pragma unroll
+            for (int j = 1; j < kTerms; ++j) a += __uint_as_float(x[j][k]), b += __uint_as_float(x[j][k + 1]);
+            a = weight(a, i + k);
+            b = weight(b, i + k + 1);
+            if (i + k < i_to) sum0 += a;
+            if (i + k + 1 < i_to) sum1 += b;
           }
         }
         s.sum[g & 1u][r][2 * half + part] = sum0 + sum1;
@@ -523,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
   tc_fence_before();
   cluster_sync();  // nobody arrives at a block that has left
   tc_fence_after();
-  if (warp == 3) tmem_dealloc_pair(tmem, kCols);
+  if (warp == 3) tmem_dealloc_pair(tmem, Z::kCols);
 }
 
 // ---------------------------------------------------------------------------- host

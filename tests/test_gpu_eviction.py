@@ -235,7 +235,7 @@ def test_mass_more_requests_than_threads(mla, heads, batch, fp8):
 @pytest.mark.parametrize("heads", [3, 40])
 def test_mass_long(mla, heads, fp8):
     """More tiles than the rings' rounds and S's buffers, on every pair of SMs."""
-    c = mass_case(np.random.default_rng(28), heads, 64, [30001, 700, 5000], fp8)
+    c = mass_case(np.random.default_rng(28), heads, 64, [12001, 700, 3000], fp8)
     run_mass(mla, c)
     assert int(c["status"]) == 0
     check_mass(c, 0.0, None)

@@ -518,8 +518,9 @@ mla_status_t mla_prefill(const void *q_nope, int64_t q_nope_token_stride,
  * out of place.  Rows that no request sees are never part of a result, whatever
  * they hold; a row that is not finite reaches the requests that see it.
  * block_size in {16, 32, 64, 128, 256}; max_blocks_per_seq * block_size and
- * max_shared_blocks * block_size <= 2^30; batch <= 2^20.  Split results are
- * merged as mla_decode's: bf16 with fp32 log-sum-exps.
+ * max_shared_blocks * block_size <= 2^30, num_blocks * block_size < 2^31; batch <=
+ * 2^20.  Partial results are merged by their fp32 log-sum-exps, as mla_decode's
+ * are; they are held in f16 with a power of two for each 64 dims.
  */
 size_t mla_decode_shared_workspace_size(int32_t batch, int32_t num_heads);
 mla_status_t mla_decode_shared(const void *q, const void *cache, int64_t num_blocks,
@@ -555,7 +556,7 @@ mla_status_t mla_decode_shared(const void *q, const void *cache, int64_t num_blo
  * A length outside [0, min(max_tokens, max_blocks_per_seq * block_size)] is clamped
  * and reported as MLA_ERR_DEVICE_RANGE; the weights of a page outside the pool
  * are unspecified, and it is reported.  Strides in elements, >= max_tokens.
- * block_size in {16, 32, 64, 128, 256}; batch < 2^24.
+ * block_size in {16, 32, 64, 128, 256}; num_blocks * block_size < 2^31; batch < 2^24.
  *
  * mla_attention_mass_fp8 — the same over an FP8 cache (rows value(code) * kv_scale).
  * The products run on the codes and on q as the sum of two E4M3 numbers a dim,
@@ -590,13 +591,15 @@ mla_status_t mla_decode_shared(const void *q, const void *cache, int64_t num_blo
  * puts there), and so is a block outside the pool; each is reported as
  * MLA_ERR_DEVICE_RANGE.  A page that several requests share must be one whose
  * rows stay at their place in all of them (sink >= the tokens in common).
- * Any block_size >= 1 with max_blocks_per_seq * block_size <= 2^30.
+ * Any block_size >= 1 with max_blocks_per_seq * block_size <= 2^30 and num_blocks *
+ * block_size < 2^31.
  *
  * mla_cache_compact_fp8 — the same for an FP8 cache (uint8, codes moved as they are).
  *
  * Launch order: these calls and mla_decode_shared are programmatic dependents
  * of the kernel before them (see mla_decode): they wait for it to complete
- * before they touch memory.
+ * before they touch memory.  mla_decode_shared and mla_attention_mass release
+ * their own dependents early, as the 128-head decode does.
  */
 mla_status_t mla_attention_mass(const void *q, const void *cache, int64_t num_blocks,
                                 int32_t block_size, const int32_t *block_table,

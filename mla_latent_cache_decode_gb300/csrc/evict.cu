@@ -14,6 +14,14 @@
 // takes a contiguous part, the histograms and counts are added up through
 // distributed shared memory, and nothing depends on the order of atomics.
 //
+// What bounds it: latency.  131,072 + 7 x 1,024 tokens take 23 us on eight blocks a
+// request: 10 without the three passes (loads, counts, the places), and 3.3 to 5 a
+// pass, of which the histograms' atomics are nothing measurable and two meetings
+// of the cluster with three trips through distributed shared memory most.  (Every
+// block adding up all bins of all blocks took 32 us; keys in registers 23, and 9.8
+// instead of 5.2 for four short requests by the code's size; equal digits counted
+// once for a warp 35.)  20 x 4,096 tokens: 7.9 us, a block each.
+//
 // Compact.  keep[b][0..n) ascends strictly, so token j comes from keep[j] >= j
 // and a row's target is never behind its source: in order of j, writing rows
 // below J touches no source of rows from J on.  A phase loads a run of rows into
@@ -21,7 +29,14 @@
 // of the same phase at most), and stores them; nothing waits between phases.
 // Columns do not depend on each other, so a row is cut into nine slices (128
 // bytes of a bf16 row, 64 of an E4M3 one) and a cluster moves one slice of one
-// request of one layer.
+// request of one layer.  A row's two pages are looked up once, by one thread, a
+// phase ahead.
+//
+// What bounds it: memory, by the bytes in flight.  20 x 4,096 tokens cut to 2,048: 94 MB
+// in 20.5 us (4.6 TB/s, 68% of the copy rate); eight E4M3 layers: 138 MB in 32 us.
+// From the same: eight units a thread 22.7 and 35.7 us, sixteen 26 and 44; three
+// slices a row 25 and 36, whole rows 40; two blocks an SM asked for instead of
+// four 26 us, eight 20.9 by spilling.
 #include <algorithm>
 #include <atomic>
 #include <cmath>

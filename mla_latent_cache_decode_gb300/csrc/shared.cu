@@ -14,11 +14,11 @@
 // (Packing that leaves as many chains as there are requests, 128 heads for one,
 // saves nothing: then there is no kind A and B runs over all tokens.  A request
 // shorter than the shared part is a B over what it sees.)  Chains are cut into
-// units of 256 tokens and the units dealt out to the pairs of SMs in order, in
-// runs of equal cost; every block works the deal out from the lengths, so that
-// there is no plan to keep.  A run's piece of a chain leaves a partial result
-// (normalised, bf16, with its log-sum-exp) and merge_kernel joins them; a whole
-// request in one piece is written at once.
+// units of 64 tokens (128 where pages hold that) and the units dealt out to the
+// pairs of SMs in order, in runs of equal cost; every block works the deal out
+// from the lengths, so that there is no plan to keep.  A run's piece of a chain
+// leaves a partial result with its log-sum-exp and merge_kernel joins them; a
+// whole request in one piece is written at once.
 //
 // A pair of SMs shares each MMA (cta_group::2, M = 128: 64 rows in each SM,
 // 128 lanes hold two halves of N).  An SM's tensor memory then holds O of 64 rows
@@ -26,21 +26,41 @@
 // no single-SM shape does without computing scores twice.
 //   S [128 x 256] = Q K^T   B operand: each block's 128 tokens x 576 dims
 //   O [128 x 512] += P V    B operand: all 256 tokens, each block's 256 dims
-// So a token's row comes into the pair's shared memory almost twice (278 KB a
-// tile and SM against 4,352 clk of MMAs: 64 bytes a clock).  Operands stream
-// through one ring of seven 16 KB slots in the order of use: K(0), K(1), V(0),
-// K(2), V(1), ...; nine items of K and eight of V, each 256 clk of MMAs.  The
-// softmax of tile t runs under P V(t-1) and Q K(t+1).
+// So a token's row comes into the pair's shared memory almost twice: 17 items of
+// 16 KB a tile and SM, against 4,352 clk of MMAs.  K and V stream through rings of
+// four and three slots, each with an issuing thread of its own for its MMAs; P is
+// handed over and its room freed by halves of the tile, so that the softmax of
+// tile t runs under P V(t-1) and Q K(t+1).
+//
+// What bounds it: a tile takes ~4,900 clk on the whole chain of 8,192 tokens.  A slot's round
+// (its MMAs, the news to the loader, ~900 clk from L2, the news to the issuer) is
+// ~1,850 clk, and seven slots of it are 60 bytes a clock of the 64 that the MMAs
+// would take; queries (72 KB), P (32 KB) and the rings fill the shared memory.
+// Around the tiles a call has ~2 us of deal and set-up, ~4 us until the first P V,
+// ~4 us at each change of chain, and 5 us of merge with its launch.  64 requests
+// of 128 heads on 8,192 + 1 to 777 tokens: 110 us (1.35 PFLOP/s), 58% of the
+// tensor cores' cycles.  From the same 64: one ring and one issuing thread 195 us;
+// two rings and two threads 163; P by halves 140; eight softmax warps for four
+// 110.  Waits that acquire at cluster scope instead of the block's cost a
+// microsecond each in such a chain (436 us).  Issuing threads as converged warps
+// 116 to 126 us, the K loader so 121, the V loader as one thread 113; each
+// tile's maximum found a tile ahead 123; a piece's O stored under the next
+// one's first scores 113; rows prefetched to L2 by the tensor copies 111 for 104.
+//
+// Pieces are f16 in units of a power of two for 64 dims of a row.  bf16 (as
+// mla_decode's) made the error of `out` 0.0024 of its size, this 0.0019, for 3% of
+// the time; fp32 took 4 to 10%.  P is bf16, as V is: one MMA has one type.
 //
 // Rows behind the last token of a chain.  Scores of their columns are masked, and
 // P V stops at the next multiple of 16 tokens; V rows up to there have to be
 // zeros (0 * NaN is NaN), which a tensor copy cannot write for rows that exist.
 // The last items of such a chain are copied by a warp's threads instead.
 //
-// Warp roles: 0 loads K and V, 1 issues the MMAs (first block of the pair), 2
-// loads Q, 3 owns the tensor memory, 4-7 run the softmax and write results
-// (thread = 64 rows x 2 halves of a tile's tokens, or of 256 dims).  Every wait is bounded; one that runs out reports
-// MLA_ERR_DEVICE_TIMEOUT and ends the block's other waits.
+// Warp roles: 0 loads Q and K, 1 issues Q K^T (first block of the pair; in the
+// other it passes on that P is written), 2 loads V, 3 issues P V and owns the
+// tensor memory, 4-11 run the softmax and write results (thread = a row and a
+// quarter of a tile's tokens, or of the 512 dims).  Every wait is bounded; one that
+// runs out reports MLA_ERR_DEVICE_TIMEOUT and ends the block's other waits.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -74,7 +94,9 @@ constexpr int kSlotsK = 4, kSlotsV = 3;
 constexpr int kThreads = 384;
 constexpr int kSoftmaxWarp0 = 4, kSoftmaxWarps = 8;
 constexpr uint32_t kColO = 0, kColS = 256, kCols = 512;
-constexpr int64_t kUnitCost = 2, kChainCost = 16;  // a chain's start: queries and first keys without MMAs under them
+// A chain's start (queries and first keys without MMAs under them, its end's O) costs as much as eight units:
+// 12 and 20 instead of 16 took 49.5 and 51.5 us for 49 (159 requests of 16 heads on 4,096 + 16 to 1,024 tokens).
+constexpr int64_t kUnitCost = 2, kChainCost = 16;
 constexpr int kMaxPairs = 256;
 constexpr uint64_t kWaitBudgetNs = 100000000ull;
 constexpr uint64_t kDrainBudgetNs = 10000000ull;

@@ -33,8 +33,8 @@
 // phase ahead.
 //
 // What bounds it: memory, by the bytes in flight.  20 x 4,096 tokens cut to 2,048: 94 MB
-// in 20.5 us (4.6 TB/s, 68% of the copy rate); eight E4M3 layers: 138 MB in 32 us.
-// From the same: eight units a thread 22.7 and 35.7 us, sixteen 26 and 44; three
+// in 18.8 us (5.0 TB/s, 74% of the copy rate); eight E4M3 layers: 138 MB in 27.5 us.
+// Before the blocks met without ordering memory, 20.5 and 32 us; from there: eight units a thread 22.7 and 35.7 us, sixteen 26 and 44; three
 // slices a row 25 and 36, whole rows 40; two blocks an SM asked for instead of
 // four 26 us, eight 20.9 by spilling.
 #include <algorithm>
@@ -306,8 +306,13 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveBlocks) compact_kernel(cons
     n = min(max(n, 0), min(L, p.budget));
   }
   const int32_t *keep = p.keep + (int64_t)b * p.budget;
-  auto meet = [&]() {
-    if (nb > 1) cluster_sync(); else __syncthreads();
+  // Every block of the cluster has this phase's values in registers.  That is all that has to be so before
+  // the stores: no block reads what another writes, and a load whose value is here cannot see a later store.
+  // So the blocks meet without ordering memory, which would wait for the last phase's stores to arrive.  The
+  // block's own barrier takes in a bit of every value (`seen`), so that no thread passes it with a load under way.
+  auto meet = [&](uint32_t seen) {
+    if (__syncthreads_or(seen == 0x9e3779b9u)) __threadfence_block();  // (the answer is used, or the question would go)
+    if (nb > 1) cluster_meet();
   };
   if (weights) {
     float *mass = p.mass + (int64_t)b * p.mass_stride;
@@ -322,7 +327,11 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveBlocks) compact_kernel(cons
         put[u] = t >= 0;
         if (put[u]) x[u] = __ldcg(mass + t);
       }
-      meet();
+      uint32_t seen = 0;
+#pragma unroll
+      for (int u = 0; u < kMoveUnits; ++u)
+        if (put[u]) seen ^= __float_as_uint(x[u]);
+      meet(seen);
 #pragma unroll
       for (int u = 0; u < kMoveUnits; ++u)
         if (put[u]) mass[j0 + u * kMoveThreads] = x[u];
@@ -354,7 +363,11 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveBlocks) compact_kernel(cons
       if (row.y >= 0) x[u] = __ldcg(reinterpret_cast<const uint4 *>(cache + row.x * kRowBytes));
     }
     look_up(base + (int64_t)nb * kRows, s_rows[turn ^ 1]);  // the next phase's, while these load
-    meet();
+    uint32_t seen = 0;
+#pragma unroll
+    for (int u = 0; u < kMoveUnits; ++u)
+      if (to[u] >= 0) seen ^= x[u].x;
+    meet(seen);
 #pragma unroll
     for (int u = 0; u < kMoveUnits; ++u)
       if (to[u] >= 0) *reinterpret_cast<uint4 *>(cache + to[u] * kRowBytes) = x[u];

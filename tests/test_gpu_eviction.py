@@ -460,6 +460,29 @@ def test_compact_shapes_of_what_stays(mla, kind):
     assert np.array_equal(bits(c["cache"]), want) and np.array_equal(f64(c["mass"]), weights)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("requests,n,layers", [(1, 30000, 1), (3, 9000, 2), (20, 4096, 1), (40, 700, 4)])
+def test_compact_again_and_again(mla, requests, n, layers, fp8):
+    """Targets that are other blocks' sources: fresh rows, moved a little each time, always the same bits."""
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    page, blocks = 64, requests * -(-n // 64)
+    table = torch.randperm(blocks, generator=gen, device="cuda").to(torch.int32).view(requests, -1)
+    cache = torch.randint(0, 256, (layers, blocks, page, 576 if fp8 else 1152), generator=gen, device="cuda", dtype=torch.uint8)
+    cache = cache if fp8 else cache.view(torch.bfloat16)
+    slots = (table.long()[..., None] * page + torch.arange(page, device="cuda")).flatten(1)
+    for gone in (1, 7, n // 2, n // 3, 1, 2, 3, 40, 50, 60):
+        keep = torch.stack([torch.randperm(n, generator=gen, device="cuda")[gone:].sort()[0] for _ in range(requests)])
+        want = cache.clone()
+        rows = want.view(layers, blocks * page, -1).view(torch.uint8)
+        rows[:, slots[:, :n - gone].flatten()] = rows[:, slots.gather(1, keep).flatten()]
+        c = dict(cache=cache.clone(), block_table=table, keep_t=keep.to(torch.int32), seq_lens=i32([n] * requests),
+                 new_lens=i32([n - gone] * requests), mass=torch.rand(requests, n, generator=gen, device="cuda"), fp8=fp8, status=word())
+        weights = torch.cat([c["mass"].gather(1, keep), torch.zeros(requests, gone, device="cuda")], 1)
+        run_compact(mla, c)
+        assert torch.equal(c["mass"], weights)
+        assert int(c["status"]) == 0 and torch.equal(c["cache"].view(torch.uint8), want.view(torch.uint8))
+
+
 def test_compact_reports_what_lies_outside(mla):
     c = compact_case(np.random.default_rng(44), [300, 200], 16, 100, 1, False)
     start = c["cache"].clone()

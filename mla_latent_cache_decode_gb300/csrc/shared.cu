@@ -853,10 +853,10 @@ constexpr int kMergeThreads = 256, kMergeFlight = 4;
 
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p) {
   const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
+  const uint32_t row = blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);  // (below 2^27)
+  const uint32_t b = row / (uint32_t)p.heads, h = row - b * p.heads, in_a = row % kRows;
   griddep_wait();
-  if (row >= (int64_t)p.batch * p.heads) return;
-  const int32_t b = (int32_t)(row / p.heads), h = (int32_t)(row % p.heads);
+  if (b >= (uint32_t)p.batch) return;
   // all at once: what is not there is not looked at
   const int32_t shared_blocks = *p.shared_blocks, length = p.seq_lens[b];
   const Pieces all_own = p.pieces_b[b], all_com = p.pieces_a[row / kRows], none = {0, -1};
@@ -866,8 +866,12 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p) {
   const Pieces com = ch.packed > 0 && L >= ch.shared ? all_com : none;
   const int na = com.last - com.first + 1, nb = own.last - own.first + 1;
   if (ch.from(L) == 0 && nb == 1) return;  // written at once
-  const int64_t a0 = (row / kRows + com.first) * kRows + row % kRows;
-  const int64_t b0 = ((int64_t)b + own.first) * p.heads + h;
+  // the first piece of either kind: its rows, its units (of this lane's 8 dims of each half) and its lse
+  const int64_t slot_a = (int64_t)(row / kRows) + com.first, slot_b = (int64_t)b + own.first;
+  const uint4 *oa = reinterpret_cast<const uint4 *>(p.o_a + (slot_a * kRows + in_a) * kVDim) + lane;
+  const uint4 *ob = reinterpret_cast<const uint4 *>(p.o_b + (slot_b * p.heads + h) * kVDim) + lane;
+  const float *ua = p.unit_a + (slot_a * 8 + (lane >> 3)) * kRows + in_a, *ub = p.unit_b + (slot_b * 8 + (lane >> 3)) * p.heads + h;
+  const float *la = p.lse_a + slot_a * kRows + in_a, *lb = p.lse_b + slot_b * p.heads + h;
   float m = -INFINITY, z = 0.f, acc[16];
 #pragma unroll
   for (int k = 0; k < 16; ++k) acc[k] = 0.f;
@@ -876,17 +880,21 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p) {
     uint4 x[kMergeFlight][2];
 #pragma unroll
     for (int u = 0; u < kMergeFlight; ++u) {
-      const int i = min(i0 + u, na + nb - 1);
-      const bool in_a = i < na;
-      const int rows = in_a ? kRows : p.heads, r = in_a ? (int)(row % kRows) : h;
-      const int64_t at = in_a ? a0 + (int64_t)i * kRows : b0 + (int64_t)(i - na) * p.heads;
-      l[u] = i0 + u < na + nb ? (in_a ? p.lse_a : p.lse_b)[at] : -INFINITY;
-      const float *units = (in_a ? p.unit_a : p.unit_b) + (at - r) * 8 + (lane >> 3) * rows + r;
-      unit[u][0] = units[0];
-      unit[u][1] = units[4 * rows];
-      const uint4 *src = reinterpret_cast<const uint4 *>((in_a ? p.o_a : p.o_b) + at * kVDim);
-      x[u][0] = src[lane];
-      x[u][1] = src[32 + lane];
+      const int i = i0 + u, j = i - na;
+      l[u] = -INFINITY;
+      unit[u][0] = unit[u][1] = 0.f;
+      x[u][0] = x[u][1] = make_uint4(0, 0, 0, 0);
+      if (j < nb) {
+        const bool a = j < 0;
+        const int step = a ? i : j, rows = a ? kRows : p.heads;
+        const uint4 *o = (a ? oa : ob) + (int64_t)step * rows * (kVDim / 8);
+        const float *units = (a ? ua : ub) + (int64_t)step * rows * 8;
+        l[u] = (a ? la : lb)[(int64_t)step * rows];
+        unit[u][0] = units[0];
+        unit[u][1] = units[4 * rows];
+        x[u][0] = o[0];
+        x[u][1] = o[32];
+      }
     }
     float top = m;
 #pragma unroll
@@ -920,7 +928,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p) {
     __nv_bfloat162 two = __floats2bfloat162_rn(acc[2 * k] * inv, acc[2 * k + 1] * inv);
     ow[k] = *reinterpret_cast<uint32_t *>(&two);
   }
-  uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * kVDim);
+  uint4 *dst = reinterpret_cast<uint4 *>(p.out + (int64_t)row * kVDim);
   dst[lane] = o[0];
   dst[32 + lane] = o[1];
   if (lane == 0 && p.lse) p.lse[row] = z == 0.f ? -INFINITY : m + logf(z);

@@ -660,7 +660,11 @@ def mla_decode_shared(q, cache, shared_table, shared_blocks, block_table, seq_le
     N = _shape(shared_table, 1, "shared_table")[0]
     M = _shape(block_table, 2, "block_table")[1]
     if workspace is None:
-        workspace = make_shared_workspace(B, H)
+        # of the stream that the call uses: it may be handed out again as soon as this returns
+        own = (None if stream is None else torch.cuda.ExternalStream(stream) if isinstance(stream, int) and stream
+               else torch.cuda.default_stream() if isinstance(stream, int) else stream)
+        with torch.cuda.stream(own):
+            workspace = make_shared_workspace(B, H)
     nbytes = _shape(workspace, 1, "workspace")[0]
     _check(get_lib().mla_decode_shared(
         _dense(q, bf16, (B, H, ROW_DIM), dev, "q"), _dense(cache, bf16, (NB, BS, ROW_DIM), dev, "cache"),

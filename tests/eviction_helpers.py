@@ -122,7 +122,7 @@ def run_shared(mla, c, **kw):
 def mass_case(rng, heads, page, lens, fp8=False, width=None, by=1.0):
     import torch
     table, _, blocks = paged(rng, lens, page)
-    B, S = len(lens), width or max(lens)
+    B, S = len(lens), width or max(max(lens), 1)
     c = dict(lens=lens, table=table, q=bf16(rng, B, heads, 576, by=by), cache=bf16(rng, blocks, page, 576), block_table=i32(table), fp8=fp8,
              seq_lens=i32(lens), kv_scale=0.037 if fp8 else 1.0, status=word(), mass=torch.full((B, S), 3.0, device="cuda"),
              previous=torch.from_numpy(rng.random((B, S)).astype(np.float32)).cuda())

@@ -72,7 +72,7 @@ def test_shared_non_finite_rows_stay_with_those_that_see_them(mla, heads):
     assert (out[4] == 0).all()
 
 
-@pytest.mark.parametrize("heads,batch", [(16, 40), (2, 200), (128, 30)])
+@pytest.mark.parametrize("heads,batch", [(16, 40), (2, 200), (128, 30), (100, 12), (33, 21)])
 def test_shared_many_requests(mla, heads, batch):
     rng = np.random.default_rng(batch)
     lens = [int(512 + n) for n in rng.integers(1, 300, batch)]
@@ -191,6 +191,21 @@ def test_shared_two_at_once(mla):
         check_shared(c)
 
 
+def test_shared_on_another_stream_without_workspace(mla):
+    """Its workspace is that stream's, whatever the current one allocates next."""
+    c = shared_case(np.random.default_rng(17), 16, 64, 6, [384 + 100 * i + 5 for i in range(8)])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        c["out"].zero_()
+        torch.cuda.synchronize()
+        for _ in range(20):
+            run_shared(mla, c, stream=stream)
+            torch.full((mla.mla_decode_shared_workspace_size(8, 16),), 255, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        check_shared(c)
+
+
 @pytest.mark.parametrize("heads", [16, 128])
 def test_shared_reports_what_lies_outside(mla, heads):
     c = shared_case(np.random.default_rng(16), heads, 64, 5, [320 + 100, 320 + 90, 500])
@@ -211,7 +226,7 @@ def test_shared_reports_what_lies_outside(mla, heads):
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("heads,page,lens", [
     (128, 64, [201]), (128, 16, [2, 18, 65, 201]), (16, 64, [1, 127, 128, 129, 700]), (1, 16, [5, 33]), (5, 32, [64, 63, 300, 1]),
-    (40, 256, [1000, 256]), (128, 128, [129, 511, 1024]), (100, 64, [77]), (32, 64, [0, 100, 0, 3]), (17, 16, [640] * 9)])
+    (40, 256, [1000, 256]), (128, 128, [129, 511, 1024]), (100, 64, [77]), (128, 64, [0, 0]), (32, 64, [0, 100, 0, 3]), (17, 16, [640] * 9)])
 def test_mass_against_definition(mla, heads, page, lens, fp8):
     c = mass_case(np.random.default_rng(heads + page), heads, page, lens, fp8)
     run_mass(mla, c)

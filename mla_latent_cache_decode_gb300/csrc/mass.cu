@@ -484,7 +484,8 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
       const float *lse = &s.lse[turn][at], *lse_rest = &s.lse_rest[turn][at], *factor = &s.factor[turn][at], *factor_rest = &s.factor_rest[turn][at];
       auto weight = [&](float x, int h) {
         const float c = kFp8 ? factor[h] : p.scale_log2, rest = kFp8 ? factor_rest[h] : p.scale_rest;
-        return ex2_approx(fmaf(x, c, -lse[h]) + fmaf(x, rest, -lse_rest[h]));
+        // (the bound: a score of -inf times the rest, which may be 0 or negative, must not undo the -inf)
+        return ex2_approx(fmaf(x, c, -lse[h]) + fminf(fmaf(x, rest, -lse_rest[h]), 1e30f));
       };
       for (int32_t tt = walk.t0; tt < walk.t1; tt += kTile, ++g) {
         const int32_t t = tt + (int)rank * kOwn + r;

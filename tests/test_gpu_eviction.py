@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 import oracle.eviction as oe
-from eviction_helpers import (SCALE, bf16, check_mass, check_shared, i32, mass_case, paged, run_mass, run_shared, shared_case, word)
+from eviction_helpers import (SCALE, bf16, check_mass, check_shared, i32, mass_case, mass_rows, paged, run_mass, run_shared, shared_case, word)
 from prompt_helpers import f64
 
 pytestmark = pytest.mark.gpu
@@ -271,6 +271,25 @@ def test_mass_rows_and_queries_that_are_not_finite(mla, fp8):
     got = f64(c["mass"])
     assert np.isnan(got[0, 71]) and np.array_equal(np.delete(got[0], 71), np.delete(clean[0], 71)) and np.array_equal(got[1], clean[1])
     assert not np.isfinite(got[2, :90]).any() or not fp8
+
+
+@pytest.mark.parametrize("scale", [SCALE, 0.1, 0.125, 1.0])  # scale * log2(e) rounds up in some, down in others
+@pytest.mark.parametrize("low", [-float("inf"), torch.finfo(torch.bfloat16).min])
+def test_mass_rows_of_nothing(mla, low, scale):
+    """A row that every head scores -inf, or lowest, has weight 0; what was there before stays."""
+    c = mass_case(np.random.default_rng(30), 40, 32, [200, 100], False)
+    c["q"][:, :, 3] = c["q"][:, :, 3].abs() + 1
+    for b in range(2):
+        c["lse"][b] = torch.from_numpy(oe.decode(f64(c["q"])[b], mass_rows(c, b), scale)[1]).float().cuda()
+
+    def weigh(**kw):
+        mla.mla_attention_mass(c["q"], c["cache"], c["block_table"], c["seq_lens"], scale, c["lse"], c["mass"], **kw)
+        return f64(c["mass"])
+    clean = weigh()
+    c["cache"][int(c["table"][0][2]), 7, 3] = low  # token 71
+    got = weigh()
+    assert got[0, 71] == 0 and np.array_equal(np.delete(got[0], 71), np.delete(clean[0], 71)) and np.array_equal(got[1], clean[1])
+    assert weigh(previous=c["previous"], decay=0.5)[0, 71] == 0.5 * f64(c["previous"])[0, 71]
 
 
 @pytest.mark.parametrize("fp8", [False, True])

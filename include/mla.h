@@ -552,7 +552,7 @@ mla_status_t mla_decode_shared(const void *q, const void *cache, int64_t num_blo
  *                  is added.  May be mass itself (same stride)
  *   decay          >= 0 and finite (1: a plain sum); not looked at without previous
  *   mass           fp32, row b at mass + b * mass_stride, max_tokens wide; entries
- *                  behind seq_lens[b] are left as they are
+ *                  behind seq_lens[b] are left as they are.  max_tokens = 0: nothing is done
  * A length outside [0, min(max_tokens, max_blocks_per_seq * block_size)] is clamped
  * and reported as MLA_ERR_DEVICE_RANGE; the weights of a page outside the pool
  * are unspecified, and it is reported.  Strides in elements, >= max_tokens.

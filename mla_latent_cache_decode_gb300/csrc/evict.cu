@@ -34,9 +34,10 @@
 //
 // What bounds it: memory, by the bytes in flight.  20 x 4,096 tokens cut to 2,048: 94 MB
 // in 18.8 us (5.0 TB/s, 74% of the copy rate); eight E4M3 layers: 138 MB in 27.5 us.
-// Before the blocks met without ordering memory, 20.5 and 32 us; from there: eight units a thread 22.7 and 35.7 us, sixteen 26 and 44; three
-// slices a row 25 and 36, whole rows 40; two blocks an SM asked for instead of
-// four 26 us, eight 20.9 by spilling.
+// Before the blocks met without ordering memory: 20.5 and 32 us.  From there: eight
+// units a thread 22.7 and 35.7 us, sixteen 26 and 44; three slices a row 25 and 36,
+// whole rows 40; two blocks an SM asked for instead of four 26 us, eight 20.9 by
+// spilling.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -439,7 +440,8 @@ mla_status_t run_compact(CompactParams p, int64_t num_blocks, int row_bytes, int
   if (p.block_size <= 0 || num_blocks <= 0 || num_blocks > INT32_MAX || num_blocks * p.block_size > INT32_MAX ||
       p.max_blocks_per_seq <= 0)
     return invalid("block_size, num_blocks and max_blocks_per_seq must be > 0, num_blocks * block_size below 2^31");
-  if ((int64_t)p.max_blocks_per_seq * p.block_size > INT32_MAX / 2) return invalid("max_blocks_per_seq * block_size > 2^30");
+  if ((int64_t)p.max_blocks_per_seq * p.block_size > 1 << 30) return invalid("max_blocks_per_seq * block_size > 2^30");
+  if ((int64_t)p.batch * layers > INT32_MAX) return invalid("batch * num_layers too large");
   if (p.batch == 0) return MLA_OK;
   if (!p.block_table || !p.seq_lens || !p.new_lens || (p.budget > 0 && !p.keep) || (layers > 0 && !p.cache)) return invalid("null pointer");
   if (!aligned(p.cache, 16)) return invalid("cache must be 16-byte aligned");

@@ -640,7 +640,7 @@ mla_status_t run(const Args &a, void *stream) {
   if (!std::isfinite(a.kv_scale) || !(a.kv_scale > 0.f) || !std::isfinite(a.scale * a.kv_scale) || !(a.scale * a.kv_scale > 0.f))
     return invalid("kv_scale, and its product with softmax_scale, must be positive and finite");
   if (!std::isfinite(a.decay) || !(a.decay >= 0.f)) return invalid("decay must be finite and not negative");
-  if (a.num_blocks <= 0 || a.num_blocks * a.block_size > INT32_MAX || a.max_blocks_per_seq <= 0 ||
+  if (a.num_blocks <= 0 || a.num_blocks > INT32_MAX || a.num_blocks * a.block_size > INT32_MAX || a.max_blocks_per_seq <= 0 ||
       (int64_t)a.max_blocks_per_seq * a.block_size > 1 << 30)
     return invalid("num_blocks or max_blocks_per_seq out of range");
   if ((int64_t)a.batch * kHeads > INT32_MAX) return invalid("batch too large");

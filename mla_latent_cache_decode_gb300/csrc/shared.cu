@@ -1032,7 +1032,7 @@ mla_status_t mla_decode_shared(const void *q, const void *cache, int64_t num_blo
     return MLA_ERR_UNSUPPORTED;
   }
   if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.f)) return invalid("softmax_scale must be positive and finite");
-  if (num_blocks <= 0 || num_blocks * block_size > INT32_MAX || max_blocks_per_seq <= 0 ||
+  if (num_blocks <= 0 || num_blocks > INT32_MAX || num_blocks * block_size > INT32_MAX || max_blocks_per_seq <= 0 ||
       (int64_t)max_blocks_per_seq * block_size > 1 << 30 || (int64_t)max_shared_blocks * block_size > 1 << 30)
     return invalid("num_blocks, max_blocks_per_seq or max_shared_blocks out of range");
   if (batch > 1 << 20) return invalid("batch > 2^20");

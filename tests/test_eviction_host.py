@@ -148,3 +148,18 @@ def test_weights_add_up_and_decode_splits():
     w = oe.mass(q[:1], rows, 0.07, one[1])
     assert abs(w.sum() - 1) < 1e-12 and np.allclose(w @ rows[:, :512], one[0][0], atol=1e-12)
     assert np.allclose(oe.mass(q, rows, 0.07, lse), sum(oe.mass(q[h:h + 1], rows, 0.07, lse[h:h + 1]) for h in range(3)))
+
+
+# ------------------------------------------------------------------------- sizes whose products wrap
+
+@pytest.mark.parametrize("call", [shared, mass, lambda lib, **kw: mass(lib, True, **kw), compact, lambda lib, **kw: compact(lib, True, **kw)])
+def test_pools_beyond_64_bits_are_refused(lib, call):
+    assert call(lib, block_size=64, num_blocks=(1 << 58) + 1) == 1  # 64 rows more than 2^64
+    assert lib.mla_last_error_detail() != b""
+
+
+def test_moves_beyond_64_bits_are_refused(lib):
+    assert compact(lib, batch=1 << 30, layers=(1 << 31) - 1) == 1
+    assert b"num_layers" in lib.mla_last_error_detail()
+    assert compact(lib, width=(1 << 26) + 1) == 1
+    assert compact(lib, width=1 << 26, layers=0, mass=None) == 0  # 2^30 tokens

@@ -572,7 +572,8 @@ mla_status_t mla_decode_shared(const void *q, const void *cache, int64_t num_blo
  *   sink, recent   >= 0, sink + recent <= max_keep
  *   keep       int32 [batch, max_keep], written: the positions that stay,
  *              ascending, then -1
- *   new_lens   int32 [batch], written: how many, min(L, max_keep)
+ *   new_lens   int32 [batch], written: how many, min(L, max_keep); an array of its own:
+ *              keep and new_lens over any part of seq_lens are refused
  * A length outside [0, max_tokens] is clamped and reported.
  * 1 <= max_keep; max_tokens <= 2^30.
  *

@@ -722,7 +722,8 @@ def mla_evict_select(mass, seq_lens, keep, new_lens, sink=0, recent=0, dev_statu
                      stream=None):
     """The tokens that stay when every request may keep K: keep int32 [B, K] gets their positions,
     ascending (then -1), new_lens int32 [B] how many.  Of a longer request the first `sink`, the
-    last `recent`, and of the others those of the largest mass (fp32 [B, S])."""
+    last `recent`, and of the others those of the largest mass (fp32 [B, S]).  keep and new_lens lie
+    over no part of seq_lens."""
     import torch
     i32 = torch.int32
     B, S = _shape(mass, 2, "mass")

@@ -384,6 +384,10 @@ mla_status_t invalid(const char *why) {
 
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
+bool overlap(const int32_t *a, int64_t na, const int32_t *b, int64_t nb) {
+  return (uintptr_t)a < (uintptr_t)(b + nb) && (uintptr_t)b < (uintptr_t)(a + na);
+}
+
 mla_status_t status_of(cudaError_t e) {
   if (e == cudaSuccess) return MLA_OK;
   set_error_detail(cudaGetErrorString(e));
@@ -505,6 +509,10 @@ mla_status_t mla_evict_select(const float *mass, int64_t mass_stride, int32_t ma
   if ((max_tokens > 0 && !mass) || !seq_lens || !keep || !new_lens) return evict::invalid("null pointer");
   if (!evict::aligned(mass, 4) || !evict::aligned(seq_lens, 4) || !evict::aligned(keep, 4) || !evict::aligned(new_lens, 4))
     return evict::invalid("mass, seq_lens, keep and new_lens must be 4-byte aligned");
+  // (blocks of a request read its length each for itself: written over, some would go through the passes
+  // without the others)
+  if (evict::overlap(seq_lens, batch, new_lens, batch) || evict::overlap(seq_lens, batch, keep, (int64_t)batch * max_keep))
+    return evict::invalid("keep and new_lens must not overlap seq_lens");
   if (batch > 1 && mass_stride < max_tokens) return evict::invalid("mass_stride is below max_tokens");
   cudaError_t e;
   const int sms = evict::device_sms(&e);

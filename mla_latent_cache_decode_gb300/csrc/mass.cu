@@ -286,10 +286,9 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
     if (elect_one_sync()) {
       constexpr int kBoxes = kOwn / kBox;
       const uint32_t full0 = cluster_addr(smem_u32(&s.full[0]), 0);
-      uint32_t sl = 0, turn = 1, items = 0, piece = 0;
+      uint32_t sl = 0, turn = 1, items = 0;
       bool ok = true;
       while (ok && walk.next()) {
-        ++piece;
         const int32_t *table = p.block_table + (int64_t)walk.b * p.max_blocks_per_seq;
         int32_t blk[kBoxes];  // read a tile ahead
         // This block's tokens (both blocks load at least a box of every item, so that neither falls behind
@@ -336,11 +335,6 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
           }
         }
       }
-      if (ok && !first_block) {  // what the MMAs say to this block arrives before it leaves
-        for (uint32_t i = items > (uint32_t)p.slots ? items - p.slots : 0; ok && i < items; ++i)
-          ok = wait(&s.empty[i % p.slots], (i / p.slots) & 1u);
-        if (ok && piece > 0) (void)wait(&s.q_free, (piece - 1) & 1u);
-      }
       if (s.abort && first_block)  // let the loads in flight land in both blocks
         for (uint32_t i = items > (uint32_t)p.slots ? items - p.slots : 0; i < items; ++i)
           (void)mbar_wait(smem_u32(&s.full[i % p.slots]), (i / p.slots) & 1u, nullptr, kDrainBudgetNs);
@@ -386,7 +380,8 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
       }
       mma_commit_pair(smem_u32(&s.mma_end));
     }
-    // both blocks stay until the last MMA has said so to both
+    // Both blocks stay until the end of all MMAs has been said to both: that is the last arrival of the MMAs at
+    // a block's barriers, and the meeting at the end does not wait for them.
     if (one && !mbar_wait(smem_u32(&s.mma_end), 0, nullptr, kWaitBudgetNs)) report(p.dev_status, MLA_ERR_DEVICE_TIMEOUT);
   } else if (warp == 2) {
     // ---------------------------------------------------------------- queries, bf16

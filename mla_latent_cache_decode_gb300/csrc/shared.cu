@@ -476,10 +476,6 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
         walk = ahead;
         have = more;
       }
-      if (ok && !first_block) {  // what the MMAs say to this block arrives before it leaves
-        for (uint32_t i = items > kSlotsK ? items - kSlotsK : 0; ok && i < items; ++i) ok = wait(&s.k_empty[i % kSlotsK], (i / kSlotsK) & 1u);
-        for (uint32_t i = piece > 2 ? piece - 2 : 0; ok && i < piece; ++i) ok = wait(&s.q_free[i & 1u], (i >> 1) & 1u);
-      }
       if (s.abort && first_block) {  // let the loads in flight land in both blocks
         for (uint32_t i = items > kSlotsK ? items - kSlotsK : 0; i < items; ++i)
           (void)mbar_wait(smem_u32(&s.k_full[i % kSlotsK]), (i / kSlotsK) & 1u, nullptr, kDrainBudgetNs);
@@ -563,9 +559,6 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
         }
       }
     }
-    if (ok && !first_block)
-      for (uint32_t i = items > kSlotsV ? items - kSlotsV : 0; ok && i < items; ++i)
-        ok = warp_wait(s, &s.v_empty[i % kSlotsV], (i / kSlotsV) & 1u, p.dev_status);
     if (s.abort && first_block && lane == 0)
       for (uint32_t i = items > kSlotsV ? items - kSlotsV : 0; i < items; ++i)
         (void)mbar_wait(smem_u32(&s.v_full[i % kSlotsV]), (i / kSlotsV) & 1u, nullptr, kDrainBudgetNs);
@@ -608,7 +601,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
             for (int h = 0; ok && h < 2; ++h)
               if ((ok = wait(&s.p_here[h], g & 1u))) mbar_arrive_release_cluster(bar + 8 * h);
       }
-      // both blocks stay until the last MMA has said so to both
+      // Both blocks stay until the end of all MMAs has been said to both: that is the last arrival of the MMAs at
+      // a block's barriers, and the meeting at the end does not wait for them.
       if (!mbar_wait(smem_u32(&s.mma_end), 0, nullptr, kWaitBudgetNs)) report(p.dev_status, MLA_ERR_DEVICE_TIMEOUT);
     }
   } else if (warp == 3) {
@@ -842,10 +836,6 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(o_bar);
-    }
-    if (ok && !first_block && g > 0) {  // (the others of these barriers' phases have been waited for)
-      ok = warp_wait(s, &s.p_free[half], (g - 1) & 1u, p.dev_status);
-      if (ok && g > 1) (void)warp_wait(s, &s.pv_done[g & 1u], ((g - 2) >> 1) & 1u, p.dev_status);
     }
   }
 

@@ -547,7 +547,8 @@ mla_status_t mla_decode_shared(const void *q, const void *cache, int64_t num_blo
  * weight below 2^-126 counts as 0).
  *   q, cache, num_blocks, block_size, block_table, max_blocks_per_seq, seq_lens
  *                  as in mla_decode; 1 <= num_heads <= 128
- *   lse            fp32 [batch, num_heads]; a head with -inf gives nothing
+ *   lse            fp32 [batch, num_heads]; a head with -inf gives nothing, whatever its
+ *                  query or a row holds
  *   previous       fp32, row b at previous + b * previous_stride, or NULL: nothing
  *                  is added.  May be mass itself (same stride)
  *   decay          >= 0 and finite (1: a plain sum); not looked at without previous

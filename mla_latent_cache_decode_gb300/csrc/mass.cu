@@ -410,12 +410,12 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
     bool ok = true;
     while (ok && walk.next()) {
       const uint32_t turn = piece & 1u;
-      // every head's lse and scale, for 2^x; nothing from a head with -inf
+      // every head's lse and scale, for 2^x; a rest of +inf, which no lse has, marks a head with -inf
       for (int h = thread; h < p.heads; h += 32 * kWeighWarps) {
         const float l = p.lse[(int64_t)walk.b * p.heads + h];
         const float x = l * kLog2e;
-        s.lse[turn][h] = l == -INFINITY ? INFINITY : x;
-        s.lse_rest[turn][h] = fabsf(x) < INFINITY ? fmaf(l, kLog2e, -x) + l * kLog2eRest : 0.f;
+        s.lse[turn][h] = x;
+        s.lse_rest[turn][h] = l == -INFINITY ? INFINITY : fabsf(x) < INFINITY ? fmaf(l, kLog2e, -x) + l * kLog2eRest : 0.f;
       }
       if (kFp8) {
         // the queries as sums of two E4M3 numbers: both blocks find every head's scale, each splits its own
@@ -490,6 +490,10 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
         // (the bound: a score of -inf times the rest, which may be 0 or negative, must not undo the -inf)
         return ex2_approx(fmaf(x, c, -lse[h]) + fminf(fmaf(x, rest, -lse_rest[h]), 1e30f));
       };
+      // This warp's heads (32 at most) that count, a bit each: those there are, without those of lse -inf, whose
+      // weights, NaN for a score of NaN or +inf, are not added.  (A comparison a weight in place of the bit took
+      // 22.3 us for 21.3, 20 x 4,096 tokens of 128 heads, and 17 registers more.)
+      const uint32_t live = __ballot_sync(0xffffffffu, i_from + lane < i_to && lse_rest[i_from + lane] < INFINITY);
       for (int32_t tt = walk.t0; tt < walk.t1; tt += kTile, ++g) {
         const int32_t t = tt + (int)rank * kOwn + r;
         const bool mine = half == 0 && part == 0 && t < walk.t1;
@@ -500,6 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
         float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll 1
         for (int i = i_from; i < i_to; i += 16) {
+          const uint32_t counts = live >> (i - i_from);
           // what adds up to a score: hi and lo, or the thirds of the dims
           constexpr int kTerms = kFp8 ? 2 : Z::kSums;
           uint32_t x[kTerms][16];
@@ -515,8 +520,8 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
             for (int j = 1; j < kTerms; ++j) a += __uint_as_float(x[j][k]), b += __uint_as_float(x[j][k + 1]);
             a = weight(a, i + k);
             b = weight(b, i + k + 1);
-            if (i + k < i_to) sum0 += a;
-            if (i + k + 1 < i_to) sum1 += b;
+            if (counts & 1u << k) sum0 += a;
+            if (counts & 2u << k) sum1 += b;
           }
         }
         s.sum[g & 1u][r][2 * half + part] = sum0 + sum1;

@@ -4,7 +4,9 @@ eviction_helpers; a head with a log-sum-exp of -inf has no part in them.)"""
 import numpy as np
 import pytest
 
-from eviction_helpers import check_mass, check_shared, mass_case, run_mass, run_shared, shared_case
+import oracle.eviction as oe
+from eviction_helpers import SCALE, check_mass, check_shared, mass_case, mass_rows, mass_tol, run_mass, run_shared, shared_case
+from prompt_helpers import assert_within, f64
 
 pytestmark = pytest.mark.gpu
 
@@ -16,6 +18,22 @@ def mla():
     import mla_latent_cache_decode_gb300 as mla
     torch.cuda.set_device(0)
     return mla
+
+
+def weigh(mla, c, scale=SCALE, **kw):
+    """The weights at this scale (a cache of E4M3 has its own)."""
+    if c["fp8"]:
+        mla.mla_attention_mass_fp8(c["q"], c["cache"], c["block_table"], c["seq_lens"], scale, c["lse"], c["mass"], kv_scale=c["kv_scale"], **kw)
+    else:
+        mla.mla_attention_mass(c["q"], c["cache"], c["block_table"], c["seq_lens"], scale, c["lse"], c["mass"], **kw)
+    return f64(c["mass"])
+
+
+def weights_of(c, b, heads):
+    """Request b's weights from these heads alone, and their tolerance."""
+    q, rows, lse = f64(c["q"])[b][heads], mass_rows(c, b), f64(c["lse"])[b][heads]
+    given = oe.mass(q, rows, SCALE, lse)
+    return given, mass_tol(q, rows, SCALE, lse, given, 0.0 * given, c["fp8"]) if len(q) else 0.0 * given
 
 
 @pytest.mark.parametrize("heads", [16, 128])
@@ -36,3 +54,30 @@ def test_shared_and_mass_with_nothing_to_do_for_most(mla, heads):
         assert all(torch.equal(a, b) for a, b in zip(first, (c["out"], c["lse"], d["mass"])))
         check_shared(c)
         check_mass(d, 0.0, None)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("what", ["nan", "inf", "one nan", "one inf", "one -inf"])
+def test_mass_heads_of_no_weight_hold_anything(mla, what, fp8):
+    """A head whose lse is -inf gives nothing, whatever its query: a padding head's may never have been
+    set.  Of a request that has only such heads not even a row of NaN counts."""
+    c = mass_case(np.random.default_rng(61), 20, 32, [100, 64, 70], fp8)
+    live = np.ones((3, 20), bool)
+    live[0, 3] = live[1, ::2] = live[2] = False
+    dead = torch.from_numpy(~live).cuda()
+    c["lse"][dead] = -float("inf")
+    queries = c["q"][dead]
+    queries[:, 100 if what.startswith("one") else slice(None)] = float(what.split()[-1])
+    c["q"][dead] = queries
+    if fp8:
+        c["cache"][int(c["table"][2][1]), 5] = 0x7F  # token 37 of request 2
+    else:
+        c["cache"][int(c["table"][2][1]), 5] = float("nan")
+    got = weigh(mla, c, dev_status=c["status"])
+    assert int(c["status"]) == 0
+    for b in range(2):
+        want, tol = weights_of(c, b, np.flatnonzero(live[b]))
+        assert_within(got[b, :c["lens"][b]], want, tol, f"request {b}")
+    assert (got[2, :70] == 0).all()
+    before = f64(c["previous"])
+    assert np.array_equal(weigh(mla, c, previous=c["previous"], decay=0.5)[2, :70], 0.5 * before[2, :70])

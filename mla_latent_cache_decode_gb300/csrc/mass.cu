@@ -107,7 +107,7 @@ struct Params {
   int32_t head_stride;  // heads of the first block
   int32_t half_heads;   // columns for a block's heads, a multiple of 16
   int32_t slots;
-  float scale_log2, scale_rest, decay;  // scale * log2(e) is the sum of the two
+  float scale_log2, scale_rest, decay;  // scale * log2(e) is the sum of the first two, the second >= 0
 };
 
 template <bool kFp8>
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
       const float *lse = &s.lse[turn][at], *lse_rest = &s.lse_rest[turn][at], *factor = &s.factor[turn][at], *factor_rest = &s.factor_rest[turn][at];
       auto weight = [&](float x, int h) {
         const float c = kFp8 ? factor[h] : p.scale_log2, rest = kFp8 ? factor_rest[h] : p.scale_rest;
-        // (the bound: a score of -inf times the rest, which may be 0 or negative, must not undo the -inf)
+        // (An infinite score stays what it is: the rest is not negative, and where it is 0 the bound takes the NaN.)
         return ex2_approx(fmaf(x, c, -lse[h]) + fminf(fmaf(x, rest, -lse_rest[h]), 1e30f));
       };
       // This warp's heads (32 at most) that count, a bit each: those there are, without those of lse -inf, whose
@@ -684,6 +684,7 @@ mla_status_t run(const Args &a, void *stream) {
   p.half_heads = (p.head_stride + 15) / 16 * 16;
   const double scale = (double)a.scale * a.kv_scale * kLog2eExact;
   p.scale_log2 = (float)scale;
+  if ((double)p.scale_log2 > scale) p.scale_log2 = std::nextafterf(p.scale_log2, 0.f);
   p.scale_rest = (float)(scale - (double)p.scale_log2);
   p.decay = a.decay;
   Maps maps;

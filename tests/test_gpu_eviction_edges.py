@@ -81,3 +81,47 @@ def test_mass_heads_of_no_weight_hold_anything(mla, what, fp8):
     assert (got[2, :70] == 0).all()
     before = f64(c["previous"])
     assert np.array_equal(weigh(mla, c, previous=c["previous"], decay=0.5)[2, :70], 0.5 * before[2, :70])
+
+
+@pytest.mark.parametrize("scale", [SCALE, 0.1, 0.1352, 0.125, 1.0])  # scale * log2(e) rounds up in some, down in others
+@pytest.mark.parametrize("row", [float("inf"), -float("inf")])
+def test_mass_rows_that_score_plus_infinity(mla, row, scale):
+    """One head of forty scores a token +inf, the others -inf: its weight is +inf by the definition, at
+    any scale; the other tokens' are what they were."""
+    c = mass_case(np.random.default_rng(62), 40, 32, [200, 100], False)
+    sign = torch.full((40,), -1.0, device="cuda")
+    sign[27] = 1.0
+    c["q"][:, :, 3] = (c["q"][:, :, 3].abs() + 1) * (sign * np.sign(row)).to(torch.bfloat16)
+    for b in range(2):
+        c["lse"][b] = torch.from_numpy(oe.decode(f64(c["q"])[b], mass_rows(c, b), scale)[1]).float().cuda()
+    clean = weigh(mla, c, scale)
+    c["cache"][int(c["table"][0][2]), 7, 3] = row  # token 71
+    got = weigh(mla, c, scale)
+    assert got[0, 71] == np.inf
+    assert np.array_equal(np.delete(got[0], 71), np.delete(clean[0], 71)) and np.array_equal(got[1], clean[1])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("dim", [3, 100, 200, 575])  # of each of the parts that a score is summed in
+def test_mass_queries_that_are_not_finite(mla, dim, fp8):
+    """An infinite dim of a query gives each token +inf, nothing or NaN, by the sign of its row there
+    (E4M3 has no infinities: NaN); a NaN gives every token of its request NaN.  Other requests are
+    not touched."""
+    c = mass_case(np.random.default_rng(63), 16, 32, [200, 100, 90], fp8)
+    clean = weigh(mla, c)
+    zero = int(c["table"][2][1]), 9  # token 41 of request 2
+    c["cache"][zero[0], zero[1], dim] = 0
+    c["q"][2, 5, dim] = float("inf")
+    got = weigh(mla, c)
+    assert np.array_equal(got[:2], clean[:2])
+    at = mass_rows(c, 2)[:, dim]
+    assert at[41] == 0
+    if fp8:
+        assert np.isnan(got[2, :90]).all()
+    else:
+        assert (got[2, :90][at > 0] == np.inf).all() and np.isnan(got[2, :90][at == 0]).all()
+        want, tol = weights_of(c, 2, [h for h in range(16) if h != 5])
+        assert_within(got[2, :90][at < 0], want[at < 0], tol[at < 0])
+    c["q"][2, 5, dim] = float("nan")
+    got = weigh(mla, c)
+    assert np.array_equal(got[:2], clean[:2]) and np.isnan(got[2, :90]).all()

@@ -335,14 +335,17 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
           }
         }
       }
+      // Both blocks stay until the end of all MMAs has been said to both: that is the last arrival of the MMAs at
+      // a block's barriers, and the meeting at the end does not wait for them.  (From here on, as the first block's
+      // issuer: the budget is that of the last rows, not of the call.)
+      if (!first_block && !mbar_wait(smem_u32(&s.mma_end), 0, nullptr, kWaitBudgetNs)) report(p.dev_status, MLA_ERR_DEVICE_TIMEOUT);
       if (s.abort && first_block)  // let the loads in flight land in both blocks
         for (uint32_t i = items > (uint32_t)p.slots ? items - p.slots : 0; i < items; ++i)
           (void)mbar_wait(smem_u32(&s.full[i % p.slots]), (i / p.slots) & 1u, nullptr, kDrainBudgetNs);
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- S = K Q^T
-    const bool one = elect_one_sync();
-    if (first_block && one) {
+    if (first_block && elect_one_sync()) {
       const uint32_t n8 = (uint32_t)(2 * cols) >> 3;
       // (E4M3: format 0 of A and B; bf16: 1)
       const uint32_t id = (1u << 4) | (kFp8 ? 0u : (1u << 7) | (1u << 10)) | (n8 << 17) | ((uint32_t)(kTile >> 4) << 24);
@@ -379,10 +382,8 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
         mma_commit_pair(smem_u32(&s.q_free));
       }
       mma_commit_pair(smem_u32(&s.mma_end));
+      if (!mbar_wait(smem_u32(&s.mma_end), 0, nullptr, kWaitBudgetNs)) report(p.dev_status, MLA_ERR_DEVICE_TIMEOUT);
     }
-    // Both blocks stay until the end of all MMAs has been said to both: that is the last arrival of the MMAs at
-    // a block's barriers, and the meeting at the end does not wait for them.
-    if (one && !mbar_wait(smem_u32(&s.mma_end), 0, nullptr, kWaitBudgetNs)) report(p.dev_status, MLA_ERR_DEVICE_TIMEOUT);
   } else if (warp == 2) {
     // ---------------------------------------------------------------- queries, bf16
     if (!kFp8 && elect_one_sync()) {

@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 import oracle.eviction as oe
-from eviction_helpers import SCALE, check_mass, check_shared, mass_case, mass_rows, mass_tol, run_mass, run_shared, shared_case
+from eviction_helpers import SCALE, bf16, check_mass, check_shared, i32, mass_case, mass_rows, mass_tol, run_mass, run_shared, shared_case, word
 from prompt_helpers import assert_within, f64
 
 pytestmark = pytest.mark.gpu
@@ -125,3 +125,25 @@ def test_mass_queries_that_are_not_finite(mla, dim, fp8):
     c["q"][2, 5, dim] = float("nan")
     got = weigh(mla, c)
     assert np.array_equal(got[:2], clean[:2]) and np.isnan(got[2, :90]).all()
+
+
+@pytest.mark.parametrize("share", [0.0])
+def test_mass_waits_for_as_long_as_a_piece_takes(mla, share):
+    """Every pair of SMs weighs 27 million tokens (more than 0.1 s), one of them 95% of its own before it
+    comes to the next request's: no wait runs out while tiles go by.  All pages are one."""
+    pairs = torch.cuda.get_device_properties(0).multi_processor_count // 2
+    # of two requests' tokens every pair gets 1 / pairs: the pair whose share ends the first has this part of its own there
+    n = [1 << 30, int((1 << 30) * (pairs / (pairs // 2 + share) - 1)) // 256 * 256]
+    rng = np.random.default_rng(64)
+    cache, q = bf16(rng, 1, 256, 576), bf16(rng, 2, 1, 576)
+    lse = torch.logsumexp((q.double() @ cache[0].double().T) * SCALE, -1).float()
+    mass, status = torch.zeros(2, 1 << 30, device="cuda"), word()
+    mla.mla_attention_mass(q, cache, torch.zeros(2, 1 << 22, dtype=torch.int32, device="cuda"), i32(n), SCALE, lse, mass, dev_status=status)
+    assert int(status) == 0
+    for b in range(2):
+        rows, qb, lb = f64(cache)[0], f64(q)[b], f64(lse)[b]
+        want = oe.mass(qb, rows, SCALE, lb)
+        assert_within(f64(mass[b, :256]), want, mass_tol(qb, rows, SCALE, lb, want, 0.0, False))
+        pages = mass[b, :n[b]].view(-1, 256)
+        assert bool((pages == pages[0]).all())
+        assert not mass[b, n[b]:].any()

@@ -84,7 +84,7 @@ struct Control {
   float sum[2][kOwn][4];                    // of a token's heads, by quarters, by tile parity
   int64_t start_cost, share[2], warp_cost[kThreads / 32];
   int32_t start_chain;
-  uint32_t tmem_base;
+  uint32_t tmem_base, items;  // (items of rows that the loader has asked for)
   int abort;
 };
 
@@ -205,6 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
     init(&s.head_full, kWeighWarps);
     init(&s.mma_end, 1);
     s.abort = 0;
+    s.items = 0;
     fence_mbarrier_init_cluster();
     prefetch_tmap(kBox >= kOwn ? &maps.k3 : &maps.k);
     if (!kFp8) prefetch_tmap(&maps.q);
@@ -330,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
                   for (int k = 0; k < kItemChunks; ++k)
                     tma_load_2d_pair(dst + k * Z::kChunkBytes + i * kBox * Z::kChunkRow, &maps.k, 64 * (c + k), y[i], bar);
             }
-            ++items;
+            *(volatile uint32_t *)&s.items = ++items;
             if (++sl == (uint32_t)p.slots) sl = 0, turn ^= 1u;
           }
         }
@@ -389,8 +390,20 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
     if (!kFp8 && elect_one_sync()) {
       const uint32_t bar = cluster_addr(smem_u32(&s.q_full), 0);
       uint32_t piece = 0;
+      // The last piece's queries are free with its last MMA, which may be any time away: the budget starts
+      // again as long as rows come in.
+      auto wait_piece = [&](uint32_t parity) {
+        for (uint32_t seen = *(volatile uint32_t *)&s.items;;) {
+          if (mbar_wait(smem_u32(&s.q_free), parity, &s.abort, kWaitBudgetNs)) return true;
+          const uint32_t now = *(volatile uint32_t *)&s.items;
+          if (now == seen || *(volatile int *)&s.abort) break;
+          seen = now;
+        }
+        set_abort(s, p.dev_status);
+        return false;
+      };
       while (walk.next()) {
-        if (piece > 0 && !wait(&s.q_free, (piece - 1) & 1u)) break;
+        if (piece > 0 && !wait_piece((piece - 1) & 1u)) break;
         ++piece;
         if (first_block) mbar_arrive_expect_tx(smem_u32(&s.q_full), (uint32_t)(2 * query_bytes<kFp8>(p.half_heads)));
         for (int c = 0; c < kChunks; c += 3)

@@ -127,7 +127,7 @@ def test_mass_queries_that_are_not_finite(mla, dim, fp8):
     assert np.array_equal(got[:2], clean[:2]) and np.isnan(got[2, :90]).all()
 
 
-@pytest.mark.parametrize("share", [0.0])
+@pytest.mark.parametrize("share", [0.0, 0.95])
 def test_mass_waits_for_as_long_as_a_piece_takes(mla, share):
     """Every pair of SMs weighs 27 million tokens (more than 0.1 s), one of them 95% of its own before it
     comes to the next request's: no wait runs out while tiles go by.  All pages are one."""

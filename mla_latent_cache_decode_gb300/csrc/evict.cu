@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveBlocks) compact_kernel(cons
   // Every block of the cluster has this phase's values in registers.  That is all that has to be so before
   // the stores: no block reads what another writes, and a load whose value is here cannot see a later store.
   // So the blocks meet without ordering memory, which would wait for the last phase's stores to arrive.  The
-  // block's own barrier takes in a bit of every value (`seen`), so that no thread passes it with a load under way.
+  // block's own barrier takes in every word that was loaded (`seen`), so that no thread passes it with a load under way.
   auto meet = [&](uint32_t seen) {
     if (__syncthreads_or(seen == 0x9e3779b9u)) __threadfence_block();  // (the answer is used, or the question would go)
     if (nb > 1) cluster_meet();
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveBlocks) compact_kernel(cons
     uint32_t seen = 0;
 #pragma unroll
     for (int u = 0; u < kMoveUnits; ++u)
-      if (to[u] >= 0) seen ^= x[u].x;
+      if (to[u] >= 0) seen ^= x[u].x ^ x[u].y ^ x[u].z ^ x[u].w;
     meet(seen);
 #pragma unroll
     for (int u = 0; u < kMoveUnits; ++u)

@@ -561,8 +561,9 @@ mla_status_t mla_decode_shared(const void *q, const void *cache, int64_t num_blo
  *
  * mla_attention_mass_fp8 — the same over an FP8 cache (rows value(code) * kv_scale).
  * The products run on the codes and on q as the sum of two E4M3 numbers a dim,
- * which is exact for dims of 2^-10 of their head's largest and more, and off by at
- * most 2^-17 of the largest below.
+ * which is exact for dims of 2^-9 of their head's largest and more, and off by at
+ * most 2^-17 of the largest below.  A head whose query is not finite gives every
+ * token NaN (unless its lse is -inf).
  *
  * mla_evict_select — the tokens of each request that stay when it may keep
  * max_keep.  With L = seq_lens[b]: all of them if L <= max_keep; else the first

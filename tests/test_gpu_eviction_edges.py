@@ -5,7 +5,8 @@ import numpy as np
 import pytest
 
 import oracle.eviction as oe
-from eviction_helpers import SCALE, bf16, check_mass, check_shared, i32, mass_case, mass_rows, mass_tol, run_mass, run_shared, shared_case, word
+from eviction_helpers import (SCALE, bf16, check_mass, check_shared, i32, mass_case, mass_rows, mass_tol, paged, run_mass, run_shared,
+                              shared_case, word)
 from prompt_helpers import assert_within, f64
 
 pytestmark = pytest.mark.gpu
@@ -147,3 +148,39 @@ def test_mass_waits_for_as_long_as_a_piece_takes(mla, share):
         pages = mass[b, :n[b]].view(-1, 256)
         assert bool((pages == pages[0]).all())
         assert not mass[b, n[b]:].any()
+
+
+def peaks_case(rng, heads, page, shared_blocks, lens, every=700, rise=11.0):
+    """Scores that are nearly flat but for a token in every 700, four kinds of them in turn: a head of
+    the same kind scores it 2^11 times as high.  A run of tiles that meets its first such token behind
+    its first tile takes what it has so far to the new scale, and by then that is a good part of the
+    result (some 2,800 tokens of 2^-11 a peak)."""
+    table, shared, blocks = paged(rng, lens, page, shared_blocks)
+    B = len(lens)
+    q, cache = bf16(rng, B, heads, 576, by=0.2), bf16(rng, blocks, page, 576)
+    kind = torch.arange(heads, device="cuda") % 4
+    q[..., 512:] = 0
+    q[:, torch.arange(heads, device="cuda"), 512 + kind] = 8.0
+    cache[..., 512:] = 0
+    for b, n in enumerate(lens):
+        for i, t in enumerate(range(every // 2, n, every)):
+            block = shared[t // page] if t < shared_blocks * page else table[b][t // page]
+            cache[int(block), t % page, 512 + i % 4] = rise * np.log(2) / SCALE / 8
+    return dict(lens=lens, table=table, shared=shared, q=q, cache=cache, shared_table=i32(shared), shared_blocks=i32([shared_blocks]),
+                block_table=i32(table), seq_lens=i32(lens), out=torch.full((B, heads, 512), 7.0, dtype=torch.bfloat16, device="cuda"),
+                lse=torch.full((B, heads), 7.0, dtype=torch.float32, device="cuda"), status=word())
+
+
+@pytest.mark.parametrize("heads,page,shared,lens", [
+    (16, 64, 0, [100001]),                                        # a request's own tokens, few heads
+    (128, 128, 0, [90007, 3000]),                                 # ... a full set
+    (16, 64, 700, [44800 + n for n in (1, 77, 600) * 5]),         # packed rows on the shared part, 15 requests
+    (5, 16, 3000, [48000 + n for n in (1, 300) * 13]),            # ... on short pages, a block's second half of the rows empty
+])
+def test_shared_maxima_that_rise_within_a_piece(mla, heads, page, shared, lens):
+    """Pieces of four tiles and more, most of which rescale what they have summed up."""
+    c = peaks_case(np.random.default_rng(65), heads, page, shared, lens)
+    run_shared(mla, c)
+    assert int(c["status"]) == 0
+    some = sorted({0, 1, len(lens) // 2, len(lens) - 1} & set(range(len(lens))))
+    check_shared(dict(c, lens=[lens[b] for b in some], table=c["table"][some], **{k: c[k][some] for k in ("q", "out", "lse")}))

@@ -184,3 +184,13 @@ def test_shared_maxima_that_rise_within_a_piece(mla, heads, page, shared, lens):
     assert int(c["status"]) == 0
     some = sorted({0, 1, len(lens) // 2, len(lens) - 1} & set(range(len(lens))))
     check_shared(dict(c, lens=[lens[b] for b in some], table=c["table"][some], **{k: c[k][some] for k in ("q", "out", "lse")}))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("heads", [3, 40, 100])
+def test_mass_pieces_of_many_tiles(mla, heads, fp8):
+    """Ten tiles and more on every pair of SMs: several rounds of the rings and of S's buffers in a piece."""
+    c = mass_case(np.random.default_rng(66), heads, 64, [100001, 700, 5000], fp8)
+    run_mass(mla, c, previous=c["previous"], decay=0.5)
+    assert int(c["status"]) == 0
+    check_mass(c, 0.5, f64(c["previous"]))

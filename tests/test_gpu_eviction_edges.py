@@ -194,3 +194,24 @@ def test_mass_pieces_of_many_tiles(mla, heads, fp8):
     run_mass(mla, c, previous=c["previous"], decay=0.5)
     assert int(c["status"]) == 0
     check_mass(c, 0.5, f64(c["previous"]))
+
+
+@pytest.mark.parametrize("heads,shared,lens", [(128, 0, [3000] * 6), (16, 32, [2048 + n for n in (100, 700, 300, 500, 600)])])
+def test_shared_partial_results_cost_next_to_nothing(mla, heads, shared, lens):
+    """out's error in units of what two roundings alone leave, the weights' to bf16 and out's own
+    (0.0018 of its size here).  Partial results add at most 2^-12 of the largest of 64 dims, some 2^-10.5
+    of a dim's size; by half steps evenly spread (1 / sqrt 3) and independent of the others' that is
+    0.0004, 2% together.  In bf16 they would add as much as out's own rounding: 20% and more."""
+    c = shared_case(np.random.default_rng(67), heads, 64, shared, lens)
+    run_shared(mla, c)
+    error = least = 0.0
+    for b, n in enumerate(lens):
+        rows = torch.from_numpy(oe.rows_of(f64(c["cache"]), c["table"], b, n, c["shared"])).cuda()
+        x = (c["q"][b].double() @ rows.T) * SCALE
+        w = (x - x.amax(1, keepdim=True)).exp()
+        out, total = w @ rows[:, :512], w.sum(1, keepdim=True)
+        rounded = ((w.to(torch.bfloat16).double() @ rows[:, :512]) / total).to(torch.bfloat16).double()
+        out = out / total
+        least += float(((rounded - out) ** 2).sum())
+        error += float(((c["out"][b].double() - out) ** 2).sum())
+    assert (error / least) ** 0.5 < 1.1

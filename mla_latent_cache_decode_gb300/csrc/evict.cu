@@ -36,8 +36,8 @@
 // in 18.8 us (5.0 TB/s, 74% of the copy rate); eight E4M3 layers: 138 MB in 27.5 us.
 // Before the blocks met without ordering memory: 20.5 and 32 us.  From there: eight
 // units a thread 22.7 and 35.7 us, sixteen 26 and 44; three slices a row 25 and 36,
-// whole rows 40; two blocks an SM asked for instead of four 26 us, eight 20.9 by
-// spilling.
+// whole rows 40; two blocks an SM asked for instead of four 26 us; registers for eight
+// to an SM 20.9, by spilling (for six, as it is, 40 registers and one or two spilled).
 #include <algorithm>
 #include <atomic>
 #include <cmath>

@@ -35,13 +35,13 @@
 // bounded; one that runs out reports MLA_ERR_DEVICE_TIMEOUT and ends the block's
 // others.
 //
-// Measured: 20 x 4,096 tokens, 128 heads 21 us (98 MB, 4.6 TB/s, 68% of the copy
+// Measured: 20 x 4,096 tokens, 128 heads 21.3 us (98 MB, 4.6 TB/s, 68% of the copy
 // rate): 2 us of deal and set-up, then the first tiles of all SMs and 11 MB of
 // queries at once, then ~1.45 us a tile, which is the memory's rate.  E4M3, 131,072
 // + 7 x 1,024 tokens, 16 heads 22 us: 6.6 us until the queries are split and
 // the first tile weighed, then 0.75 us a tile, the memory's rate.  Four weighing
 // warps instead of eight took 2 us more there; a thread that loads its quarter of
-// a query instead of a warp that loads four queries, 2 us.  201 tokens: 5.1 us.
+// a query instead of a warp that loads four queries, 2 us.  201 tokens: 5.2 us.
 #include <algorithm>
 #include <atomic>
 #include <cmath>

@@ -38,8 +38,10 @@
 // would take; queries (72 KB), P (32 KB) and the rings fill the shared memory.
 // Around the tiles a call has ~2 us of deal and set-up, ~4 us until the first P V,
 // ~4 us at each change of chain, and 5 us of merge with its launch.  64 requests
-// of 128 heads on 8,192 + 1 to 777 tokens: 110 us (1.35 PFLOP/s), 58% of the
-// tensor cores' cycles.  From the same 64: one ring and one issuing thread 195 us;
+// of 128 heads on 8,192 + 1 to 777 tokens: 110 us (1.35 PFLOP/s), 59% of the
+// tensor cores' cycles.  Its 28.3 tiles a pair are 139,000 of the kernel's 206,000 clk,
+// deal, first P V and changes of chain some 20,000; where the rest, a fifth, goes
+// has not been measured.  From the same 64: one ring and one issuing thread 195 us;
 // two rings and two threads 163; P by halves 140; eight softmax warps for four
 // 110.  Waits that acquire at cluster scope instead of the block's cost a
 // microsecond each in such a chain (436 us).  Issuing threads as converged warps
@@ -333,7 +335,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
   tc_fence_before();
   cluster_arrive();  // barriers and tensor memory, to both blocks
   griddep_wait();
-  griddep_launch_dependents();  // the merge waits for this grid's end, on the SMs' free threads
+  // The merge's launch is over with before this grid's end; its blocks come as this grid's leave (384 threads of 168
+  // registers, two of them spilled, leave none for a warp of 90).
+  griddep_launch_dependents();
 
   // ---------------------------------------------------------------- the deal
   const int32_t shared_blocks = *p.shared_blocks, my_length = tid < p.batch ? p.seq_lens[tid] : 0;

@@ -528,7 +528,9 @@ mla_status_t mla_prefill(const void *q_nope, int64_t q_nope_token_stride,
  * block_size in {16, 32, 64, 128, 256}; max_blocks_per_seq * block_size and
  * max_shared_blocks * block_size <= 2^30, num_blocks * block_size < 2^31; batch <=
  * 2^20.  Partial results are merged by their fp32 log-sum-exps, as mla_decode's
- * are; they are held in f16 with a power of two for each 64 dims.
+ * are; they are held in f16 with a power of two for each 64 dims.  A partial result's
+ * sum over its tokens is the tensor cores' fp32, which cut: out was 0.6% off with
+ * 3.5 million like tokens to a pair of SMs, 3% with 28 million.
  */
 size_t mla_decode_shared_workspace_size(int32_t batch, int32_t num_heads);
 mla_status_t mla_decode_shared(const void *q, const void *cache, int64_t num_blocks,
